@@ -8,7 +8,8 @@ fallback.
 Low-level functions carry the C names (``rs_sort_keys_u32``, ``rs_sort_pairs_f32``,
 ``rs_temp_bytes``, ``rs_sort``, ...) and accept torch tensors or raw integer
 addresses for pointers.  ``sort()`` is the convenience wrapper that allocates
-outputs and temp with torch.
+outputs and temp with torch.  The expert operators (include/rs_experts.h) are
+bound in ``experts.py`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -72,6 +73,15 @@ SIGNATURES = {
     "rs_sort_host_batches": (_i, [_i, _i, _vp, _vp, _vp, _vp, _sz, _i, _i, _vp, _sz, _vp]),
 }
 SIGNATURES["rs_sort_keys_u32_noalloc"] = (_i, [_vp, _vp, _sz, _i, _i, _vp])
+SIGNATURES["rs_expert_sort_temp_bytes"] = (_sz, [_sz, _i])
+SIGNATURES["rs_expert_sort"] = (_i, [_vp, _i, _sz, _i, _vp, _vp, _vp, _vp, _sz, _vp])
+SIGNATURES["rs_expert_dispatch"] = (_i, [_i, _vp, _sz, _vp, _vp, _sz, _i, _sz, _vp, _sz, _vp])
+SIGNATURES["rs_expert_combine"] = (_i, [_i, _vp, _sz, _vp, _i, _vp, _vp, _sz, _i, _sz, _vp, _sz, _vp])
+SIGNATURES["rs_expert_combine_grad"] = (_i, [_i, _vp, _sz, _vp, _sz, _vp, _i, _vp, _vp, _sz, _i, _sz, _vp, _sz,
+                                             _vp, _vp])
+for _t in ("rs_expert_matmul", "rs_expert_matmul_grad"):
+    SIGNATURES[_t] = (_i, [_vp])
+    SIGNATURES[_t + "_temp_bytes"] = (_sz, [_vp])
 SIGNATURES["rs_lbvh_build"] = (_i, [_vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 LBVH_LEAF = 0x80000000
 NOALLOC_MAX_N = 1 << 22
@@ -349,3 +359,12 @@ def sort(keys, values=None, *, key_type=None, begin_bit=0, end_bit=None, algo="a
                      temp.numel(), stream, algo, radix_bits, descending=descending, value_bytes=vb)
     _check(rs_sort(desc), "rs_sort")
     return keys_out, values_out
+
+
+# The expert operators: tokens sorted by expert and back, and the experts' products.
+from .experts import (ACTIVATIONS, EXPERTS_MAX, FLOAT_TYPES, ExpertMatmulDesc, expert_combine,  # noqa: E402
+                      expert_combine_grad, expert_dispatch, expert_dispatch_grad, expert_matmul,
+                      expert_matmul_grad, expert_sort, rs_expert_combine, rs_expert_combine_grad,
+                      rs_expert_dispatch, rs_expert_matmul, rs_expert_matmul_grad,
+                      rs_expert_matmul_grad_temp_bytes, rs_expert_matmul_temp_bytes, rs_expert_sort,
+                      rs_expert_sort_temp_bytes)

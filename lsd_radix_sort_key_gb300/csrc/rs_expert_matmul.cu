@@ -1,0 +1,446 @@
+// rs_expert_matmul.cu -- rs_expert_matmul and rs_expert_matmul_grad: the
+// experts' products over rows that are laid out by expert.
+//
+// Three products share one form, D = A B^T summed over the reduction index:
+//   forward  D = y [rows, outer],   A = x,    B = w[e],    reduces over inner
+//   dx       D = dx [rows, inner],  A = dz,   B = w[e]^T,  reduces over outer
+//   dw       D = dw[e] [outer, inner], A = dz^T, B = x^T,  reduces over the expert's rows
+// The first two are ragged in D's rows, the third in the reduction.
+#include "rs_expert_groups.cuh"
+
+namespace {
+
+using namespace rsx;
+
+// ------------------------------------------------- products with any strides
+
+// Element (i, k) of A in range e is a[e*a_e + i*a_i + k*a_k]; likewise B(j, k).
+template <typename T>
+struct AnyArgs {
+    const T* a;
+    size_t a_e, a_i, a_k;
+    const T* b;
+    size_t b_e, b_j, b_k;
+    T* d;
+    size_t d_e, d_i;
+    uint32_t cols;       // of D
+    uint32_t reduce;     // ragged rows: the reduction's length
+    uint32_t out_rows;   // ragged reduction: D's rows
+    const int32_t* offsets;
+    uint32_t experts, rows;
+    const T* bias;
+    size_t bias_e;
+    const T* residual;
+    size_t residual_i;
+    T* pre;
+    size_t pre_i;
+};
+
+constexpr int kAnyTile = 64, kAnyK = 16, kAnyThreads = 256;
+
+// One 64 x 64 tile of D per block, 4 x 4 per thread, float32 multiply-adds.
+template <typename T, int ACT, bool RAGGED_K>
+__global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
+{
+    extern __shared__ uint32_t mem[];
+    __shared__ float as[kAnyK][kAnyTile + 4], bs[kAnyK][kAnyTile + 4];
+    const Groups g = Groups::make(mem, p.offsets, p.experts, p.rows, kAnyTile, !RAGGED_K);
+    uint32_t e, i0, i_end, k0, k_end;  // rows of D in [i0, i_end), reduction over [k0, k_end)
+    if constexpr (RAGGED_K) {
+        const uint32_t per = (p.out_rows + kAnyTile - 1) / kAnyTile;
+        e = blockIdx.x / per;
+        i0 = (blockIdx.x - e * per) * kAnyTile;
+        i_end = p.out_rows;
+        k0 = g.off[e];
+        k_end = g.off[e + 1];
+    } else {
+        if (blockIdx.x >= g.tiles()) return;
+        e = g.find(blockIdx.x);
+        i0 = g.off[e] + (blockIdx.x - g.tile[e]) * kAnyTile;
+        i_end = g.off[e + 1];
+        k0 = 0;
+        k_end = e < p.experts ? p.reduce : 0;
+    }
+    const uint32_t j0 = blockIdx.y * kAnyTile, tid = threadIdx.x;
+    const T* a = p.a + e * p.a_e;
+    const T* b = p.b + (e < p.experts ? e * p.b_e : 0);
+    float acc[4][4] = {};
+    for (uint32_t k = k0; k < k_end; k += kAnyK) {
+        for (int l = tid; l < kAnyTile * kAnyK; l += kAnyThreads) {
+            // neighbouring threads read neighbouring elements
+            const uint32_t ai = p.a_k == 1 ? l / kAnyK : l % kAnyTile, ak = p.a_k == 1 ? l % kAnyK : l / kAnyTile;
+            as[ak][ai] = i0 + ai < i_end && k + ak < k_end ? to_float(a[(i0 + ai) * p.a_i + (k + ak) * p.a_k]) : 0.0f;
+            const uint32_t bj = p.b_k == 1 ? l / kAnyK : l % kAnyTile, bk = p.b_k == 1 ? l % kAnyK : l / kAnyTile;
+            bs[bk][bj] = j0 + bj < p.cols && k + bk < k_end ? to_float(b[(j0 + bj) * p.b_j + (k + bk) * p.b_k]) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kk = 0; kk < kAnyK; ++kk) {
+            float av[4], bv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                av[q] = as[kk][tid / 16 + 16 * q];
+                bv[q] = bs[kk][tid % 16 + 16 * q];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t i = i0 + tid / 16 + 16 * r;
+        if (i >= i_end) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t j = j0 + tid % 16 + 16 * c;
+            if (j >= p.cols) continue;
+            float z = acc[r][c], y = 0.0f;
+            if (e < p.experts) {
+                if (p.bias) z += to_float(p.bias[e * p.bias_e + j]);
+                y = activate<ACT>(z);
+                if (p.residual) y += to_float(p.residual[i * p.residual_i + j]);
+            }
+            if (p.pre) p.pre[i * p.pre_i + j] = from_float<T>(z);
+            p.d[(RAGGED_K ? e * p.d_e : 0) + i * p.d_i + j] = from_float<T>(y);
+        }
+    }
+}
+
+template <typename T, int ACT>
+rs_status launch_any_rows(const AnyArgs<T>& p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)max_tiles(p.rows, p.experts, kAnyTile), (unsigned)ceil_div(p.cols, kAnyTile));
+    k_product_any<T, ACT, false><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+template <typename T>
+rs_status launch_any_reduce(const AnyArgs<T>& p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)(ceil_div(p.out_rows, kAnyTile) * p.experts), (unsigned)ceil_div(p.cols, kAnyTile));
+    k_product_any<T, RS_ACT_NONE, true><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+// ------------------------------------------- dz = dy * act'(pre), and dbias
+
+constexpr int kDzRows = 64, kDzThreads = 256, kDzWarps = kDzThreads / 32;
+
+// One block takes a tile of at most 64 rows of one expert and 32 vectors of
+// columns; each warp every eighth row.  part (if given) receives the tile's
+// column sums, [row tile][cols].
+template <typename T, int ACT, int N>
+__global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ dy, size_t dy_i,
+                                                         const T* __restrict__ pre, size_t pre_i, T* __restrict__ dz,
+                                                         size_t dz_i, float* __restrict__ part,
+                                                         const int32_t* __restrict__ offsets, uint32_t experts,
+                                                         uint32_t rows, uint32_t cols)
+{
+    extern __shared__ uint32_t mem[];
+    __shared__ float sums[kDzWarps][32 * N];
+    const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
+    if (blockIdx.x >= g.tiles()) return;
+    const uint32_t e = g.find(blockIdx.x), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t r0 = g.off[e] + (blockIdx.x - g.tile[e]) * kDzRows;
+    const uint32_t r_end = min(r0 + kDzRows, g.off[e + 1]);
+    const uint32_t c = (blockIdx.y * 32 + lane) * N;
+    float sum[N] = {};
+    if (c < cols)
+#pragma unroll 4
+        for (uint32_t r = r0 + warp; r < r_end; r += kDzWarps) {
+            const Vec<T, N> d = load_vec<T, N>(dy + r * dy_i + c);
+            Vec<T, N> z{};
+            if constexpr (ACT != RS_ACT_NONE) z = load_vec<T, N>(pre + r * pre_i + c);
+            Vec<T, N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float v = to_float(d.v[i]) * activate_grad<ACT>(to_float(z.v[i]));
+                sum[i] += v;
+                o.v[i] = from_float<T>(v);
+            }
+            if (dz) store_vec<T, N>(dz + r * dz_i + c, o);
+        }
+    if (!part) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[warp][lane * N + i] = sum[i];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 32 * N; i += kDzThreads) {
+        const uint32_t col = blockIdx.y * 32 * N + i;
+        if (col >= cols) break;
+        float s = 0.0f;
+        for (int w = 0; w < kDzWarps; ++w) s += sums[w][i];
+        part[(size_t)blockIdx.x * cols + col] = s;
+    }
+}
+
+// dbias[e] = the sum of its row tiles' sums, in order.
+template <typename T>
+__global__ void __launch_bounds__(kDzThreads) k_bias_grad(const float* __restrict__ part, T* __restrict__ dbias,
+                                                          const int32_t* __restrict__ offsets, uint32_t experts,
+                                                          uint32_t rows, uint32_t cols)
+{
+    extern __shared__ uint32_t mem[];
+    const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
+    const uint32_t e = blockIdx.x, c = blockIdx.y * kDzThreads + threadIdx.x;
+    if (c >= cols) return;
+    float s = 0.0f;
+    for (uint32_t t = g.tile[e]; t < g.tile[e + 1]; ++t) s += part[(size_t)t * cols + c];
+    dbias[(size_t)e * cols + c] = from_float<T>(s);
+}
+
+// ------------------------------------------------------------- host side
+
+struct GradLayout {
+    size_t dz;  // byte offsets in temp; dz rows are padded to 16 bytes
+    size_t dz_stride;
+    size_t part;
+    size_t total;
+};
+
+GradLayout grad_layout(const rs_expert_matmul_desc* d)
+{
+    const size_t eb = type_bytes(d->type);
+    GradLayout l{};
+    size_t at = 0;
+    if (d->activation != RS_ACT_NONE && (d->dx || d->dw)) {
+        l.dz_stride = align_up(d->outer, 16 / eb);
+        at += align_up(d->rows * l.dz_stride * eb, 256);
+    }
+    l.part = at;
+    if (d->dbias) at += align_up(max_tiles(d->rows, d->num_experts, kDzRows) * d->outer * 4, 256);
+    l.total = at;
+    return l;
+}
+
+rs_status check_common(const rs_expert_matmul_desc* d)
+{
+    if (!d || !valid_type(d->type)) return RS_ERR_INVALID_ARG;
+    if (d->activation < RS_ACT_NONE || d->activation > RS_ACT_SILU) return RS_ERR_INVALID_ARG;
+    if (d->num_experts < 1 || d->num_experts > RS_EXPERTS_MAX) return RS_ERR_INVALID_ARG;
+    if (d->rows > RS_EXPERT_SLOTS_MAX || d->inner > RS_EXPERT_WIDTH_MAX || d->outer > RS_EXPERT_WIDTH_MAX)
+        return RS_ERR_INVALID_ARG;
+    return RS_OK;
+}
+
+// The last weight's element offset plus one, checked against 2^62 bytes.
+size_t weight_span(const rs_expert_matmul_desc* d)
+{
+    return (size_t)(d->num_experts - 1) * d->w_expert_stride + (d->outer - 1) * d->w_outer_stride +
+           (d->inner - 1) * d->w_inner_stride + 1;
+}
+
+rs_status check_weights(const rs_expert_matmul_desc* d)
+{
+    const size_t most = (size_t)1 << 40, eb = type_bytes(d->type);
+    if (!d->w || (uintptr_t)d->w % eb) return RS_ERR_INVALID_ARG;
+    if (d->w_expert_stride > most || d->w_outer_stride > most || d->w_inner_stride > most) return RS_ERR_INVALID_ARG;
+    if (d->w_inner_stride != 1 && d->w_outer_stride != 1 && d->inner != 1 && d->outer != 1) return RS_ERR_INVALID_ARG;
+    return RS_OK;
+}
+
+template <typename F>
+rs_status by_act(int act, F f)
+{
+    switch (act) {
+    case RS_ACT_NONE: return f(Int<RS_ACT_NONE>{});
+    case RS_ACT_RELU: return f(Int<RS_ACT_RELU>{});
+    case RS_ACT_GELU: return f(Int<RS_ACT_GELU>{});
+    default:          return f(Int<RS_ACT_SILU>{});
+    }
+}
+
+template <typename T>
+AnyArgs<T> any_args(const rs_expert_matmul_desc* d)
+{
+    AnyArgs<T> p{};
+    p.offsets = d->offsets;
+    p.experts = (uint32_t)d->num_experts;
+    p.rows = (uint32_t)d->rows;
+    return p;
+}
+
+template <typename T>
+rs_status forward(const rs_expert_matmul_desc* d)
+{
+    AnyArgs<T> p = any_args<T>(d);
+    p.a = static_cast<const T*>(d->x);
+    p.a_i = d->x_stride;
+    p.a_k = 1;
+    p.b = static_cast<const T*>(d->w);
+    p.b_e = d->w_expert_stride;
+    p.b_j = d->w_outer_stride;
+    p.b_k = d->w_inner_stride;
+    p.d = static_cast<T*>(d->y);
+    p.d_i = d->y_stride;
+    p.cols = (uint32_t)d->outer;
+    p.reduce = (uint32_t)d->inner;
+    p.bias = static_cast<const T*>(d->bias);
+    p.bias_e = d->bias_stride;
+    p.residual = static_cast<const T*>(d->residual);
+    p.residual_i = d->residual_stride;
+    p.pre = static_cast<T*>(d->pre);
+    p.pre_i = d->pre_stride;
+    return by_act(d->activation, [&](auto act) {
+        return launch_any_rows<T, decltype(act)::value>(p, static_cast<cudaStream_t>(d->stream));
+    });
+}
+
+template <typename T>
+rs_status gradient(const rs_expert_matmul_desc* d)
+{
+    cudaStream_t s = static_cast<cudaStream_t>(d->stream);
+    const size_t eb = sizeof(T), groups = Groups::words(d->num_experts) * 4;
+    const uint32_t experts = (uint32_t)d->num_experts, rows = (uint32_t)d->rows, cols = (uint32_t)d->outer;
+    const GradLayout l = grad_layout(d);
+    char* temp = static_cast<char*>(d->temp);
+    const bool act = d->activation != RS_ACT_NONE;
+    const T* dy = static_cast<const T*>(d->y);
+    const T* pre = static_cast<const T*>(d->pre);
+    T* dz = act && (d->dx || d->dw) ? reinterpret_cast<T*>(temp + l.dz) : nullptr;
+    const T* g = act ? dz : dy;
+    const size_t g_stride = act ? l.dz_stride : d->y_stride;
+    float* part = d->dbias ? reinterpret_cast<float*>(temp + l.part) : nullptr;
+    if ((dz || part) && cols) {
+        constexpr int kVec = 16 / sizeof(T);
+        const bool vec = aligned16(dy, d->y_stride, eb) && (!act || aligned16(pre, d->pre_stride, eb)) &&
+                         d->outer % kVec == 0;
+        const rs_status st = by_act(d->activation, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+            const unsigned tiles = (unsigned)max_tiles(rows, experts, kDzRows);
+            if (vec)
+                k_act_grad<T, ACT, kVec><<<dim3(tiles, (unsigned)ceil_div(cols, 32 * kVec)), kDzThreads, groups, s>>>(
+                    dy, d->y_stride, pre, d->pre_stride, dz, l.dz_stride, part, d->offsets, experts, rows, cols);
+            else
+                k_act_grad<T, ACT, 1><<<dim3(tiles, (unsigned)ceil_div(cols, 32)), kDzThreads, groups, s>>>(
+                    dy, d->y_stride, pre, d->pre_stride, dz, l.dz_stride, part, d->offsets, experts, rows, cols);
+            return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+        });
+        if (st != RS_OK) return st;
+    }
+    if (part && cols) {
+        k_bias_grad<T><<<dim3(experts, (unsigned)ceil_div(cols, kDzThreads)), kDzThreads, groups, s>>>(
+            part, static_cast<T*>(d->dbias), d->offsets, experts, rows, cols);
+        if (cudaGetLastError() != cudaSuccess) return RS_ERR_CUDA;
+    }
+    if (d->dx && rows && d->inner) {
+        AnyArgs<T> p = any_args<T>(d);
+        p.a = g;
+        p.a_i = g_stride;
+        p.a_k = 1;
+        p.b = static_cast<const T*>(d->w);
+        p.b_e = d->w_expert_stride;
+        p.b_j = d->w_inner_stride;
+        p.b_k = d->w_outer_stride;
+        p.d = static_cast<T*>(d->dx);
+        p.d_i = d->dx_stride;
+        p.cols = (uint32_t)d->inner;
+        p.reduce = cols;
+        const rs_status st = launch_any_rows<T, RS_ACT_NONE>(p, s);
+        if (st != RS_OK) return st;
+    }
+    if (d->dw && d->inner && cols) {
+        AnyArgs<T> p = any_args<T>(d);
+        p.a = g;
+        p.a_i = 1;
+        p.a_k = g_stride;
+        p.b = static_cast<const T*>(d->x);
+        p.b_j = 1;
+        p.b_k = d->x_stride;
+        p.d = static_cast<T*>(d->dw);
+        p.d_e = d->outer * d->inner;
+        p.d_i = d->inner;
+        p.cols = (uint32_t)d->inner;
+        p.out_rows = cols;
+        const rs_status st = launch_any_reduce<T>(p, s);
+        if (st != RS_OK) return st;
+    }
+    return RS_OK;
+}
+
+template <typename F>
+rs_status by_type(int type, F f)
+{
+    switch (type) {
+    case RS_FLOAT32: return f(float{});
+    case RS_FLOAT16: return f(__half{});
+    default:         return f(__nv_bfloat16{});
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rs_expert_matmul_temp_bytes(const rs_expert_matmul_desc* d)
+{
+    return check_common(d) == RS_OK ? 0 : (size_t)-1;
+}
+
+rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
+{
+    rs_status st = check_common(d);
+    if (st != RS_OK) return st;
+    if (d->rows == 0 || d->outer == 0) return RS_OK;
+    const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows;
+    if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
+    if (!valid_rows(d->y, eb, yw, d->y_stride, false)) return RS_ERR_INVALID_ARG;
+    if (d->pre && !valid_rows(d->pre, eb, yw, d->pre_stride, false)) return RS_ERR_INVALID_ARG;
+    if (d->bias && !valid_rows(d->bias, eb, yw, d->bias_stride, true)) return RS_ERR_INVALID_ARG;
+    if (d->residual && !valid_rows(d->residual, eb, yw, d->residual_stride, true)) return RS_ERR_INVALID_ARG;
+    if (xw) {
+        if (!valid_rows(d->x, eb, xw, d->x_stride, true)) return RS_ERR_INVALID_ARG;
+        if ((st = check_weights(d)) != RS_OK) return st;
+    }
+    const Range r[] = {{d->y, span_bytes(n, yw, d->y_stride, eb)},
+                       {d->pre, d->pre ? span_bytes(n, yw, d->pre_stride, eb) : 0},
+                       {d->x, span_bytes(n, xw, d->x_stride, eb)},
+                       {d->w, xw ? weight_span(d) * eb : 0},
+                       {d->bias, d->bias ? span_bytes(d->num_experts, yw, d->bias_stride, eb) : 0},
+                       {d->residual, d->residual ? span_bytes(n, yw, d->residual_stride, eb) : 0},
+                       {d->offsets, ((size_t)d->num_experts + 1) * 4}};
+    if (any_alias(r, 2, 7)) return RS_ERR_ALIAS;
+    return by_type(d->type, [&](auto t) { return forward<decltype(t)>(d); });
+}
+
+size_t rs_expert_matmul_grad_temp_bytes(const rs_expert_matmul_desc* d)
+{
+    return check_common(d) == RS_OK ? grad_layout(d).total : (size_t)-1;
+}
+
+rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
+{
+    rs_status st = check_common(d);
+    if (st != RS_OK) return st;
+    if (!d->dx && !d->dw && !d->dbias) return RS_OK;
+    const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows, need = grad_layout(d).total;
+    const bool act = d->activation != RS_ACT_NONE;
+    if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
+    if (need && (!d->temp || (uintptr_t)d->temp % 256)) return RS_ERR_INVALID_ARG;
+    if (need && d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+    if ((uintptr_t)d->dw % eb || (uintptr_t)d->dbias % eb) return RS_ERR_INVALID_ARG;
+    if (n && yw) {
+        if (!valid_rows(d->y, eb, yw, d->y_stride, true)) return RS_ERR_INVALID_ARG;
+        if (act && !valid_rows(d->pre, eb, yw, d->pre_stride, true)) return RS_ERR_INVALID_ARG;
+    }
+    if (d->dw && n && xw && !valid_rows(d->x, eb, xw, d->x_stride, true)) return RS_ERR_INVALID_ARG;
+    if (d->dx && n && xw) {
+        if (!valid_rows(d->dx, eb, xw, d->dx_stride, false)) return RS_ERR_INVALID_ARG;
+        if (yw && (st = check_weights(d)) != RS_OK) return st;
+    }
+    const Range r[] = {{d->dx, d->dx ? span_bytes(n, xw, d->dx_stride, eb) : 0},
+                       {d->dw, d->dw ? (size_t)d->num_experts * xw * yw * eb : 0},
+                       {d->dbias, d->dbias ? (size_t)d->num_experts * yw * eb : 0},
+                       {d->temp, need},
+                       {d->y, span_bytes(n, yw, d->y_stride, eb)},
+                       {act ? d->pre : nullptr, span_bytes(n, yw, d->pre_stride, eb)},
+                       {d->dw ? d->x : nullptr, span_bytes(n, xw, d->x_stride, eb)},
+                       {d->dx ? d->w : nullptr, xw && yw ? weight_span(d) * eb : 0},
+                       {d->offsets, ((size_t)d->num_experts + 1) * 4}};
+    if (any_alias(r, 4, 9)) return RS_ERR_ALIAS;
+    return by_type(d->type, [&](auto t) { return gradient<decltype(t)>(d); });
+}
+
+}  // extern "C"
