@@ -130,8 +130,12 @@ rs_status rs_expert_combine_grad(rs_float_type type, const void* dout, size_t do
  * and w are; dbias sums the unrounded values.
  *
  * temp: 256-byte aligned scratch of at least rs_expert_matmul_temp_bytes /
- * rs_expert_matmul_grad_temp_bytes bytes (NULL when that is 0), computed from
- * the same descriptor; (size_t)-1 for one the call would reject.
+ * rs_expert_matmul_grad_temp_bytes bytes, computed from the same descriptor;
+ * (size_t)-1 for one the call would reject.  rs_expert_matmul_status waits for
+ * `stream` and says whether the last call with this temp ran to its end:
+ * RS_OK, RS_ERR_DEVICE_TIMEOUT (a wait inside a tensor-core kernel ran out
+ * after about two seconds; its outputs are then not complete), RS_ERR_CUDA.
+ * Meaningful after a call that enqueued work.
  * rows == 0: dw and dbias are still written (zero).  Sizes: rows <=
  * RS_EXPERT_SLOTS_MAX, inner and outer <= RS_EXPERT_WIDTH_MAX; inner == 0 is
  * allowed (a product of nothing), outer == 0 is a no-op.
@@ -165,12 +169,16 @@ typedef struct rs_expert_matmul_desc {
     void* temp;
     size_t temp_bytes;
     void* stream;
+    /* Testing hook, 0 in normal use: t + 1 makes the tensor-core kernels never
+     * copy the operands of output tile t, so the waits for them run out. */
+    int32_t stall_tile;
 } rs_expert_matmul_desc;
 
 size_t rs_expert_matmul_temp_bytes(const rs_expert_matmul_desc* desc);
 rs_status rs_expert_matmul(const rs_expert_matmul_desc* desc);
 size_t rs_expert_matmul_grad_temp_bytes(const rs_expert_matmul_desc* desc);
 rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* desc);
+rs_status rs_expert_matmul_status(const void* temp, void* stream);
 
 #ifdef __cplusplus
 }

@@ -82,6 +82,7 @@ SIGNATURES["rs_expert_combine_grad"] = (_i, [_i, _vp, _sz, _vp, _sz, _vp, _i, _v
 for _t in ("rs_expert_matmul", "rs_expert_matmul_grad"):
     SIGNATURES[_t] = (_i, [_vp])
     SIGNATURES[_t + "_temp_bytes"] = (_sz, [_vp])
+SIGNATURES["rs_expert_matmul_status"] = (_i, [_vp, _vp])
 SIGNATURES["rs_lbvh_build"] = (_i, [_vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 LBVH_LEAF = 0x80000000
 NOALLOC_MAX_N = 1 << 22
@@ -366,5 +367,5 @@ from .experts import (ACTIVATIONS, EXPERTS_MAX, FLOAT_TYPES, ExpertMatmulDesc, e
                       expert_combine_grad, expert_dispatch, expert_dispatch_grad, expert_matmul,
                       expert_matmul_grad, expert_sort, rs_expert_combine, rs_expert_combine_grad,
                       rs_expert_dispatch, rs_expert_matmul, rs_expert_matmul_grad,
-                      rs_expert_matmul_grad_temp_bytes, rs_expert_matmul_temp_bytes, rs_expert_sort,
-                      rs_expert_sort_temp_bytes)
+                      rs_expert_matmul_grad_temp_bytes, rs_expert_matmul_status, rs_expert_matmul_temp_bytes,
+                      rs_expert_sort, rs_expert_sort_temp_bytes)

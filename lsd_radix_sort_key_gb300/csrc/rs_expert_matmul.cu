@@ -5,8 +5,25 @@
 //   forward  D = y [rows, outer],   A = x,    B = w[e],    reduces over inner
 //   dx       D = dx [rows, inner],  A = dz,   B = w[e]^T,  reduces over outer
 //   dw       D = dw[e] [outer, inner], A = dz^T, B = x^T,  reduces over the expert's rows
-// The first two are ragged in D's rows, the third in the reduction.
+// The first two are ragged in D's rows, the third in the reduction.  16-bit
+// operands whose rows are 16-byte aligned take the tensor cores
+// (rs_expert_tc.cuh); float32 and every other layout the kernel below.
 #include "rs_expert_groups.cuh"
+#include "rs_expert_tc.cuh"
+
+// Instantiated in rs_expert_tc_<type>.cu; not here.
+namespace rsx {
+extern template rs_status tc_ragged_rows<__half>(const TcOperand<__half>&, const TcOperand<__half>&, TcArgs<__half>,
+                                                 cudaStream_t);
+extern template rs_status tc_ragged_reduce<__half>(const TcOperand<__half>&, const TcOperand<__half>&, TcArgs<__half>,
+                                                   cudaStream_t);
+extern template rs_status tc_ragged_rows<__nv_bfloat16>(const TcOperand<__nv_bfloat16>&,
+                                                        const TcOperand<__nv_bfloat16>&, TcArgs<__nv_bfloat16>,
+                                                        cudaStream_t);
+extern template rs_status tc_ragged_reduce<__nv_bfloat16>(const TcOperand<__nv_bfloat16>&,
+                                                          const TcOperand<__nv_bfloat16>&, TcArgs<__nv_bfloat16>,
+                                                          cudaStream_t);
+}  // namespace rsx
 
 namespace {
 
@@ -193,6 +210,9 @@ __global__ void __launch_bounds__(kDzThreads) k_bias_grad(const float* __restric
 
 // ------------------------------------------------------------- host side
 
+// temp starts with the status words of the tensor-core kernels.
+constexpr size_t kStatusBytes = kStatusWords * 4;
+
 struct GradLayout {
     size_t dz;  // byte offsets in temp; dz rows are padded to 16 bytes
     size_t dz_stride;
@@ -204,8 +224,9 @@ GradLayout grad_layout(const rs_expert_matmul_desc* d)
 {
     const size_t eb = type_bytes(d->type);
     GradLayout l{};
-    size_t at = 0;
+    size_t at = kStatusBytes;
     if (d->activation != RS_ACT_NONE && (d->dx || d->dw)) {
+        l.dz = at;
         l.dz_stride = align_up(d->outer, 16 / eb);
         at += align_up(d->rows * l.dz_stride * eb, 256);
     }
@@ -219,7 +240,7 @@ rs_status check_common(const rs_expert_matmul_desc* d)
 {
     if (!d || !valid_type(d->type)) return RS_ERR_INVALID_ARG;
     if (d->activation < RS_ACT_NONE || d->activation > RS_ACT_SILU) return RS_ERR_INVALID_ARG;
-    if (d->num_experts < 1 || d->num_experts > RS_EXPERTS_MAX) return RS_ERR_INVALID_ARG;
+    if (d->num_experts < 1 || d->num_experts > RS_EXPERTS_MAX || d->stall_tile < 0) return RS_ERR_INVALID_ARG;
     if (d->rows > RS_EXPERT_SLOTS_MAX || d->inner > RS_EXPERT_WIDTH_MAX || d->outer > RS_EXPERT_WIDTH_MAX)
         return RS_ERR_INVALID_ARG;
     return RS_OK;
@@ -253,6 +274,33 @@ rs_status by_act(int act, F f)
 }
 
 template <typename T>
+TcArgs<T> tc_args(const rs_expert_matmul_desc* d, size_t first_word, size_t words)
+{
+    TcArgs<T> p{};
+    p.offsets = d->offsets;
+    p.experts = (uint32_t)d->num_experts;
+    p.rows = (uint32_t)d->rows;
+    p.status = static_cast<uint32_t*>(d->temp) + first_word;
+    p.status_words = (uint32_t)words;
+    p.stall = (uint32_t)d->stall_tile;
+    return p;
+}
+
+// The weights as an operand whose rows run over outer (forward) or inner (dx);
+// false if neither of the matrix's sides is adjacent.
+template <typename T>
+bool weight_operand(const rs_expert_matmul_desc* d, bool rows_are_outer, TcOperand<T>* b)
+{
+    const bool k_adjacent = rows_are_outer ? d->w_inner_stride == 1 : d->w_outer_stride == 1;
+    const bool mn_adjacent = rows_are_outer ? d->w_outer_stride == 1 : d->w_inner_stride == 1;
+    const size_t other = d->w_inner_stride == 1 ? d->w_outer_stride : d->w_inner_stride;
+    const size_t width = d->w_inner_stride == 1 ? d->inner : d->outer;
+    if ((!k_adjacent && !mn_adjacent) || other < width) return false;
+    *b = TcOperand<T>{static_cast<const T*>(d->w), other, d->num_experts > 1 ? d->w_expert_stride : 0, !k_adjacent};
+    return true;
+}
+
+template <typename T>
 AnyArgs<T> any_args(const rs_expert_matmul_desc* d)
 {
     AnyArgs<T> p{};
@@ -265,6 +313,27 @@ AnyArgs<T> any_args(const rs_expert_matmul_desc* d)
 template <typename T>
 rs_status forward(const rs_expert_matmul_desc* d)
 {
+    cudaStream_t s = static_cast<cudaStream_t>(d->stream);
+    if constexpr (sizeof(T) == 2) {
+        TcOperand<T> b;
+        if (d->inner && weight_operand<T>(d, true, &b)) {
+            TcArgs<T> p = tc_args<T>(d, 0, kStatusWords);
+            p.cols = (uint32_t)d->outer;
+            p.reduce = (uint32_t)d->inner;
+            p.act = d->activation;
+            p.d = static_cast<T*>(d->y);
+            p.d_i = d->y_stride;
+            p.bias = static_cast<const T*>(d->bias);
+            p.bias_e = d->bias_stride;
+            p.residual = static_cast<const T*>(d->residual);
+            p.residual_i = d->residual_stride;
+            p.pre = static_cast<T*>(d->pre);
+            p.pre_i = d->pre_stride;
+            const rs_status st = tc_ragged_rows<T>({static_cast<const T*>(d->x), d->x_stride, 0, false}, b, p, s);
+            if (st != RS_ERR_UNSUPPORTED) return st;
+        }
+    }
+    if (cudaMemsetAsync(d->temp, 0, kStatusBytes, s) != cudaSuccess) return RS_ERR_CUDA;
     AnyArgs<T> p = any_args<T>(d);
     p.a = static_cast<const T*>(d->x);
     p.a_i = d->x_stride;
@@ -284,7 +353,7 @@ rs_status forward(const rs_expert_matmul_desc* d)
     p.pre = static_cast<T*>(d->pre);
     p.pre_i = d->pre_stride;
     return by_act(d->activation, [&](auto act) {
-        return launch_any_rows<T, decltype(act)::value>(p, static_cast<cudaStream_t>(d->stream));
+        return launch_any_rows<T, decltype(act)::value>(p, s);
     });
 }
 
@@ -325,7 +394,43 @@ rs_status gradient(const rs_expert_matmul_desc* d)
             part, static_cast<T*>(d->dbias), d->offsets, experts, rows, cols);
         if (cudaGetLastError() != cudaSuccess) return RS_ERR_CUDA;
     }
-    if (d->dx && rows && d->inner) {
+    // dx and dw share the status words; what takes none of them leaves them clear.
+    const bool want_dx = d->dx && rows && d->inner, want_dw = d->dw && d->inner && cols;
+    bool tc_dx = false, tc_dw = false;
+    if constexpr (sizeof(T) == 2) {
+        TcOperand<T> b;
+        if (want_dx && cols && weight_operand<T>(d, false, &b)) {
+            TcArgs<T> p = tc_args<T>(d, 0, want_dw ? kStatusWords / 2 : kStatusWords);
+            p.cols = (uint32_t)d->inner;
+            p.reduce = cols;
+            p.d = static_cast<T*>(d->dx);
+            p.d_i = d->dx_stride;
+            const rs_status st = tc_ragged_rows<T>({g, g_stride, 0, false}, b, p, s);
+            if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
+            tc_dx = st == RS_OK;
+        }
+        if (want_dw && rows) {
+            TcArgs<T> p = tc_args<T>(d, want_dx ? kStatusWords / 2 : 0, want_dx ? kStatusWords / 2 : kStatusWords);
+            p.cols = (uint32_t)d->inner;
+            p.out_rows = cols;
+            p.d = static_cast<T*>(d->dw);
+            p.d_e = d->outer * d->inner;
+            p.d_i = d->inner;
+            const rs_status st =
+                tc_ragged_reduce<T>({g, g_stride, 0, true}, {static_cast<const T*>(d->x), d->x_stride, 0, true}, p, s);
+            if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
+            tc_dw = st == RS_OK;
+        }
+    }
+    if (!tc_dx && (!want_dw || want_dx)) {
+        const size_t bytes = want_dx && want_dw ? kStatusBytes / 2 : kStatusBytes;
+        if (cudaMemsetAsync(temp, 0, bytes, s) != cudaSuccess) return RS_ERR_CUDA;
+    }
+    if (!tc_dw && want_dw) {
+        const size_t skip = want_dx ? kStatusBytes / 2 : 0;
+        if (cudaMemsetAsync(temp + skip, 0, kStatusBytes - skip, s) != cudaSuccess) return RS_ERR_CUDA;
+    }
+    if (want_dx && !tc_dx) {
         AnyArgs<T> p = any_args<T>(d);
         p.a = g;
         p.a_i = g_stride;
@@ -341,7 +446,7 @@ rs_status gradient(const rs_expert_matmul_desc* d)
         const rs_status st = launch_any_rows<T, RS_ACT_NONE>(p, s);
         if (st != RS_OK) return st;
     }
-    if (d->dw && d->inner && cols) {
+    if (want_dw && !tc_dw) {
         AnyArgs<T> p = any_args<T>(d);
         p.a = g;
         p.a_i = 1;
@@ -376,7 +481,7 @@ extern "C" {
 
 size_t rs_expert_matmul_temp_bytes(const rs_expert_matmul_desc* d)
 {
-    return check_common(d) == RS_OK ? 0 : (size_t)-1;
+    return check_common(d) == RS_OK ? kStatusBytes : (size_t)-1;
 }
 
 rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
@@ -386,6 +491,8 @@ rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
     if (d->rows == 0 || d->outer == 0) return RS_OK;
     const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows;
     if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
+    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
+    if (d->temp_bytes < kStatusBytes) return RS_ERR_TEMP_TOO_SMALL;
     if (!valid_rows(d->y, eb, yw, d->y_stride, false)) return RS_ERR_INVALID_ARG;
     if (d->pre && !valid_rows(d->pre, eb, yw, d->pre_stride, false)) return RS_ERR_INVALID_ARG;
     if (d->bias && !valid_rows(d->bias, eb, yw, d->bias_stride, true)) return RS_ERR_INVALID_ARG;
@@ -396,12 +503,13 @@ rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
     }
     const Range r[] = {{d->y, span_bytes(n, yw, d->y_stride, eb)},
                        {d->pre, d->pre ? span_bytes(n, yw, d->pre_stride, eb) : 0},
+                       {d->temp, kStatusBytes},
                        {d->x, span_bytes(n, xw, d->x_stride, eb)},
                        {d->w, xw ? weight_span(d) * eb : 0},
                        {d->bias, d->bias ? span_bytes(d->num_experts, yw, d->bias_stride, eb) : 0},
                        {d->residual, d->residual ? span_bytes(n, yw, d->residual_stride, eb) : 0},
                        {d->offsets, ((size_t)d->num_experts + 1) * 4}};
-    if (any_alias(r, 2, 7)) return RS_ERR_ALIAS;
+    if (any_alias(r, 3, 8)) return RS_ERR_ALIAS;
     return by_type(d->type, [&](auto t) { return forward<decltype(t)>(d); });
 }
 
@@ -418,8 +526,8 @@ rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
     const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows, need = grad_layout(d).total;
     const bool act = d->activation != RS_ACT_NONE;
     if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
-    if (need && (!d->temp || (uintptr_t)d->temp % 256)) return RS_ERR_INVALID_ARG;
-    if (need && d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
+    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
+    if (d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
     if ((uintptr_t)d->dw % eb || (uintptr_t)d->dbias % eb) return RS_ERR_INVALID_ARG;
     if (n && yw) {
         if (!valid_rows(d->y, eb, yw, d->y_stride, true)) return RS_ERR_INVALID_ARG;
@@ -441,6 +549,19 @@ rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
                        {d->offsets, ((size_t)d->num_experts + 1) * 4}};
     if (any_alias(r, 4, 9)) return RS_ERR_ALIAS;
     return by_type(d->type, [&](auto t) { return gradient<decltype(t)>(d); });
+}
+
+rs_status rs_expert_matmul_status(const void* temp, void* stream)
+{
+    if (!temp) return RS_ERR_INVALID_ARG;
+    uint32_t words[kStatusWords];
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cudaMemcpyAsync(words, temp, sizeof words, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return RS_ERR_CUDA;
+    for (uint32_t w : words)
+        if (w) return RS_ERR_DEVICE_TIMEOUT;
+    return RS_OK;
 }
 
 }  // extern "C"

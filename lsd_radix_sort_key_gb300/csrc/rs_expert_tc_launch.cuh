@@ -1,0 +1,73 @@
+// rs_expert_tc_launch.cuh -- the host side of rs_expert_tc.cuh: tensor maps
+// and launches.  Included by one translation unit per element type.
+#pragma once
+
+#include "rs_expert_tc.cuh"
+
+namespace rsx {
+
+constexpr int kMaxDevices = 64;
+
+// SMs of the current device; 0 on failure.
+inline int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+template <typename T, int BN, bool RAGGED_K, bool B_MN>
+rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T>& args, size_t tiles, cudaStream_t s)
+{
+    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN>;
+    const size_t smem = TcShape<BN>::smem(args.experts);
+    const int sms = sm_count();
+    if (sms < 1) return RS_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return RS_ERR_CUDA;
+    size_t grid = (size_t)sms < tiles ? (size_t)sms : tiles;
+    if (grid > kTcMaxBlocks) grid = kTcMaxBlocks;
+    kernel<<<(unsigned)grid, kTcThreads, smem, s>>>(ma, mb, args);
+    return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+template <typename T>
+rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
+{
+    constexpr bool kBf16 = !__is_same(T, __half);
+    const bool wide = args.cols > 128;
+    const uint64_t experts = b.expert_stride ? args.experts : 1;
+    args.b_expert = b.expert_stride ? 1 : 0;
+    CUtensorMap ma, mb;
+    const uint64_t da[2] = {args.reduce, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
+    const uint64_t db[3] = {b.mn ? args.cols : args.reduce, b.mn ? args.reduce : args.cols, experts};
+    const uint64_t sb[2] = {(uint64_t)b.row_stride * 2,
+                            experts > 1 ? (uint64_t)b.expert_stride * 2 : (uint64_t)b.row_stride * 2};
+    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, kTcRows) ||
+        !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : wide ? 256 : 128))
+        return RS_ERR_UNSUPPORTED;
+    const size_t tiles = max_tiles(args.rows, args.experts, kTcRows) * ceil_div(args.cols, wide ? 256 : 128);
+    if (wide)
+        return b.mn ? tc_launch<T, 256, false, true>(ma, mb, args, tiles, stream)
+                    : tc_launch<T, 256, false, false>(ma, mb, args, tiles, stream);
+    return b.mn ? tc_launch<T, 128, false, true>(ma, mb, args, tiles, stream)
+                : tc_launch<T, 128, false, false>(ma, mb, args, tiles, stream);
+}
+
+template <typename T>
+rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
+{
+    constexpr bool kBf16 = !__is_same(T, __half);
+    const bool wide = args.cols > 128;
+    CUtensorMap ma, mb;
+    const uint64_t da[2] = {args.out_rows, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
+    const uint64_t db[2] = {args.cols, args.rows}, sb[1] = {(uint64_t)b.row_stride * 2};
+    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, 64) || !rstc::encode_map(&mb, kBf16, 2, b.p, db, sb, 64))
+        return RS_ERR_UNSUPPORTED;
+    const size_t tiles = ceil_div(args.out_rows, kTcRows) * args.experts * ceil_div(args.cols, wide ? 256 : 128);
+    return wide ? tc_launch<T, 256, true, true>(ma, mb, args, tiles, stream)
+                : tc_launch<T, 128, true, true>(ma, mb, args, tiles, stream);
+}
+
+}  // namespace rsx

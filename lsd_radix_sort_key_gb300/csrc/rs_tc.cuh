@@ -1,0 +1,215 @@
+// rs_tc.cuh -- the tensor-core side of sm_103a in inline PTX: mbarriers with
+// bounded waits, tiled bulk copies (TMA), tensor memory and tcgen05.mma, and
+// the descriptors they take.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace rstc {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// ---- mbarriers
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+// Makes initialised barriers visible to the async proxy and the cluster.
+__device__ __forceinline__ void bar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A wait gives up after this many SM clocks (about two seconds): far longer
+// than any wait of a working kernel, short enough that a call with a fault
+// still ends.
+constexpr long long kWaitClocks = 1ll << 32;
+
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Waits for phase `parity` of bar to complete; false if the time ran out.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity)
+{
+    if (bar_try(bar, parity)) return true;
+    const long long start = clock64();
+    while (clock64() - start < kWaitClocks)
+        if (bar_try(bar, parity)) return true;
+    return false;
+}
+
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity)
+{
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity));
+}
+
+// This thread's ordinary writes to shared memory before later reads of it by
+// the async proxy (tensor cores, bulk copies).
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- tiled copies into shared memory, counted on bar
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)map) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_addr(dst)),
+        "l"((uint64_t)map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// ---- tensor memory
+
+// One whole warp; the address of `cols` columns (a power of two >= 32) lands
+// in *slot (shared memory).
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: r[c] = column addr + c of lane laneid.
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ---- the matrix instruction
+
+// D (tensor memory, float32) = or += A B^T for K = 16 of 16-bit elements.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// An arrival on bar once every mma this thread issued so far is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Instruction descriptor: float32 accumulator, A and B both binary16 or both
+// bfloat16, each either with the reduction index adjacent in memory (K-major)
+// or with the row index adjacent (MN-major); m x n tile.
+__host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn, uint32_t m, uint32_t n)
+{
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// Shared-memory operand descriptor for tiles copied with the 128-byte
+// swizzle (rows of 128 bytes, groups of 8 rows = 1024 bytes, 1024-aligned).
+//   K-major:  a row holds 64 reduction elements of one operand row; the next
+//             8 operand rows are 1024 bytes on; a step of 16 in the reduction
+//             is 32 bytes.
+//   MN-major: a row holds 64 operand rows of one reduction index; the next 8
+//             reduction indexes are 1024 bytes on, the next 64 operand rows
+//             `mn_stride` bytes on; a step of 16 in the reduction is 2048.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t mn_stride)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// ---- host side
+
+// cuTensorMapEncodeTiled through the runtime (no link dependency on the
+// driver library); nullptr if there is none.
+inline decltype(&cuTensorMapEncodeTiled) tensor_map_encoder()
+{
+    static const auto fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p);
+    }();
+    return fn;
+}
+
+// A map of 16-bit elements with the 128-byte swizzle: dims[0] adjacent,
+// strides (bytes) of dims 1.., boxes of 64 x box1 (x 1).
+inline bool encode_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, uint32_t box1)
+{
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    cuuint64_t d[3], s[2];
+    cuuint32_t box[3] = {64, box1, 1}, step[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        if (dims[i] == 0 || dims[i] > 0xFFFFFFFFull) return false;
+        d[i] = dims[i];
+    }
+    for (int i = 0; i + 1 < rank; ++i) {
+        if (strides[i] == 0 || strides[i] % 16 || strides[i] >= (1ull << 40)) return false;
+        s[i] = strides[i];
+    }
+    if ((uintptr_t)base % 16) return false;
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                  const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace rstc

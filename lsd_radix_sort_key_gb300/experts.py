@@ -40,7 +40,8 @@ class ExpertMatmulDesc(ctypes.Structure):
                 ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_size_t),
                 ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_size_t),
                 ("dw", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
-                ("temp", ctypes.c_void_p), ("temp_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p)]
+                ("temp", ctypes.c_void_p), ("temp_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+                ("stall_tile", ctypes.c_int32)]
 
 
 def _rs():
@@ -105,6 +106,11 @@ def rs_expert_matmul_grad_temp_bytes(desc: ExpertMatmulDesc) -> int:
 
 def rs_expert_matmul_grad(desc: ExpertMatmulDesc) -> int:
     return _rs().rs_expert_matmul_grad(ctypes.byref(desc))
+
+
+def rs_expert_matmul_status(temp, stream=None) -> int:
+    """Waits for the stream; whether the last product with this temp ran to its end."""
+    return _rs().rs_expert_matmul_status(_addr(temp), _raw_stream(stream))
 
 
 # --------------------------------------------------------------- convenience
@@ -331,7 +337,8 @@ def _matmul_desc(x, w, offsets, activation):
     return d
 
 
-def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None, return_pre=False, stream=None):
+def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None, return_pre=False, temp=None,
+                  stream=None):
     """Each expert's rows times its matrix: y[r] = act(x[r] w[e]^T + bias[e]) +
     residual[r] for rows offsets[e] <= r < offsets[e+1]; rows from
     offsets[experts] on are zero.
@@ -340,7 +347,8 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
     adjacent in memory; bias [experts, outer]; residual [rows, outer]; all of
     x's type.  activation: none, relu, gelu (erf) or silu.  Returns y [rows,
     outer], or (y, pre) with the values before the activation, which
-    expert_matmul_grad needs.
+    expert_matmul_grad needs.  temp: scratch of the caller's (uint8, at least
+    rs_expert_matmul_temp_bytes), for rs_expert_matmul_status.
     """
     import torch
     d = _matmul_desc(x, w, offsets, activation)
@@ -363,15 +371,15 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
         tb = h.rs_expert_matmul_temp_bytes(ref)
         if tb == _SIZE_ERROR:
             _check(1, "rs_expert_matmul")
-        if tb:
+        if temp is None:
             temp = torch.empty(tb, dtype=torch.uint8, device=x.device)
-            d.temp, d.temp_bytes = temp.data_ptr(), tb
+        d.temp, d.temp_bytes = temp.data_ptr(), temp.numel()
         _check(h.rs_expert_matmul(ref), "rs_expert_matmul")
     return (y, pre) if return_pre else y
 
 
 def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=True, need_dx=True, need_dw=True,
-                       stream=None):
+                       temp=None, stream=None):
     """The gradient of expert_matmul for dy [rows, outer]: (dx like x, dw
     [experts, outer, inner], dbias [experts, outer]); None for the ones not
     wanted (need_dx, need_dw, bias).  `pre` is what return_pre gave; not
@@ -404,8 +412,8 @@ def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=T
         if tb == _SIZE_ERROR:
             _check(1, "rs_expert_matmul_grad")
         d.stream = s
-        if tb:
+        if temp is None:
             temp = torch.empty(tb, dtype=torch.uint8, device=x.device)
-            d.temp, d.temp_bytes = temp.data_ptr(), tb
+        d.temp, d.temp_bytes = temp.data_ptr(), temp.numel()
         _check(h.rs_expert_matmul_grad(ref), "rs_expert_matmul_grad")
     return dx, dw, dbias

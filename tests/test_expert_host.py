@@ -108,7 +108,8 @@ def desc(**kw):
 
 MATMUL = [(dict(type=3), 1), (dict(type=-1), 1), (dict(activation=4), 1), (dict(num_experts=0), 1),
           (dict(num_experts=1025), 1), (dict(rows=(1 << 30) + 1), 1), (dict(inner=(1 << 20) + 1), 1),
-          (dict(outer=(1 << 20) + 1), 1), (dict(offsets=None), 1), (dict(offsets=F + 2), 1), (dict(y=None), 1)]
+          (dict(outer=(1 << 20) + 1), 1), (dict(stall_tile=-1), 1), (dict(temp=None), 1),
+          (dict(temp=11 * F + 128), 1), (dict(temp_bytes=100), 2), (dict(offsets=None), 1), (dict(offsets=F + 2), 1), (dict(y=None), 1)]
 
 
 @pytest.mark.parametrize("kw,code", MATMUL + [
@@ -123,7 +124,7 @@ def test_matmul_refuses(kw, code):
 
 @pytest.mark.parametrize("kw,code", MATMUL + [
     (dict(pre=None), 1), (dict(x=None), 1), (dict(w=None), 1), (dict(dx_stride=63), 1), (dict(dw=9 * F + 1), 1),
-    (dict(dbias=10 * F + 1), 1), (dict(temp=None), 1), (dict(temp=11 * F + 128), 1), (dict(temp_bytes=100), 2),
+    (dict(dbias=10 * F + 1), 1),
     (dict(dx=2 * F), 3), (dict(dx=3 * F), 3), (dict(dw=6 * F), 3), (dict(dbias=7 * F), 3), (dict(dx=11 * F), 3),
     (dict(dx=9 * F), 3), (dict(dx=None, dw=None, dbias=None), 0)])
 def test_matmul_grad_refuses(kw, code):
@@ -137,7 +138,8 @@ def test_matmul_temp_bytes():
     both = rs.rs_expert_matmul_grad_temp_bytes(desc())
     assert both >= 100 * 128 * 2  # dz
     assert rs.rs_expert_matmul_grad_temp_bytes(desc(activation=0)) < both
-    assert rs.rs_expert_matmul_grad_temp_bytes(desc(activation=0, dbias=None)) == 0
+    assert rs.rs_expert_matmul_grad_temp_bytes(desc(activation=0, dbias=None)) == rs.rs_expert_matmul_temp_bytes(desc())
+    assert rs.rs_expert_matmul_status(None, 0) == 1
 
 
 def test_the_binding_checks_its_tensors():

@@ -275,3 +275,20 @@ def test_same_call_same_bits():
         assert torch.equal(rs.expert_matmul(a["x"], a["w"], a["offsets"]), y)
         for p, q in zip(rs.expert_matmul_grad(dy, a["x"], a["w"], a["offsets"]), first):
             assert torch.equal(p, q)
+
+
+def test_a_wait_that_runs_out_is_reported():
+    a = make([300, 200], 0, 256, 512, torch.bfloat16, 27)
+    temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    y = rs.expert_matmul(a["x"], a["w"], a["offsets"], temp=temp)
+    assert rs.rs_expert_matmul_status(temp) == 0
+    out = torch.empty_like(y)
+    d = rs.ExpertMatmulDesc(2, 0, 2, 500, 256, 512, a["offsets"].data_ptr(), a["x"].data_ptr(), 256, a["w"].data_ptr(),
+                            256 * 512, 256, 1)
+    d.y, d.y_stride, d.temp, d.temp_bytes = out.data_ptr(), 512, temp.data_ptr(), temp.numel()
+    d.stream, d.stall_tile = torch.cuda.current_stream().cuda_stream, 4
+    assert rs.rs_expert_matmul(d) == 0
+    assert rs.rs_expert_matmul_status(temp) == 5  # RS_ERR_DEVICE_TIMEOUT
+    d.stall_tile = 0  # the next call works
+    assert rs.rs_expert_matmul(d) == 0
+    assert rs.rs_expert_matmul_status(temp) == 0 and torch.equal(out, y)
