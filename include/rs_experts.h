@@ -73,7 +73,7 @@ typedef enum rs_activation {
     RS_ACT_SILU = 3  /* z / (1 + exp(-z))                    */
 } rs_activation;
 
-/* Bytes of scratch rs_expert_sort needs for n slots; 0 for n == 0,
+/* Bytes of scratch rs_expert_sort needs for n slots (0 for small n),
  * (size_t)-1 for arguments it would reject. */
 size_t rs_expert_sort_temp_bytes(size_t n, int num_experts);
 
@@ -81,7 +81,7 @@ size_t rs_expert_sort_temp_bytes(size_t n, int num_experts);
  * ids: n expert numbers, int32 or int64 (id_bytes 4 or 8); any value is
  * allowed, one outside [0, num_experts) marks a dropped slot.  order and
  * position: n int32 each; offsets: num_experts + 1 int32.  temp: 256-byte
- * aligned.  n == 0 writes zero offsets.  Errors: RS_ERR_INVALID_ARG (a NULL or
+ * aligned, NULL if it needs none.  n == 0 writes zero offsets.  Errors: RS_ERR_INVALID_ARG (a NULL or
  * misaligned pointer, n > RS_EXPERT_SLOTS_MAX, num_experts outside
  * [1, RS_EXPERTS_MAX], id_bytes), RS_ERR_TEMP_TOO_SMALL, RS_ERR_ALIAS,
  * RS_ERR_CUDA.

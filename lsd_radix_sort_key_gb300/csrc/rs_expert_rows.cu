@@ -54,8 +54,11 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const T* __restrict__ x, 
     }
 }
 
-// One warp sums one vector per lane over a token's slots.
-template <typename T, typename W, int N>
+// One warp sums a piece of V vectors per lane over a token's slots, G slots at
+// a time: G * V row loads per lane are in flight before the first is used.
+// The positions and weights of up to 32 slots are one load each, a slot per
+// lane, and handed around by shuffles.
+template <typename T, typename W, int N, int G, int V>
 __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, size_t y_stride,
                                                       const W* __restrict__ weights,
                                                       const int32_t* __restrict__ position,
@@ -66,39 +69,52 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
     const uint32_t item = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t t = item / pieces;
     if (t >= tokens) return;
-    const uint32_t v = (item - t * pieces) * 32 + lane;
-    if (v >= vecs) return;
+    const uint32_t v0 = (item - t * pieces) * (32 * V) + lane;
     const uint32_t limit = routed_rows(routed, slots_total);
-    float acc[N] = {};
-    constexpr int kAhead = 4;  // rows in flight
-    for (uint32_t k0 = 0; k0 < slots; k0 += kAhead) {
-        Vec<T, N> r[kAhead];
-        float w[kAhead];
-        bool kept[kAhead];
+    float acc[V][N] = {};
+    for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
+        const uint32_t here = min(slots - k0, 32u);
+        uint32_t my_row = 0xFFFFFFFFu;
+        float my_weight = 1.0f;
+        if (lane < here) {
+            const size_t s = (size_t)t * slots + k0 + lane;
+            my_row = (uint32_t)__ldg(position + s);
+            if (weights) my_weight = to_float(weights[s]);
+        }
+        for (uint32_t k = 0; k < here; k += G) {
+            Vec<T, N> r[G][V];
+            bool kept[G];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            kept[j] = false;
-            if (k0 + j < slots) {
-                const size_t s = (size_t)t * slots + k0 + j;
-                const uint32_t p = (uint32_t)__ldg(position + s);
-                kept[j] = p < limit;
+            for (int j = 0; j < G; ++j) {
+                const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_row, (k + j) & 31);
+                kept[j] = k + j < here && p < limit;
                 if (kept[j]) {
-                    r[j] = load_vec<T, N>(y + p * y_stride + (size_t)v * N);
-                    w[j] = weights ? to_float(weights[s]) : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (v0 + i * 32 < vecs)
+                            r[j][i] = load_vec<T, N>(y + p * y_stride + (size_t)(v0 + i * 32) * N);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const float w = __shfl_sync(0xFFFFFFFFu, my_weight, (k + j) & 31);
+                if (kept[j]) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int c = 0; c < N; ++c) acc[i][c] = fmaf(w, to_float(r[j][i].v[c]), acc[i][c]);
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (kept[j]) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_float(r[j].v[i]), acc[i]);
-            }
     }
-    Vec<T, N> o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o.v[i] = from_float<T>(acc[i]);
-    store_vec<T, N>(out + t * out_stride + (size_t)v * N, o);
+    for (int i = 0; i < V; ++i)
+        if (v0 + i * 32 < vecs) {
+            Vec<T, N> o;
+#pragma unroll
+            for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(acc[i][c]);
+            store_vec<T, N>(out + t * out_stride + (size_t)(v0 + i * 32) * N, o);
+        }
 }
 
 // A group of WT warps takes one token: every lane walks its share of the row,
@@ -212,18 +228,27 @@ rs_status run_dispatch(const RowArgs& a, const T* x, size_t x_stride, T* out, si
     return launched();
 }
 
-template <typename T, typename W, int N>
-rs_status run_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
+template <typename T, typename W, int N, int G, int V>
+rs_status launch_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
 {
-    const uint32_t vecs = (uint32_t)(a.width / N), pieces = (uint32_t)ceil_div(vecs, 32);
+    const uint32_t vecs = (uint32_t)(a.width / N), pieces = (uint32_t)ceil_div(vecs, 32 * V);
     const size_t step = tokens_per_launch(pieces);
     for (size_t t = 0; t < a.tokens; t += step) {
         const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
-        k_combine<T, W, N><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
+        k_combine<T, W, N, G, V><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
             y, y_stride, weights ? weights + t * a.slots : nullptr, a.position + t * a.slots, a.routed,
             a.slots_total(), here, a.slots, vecs, pieces, out + t * out_stride, out_stride);
     }
     return launched();
+}
+
+template <typename T, typename W, int N>
+rs_status run_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
+{
+    // eight loads in flight per lane, whatever the number of slots
+    if (a.slots > 4) return launch_combine<T, W, N, 8, 1>(a, y, y_stride, weights, out, out_stride);
+    if (a.slots > 2) return launch_combine<T, W, N, 4, 2>(a, y, y_stride, weights, out, out_stride);
+    return launch_combine<T, W, N, 2, 4>(a, y, y_stride, weights, out, out_stride);
 }
 
 template <typename T, typename W, int N>

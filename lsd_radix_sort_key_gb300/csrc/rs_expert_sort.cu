@@ -5,36 +5,42 @@
 // This is one counting-sort pass on a digit of up to 1025 values (the experts
 // and one more for dropped slots):
 //     position(s) = base(e) + #{s' < s : expert(s') = e},  e = expert(s),
-// base the exclusive scan of the experts' counts.  Slots are cut into chunks
-// of kSlotsPerBlock in order; each chunk into one run of consecutive slots per
-// warp.  Then #{s' < s, same expert} = slots of e in earlier chunks + in
-// earlier warps of this chunk + in earlier slots of this warp, and
-//   k_expert_count  counts every chunk's experts (integer counters in shared
-//                   memory: their order does not matter),
-//   k_expert_scan   scans each expert's chunk counts (one warp per expert),
-//   k_expert_place  scans the experts' totals, ranks each warp's slots with
-//                   __match_any_sync against its own counters, scans those
-//                   over the warps and writes order and position.
+// base the exclusive scan of the experts' counts.  Slots are cut into one
+// chunk of consecutive slots per block, a chunk into tiles of at most
+// kTileSlots, a tile into one run of consecutive slots per warp.  Then
+// #{s' < s, same expert} = slots of e in earlier chunks + in earlier tiles +
+// in earlier warps of this tile + in earlier slots of this warp; the last two
+// come from __match_any_sync and one counter per (warp, expert) in shared
+// memory.  The whole sort is ONE kernel: up to kOneBlockSlots one block, above
+// that a cooperative launch of at most one block per SM in which every block
+// publishes its counts, the grid meets once, and every block then sums the
+// counts before its own (blocks * experts words, from L2).
+//
+// The bytes are few (12 or 16 per slot), so the time is launches and
+// dependent round trips.
+#include <cooperative_groups.h>
+
 #include "rs_expert_common.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kItems = 16;  // slots per thread
-constexpr int kSlotsPerBlock = kThreads * kItems;
+constexpr int kMaxThreads = 1024;
+constexpr int kItems = 8;  // slots per thread of a tile
+constexpr uint32_t kTileSlots = kMaxThreads * kItems;
+constexpr uint32_t kOneBlockSlots = kTileSlots;
+constexpr uint32_t kChunkSlots = 2048;  // least slots per block of a cooperative launch
+constexpr uint32_t kMaxBlocks = 256;
 
 struct SortParams {
     const void* ids;
     int id_bytes;
     uint32_t n;
     uint32_t experts;
-    uint32_t blocks;
+    uint32_t chunk;  // slots per block
     int32_t* order;
     int32_t* position;
     int32_t* offsets;
-    uint32_t* counts;  // [experts + 1][blocks]: first counts, then earlier chunks' sums
-    uint32_t* totals;  // [experts + 1]
+    uint32_t* counts;  // [blocks][experts + 1], unused by a single block
 };
 
 // The slot's expert, or `experts` for a dropped slot.
@@ -48,57 +54,91 @@ __device__ __forceinline__ uint32_t load_expert(const SortParams& p, uint32_t s)
     return v < p.experts ? v : p.experts;
 }
 
-__global__ void __launch_bounds__(kThreads) k_expert_count(SortParams p)
+// A block's shared memory: per expert the first free row (base) and two
+// working sums, and per (warp, expert) a counter.
+struct Shared {
+    uint32_t *base, *total, *before;
+    uint16_t* counter;
+    uint32_t bins;
+    __device__ __forceinline__ Shared(uint32_t* mem, uint32_t bins)
+        : base(mem), total(mem + bins), before(mem + 2 * bins), counter(reinterpret_cast<uint16_t*>(mem + 3 * bins)),
+          bins(bins)
+    {
+    }
+    static size_t bytes(size_t bins, size_t warps) { return 12 * bins + 2 * rsx::align_up(bins * warps, 2); }
+};
+
+// Where a thread's slots of a tile are: slots first + 32 * i, below end.
+struct Run {
+    uint32_t first, end;
+    __device__ __forceinline__ Run(uint32_t begin, uint32_t len)
+    {
+        const uint32_t warps = blockDim.x / 32, warp = threadIdx.x / 32;
+        const uint32_t per = ((len + warps - 1) / warps + 31) / 32 * 32;
+        first = begin + warp * per + threadIdx.x % 32;
+        end = min(begin + len, begin + (warp + 1) * per);
+    }
+};
+
+// Ranks a tile's slots: rank[i] = expert << 16 | slots of that expert before
+// this one in the warp's run; the counters end up as the warps' counts.
+__device__ __forceinline__ void rank_tile(const SortParams& p, const Shared& sh, const Run& run,
+                                          uint32_t (&rank)[kItems])
 {
-    extern __shared__ uint32_t cnt[];
-    const uint32_t bins = p.experts + 1;
-    for (uint32_t e = threadIdx.x; e < bins; e += kThreads) cnt[e] = 0;
-    __syncthreads();
-    const uint32_t begin = blockIdx.x * kSlotsPerBlock;
+    for (uint32_t i = threadIdx.x; i < sh.bins * (blockDim.x / 32); i += blockDim.x) sh.counter[i] = 0;
+    uint32_t expert[kItems];
+#pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const uint32_t s = begin + i * kThreads + threadIdx.x;
-        if (s < p.n) atomicAdd(&cnt[load_expert(p, s)], 1u);
+        const uint32_t s = run.first + 32 * i;
+        expert[i] = s < run.end ? load_expert(p, s) : sh.bins;  // past the end: a value of its own
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < bins; e += kThreads) p.counts[(size_t)e * p.blocks + blockIdx.x] = cnt[e];
-}
-
-__global__ void __launch_bounds__(kThreads) k_expert_scan(SortParams p)
-{
-    const uint32_t e = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (e > p.experts) return;
-    uint32_t* row = p.counts + (size_t)e * p.blocks;
-    uint32_t carry = 0;
-    for (uint32_t b0 = 0; b0 < p.blocks; b0 += 32) {
-        const uint32_t b = b0 + lane;
-        const uint32_t c = b < p.blocks ? row[b] : 0u;
-        uint32_t inc = c;
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-            if (lane >= d) inc += up;
-        }
-        if (b < p.blocks) row[b] = carry + inc - c;
-        carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+    const uint32_t lane = threadIdx.x % 32;
+    uint16_t* mine = sh.counter + threadIdx.x / 32 * sh.bins;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const uint32_t e = expert[i];
+        if (__all_sync(0xFFFFFFFFu, e == sh.bins)) break;  // the run ended (the ranks of the rest are not used)
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
+        const uint32_t earlier = __popc(peers & ((1u << lane) - 1));
+        const uint32_t before = e < sh.bins ? mine[e] : 0u;
+        __syncwarp();
+        if (e < sh.bins && earlier == 0) mine[e] = (uint16_t)(before + __popc(peers));
+        __syncwarp();
+        rank[i] = e << 16 | (before + earlier);
     }
-    if (lane == 0) p.totals[e] = carry;
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) k_expert_place(SortParams p)
+// Counters -> slots of the expert in earlier warps (below kTileSlots, so 16
+// bits hold it); total[e] = the tile's count.
+__device__ __forceinline__ void scan_warps(const Shared& sh)
 {
-    // [bins] the first row of the chunk's slots of each expert, then [warps][bins] counters
-    extern __shared__ uint32_t sm[];
-    __shared__ uint32_t warp_sum[kWarps];
-    const uint32_t bins = p.experts + 1, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    uint32_t* base = sm;
-    uint32_t* mine = sm + bins + warp * bins;
-    for (uint32_t e = tid; e < bins * kWarps; e += kThreads) sm[bins + e] = 0;
+    const uint32_t warps = blockDim.x / 32;
+    for (uint32_t e = threadIdx.x; e < sh.bins; e += blockDim.x) {
+        uint32_t at = 0;
+#pragma unroll 8
+        for (uint32_t w = 0; w < warps; ++w) {
+            const uint32_t c = sh.counter[w * sh.bins + e];
+            sh.counter[w * sh.bins + e] = (uint16_t)at;
+            at += c;
+        }
+        sh.total[e] = at;
+    }
+    __syncthreads();
+}
 
-    // base = exclusive scan of the totals + this expert's slots in earlier chunks
+// base[e] = sum of total over the experts below e, + before[e].
+__device__ __forceinline__ void scan_experts(const SortParams& p, const Shared& sh)
+{
+    __shared__ uint32_t warp_sum[kMaxThreads / 32];
+    const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, warps = blockDim.x / 32;
     uint32_t carry = 0;
-    for (uint32_t e0 = 0; e0 < bins; e0 += kThreads) {
+    for (uint32_t e0 = 0; e0 < sh.bins; e0 += blockDim.x) {
         const uint32_t e = e0 + tid;
-        const uint32_t c = e < bins ? p.totals[e] : 0u;
+        const uint32_t c = e < sh.bins ? sh.total[e] : 0u;
         uint32_t inc = c;
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, d);
             if (lane >= d) inc += up;
@@ -106,55 +146,106 @@ __global__ void __launch_bounds__(kThreads) k_expert_place(SortParams p)
         __syncthreads();
         if (lane == 31) warp_sum[warp] = inc;
         __syncthreads();
-        uint32_t before = carry, all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            before += w < warp ? warp_sum[w] : 0u;
-            all += warp_sum[w];
+        // every warp scans the warps' sums for itself
+        uint32_t sums = lane < warps ? warp_sum[lane] : 0u;
+        const uint32_t own = sums;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sums, d);
+            if (lane >= d) sums += up;
         }
-        if (e < bins) {
-            const uint32_t first = before + inc - c;
-            base[e] = first + p.counts[(size_t)e * p.blocks + blockIdx.x];
+        const uint32_t earlier = __shfl_sync(0xFFFFFFFFu, sums - own, warp);
+        if (e < sh.bins) {
+            const uint32_t first = carry + earlier + inc - c;
+            sh.base[e] = first + sh.before[e];
             if (blockIdx.x == 0) p.offsets[e] = (int32_t)first;
         }
-        carry += all;
+        carry += __shfl_sync(0xFFFFFFFFu, sums, 31);
     }
     __syncthreads();
+}
 
-    // rank among the warp's own earlier slots of the same expert
-    const uint32_t begin = blockIdx.x * kSlotsPerBlock + warp * (32 * kItems) + lane;
-    uint32_t packed[kItems];  // expert << 16 | rank; rank < 512
+__device__ __forceinline__ void place_tile(const SortParams& p, const Shared& sh, const Run& run,
+                                           const uint32_t (&rank)[kItems])
+{
+    const uint16_t* mine = sh.counter + threadIdx.x / 32 * sh.bins;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const uint32_t s = begin + i * 32;
-        const uint32_t e = s < p.n ? load_expert(p, s) : bins;  // past the end: a value of its own
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
-        const uint32_t earlier = __popc(peers & ((1u << lane) - 1));
-        uint32_t before = 0;
-        if (e < bins) before = mine[e];
-        __syncwarp();
-        if (e < bins && earlier == 0) mine[e] = before + __popc(peers);
-        __syncwarp();
-        packed[i] = e << 16 | (before + earlier);
-    }
-    __syncthreads();
-    // counters -> first row of each warp's slots
-    for (uint32_t e = tid; e < bins; e += kThreads) {
-        uint32_t at = base[e];
-        for (int w = 0; w < kWarps; ++w) {
-            const uint32_t c = sm[bins + w * bins + e];
-            sm[bins + w * bins + e] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t s = begin + i * 32;
-        if (s < p.n) {
-            const uint32_t at = mine[packed[i] >> 16] + (packed[i] & 0xFFFFu);
+        const uint32_t s = run.first + 32 * i;
+        if (s < run.end) {
+            const uint32_t e = rank[i] >> 16, at = sh.base[e] + mine[e] + (rank[i] & 0xFFFFu);
             p.position[s] = (int32_t)at;
             if (at < p.n) p.order[at] = (int32_t)s;
         }
+    }
+}
+
+__global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
+{
+    extern __shared__ uint32_t mem[];
+    const uint32_t bins = p.experts + 1, tid = threadIdx.x;
+    const Shared sh(mem, bins);
+    const uint32_t begin = blockIdx.x * p.chunk, end = min(p.n, begin + p.chunk);  // begin <= n by the grid's size
+    uint32_t rank[kItems];
+
+    // This block's counts; a chunk of one tile is ranked on the way.
+    const bool one_tile = end - begin <= kTileSlots;
+    const Run run(begin, min(end - begin, kTileSlots));
+    if (one_tile) {
+        rank_tile(p, sh, run, rank);
+        scan_warps(sh);
+    } else {
+        for (uint32_t e = tid; e < bins; e += blockDim.x) sh.total[e] = 0;
+        __syncthreads();
+        for (uint32_t s = begin + tid; s < end; s += blockDim.x) atomicAdd(&sh.total[load_expert(p, s)], 1u);
+        __syncthreads();
+    }
+
+    // Every block's counts -> the first row of this block's slots of each expert.
+    if (gridDim.x > 1) {
+        for (uint32_t e = tid; e < bins; e += blockDim.x) {
+            p.counts[(size_t)blockIdx.x * bins + e] = sh.total[e];
+            sh.total[e] = 0;
+            sh.before[e] = 0;
+        }
+        cooperative_groups::this_grid().sync();
+        // neighbouring threads take neighbouring experts, thread groups every groups-th block
+        const uint32_t lanes = (bins + 31) / 32 * 32, groups = max(1u, blockDim.x / lanes);
+        const uint32_t group = tid / lanes;
+        for (uint32_t e = groups > 1 ? tid % lanes : tid; group < groups && e < bins; e += groups > 1 ? lanes : blockDim.x) {
+            uint32_t sum = 0, early = 0;
+#pragma unroll 8
+            for (uint32_t b = groups > 1 ? group : 0; b < gridDim.x; b += groups) {
+                const uint32_t c = __ldcg(p.counts + (size_t)b * bins + e);
+                sum += c;
+                early += b < blockIdx.x ? c : 0u;
+            }
+            if (groups > 1) {
+                atomicAdd(&sh.total[e], sum);
+                atomicAdd(&sh.before[e], early);
+            } else {
+                sh.total[e] = sum;
+                sh.before[e] = early;
+            }
+        }
+    } else {
+        for (uint32_t e = tid; e < bins; e += blockDim.x) sh.before[e] = 0;
+    }
+    __syncthreads();
+    scan_experts(p, sh);
+
+    if (one_tile) {
+        place_tile(p, sh, run, rank);
+        return;
+    }
+    for (uint32_t at = begin; at < end; at += kTileSlots) {
+        const Run r(at, min(end - at, kTileSlots));
+        rank_tile(p, sh, r, rank);
+        scan_warps(sh);
+        place_tile(p, sh, r, rank);
+        __syncthreads();
+        for (uint32_t e = tid; e < bins; e += blockDim.x) sh.base[e] += sh.total[e];
+        // (rank_tile's barriers come before the next use of base)
     }
 }
 
@@ -165,9 +256,9 @@ extern "C" {
 size_t rs_expert_sort_temp_bytes(size_t n, int num_experts)
 {
     if (n > RS_EXPERT_SLOTS_MAX || num_experts < 1 || num_experts > RS_EXPERTS_MAX) return (size_t)-1;
-    if (n == 0) return 0;
-    const size_t bins = (size_t)num_experts + 1;
-    return rsx::align_up((bins * rsx::ceil_div(n, kSlotsPerBlock) + bins) * 4, 256);
+    if (n <= kOneBlockSlots) return 0;
+    const size_t blocks = rsx::ceil_div(n, kChunkSlots);
+    return rsx::align_up((blocks < kMaxBlocks ? blocks : kMaxBlocks) * ((size_t)num_experts + 1) * 4, 256);
 }
 
 rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_experts, int32_t* order,
@@ -179,7 +270,7 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t bins = (size_t)num_experts + 1;
     if (n == 0) return cudaMemsetAsync(offsets, 0, bins * 4, s) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
-    if (!ids || !order || !position || !temp) return RS_ERR_INVALID_ARG;
+    if (!ids || !order || !position || (need && !temp)) return RS_ERR_INVALID_ARG;
     if ((uintptr_t)ids % id_bytes || (uintptr_t)order % 4 || (uintptr_t)position % 4 || (uintptr_t)temp % 256)
         return RS_ERR_INVALID_ARG;
     if (temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
@@ -192,15 +283,35 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
     p.id_bytes = id_bytes;
     p.n = (uint32_t)n;
     p.experts = (uint32_t)num_experts;
-    p.blocks = (uint32_t)rsx::ceil_div(n, kSlotsPerBlock);
     p.order = order;
     p.position = position;
     p.offsets = offsets;
     p.counts = static_cast<uint32_t*>(temp);
-    p.totals = p.counts + bins * p.blocks;
-    k_expert_count<<<p.blocks, kThreads, bins * 4, s>>>(p);
-    k_expert_scan<<<(unsigned)rsx::ceil_div(bins, kWarps), kThreads, 0, s>>>(p);
-    k_expert_place<<<p.blocks, kThreads, bins * 4 * (kWarps + 1), s>>>(p);
+    const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32);
+    if (most_smem > 48 * 1024 - 256 &&
+        cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
+        return RS_ERR_CUDA;
+    if (n <= kOneBlockSlots) {
+        p.chunk = (uint32_t)n;
+        const unsigned threads = (unsigned)(n < kMaxThreads ? rsx::align_up(n, 32) : kMaxThreads);
+        k_expert_sort<<<1, threads, Shared::bytes(bins, threads / 32), s>>>(p);
+    } else {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+            return RS_ERR_CUDA;
+        size_t blocks = rsx::ceil_div(n, kChunkSlots);
+        if (blocks > (size_t)sms) blocks = sms;
+        if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+        p.chunk = (uint32_t)rsx::ceil_div(n, blocks);
+        blocks = rsx::ceil_div(n, p.chunk);
+        void* args[] = {&p};
+        if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(k_expert_sort), dim3((unsigned)blocks),
+                                        dim3(kMaxThreads), args, most_smem, s) != cudaSuccess) {
+            cudaGetLastError();
+            return RS_ERR_CUDA;
+        }
+    }
     return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 

@@ -19,11 +19,16 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
+import sys
+
+_pkg = sys.modules[__package__]
 
 FLOAT_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 EXPERTS_MAX = 1024  # RS_EXPERTS_MAX
 
+_MATMUL_TEMP = 2048  # rs_expert_matmul_temp_bytes of every descriptor it accepts
 _SIZE_ERROR = ctypes.c_size_t(-1).value
 
 
@@ -44,9 +49,13 @@ class ExpertMatmulDesc(ctypes.Structure):
                 ("stall_tile", ctypes.c_int32)]
 
 
+# The same structure as bytes: packing is several times cheaper than a
+# ctypes.Structure's fields one by one.
+_DESC = struct.Struct("@3i4x 3N 2PN P3N PN PN PN PN PN PP PN P i4x")
+
+
 def _rs():
-    from . import lib
-    return lib()
+    return _pkg._lib or _pkg.lib()
 
 
 def _addr(x):
@@ -93,19 +102,19 @@ def rs_expert_combine_grad(ftype, dout, dout_stride, y, y_stride, weights, weigh
 
 
 def rs_expert_matmul_temp_bytes(desc: ExpertMatmulDesc) -> int:
-    return _rs().rs_expert_matmul_temp_bytes(ctypes.byref(desc))
+    return _rs().rs_expert_matmul_temp_bytes(ctypes.addressof(desc))
 
 
 def rs_expert_matmul(desc: ExpertMatmulDesc) -> int:
-    return _rs().rs_expert_matmul(ctypes.byref(desc))
+    return _rs().rs_expert_matmul(ctypes.addressof(desc))
 
 
 def rs_expert_matmul_grad_temp_bytes(desc: ExpertMatmulDesc) -> int:
-    return _rs().rs_expert_matmul_grad_temp_bytes(ctypes.byref(desc))
+    return _rs().rs_expert_matmul_grad_temp_bytes(ctypes.addressof(desc))
 
 
 def rs_expert_matmul_grad(desc: ExpertMatmulDesc) -> int:
-    return _rs().rs_expert_matmul_grad(ctypes.byref(desc))
+    return _rs().rs_expert_matmul_grad(ctypes.addressof(desc))
 
 
 def rs_expert_matmul_status(temp, stream=None) -> int:
@@ -115,61 +124,90 @@ def rs_expert_matmul_status(temp, stream=None) -> int:
 
 # --------------------------------------------------------------- convenience
 
+_NAMES = {}  # torch dtype -> rs_float_type
+
+
 def _ftype(t, what):
-    name = str(t.dtype)[6:]  # torch.xxx
-    if name not in FLOAT_TYPES:
+    if not _NAMES:
+        import torch
+        _NAMES.update({getattr(torch, name): code for name, code in FLOAT_TYPES.items()})
+    code = _NAMES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{what}: float32, float16 or bfloat16 wanted, got {t.dtype}")
-    return FLOAT_TYPES[name]
+    return code
 
 
-def _cuda(what, t, dtype, shape, device):
-    """t is a CUDA tensor of this type and shape (None: any) on this device (None: any)."""
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{what}: a tensor on {device or 'a CUDA device'} is wanted, got one on {t.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what}: {dtype} wanted, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _like(what, t, x, shape):
+    """t has x's device and type and this shape."""
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{what}: {x.dtype} wanted, got {t.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{what}: a tensor on {x.device} is wanted, got one on {t.device}")
 
 
-def _row_stride(what, t, out=False):
-    """The row stride of a matrix whose rows' elements are adjacent."""
+def _rows(what, t):
+    """(rows, width, row stride) of a CUDA matrix whose rows' elements are adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor is wanted, got one on {t.device}")
+    if t.dim() != 2:
+        raise ValueError(f"{what}: a matrix of rows is wanted, got shape {tuple(t.shape)}")
     rows, width = t.shape
-    if width > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if inner != 1 and width > 1:
         raise ValueError(f"{what}: the elements of a row must be adjacent")
-    stride = t.stride(0)
     if rows <= 1:
-        return max(width, 1)
-    if stride < width and (out or stride != 0):
+        stride = width or 1
+    elif stride < width and stride != 0:
         raise ValueError(f"{what}: rows must not overlap")
-    return stride
+    return rows, width, stride
 
 
 def _plan(position, offsets, device):
+    """(tokens, slots, address of the number of rows in use) of a sort's result."""
     import torch
-    _cuda("position", position, torch.int32, None, device)
-    _cuda("offsets", offsets, torch.int32, None, device)
-    if position.dim() != 2 or position.shape[1] < 1:
+    for what, t, dims in (("position", position, 2), ("offsets", offsets, 1)):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{what}: torch.int32 wanted, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{what}: a tensor on {device} is wanted, got one on {t.device}")
+        if t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous tensor of {dims} dimension(s) is wanted")
+    tokens, slots = position.shape
+    if slots < 1:
         raise ValueError("position: shape [tokens, slots] wanted")
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
+    edges = offsets.shape[0]
+    if edges < 2:
         raise ValueError("offsets: shape [num_experts + 1] wanted")
-    if not position.is_contiguous() or not offsets.is_contiguous():
-        raise ValueError("position and offsets must be contiguous")
-    return position.shape[0], position.shape[1], offsets.data_ptr() + 4 * (offsets.shape[0] - 1)
+    return tokens, slots, offsets.data_ptr() + 4 * (edges - 1)
 
 
 def _weights(weights, y, shape):
     import torch
     if weights.dtype != torch.float32 and weights.dtype != y.dtype:
         raise TypeError(f"weights: float32 or {y.dtype} wanted, got {weights.dtype}")
-    _cuda("weights", weights, None, shape, y.device)
-    return weights.contiguous()
+    if weights.shape != shape:
+        raise ValueError(f"weights: shape {shape} wanted, got {tuple(weights.shape)}")
+    if weights.device != y.device:
+        raise ValueError(f"weights: a tensor on {y.device} is wanted, got one on {weights.device}")
+
+
+def _current(device, stream):
+    """The current stream's handle in the usual case: no stream is asked for
+    and the tensors are on the current device; else None."""
+    import torch
+    i = device.index
+    if stream is None and i == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(i)
+    return None
 
 
 @contextlib.contextmanager
 def _other(device, stream, inputs):
-    """Allocate on, and launch into, `stream` of `device`; the inputs' memory
-    is then not handed out again before `stream` has passed."""
+    """Allocate on, and launch into, `stream` (None: the current one) of
+    `device`; the inputs' memory is then not handed out again before `stream`
+    has passed."""
     import torch
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.device(device):
@@ -183,32 +221,9 @@ def _other(device, stream, inputs):
             yield s.cuda_stream
 
 
-class _On:
-    """The usual case of _other, without its cost: the tensors' device is the
-    current one and the call goes to its current stream."""
-    __slots__ = ("raw",)
-
-    def __init__(self, raw):
-        self.raw = raw
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *a):
-        return False
-
-
-def _on(device, stream, *inputs):
-    import torch
-    if stream is None and device.index == torch.cuda.current_device():
-        return _On(torch.cuda.current_stream().cuda_stream)
-    return _other(device, stream, inputs)
-
-
 def _check(code, where):
     if code != 0:
-        from . import RadixSortError
-        raise RadixSortError(code, where)
+        raise _pkg.RadixSortError(code, where)
 
 
 def expert_sort(ids, num_experts: int, *, stream=None):
@@ -222,57 +237,82 @@ def expert_sort(ids, num_experts: int, *, stream=None):
     rows offsets[num_experts] and on.
     """
     import torch
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype != torch.int64 and ids.dtype != torch.int32:
         raise TypeError(f"ids: int32 or int64 wanted, got {ids.dtype}")
     if not ids.is_cuda or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous CUDA tensor")
-    n, dev = ids.numel(), ids.device
-    h = _rs()
+    dev = ids.device
+    s = _current(dev, stream)
+    if s is None:
+        with _other(dev, stream, (ids,)) as s:
+            return _sort(ids, num_experts, dev, s)
+    return _sort(ids, num_experts, dev, s)
+
+
+def _sort(ids, num_experts, dev, s):
+    import torch
+    n, i32, h = ids.numel(), torch.int32, _rs()
     tb = h.rs_expert_sort_temp_bytes(n, num_experts)
     if tb == _SIZE_ERROR:
         _check(1, "rs_expert_sort")
-    with _on(dev, stream, ids) as s:
-        order = torch.empty(n, dtype=torch.int32, device=dev)
-        position = torch.empty(ids.shape, dtype=torch.int32, device=dev)
-        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-        temp = torch.empty(tb, dtype=torch.uint8, device=dev)
-        _check(h.rs_expert_sort(ids.data_ptr(), ids.element_size(), n, num_experts, order.data_ptr(),
-                                position.data_ptr(), offsets.data_ptr(), temp.data_ptr(), tb, s), "rs_expert_sort")
+    order = torch.empty(n, dtype=i32, device=dev)
+    position = torch.empty(ids.shape, dtype=i32, device=dev)
+    offsets = torch.empty(num_experts + 1, dtype=i32, device=dev)
+    temp = torch.empty(tb, dtype=torch.uint8, device=dev).data_ptr() if tb else None
+    _check(h.rs_expert_sort(ids.data_ptr(), ids.element_size(), n, num_experts, order.data_ptr(),
+                            position.data_ptr(), offsets.data_ptr(), temp, tb, s), "rs_expert_sort")
     return order, position, offsets
 
 
 def expert_dispatch(x, position, offsets, *, stream=None):
     """x [T, H] laid out by expert: [T*K, H], row position[t, k] = x[t];
     the rows of dropped slots are zero."""
-    import torch
-    ft = _ftype(x, "x")
-    t, k, routed = _plan(position, offsets, x.device)
-    if x.dim() != 2 or x.shape[0] != t:
+    ft, dev = _ftype(x, "x"), x.device
+    rows, width, xs = _rows("x", x)
+    t, k, routed = _plan(position, offsets, dev)
+    if rows != t:
         raise ValueError(f"x: shape [{t}, width] wanted, got {tuple(x.shape)}")
-    width, xs = x.shape[1], _row_stride("x", x)
-    with _on(x.device, stream, x, position, offsets) as s:
-        out = torch.empty((t * k, width), dtype=x.dtype, device=x.device)
-        _check(_rs().rs_expert_dispatch(ft, x.data_ptr(), xs, position.data_ptr(), routed, t, k, width,
-                                        out.data_ptr(), max(width, 1), s), "rs_expert_dispatch")
+    args = (ft, x, xs, position, routed, t, k, width)
+    s = _current(dev, stream)
+    if s is None:
+        with _other(dev, stream, (x, position, offsets)) as s:
+            return _dispatch(*args, s)
+    return _dispatch(*args, s)
+
+
+def _dispatch(ft, x, xs, position, routed, t, k, width, s):
+    import torch
+    out = torch.empty((t * k, width), dtype=x.dtype, device=x.device)
+    _check(_rs().rs_expert_dispatch(ft, x.data_ptr(), xs, position.data_ptr(), routed, t, k, width, out.data_ptr(),
+                                    width or 1, s), "rs_expert_dispatch")
     return out
 
 
 def _combine(y, weights, position, offsets, stream):
-    import torch
-    ft = _ftype(y, "y")
-    t, k, routed = _plan(position, offsets, y.device)
-    if y.dim() != 2 or y.shape[0] != t * k:
+    ft, dev = _ftype(y, "y"), y.device
+    rows, width, ys = _rows("y", y)
+    t, k, routed = _plan(position, offsets, dev)
+    if rows != t * k:
         raise ValueError(f"y: shape [{t * k}, width] wanted, got {tuple(y.shape)}")
-    width, ys = y.shape[1], _row_stride("y", y)
-    with _on(y.device, stream, y, weights, position, offsets) as s:
-        w, wt = None, 0
-        if weights is not None:
-            w = _weights(weights, y, (t, k))
-            wt = _ftype(w, "weights")
-        out = torch.empty((t, width), dtype=y.dtype, device=y.device)
-        _check(_rs().rs_expert_combine(ft, y.data_ptr(), ys, None if w is None else w.data_ptr(), wt,
-                                       position.data_ptr(), routed, t, k, width, out.data_ptr(), max(width, 1), s),
-               "rs_expert_combine")
+    if weights is not None:
+        _weights(weights, y, (t, k))
+    args = (ft, y, ys, weights, position, routed, t, k, width)
+    s = _current(dev, stream)
+    if s is None:
+        with _other(dev, stream, (y, weights, position, offsets)) as s:
+            return _combine_on(*args, s)
+    return _combine_on(*args, s)
+
+
+def _combine_on(ft, y, ys, weights, position, routed, t, k, width, s):
+    import torch
+    w, wt = None, 0
+    if weights is not None:
+        weights = weights.contiguous()
+        w, wt = weights.data_ptr(), _NAMES[weights.dtype]
+    out = torch.empty((t, width), dtype=y.dtype, device=y.device)
+    _check(_rs().rs_expert_combine(ft, y.data_ptr(), ys, w, wt, position.data_ptr(), routed, t, k, width,
+                                   out.data_ptr(), width or 1, s), "rs_expert_combine")
     return out
 
 
@@ -293,48 +333,60 @@ def expert_combine(y, weights, position, offsets, *, stream=None):
 def expert_combine_grad(dout, y, weights, position, offsets, *, stream=None):
     """The gradient of expert_combine for dout [T, H]: (dy [T*K, H] like y,
     dweights [T, K] like weights); zero for dropped slots."""
-    import torch
-    ft = _ftype(y, "y")
-    t, k, routed = _plan(position, offsets, y.device)
-    if y.dim() != 2 or y.shape[0] != t * k:
+    ft, dev = _ftype(y, "y"), y.device
+    rows, width, ys = _rows("y", y)
+    t, k, routed = _plan(position, offsets, dev)
+    if rows != t * k:
         raise ValueError(f"y: shape [{t * k}, width] wanted, got {tuple(y.shape)}")
-    width, ys = y.shape[1], _row_stride("y", y)
-    _cuda("dout", dout, y.dtype, (t, width), y.device)
-    ds = _row_stride("dout", dout)
-    with _on(y.device, stream, dout, y, weights, position, offsets) as s:
-        w = _weights(weights, y, (t, k))
-        dy = torch.empty((t * k, width), dtype=y.dtype, device=y.device)
-        dweights = torch.empty((t, k), dtype=w.dtype, device=y.device)
-        _check(_rs().rs_expert_combine_grad(ft, dout.data_ptr(), ds, y.data_ptr(), ys, w.data_ptr(),
-                                            _ftype(w, "weights"), position.data_ptr(), routed, t, k, width,
-                                            dy.data_ptr(), max(width, 1), dweights.data_ptr(), s),
-               "rs_expert_combine_grad")
+    _like("dout", dout, y, (t, width))
+    ds = _rows("dout", dout)[2]
+    _weights(weights, y, (t, k))
+    args = (ft, dout, ds, y, ys, weights, position, routed, t, k, width)
+    s = _current(dev, stream)
+    if s is None:
+        with _other(dev, stream, (dout, y, weights, position, offsets)) as s:
+            return _combine_grad(*args, s)
+    return _combine_grad(*args, s)
+
+
+def _combine_grad(ft, dout, ds, y, ys, weights, position, routed, t, k, width, s):
+    import torch
+    w = weights.contiguous()
+    dy = torch.empty((t * k, width), dtype=y.dtype, device=y.device)
+    dweights = torch.empty((t, k), dtype=w.dtype, device=y.device)
+    _check(_rs().rs_expert_combine_grad(ft, dout.data_ptr(), ds, y.data_ptr(), ys, w.data_ptr(), _NAMES[w.dtype],
+                                        position.data_ptr(), routed, t, k, width, dy.data_ptr(), width or 1,
+                                        dweights.data_ptr(), s), "rs_expert_combine_grad")
     return dy, dweights
 
 
-def _matmul_desc(x, w, offsets, activation):
+def _products(x, w, offsets, activation):
+    """The head of the descriptor (up to w's strides) after the checks that
+    both products share, and (rows, inner, outer, experts)."""
     import torch
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation: one of {', '.join(ACTIVATIONS)} wanted, got {activation!r}")
     ft = _ftype(x, "x")
-    if x.dim() != 2 or w.dim() != 3:
-        raise ValueError("x: [rows, inner] and w: [experts, outer, inner] wanted")
-    (rows, inner), (experts, outer, wi) = x.shape, w.shape
-    _cuda("x", x, None, None, None)
-    _cuda("w", w, x.dtype, (experts, outer, inner), x.device)
-    _cuda("offsets", offsets, torch.int32, (experts + 1,), x.device)
-    if not offsets.is_contiguous():
-        raise ValueError("offsets must be contiguous")
-    so, si = w.stride(1), w.stride(2)
-    if inner <= 1:  # a single column's stride says nothing
+    rows, inner, xs = _rows("x", x)
+    if w.dim() != 3:
+        raise ValueError("w: [experts, outer, inner] wanted")
+    experts, outer, _ = w.shape
+    _like("w", w, x, (experts, outer, inner))
+    if offsets.dtype != torch.int32:
+        raise TypeError(f"offsets: torch.int32 wanted, got {offsets.dtype}")
+    if offsets.shape != (experts + 1,) or offsets.device != x.device or not offsets.is_contiguous():
+        raise ValueError(f"offsets: a contiguous tensor of shape ({experts + 1},) on {x.device} is wanted")
+    se, so, si = w.stride()
+    if inner <= 1:  # the stride of a single column or row says nothing
         si = 1
     elif outer <= 1 and si == 1:
         so = inner
-    d = ExpertMatmulDesc(ft, ACTIVATIONS[activation], experts, rows, inner, outer, offsets.data_ptr(),
-                         x.data_ptr(), _row_stride("x", x), w.data_ptr(), w.stride(0) if experts > 1 else 0, so, si)
-    if min(inner, outer) > 1 and so != 1 and si != 1:
+    if so != 1 and si != 1 and inner > 1 and outer > 1:
         raise ValueError("w: each expert's matrix must have adjacent elements along one side")
-    return d
+    head = (ft, act, experts, rows, inner, outer, offsets.data_ptr(), x.data_ptr(), xs, w.data_ptr(),
+            se if experts > 1 else 0, so, si)
+    return head, rows, inner, outer, experts
 
 
 def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None, return_pre=False, temp=None,
@@ -350,31 +402,31 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
     expert_matmul_grad needs.  temp: scratch of the caller's (uint8, at least
     rs_expert_matmul_temp_bytes), for rs_expert_matmul_status.
     """
-    import torch
-    d = _matmul_desc(x, w, offsets, activation)
-    rows, outer = d.rows, d.outer
+    head, rows, inner, outer, experts = _products(x, w, offsets, activation)
+    extra = [None, 0, None, 0]
     if bias is not None:
-        _cuda("bias", bias, x.dtype, (d.num_experts, outer), x.device)
-        d.bias, d.bias_stride = bias.data_ptr(), _row_stride("bias", bias)
+        _like("bias", bias, x, (experts, outer))
+        extra[0:2] = bias.data_ptr(), _rows("bias", bias)[2]
     if residual is not None:
-        _cuda("residual", residual, x.dtype, (rows, outer), x.device)
-        d.residual, d.residual_stride = residual.data_ptr(), _row_stride("residual", residual)
-    h = _rs()
-    with _on(x.device, stream, x, w, offsets, bias, residual) as s:
-        y = torch.empty((rows, outer), dtype=x.dtype, device=x.device)
-        d.y, d.y_stride, d.stream = y.data_ptr(), max(outer, 1), s
-        pre = None
-        if return_pre:
-            pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device)
-            d.pre, d.pre_stride = pre.data_ptr(), max(outer, 1)
-        ref = ctypes.byref(d)
-        tb = h.rs_expert_matmul_temp_bytes(ref)
-        if tb == _SIZE_ERROR:
-            _check(1, "rs_expert_matmul")
-        if temp is None:
-            temp = torch.empty(tb, dtype=torch.uint8, device=x.device)
-        d.temp, d.temp_bytes = temp.data_ptr(), temp.numel()
-        _check(h.rs_expert_matmul(ref), "rs_expert_matmul")
+        _like("residual", residual, x, (rows, outer))
+        extra[2:4] = residual.data_ptr(), _rows("residual", residual)[2]
+    args = (head, extra, x, rows, outer, return_pre, temp)
+    s = _current(x.device, stream)
+    if s is None:
+        with _other(x.device, stream, (x, w, offsets, bias, residual)) as s:
+            return _matmul(*args, s)
+    return _matmul(*args, s)
+
+
+def _matmul(head, extra, x, rows, outer, return_pre, temp, s):
+    import torch
+    y = torch.empty((rows, outer), dtype=x.dtype, device=x.device)
+    pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device) if return_pre else None
+    if temp is None:
+        temp = torch.empty(_MATMUL_TEMP, dtype=torch.uint8, device=x.device)
+    desc = _DESC.pack(*head, *[v or 0 for v in extra], y.data_ptr(), outer or 1, pre.data_ptr() if return_pre else 0,
+                      outer or 1, 0, 0, 0, 0, temp.data_ptr(), temp.numel(), s, 0)
+    _check(_rs().rs_expert_matmul(desc), "rs_expert_matmul")
     return (y, pre) if return_pre else y
 
 
@@ -385,35 +437,34 @@ def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=T
     wanted (need_dx, need_dw, bias).  `pre` is what return_pre gave; not
     needed for activation "none".  The residual's gradient is dy.
     """
-    import torch
-    d = _matmul_desc(x, w, offsets, activation)
-    rows, inner, outer, experts = d.rows, d.inner, d.outer, d.num_experts
-    _cuda("dy", dy, x.dtype, (rows, outer), x.device)
-    d.y, d.y_stride = dy.data_ptr(), _row_stride("dy", dy)
+    head, rows, inner, outer, experts = _products(x, w, offsets, activation)
+    _like("dy", dy, x, (rows, outer))
+    grads = [dy.data_ptr(), _rows("dy", dy)[2], 0, 0]
     if activation != "none":
         if pre is None:
             raise TypeError(f"pre: needed for activation {activation!r}")
-        _cuda("pre", pre, x.dtype, (rows, outer), x.device)
-        d.pre, d.pre_stride = pre.data_ptr(), _row_stride("pre", pre)
-    h = _rs()
-    with _on(x.device, stream, dy, x, w, offsets, pre) as s:
-        dx = dw = dbias = None
-        if need_dx:
-            dx = torch.empty((rows, inner), dtype=x.dtype, device=x.device)
-            d.dx, d.dx_stride = dx.data_ptr() or None, max(inner, 1)
-        if need_dw:
-            dw = torch.empty((experts, outer, inner), dtype=x.dtype, device=x.device)
-            d.dw = dw.data_ptr() or None
-        if bias:
-            dbias = torch.empty((experts, outer), dtype=x.dtype, device=x.device)
-            d.dbias = dbias.data_ptr() or None
-        ref = ctypes.byref(d)
-        tb = h.rs_expert_matmul_grad_temp_bytes(ref)
+        _like("pre", pre, x, (rows, outer))
+        grads[2:4] = pre.data_ptr(), _rows("pre", pre)[2]
+    args = (head, grads, x, rows, inner, outer, experts, need_dx, need_dw, bias, temp)
+    s = _current(x.device, stream)
+    if s is None:
+        with _other(x.device, stream, (dy, x, w, offsets, pre)) as s:
+            return _matmul_grad(*args, s)
+    return _matmul_grad(*args, s)
+
+
+def _matmul_grad(head, grads, x, rows, inner, outer, experts, need_dx, need_dw, bias, temp, s):
+    import torch
+    dt, dev, h = x.dtype, x.device, _rs()
+    dx = torch.empty((rows, inner), dtype=dt, device=dev) if need_dx else None
+    dw = torch.empty((experts, outer, inner), dtype=dt, device=dev) if need_dw else None
+    dbias = torch.empty((experts, outer), dtype=dt, device=dev) if bias else None
+    outs = [0 if t is None else t.data_ptr() for t in (dx, dw, dbias)]
+    tail = (*head, 0, 0, 0, 0, *grads, outs[0], inner or 1, outs[1], outs[2])
+    if temp is None:
+        tb = h.rs_expert_matmul_grad_temp_bytes(_DESC.pack(*tail, 0, 0, 0, 0))
         if tb == _SIZE_ERROR:
             _check(1, "rs_expert_matmul_grad")
-        d.stream = s
-        if temp is None:
-            temp = torch.empty(tb, dtype=torch.uint8, device=x.device)
-        d.temp, d.temp_bytes = temp.data_ptr(), temp.numel()
-        _check(h.rs_expert_matmul_grad(ref), "rs_expert_matmul_grad")
+        temp = torch.empty(tb, dtype=torch.uint8, device=dev)
+    _check(h.rs_expert_matmul_grad(_DESC.pack(*tail, temp.data_ptr(), temp.numel(), s, 0)), "rs_expert_matmul_grad")
     return dx, dw, dbias

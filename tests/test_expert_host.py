@@ -35,6 +35,14 @@ def test_desc_matches_the_header():
     assert names == [n for n, _ in rs.ExpertMatmulDesc._fields_]
 
 
+def test_the_packed_descriptor_is_the_structure():
+    from lsd_radix_sort_key_gb300 import experts
+    assert experts._DESC.size == ctypes.sizeof(rs.ExpertMatmulDesc)
+    values = [3 + i for i in range(len(rs.ExpertMatmulDesc._fields_))]
+    assert experts._DESC.pack(*values) == bytes(rs.ExpertMatmulDesc(*values))
+    assert experts._MATMUL_TEMP == rs.rs_expert_matmul_temp_bytes(desc())
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(ids=None), 1), (dict(order=None), 1), (dict(position=None), 1), (dict(offsets=None), 1),
     (dict(temp=None), 1), (dict(id_bytes=2), 1), (dict(ids=F + 4), 1), (dict(order=2 * F + 2), 1),
@@ -42,7 +50,7 @@ def test_desc_matches_the_header():
     (dict(temp_bytes=0), 2), (dict(position=2 * F), 3), (dict(order=F + 8), 3), (dict(offsets=5 * F), 3),
 ])
 def test_sort_refuses(kw, code):
-    a = dict(ids=F, id_bytes=8, n=1000, experts=16, order=2 * F, position=3 * F, offsets=4 * F, temp=5 * F,
+    a = dict(ids=F, id_bytes=8, n=100_000, experts=16, order=2 * F, position=3 * F, offsets=4 * F, temp=5 * F,
              temp_bytes=1 << 20)
     a.update(kw)
     assert rs.rs_expert_sort(a["ids"], a["id_bytes"], a["n"], a["experts"], a["order"], a["position"], a["offsets"],
@@ -52,7 +60,8 @@ def test_sort_refuses(kw, code):
 def test_sort_temp_bytes():
     bad = ctypes.c_size_t(-1).value
     assert rs.rs_expert_sort_temp_bytes(0, 4) == 0
-    assert 0 < rs.rs_expert_sort_temp_bytes(1, 4) < 1 << 20
+    assert rs.rs_expert_sort_temp_bytes(512, 128) == 0
+    assert 0 < rs.rs_expert_sort_temp_bytes(100_000, 4) < 1 << 20
     assert rs.rs_expert_sort_temp_bytes(1 << 30, 1024) < 1 << 31
     assert rs.rs_expert_sort_temp_bytes((1 << 30) + 1, 4) == bad
     assert rs.rs_expert_sort_temp_bytes(1, 0) == bad and rs.rs_expert_sort_temp_bytes(1, 1025) == bad
