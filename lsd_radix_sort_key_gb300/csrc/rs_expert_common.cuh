@@ -24,8 +24,10 @@ __device__ __forceinline__ T from_float(float v)
     else return __float2bfloat16_rn(v);
 }
 
-// N adjacent elements moved as one access; N * sizeof(T) is 16 (rows whose
-// base and stride are multiples of 16 bytes) or one element.
+// N adjacent elements: 16 bytes.
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
     T v[N];
@@ -45,11 +47,161 @@ __device__ __forceinline__ Vec<T, N> load_vec(const T* p)
     return r;
 }
 
+// r, or zeros.
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> keep_if(bool kept, const Vec<T, N>& r)
+{
+    static_assert(sizeof(T) * N == 16, "16 bytes");
+    uint4 u = *reinterpret_cast<const uint4*>(&r);
+    u = make_uint4(kept ? u.x : 0, kept ? u.y : 0, kept ? u.z : 0, kept ? u.w : 0);
+    return *reinterpret_cast<const Vec<T, N>*>(&u);
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& r)
 {
     if constexpr (sizeof(T) * N == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(&r);
     else p[0] = r.v[0];
+}
+
+// A vector as floats and back (one rounding each).
+template <typename T>
+__device__ __forceinline__ void to_floats(float (&f)[kVec<T>], const Vec<T, kVec<T>>& r)
+{
+    const uint4 u = *reinterpret_cast<const uint4*>(&r);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            f[i] = __uint_as_float(w[i]);
+        } else if constexpr (__is_same(T, __half)) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        } else {  // bfloat16 is the high half of a float
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if constexpr (__is_same(T, __half)) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Vec<T, kVec<T>> from_floats(const float (&f)[kVec<T>])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+        else w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    }
+    const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
+    return *reinterpret_cast<const Vec<T, kVec<T>>*>(&u);
+}
+
+// Rows that are only element-aligned (an odd width, say) still move 16 bytes
+// at a time: the vectors of a written row are cut where its addresses are
+// multiples of 16, so element 0 of vector v of a row is v * kVec - lead(row),
+// and a row's first and last vectors may be partial.  What is read for such
+// a vector starts anywhere: it is taken from the two aligned 16-byte words
+// around it (the second is the neighbouring lane's first and comes from L1).
+// Those may reach into the rows before and after, so they are read only where
+// both lie inside the matrix.
+template <typename T>
+__device__ __forceinline__ int lead(const T* row)
+{
+    return (int)((uintptr_t)row % 16 / sizeof(T));
+}
+
+// The two words, loaded without a branch so that many can be in flight, and
+// then the elements [i, i + kVec) of a row of `width` in a matrix that occupies
+// [begin, end); what lies outside the row is unspecified (clear_outside).
+template <typename T>
+struct Shifted {
+    uint4 lo, hi;
+    bool inside;
+    __device__ __forceinline__ void load(const T* from, const T* begin, const T* end)
+    {
+        const uintptr_t p = (uintptr_t)from, a = p & ~(uintptr_t)15;
+        inside = a >= (uintptr_t)begin && a + (a != p ? 32 : 16) <= (uintptr_t)end;
+        lo = hi = make_uint4(0, 0, 0, 0);
+        if (inside) lo = __ldg(reinterpret_cast<const uint4*>(a));
+        if (inside && a != p) hi = __ldg(reinterpret_cast<const uint4*>(a) + 1);
+    }
+    __device__ __forceinline__ Vec<T, kVec<T>> get(const T* row, int i, int width) const
+    {
+        constexpr int N = kVec<T>;
+        const uint32_t m = (uint32_t)(uintptr_t)(row + i) & 15;
+        // drop the first m bytes: 8 and 4 bytes by selection, 2 by a funnel
+        // shift (named values: an array indexed like this goes to memory)
+        const bool b8 = m & 8, b4 = m & 4;
+        const uint32_t p0 = b8 ? lo.z : lo.x, p1 = b8 ? lo.w : lo.y, p2 = b8 ? hi.x : lo.z, p3 = b8 ? hi.y : lo.w;
+        const uint32_t p4 = b8 ? hi.z : hi.x, p5 = b8 ? hi.w : hi.y;
+        uint4 u = make_uint4(b4 ? p1 : p0, b4 ? p2 : p1, b4 ? p3 : p2, b4 ? p4 : p3);
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t last = b4 ? p5 : p4, bits = m & 2 ? 16 : 0;
+            u = make_uint4(__funnelshift_r(u.x, u.y, bits), __funnelshift_r(u.y, u.z, bits),
+                           __funnelshift_r(u.z, u.w, bits), __funnelshift_r(u.w, last, bits));
+        }
+        if (!inside) u = ends(row, i, width);
+        return *reinterpret_cast<const Vec<T, N>*>(&u);
+    }
+    // At the matrix's two ends: element by element.
+    __device__ __noinline__ static uint4 ends(const T* row, int i, int width)
+    {
+        constexpr int per = 4 / (int)sizeof(T);  // elements per word
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = 0;
+#pragma unroll
+            for (int h = 0; h < per; ++h) {
+                const int c = i + j * per + h;
+                if (c < 0 || c >= width) continue;
+                if constexpr (per == 1) w[j] = reinterpret_cast<const uint32_t*>(row)[c];
+                else w[j] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << h * 16;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Zeros in place of the elements of vector [i, i + kVec) outside the row.
+template <typename T>
+__device__ __forceinline__ void clear_outside(float (&f)[kVec<T>], int i, int width)
+{
+    if (i >= 0 && i + kVec<T> <= width) return;
+#pragma unroll
+    for (int c = 0; c < kVec<T>; ++c)
+        if (i + c < 0 || i + c >= width) f[c] = 0.0f;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_partial(T* row, int i, int width, const Vec<T, kVec<T>>& r)
+{
+    const uint4 u = *reinterpret_cast<const uint4*>(&r);
+    if (i >= 0 && i + kVec<T> <= width) {
+        *reinterpret_cast<uint4*>(row + i) = u;
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int c = 0; c < kVec<T>; ++c) {
+            if (i + c < 0 || i + c >= width) continue;
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[i + c] = w[c];
+            else reinterpret_cast<uint16_t*>(row)[i + c] = (uint16_t)(w[c / 2] >> (c & 1) * 16);
+        }
+    }
 }
 
 // ---- host side

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
             float z = acc[r][c], y = 0.0f;
             if (e < p.experts) {
                 if (p.bias) z += to_float(p.bias[e * p.bias_e + j]);
-                y = activate<ACT>(z);
+                y = activate<ACT, sizeof(T) == 2>(z);
                 if (p.residual) y += to_float(p.residual[i * p.residual_i + j]);
             }
             if (p.pre) p.pre[i * p.pre_i + j] = from_float<T>(z);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ d
             Vec<T, N> o;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float v = to_float(d.v[i]) * activate_grad<ACT>(to_float(z.v[i]));
+                const float v = to_float(d.v[i]) * activate_grad<ACT, sizeof(T) == 2>(to_float(z.v[i]));
                 sum[i] += v;
                 o.v[i] = from_float<T>(v);
             }

@@ -9,6 +9,8 @@
 //   combine grad  (1 + 2K)
 // with no use of `order`, and the sum over a token's slots is a loop in one
 // thread, in slot order: no atomics, the same result every time.
+#include <type_traits>
+
 #include "rs_expert_common.cuh"
 
 namespace {
@@ -25,169 +27,277 @@ __device__ __forceinline__ uint32_t routed_rows(const int32_t* routed, uint32_t 
     return r < 0 ? 0u : (uint32_t)r < slots_total ? (uint32_t)r : slots_total;
 }
 
-// One warp moves a piece of kPiece vectors per lane of one token's row to its
-// K places.
-template <typename T, int N, int PIECE>
+// A row is cut into vectors of 16 bytes, and these into pieces of 32 * V
+// (one warp, V per lane).  SHIFT: rows are only element-aligned, and the
+// vectors are cut by the written row's address (lead, Shifted,
+// store_partial in rs_expert_common.cuh).
+template <typename T, bool SHIFT>
+__device__ __forceinline__ uint32_t row_vecs(uint32_t width)
+{
+    constexpr uint32_t N = kVec<T>;
+    return (width + N - 1) / N + (SHIFT ? 1 : 0);  // a lead adds at most one
+}
+
+// A warp's slots of one token, up to 32: a slot per lane, handed around by
+// shuffles.
+template <typename W>
+struct Slots {
+    uint32_t row = 0xFFFFFFFFu;
+    float weight = 1.0f;
+    __device__ __forceinline__ void load(const int32_t* position, const W* weights, size_t first, uint32_t count)
+    {
+        const uint32_t lane = threadIdx.x % 32;
+        if (lane < count) {
+            row = (uint32_t)__ldg(position + first + lane);
+            if (weights) weight = to_float(weights[first + lane]);
+        }
+    }
+    __device__ __forceinline__ uint32_t row_of(uint32_t k) const { return __shfl_sync(0xFFFFFFFFu, row, k & 31); }
+    __device__ __forceinline__ float weight_of(uint32_t k) const { return __shfl_sync(0xFFFFFFFFu, weight, k & 31); }
+};
+
+// One warp moves one piece of a token's row to its K places.  Written bytes
+// bound it: 16384 x 8 rows of 4 KB move at 6.5 TB/s with V = 2, 5.4 when each
+// slot's position was loaded on its own.
+template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const T* __restrict__ x, size_t x_stride,
                                                        const int32_t* __restrict__ position,
                                                        const int32_t* __restrict__ routed, uint32_t slots_total,
-                                                       uint32_t tokens, uint32_t slots, uint32_t vecs,
-                                                       uint32_t pieces, T* __restrict__ out, size_t out_stride)
+                                                       uint32_t tokens, uint32_t slots, uint32_t width,
+                                                       uint32_t pieces, const T* __restrict__ x_begin,
+                                                       const T* __restrict__ x_end, T* __restrict__ out,
+                                                       size_t out_stride)
 {
+    constexpr int N = kVec<T>, V = 2;
     const uint32_t item = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t t = item / pieces;
     if (t >= tokens) return;
-    const uint32_t v0 = (item - t * pieces) * (32 * PIECE) + lane;
+    const uint32_t v0 = (item - t * pieces) * (32 * V) + lane, vecs = row_vecs<T, SHIFT>(width);
     const uint32_t limit = routed_rows(routed, slots_total);
-    Vec<T, N> r[PIECE];
+    const T* row = x + t * x_stride;
+    Vec<T, N> r[V];
+    if constexpr (!SHIFT) {
 #pragma unroll
-    for (int i = 0; i < PIECE; ++i)
-        if (v0 + i * 32 < vecs) r[i] = load_vec<T, N>(x + t * x_stride + (size_t)(v0 + i * 32) * N);
-    for (uint32_t k = 0; k < slots; ++k) {
-        const uint32_t p = (uint32_t)__ldg(position + (size_t)t * slots + k);
-        if (p >= slots_total) continue;
-        T* to = out + p * out_stride;
-        const Vec<T, N> zero{};
+        for (int i = 0; i < V; ++i)
+            if (v0 + i * 32 < vecs) r[i] = load_vec<T, N>(row + (size_t)(v0 + i * 32) * N);
+    }
+    for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
+        const uint32_t here = min(slots - k0, 32u);
+        Slots<float> sl;
+        sl.load(position, nullptr, (size_t)t * slots + k0, here);
+        for (uint32_t k = 0; k < here; ++k) {
+            const uint32_t p = sl.row_of(k);
+            if (p >= slots_total) continue;
+            T* to = out + p * out_stride;
+            const bool kept = p < limit;
+            if constexpr (SHIFT) {
+                const int skip = lead(to);
+                Shifted<T> w[V];
 #pragma unroll
-        for (int i = 0; i < PIECE; ++i)
-            if (v0 + i * 32 < vecs) store_vec<T, N>(to + (size_t)(v0 + i * 32) * N, p < limit ? r[i] : zero);
+                for (int i = 0; i < V; ++i) w[i].load(row + ((int)((v0 + i * 32) * N) - skip), x_begin, x_end);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int at = (int)((v0 + i * 32) * N) - skip;
+                    if (at < (int)width)
+                        store_partial<T>(to, at, (int)width, keep_if(kept, w[i].get(row, at, (int)width)));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (v0 + i * 32 < vecs) store_vec<T, N>(to + (size_t)(v0 + i * 32) * N, keep_if(kept, r[i]));
+            }
+        }
     }
 }
 
-// One warp sums a piece of V vectors per lane over a token's slots, G slots at
-// a time: G * V row loads per lane are in flight before the first is used.
-// The positions and weights of up to 32 slots are one load each, a slot per
-// lane, and handed around by shuffles.
-template <typename T, typename W, int N, int G, int V>
+// One warp sums `span` pieces of a token's row over its slots, G slots at a
+// time, so G * V row loads per lane are in flight before the first is used.
+// Random reads bound it, and the choice of G, V and span is the memory
+// system's: measured for 16384 x 8 rows of 4 KB, in TB/s, G x V = 8x1 3.6,
+// 4x1 5.2, 4x2 6.6, 2x2 6.5, 2x8 5.7; 65536 x 1 rows of 8 KB: 2x2 4.8 with
+// span 1, 6.1 with span 4, 1x4 6.6 with span 4; 8192 x 2 of 16 KB: 2x2 5.6,
+// 6.2, 6.4 with span 1, 2, 4.
+template <typename T, typename W, bool SHIFT, int G, int V>
 __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, size_t y_stride,
                                                       const W* __restrict__ weights,
                                                       const int32_t* __restrict__ position,
                                                       const int32_t* __restrict__ routed, uint32_t slots_total,
-                                                      uint32_t tokens, uint32_t slots, uint32_t vecs,
-                                                      uint32_t pieces, T* __restrict__ out, size_t out_stride)
+                                                      uint32_t tokens, uint32_t slots, uint32_t width, uint32_t parts,
+                                                      uint32_t span, const T* __restrict__ y_end, T* __restrict__ out,
+                                                      size_t out_stride)
 {
+    constexpr int N = kVec<T>;
     const uint32_t item = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t t = item / pieces;
+    const uint32_t t = item / parts;
     if (t >= tokens) return;
-    const uint32_t v0 = (item - t * pieces) * (32 * V) + lane;
-    const uint32_t limit = routed_rows(routed, slots_total);
-    float acc[V][N] = {};
-    for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
-        const uint32_t here = min(slots - k0, 32u);
-        uint32_t my_row = 0xFFFFFFFFu;
-        float my_weight = 1.0f;
-        if (lane < here) {
-            const size_t s = (size_t)t * slots + k0 + lane;
-            my_row = (uint32_t)__ldg(position + s);
-            if (weights) my_weight = to_float(weights[s]);
+    const uint32_t limit = routed_rows(routed, slots_total), vecs = row_vecs<T, SHIFT>(width);
+    T* to = out + t * out_stride;
+    const int skip = SHIFT ? lead(to) : 0;
+    const uint32_t first = (item - t * parts) * span * (32 * V), last = min(vecs, first + span * (32 * V));
+    Slots<W> sl;
+    sl.load(position, weights, (size_t)t * slots, min(slots, 32u));
+    for (uint32_t v0 = first; v0 < last; v0 += 32 * V) {
+        float acc[V][N] = {};
+        for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
+            const uint32_t here = min(slots - k0, 32u);
+            if (slots > 32) sl.load(position, weights, (size_t)t * slots + k0, here);
+            for (uint32_t k = 0; k < here; k += G) {
+                using Loaded = std::conditional_t<SHIFT, Shifted<T>, Vec<T, N>>;
+                Loaded r[G][V];
+                bool kept[G];
+                uint32_t p[G];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    p[j] = sl.row_of(k + j);
+                    kept[j] = k + j < here && p[j] < limit;
+                    if (!kept[j]) continue;
+                    const T* from = y + p[j] * y_stride;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t v = v0 + i * 32 + lane;
+                        if constexpr (SHIFT) r[j][i].load(from + ((int)(v * N) - skip), y, y_end);
+                        else if (v < vecs) r[j][i] = load_vec<T, N>(from + (size_t)v * N);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const float w = sl.weight_of(k + j);
+                    if (!kept[j]) continue;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float f[N];
+                        if constexpr (SHIFT)
+                            to_floats<T>(f, r[j][i].get(y + p[j] * y_stride, (int)((v0 + i * 32 + lane) * N) - skip,
+                                                        (int)width));
+                        else to_floats<T>(f, r[j][i]);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) acc[i][c] = fmaf(w, f[c], acc[i][c]);
+                    }
+                }
+            }
         }
-        for (uint32_t k = 0; k < here; k += G) {
-            Vec<T, N> r[G][V];
-            bool kept[G];
 #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const uint32_t p = __shfl_sync(0xFFFFFFFFu, my_row, (k + j) & 31);
-                kept[j] = k + j < here && p < limit;
-                if (kept[j]) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (v0 + i * 32 < vecs)
-                            r[j][i] = load_vec<T, N>(y + p * y_stride + (size_t)(v0 + i * 32) * N);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const float w = __shfl_sync(0xFFFFFFFFu, my_weight, (k + j) & 31);
-                if (kept[j]) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-#pragma unroll
-                        for (int c = 0; c < N; ++c) acc[i][c] = fmaf(w, to_float(r[j][i].v[c]), acc[i][c]);
-                }
-            }
+        for (int i = 0; i < V; ++i) {
+            const uint32_t v = v0 + i * 32 + lane;
+            if (v >= vecs) continue;
+            const Vec<T, N> o = from_floats<T>(acc[i]);
+            if constexpr (SHIFT) store_partial<T>(to, (int)(v * N) - skip, (int)width, o);
+            else store_vec<T, N>(to + (size_t)v * N, o);
         }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (v0 + i * 32 < vecs) {
-            Vec<T, N> o;
-#pragma unroll
-            for (int c = 0; c < N; ++c) o.v[c] = from_float<T>(acc[i][c]);
-            store_vec<T, N>(out + t * out_stride + (size_t)(v0 + i * 32) * N, o);
-        }
 }
 
-// A group of WT warps takes one token: every lane walks its share of the row,
-// for up to kSlots slots at a time, and the lanes' parts of the dot products
-// are summed at the end (within the warp by shuffles, over the warps through
-// shared memory), always in the same order.
-template <typename T, typename W, int N, int WT>
+// WT warps take one token and walk its row together, V vectors per lane and
+// G slots at a time; a slot's dot product is summed over the lanes at the end
+// (within the warp by shuffles, over the warps through shared memory), always
+// in the same order.  Up to 8 slots per walk.  G = V = 2 measured best or
+// within 3% of it from 1 to 8 slots (16384 x 8 rows of 4 KB 6.6 TB/s; 65536 x 1
+// of 8 KB 6.4 against 3.5 with G x V = 8x1); rows of at most 32 vectors leave
+// half of V = 2 idle and take 4x1 (131072 x 8 rows of 512 bytes 6.6 against 5.7).
+template <typename T, typename W, bool SHIFT, int G, int V, int WT>
 __global__ void __launch_bounds__(kThreads) k_combine_grad(
     const T* __restrict__ dout, size_t dout_stride, const T* __restrict__ y, size_t y_stride,
     const W* __restrict__ weights, const int32_t* __restrict__ position, const int32_t* __restrict__ routed,
-    uint32_t slots_total, uint32_t tokens, uint32_t slots, uint32_t vecs, T* __restrict__ dy, size_t dy_stride,
+    uint32_t slots_total, uint32_t tokens, uint32_t slots, uint32_t width, const T* __restrict__ dout_end,
+    const T* __restrict__ y_end, T* __restrict__ dy, size_t dy_stride,
     W* __restrict__ dweights)
 {
-    constexpr int kSlots = 8;
+    constexpr int N = kVec<T>, kSlots = 8;
     __shared__ float part[kWarps][kSlots];
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t t = blockIdx.x * (kWarps / WT) + warp / WT;
     const bool live = t < tokens;  // no early return: the block has barriers when WT > 1
-    const uint32_t limit = routed_rows(routed, slots_total);
+    const uint32_t limit = routed_rows(routed, slots_total), vecs = live ? row_vecs<T, SHIFT>(width) : 0;
+    const T* grad = dout + (live ? t : 0) * dout_stride;
     for (uint32_t k0 = 0; k0 < slots; k0 += kSlots) {
-        uint32_t p[kSlots];
-        float w[kSlots], dot[kSlots] = {};
+        const uint32_t here = live ? min(slots - k0, (uint32_t)kSlots) : 0;
+        Slots<W> sl;
+        sl.load(position, weights, (size_t)t * slots + k0, here);
+        float dot[kSlots] = {};
+        for (uint32_t v0 = (warp % WT) * (32 * V); v0 < vecs; v0 += 32 * V * WT) {
+            Vec<T, N> d[V];
+            if constexpr (!SHIFT) {
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-            p[j] = 0xFFFFFFFFu;
-            w[j] = 0.0f;
-            if (live && k0 + j < slots) {
-                const size_t s = (size_t)t * slots + k0 + j;
-                p[j] = (uint32_t)__ldg(position + s);
-                if (p[j] < limit) w[j] = to_float(weights[s]);
+                for (int i = 0; i < V; ++i)
+                    if (v0 + i * 32 + lane < vecs) d[i] = load_vec<T, N>(grad + (size_t)(v0 + i * 32 + lane) * N);
             }
-        }
-        for (uint32_t v = (warp % WT) * 32 + lane; live && v < vecs; v += 32 * WT) {
-            const Vec<T, N> d = load_vec<T, N>(dout + t * dout_stride + (size_t)v * N);
-            Vec<T, N> r[kSlots];
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (p[j] < limit) r[j] = load_vec<T, N>(y + p[j] * y_stride + (size_t)v * N);
+            for (int k = 0; k < kSlots; k += G) {
+                if (k >= here) break;
+                using Loaded = std::conditional_t<SHIFT, Shifted<T>, Vec<T, N>>;
+                Loaded r[G][V], g[SHIFT ? G : 1][V];
+                uint32_t p[G];
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
-                if (p[j] >= slots_total) continue;
-                Vec<T, N> o{};
-                if (p[j] < limit) {
+                for (int j = 0; j < G; ++j) {
+                    p[j] = sl.row_of(k + j);
+                    if (k + j >= here) p[j] = 0xFFFFFFFFu;
+                    if (p[j] >= limit) continue;
+                    const T* from = y + p[j] * y_stride;
+                    const int skip = SHIFT ? lead(dy + p[j] * dy_stride) : 0;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float g = to_float(d.v[i]);
-                        dot[j] = fmaf(g, to_float(r[j].v[i]), dot[j]);
-                        o.v[i] = from_float<T>(w[j] * g);
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t v = v0 + i * 32 + lane;
+                        if constexpr (SHIFT) {
+                            r[j][i].load(from + ((int)(v * N) - skip), y, y_end);
+                            g[j][i].load(grad + ((int)(v * N) - skip), dout, dout_end);
+                        } else if (v < vecs) {
+                            r[j][i] = load_vec<T, N>(from + (size_t)v * N);
+                        }
                     }
                 }
-                store_vec<T, N>(dy + p[j] * dy_stride + (size_t)v * N, o);
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const float w = sl.weight_of(k + j);
+                    if (p[j] >= slots_total) continue;
+                    T* to = dy + p[j] * dy_stride;
+                    const int skip = SHIFT ? lead(to) : 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const uint32_t v = v0 + i * 32 + lane;
+                        if (v >= vecs) continue;
+                        Vec<T, N> o{};
+                        if (p[j] < limit) {
+                            float q[N], f[N], e[N];
+                            if constexpr (SHIFT) {
+                                const int at = (int)(v * N) - skip;
+                                to_floats<T>(q, g[j][i].get(grad, at, (int)width));
+                                to_floats<T>(f, r[j][i].get(y + p[j] * y_stride, at, (int)width));
+                                clear_outside<T>(q, at, (int)width);
+                                clear_outside<T>(f, at, (int)width);
+                            } else {
+                                to_floats<T>(q, d[i]);
+                                to_floats<T>(f, r[j][i]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < N; ++c) {
+                                dot[k + j] = fmaf(q[c], f[c], dot[k + j]);
+                                e[c] = w * q[c];
+                            }
+                            o = from_floats<T>(e);
+                        }
+                        if constexpr (SHIFT) store_partial<T>(to, (int)(v * N) - skip, (int)width, o);
+                        else store_vec<T, N>(to + (size_t)v * N, o);
+                    }
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
+#pragma unroll
             for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+        float sum = 0.0f;  // lane j: slot j's
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j)
+            if (lane == j) sum = dot[j];
         if constexpr (WT > 1) {
             __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (lane == 0) part[warp][j] = dot[j];
+            if (lane < kSlots) part[warp][lane] = sum;
             __syncthreads();
-            if (warp % WT == 0 && lane < kSlots) {
-                float sum = 0.0f;
+            sum = 0.0f;
+            if (warp % WT == 0 && lane < kSlots)
                 for (int i = 0; i < WT; ++i) sum += part[warp + i][lane];
-                if (live && k0 + lane < slots) dweights[(size_t)t * slots + k0 + lane] = from_float<W>(sum);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-                if (lane == 0 && live && k0 + j < slots)
-                    dweights[(size_t)t * slots + k0 + j] = from_float<W>(dot[j]);
         }
+        if (warp % WT == 0 && lane < here) dweights[(size_t)t * slots + k0 + lane] = from_float<W>(sum);
     }
 }
 
@@ -213,69 +323,77 @@ rs_status check_rows(const RowArgs& a, int type)
 
 rs_status launched() { return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA; }
 
-template <typename T, int N>
+template <typename T, bool SHIFT>
 rs_status run_dispatch(const RowArgs& a, const T* x, size_t x_stride, T* out, size_t out_stride)
 {
-    constexpr int kPiece = 4;
-    const uint32_t vecs = (uint32_t)(a.width / N), pieces = (uint32_t)ceil_div(vecs, 32 * kPiece);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT, pieces = (uint32_t)ceil_div(vecs, 64);
     const size_t step = tokens_per_launch(pieces);
     for (size_t t = 0; t < a.tokens; t += step) {
         const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
-        k_dispatch<T, N, kPiece><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
-            x + t * x_stride, x_stride, a.position + t * a.slots, a.routed, a.slots_total(), here, a.slots, vecs,
-            pieces, out, out_stride);
+        k_dispatch<T, SHIFT><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
+            x + t * x_stride, x_stride, a.position + t * a.slots, a.routed, a.slots_total(), here, a.slots,
+            (uint32_t)a.width, pieces, x, x + (a.tokens - 1) * x_stride + a.width, out, out_stride);
     }
     return launched();
 }
 
-template <typename T, typename W, int N, int G, int V>
-rs_status launch_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
+// Warps that keep every SM's memory pipeline full several times over; below
+// this the spans of k_combine are cut to spread the work.
+constexpr size_t kManyWarps = 16384;
+
+template <typename T, typename W, bool SHIFT, int G, int V>
+rs_status launch_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride,
+                         uint32_t span)
 {
-    const uint32_t vecs = (uint32_t)(a.width / N), pieces = (uint32_t)ceil_div(vecs, 32 * V);
-    const size_t step = tokens_per_launch(pieces);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT, pieces = (uint32_t)ceil_div(vecs, 32 * V);
+    while (span > 1 && a.tokens * ceil_div(pieces, span) < kManyWarps) span /= 2;
+    const uint32_t parts = (uint32_t)ceil_div(pieces, span);
+    const size_t step = tokens_per_launch(parts);
     for (size_t t = 0; t < a.tokens; t += step) {
         const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
-        k_combine<T, W, N, G, V><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
+        k_combine<T, W, SHIFT, G, V><<<(unsigned)ceil_div((size_t)here * parts, kWarps), kThreads, 0, a.stream>>>(
             y, y_stride, weights ? weights + t * a.slots : nullptr, a.position + t * a.slots, a.routed,
-            a.slots_total(), here, a.slots, vecs, pieces, out + t * out_stride, out_stride);
+            a.slots_total(), here, a.slots, (uint32_t)a.width, parts, span,
+            y + ((size_t)a.slots_total() - 1) * y_stride + a.width, out + t * out_stride, out_stride);
     }
     return launched();
 }
 
-template <typename T, typename W, int N>
+template <typename T, typename W, bool SHIFT>
 rs_status run_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
 {
-    // eight loads in flight per lane, whatever the number of slots
-    if (a.slots > 4) return launch_combine<T, W, N, 8, 1>(a, y, y_stride, weights, out, out_stride);
-    if (a.slots > 2) return launch_combine<T, W, N, 4, 2>(a, y, y_stride, weights, out, out_stride);
-    return launch_combine<T, W, N, 2, 4>(a, y, y_stride, weights, out, out_stride);
+    if (a.width <= 32 * kVec<T>) return launch_combine<T, W, SHIFT, 4, 1>(a, y, y_stride, weights, out, out_stride, 1);
+    if (a.slots == 1) return launch_combine<T, W, SHIFT, 1, 4>(a, y, y_stride, weights, out, out_stride, 4);
+    return launch_combine<T, W, SHIFT, 2, 2>(a, y, y_stride, weights, out, out_stride, 2);
 }
 
-template <typename T, typename W, int N>
+template <typename T, typename W, bool SHIFT>
 rs_status run_combine_grad(const RowArgs& a, const T* dout, size_t dout_stride, const T* y, size_t y_stride,
                            const W* weights, T* dy, size_t dy_stride, W* dweights)
 {
-    const uint32_t vecs = (uint32_t)(a.width / N);
+    auto run = [&](auto kernel, int per_block) {
+        kernel<<<(unsigned)ceil_div(a.tokens, per_block), kThreads, 0, a.stream>>>(
+            dout, dout_stride, y, y_stride, weights, a.position, a.routed, a.slots_total(), (uint32_t)a.tokens,
+            (uint32_t)a.slots, (uint32_t)a.width, dout + (a.tokens - 1) * dout_stride + a.width,
+            y + ((size_t)a.slots_total() - 1) * y_stride + a.width, dy, dy_stride, dweights);
+        return launched();
+    };
+    if (a.width <= 32 * kVec<T>) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1>, kWarps);
+    // Shifted vectors take twice the registers.
+    constexpr int G = 2, V = SHIFT ? 1 : 2;
     // Few tokens: a whole block each, so that a row is spread over 256 lanes.
-    if (a.tokens < 1024)
-        k_combine_grad<T, W, N, kWarps><<<(unsigned)a.tokens, kThreads, 0, a.stream>>>(
-            dout, dout_stride, y, y_stride, weights, a.position, a.routed, a.slots_total(), (uint32_t)a.tokens,
-            a.slots, vecs, dy, dy_stride, dweights);
-    else
-        k_combine_grad<T, W, N, 1><<<(unsigned)ceil_div(a.tokens, kWarps), kThreads, 0, a.stream>>>(
-            dout, dout_stride, y, y_stride, weights, a.position, a.routed, a.slots_total(), (uint32_t)a.tokens,
-            a.slots, vecs, dy, dy_stride, dweights);
-    return launched();
+    if (a.tokens < 2048) return run(k_combine_grad<T, W, SHIFT, G, V, kWarps>, 1);
+    return run(k_combine_grad<T, W, SHIFT, G, V, 1>, kWarps);
 }
 
-// f(T{}, Int<N>{}) for the type and alignment at hand.
+// f(T{}, Int<SHIFT>{}) for the type and alignment at hand.
 template <typename F>
-rs_status by_type(int type, bool vec, F f)
+rs_status by_type(int type, bool aligned, F f)
 {
     switch (type) {
-    case RS_FLOAT32: return vec ? f(float{}, Int<4>{}) : f(float{}, Int<1>{});
-    case RS_FLOAT16: return vec ? f(__half{}, Int<8>{}) : f(__half{}, Int<1>{});
-    default:         return vec ? f(__nv_bfloat16{}, Int<8>{}) : f(__nv_bfloat16{}, Int<1>{});
+    case RS_FLOAT32: return aligned ? f(float{}, Int<0>{}) : f(float{}, Int<1>{});
+    case RS_FLOAT16: return aligned ? f(__half{}, Int<0>{}) : f(__half{}, Int<1>{});
+    default:         return aligned ? f(__nv_bfloat16{}, Int<0>{}) : f(__nv_bfloat16{}, Int<1>{});
     }
 }
 
@@ -301,7 +419,7 @@ rs_status rs_expert_dispatch(rs_float_type type, const void* x, size_t x_stride,
     const bool vec = aligned16(x, x_stride, eb) && aligned16(out, out_stride, eb) && width * eb % 16 == 0;
     return by_type(type, vec, [&](auto t, auto n) {
         using T = decltype(t);
-        return run_dispatch<T, decltype(n)::value>(a, static_cast<const T*>(x), x_stride, static_cast<T*>(out),
+        return run_dispatch<T, decltype(n)::value != 0>(a, static_cast<const T*>(x), x_stride, static_cast<T*>(out),
                                                    out_stride);
     });
 }
@@ -329,11 +447,11 @@ rs_status rs_expert_combine(rs_float_type type, const void* y, size_t y_stride, 
     const bool vec = aligned16(y, y_stride, eb) && aligned16(out, out_stride, eb) && width * eb % 16 == 0;
     return by_type(type, vec, [&](auto t, auto nn) {
         using T = decltype(t);
-        constexpr int N = decltype(nn)::value;
+        constexpr bool SHIFT = decltype(nn)::value != 0;
         if (!weights || weight_type == RS_FLOAT32)
-            return run_combine<T, float, N>(a, static_cast<const T*>(y), y_stride, static_cast<const float*>(weights),
+            return run_combine<T, float, SHIFT>(a, static_cast<const T*>(y), y_stride, static_cast<const float*>(weights),
                                             static_cast<T*>(out), out_stride);
-        return run_combine<T, T, N>(a, static_cast<const T*>(y), y_stride, static_cast<const T*>(weights),
+        return run_combine<T, T, SHIFT>(a, static_cast<const T*>(y), y_stride, static_cast<const T*>(weights),
                                     static_cast<T*>(out), out_stride);
     });
 }
@@ -367,13 +485,13 @@ rs_status rs_expert_combine_grad(rs_float_type type, const void* dout, size_t do
                      aligned16(dy, dy_stride, eb) && width * eb % 16 == 0;
     return by_type(type, vec, [&](auto t, auto nn) {
         using T = decltype(t);
-        constexpr int N = decltype(nn)::value;
+        constexpr bool SHIFT = decltype(nn)::value != 0;
         if (weight_type == RS_FLOAT32)
-            return run_combine_grad<T, float, N>(a, static_cast<const T*>(dout), dout_stride,
+            return run_combine_grad<T, float, SHIFT>(a, static_cast<const T*>(dout), dout_stride,
                                                  static_cast<const T*>(y), y_stride,
                                                  static_cast<const float*>(weights), static_cast<T*>(dy), dy_stride,
                                                  static_cast<float*>(dweights));
-        return run_combine_grad<T, T, N>(a, static_cast<const T*>(dout), dout_stride, static_cast<const T*>(y),
+        return run_combine_grad<T, T, SHIFT>(a, static_cast<const T*>(dout), dout_stride, static_cast<const T*>(y),
                                          y_stride, static_cast<const T*>(weights), static_cast<T*>(dy), dy_stride,
                                          static_cast<T*>(dweights));
     });

@@ -94,18 +94,6 @@ __device__ __forceinline__ TcTile tc_tile(const TcArgs<T>& p, const Groups& g, u
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    if constexpr (__is_same(T, __half)) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-
-template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t u)
 {
     if constexpr (__is_same(T, __half)) return __half22float2(*reinterpret_cast<const __half2*>(&u));
@@ -192,8 +180,8 @@ __device__ __forceinline__ void finish(uint32_t (&out)[16], const uint32_t (&z)[
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const float2 r = unpack2<T>(res[i]);
-        out[i] = pack2<T>(activate<ACT>(__uint_as_float(z[2 * i])) + r.x,
-                          activate<ACT>(__uint_as_float(z[2 * i + 1])) + r.y);
+        out[i] = pack2<T>(activate<ACT, true>(__uint_as_float(z[2 * i])) + r.x,
+                          activate<ACT, true>(__uint_as_float(z[2 * i + 1])) + r.y);
     }
 }
 
