@@ -17,26 +17,44 @@ inline int sm_count()
     return sms;
 }
 
-template <typename T, int BN, bool RAGGED_K, bool B_MN>
+template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR>
 rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T>& args, size_t tiles, cudaStream_t s)
 {
-    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN>;
-    const size_t smem = TcShape<BN>::smem(args.experts);
+    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN, PAIR>;
+    const size_t smem = TcShape<BN, PAIR>::smem(args.experts);
     const int sms = sm_count();
-    if (sms < 1) return RS_ERR_CUDA;
+    if (sms < 2) return RS_ERR_CUDA;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return RS_ERR_CUDA;
-    size_t grid = (size_t)sms < tiles ? (size_t)sms : tiles;
-    if (grid > kTcMaxBlocks) grid = kTcMaxBlocks;
-    kernel<<<(unsigned)grid, kTcThreads, smem, s>>>(ma, mb, args);
-    return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    size_t grid = (size_t)sms < kTcMaxBlocks ? (size_t)sms : kTcMaxBlocks;
+    if constexpr (PAIR) grid = grid / 2 * 2 < tiles * 2 ? grid / 2 * 2 : tiles * 2;
+    else grid = grid < tiles ? grid : tiles;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, ma, mb, args) != cudaSuccess) {
+        cudaGetLastError();
+        return RS_ERR_CUDA;
+    }
+    return RS_OK;
 }
+
+// Pairs of blocks from this many rows per expert on (on average).
+constexpr size_t kPairRows = 512;
 
 template <typename T>
 rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
 {
     constexpr bool kBf16 = !__is_same(T, __half);
-    const bool wide = args.cols > 128;
+    const bool wide = args.cols > 128, pair = wide && args.rows >= kPairRows * args.experts;
     const uint64_t experts = b.expert_stride ? args.experts : 1;
     args.b_expert = b.expert_stride ? 1 : 0;
     CUtensorMap ma, mb;
@@ -45,14 +63,18 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
     const uint64_t sb[2] = {(uint64_t)b.row_stride * 2,
                             experts > 1 ? (uint64_t)b.expert_stride * 2 : (uint64_t)b.row_stride * 2};
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, kTcRows) ||
-        !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : wide ? 256 : 128))
+        !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : wide && !pair ? 256 : 128))
         return RS_ERR_UNSUPPORTED;
-    const size_t tiles = max_tiles(args.rows, args.experts, kTcRows) * ceil_div(args.cols, wide ? 256 : 128);
+    const size_t tiles =
+        max_tiles(args.rows, args.experts, pair ? 2 * kTcRows : kTcRows) * ceil_div(args.cols, wide ? 256 : 128);
+    if (pair)
+        return b.mn ? tc_launch<T, 256, false, true, true>(ma, mb, args, tiles, stream)
+                    : tc_launch<T, 256, false, false, true>(ma, mb, args, tiles, stream);
     if (wide)
-        return b.mn ? tc_launch<T, 256, false, true>(ma, mb, args, tiles, stream)
-                    : tc_launch<T, 256, false, false>(ma, mb, args, tiles, stream);
-    return b.mn ? tc_launch<T, 128, false, true>(ma, mb, args, tiles, stream)
-                : tc_launch<T, 128, false, false>(ma, mb, args, tiles, stream);
+        return b.mn ? tc_launch<T, 256, false, true, false>(ma, mb, args, tiles, stream)
+                    : tc_launch<T, 256, false, false, false>(ma, mb, args, tiles, stream);
+    return b.mn ? tc_launch<T, 128, false, true, false>(ma, mb, args, tiles, stream)
+                : tc_launch<T, 128, false, false, false>(ma, mb, args, tiles, stream);
 }
 
 template <typename T>
@@ -66,8 +88,8 @@ rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, 64) || !rstc::encode_map(&mb, kBf16, 2, b.p, db, sb, 64))
         return RS_ERR_UNSUPPORTED;
     const size_t tiles = ceil_div(args.out_rows, kTcRows) * args.experts * ceil_div(args.cols, wide ? 256 : 128);
-    return wide ? tc_launch<T, 256, true, true>(ma, mb, args, tiles, stream)
-                : tc_launch<T, 128, true, true>(ma, mb, args, tiles, stream);
+    return wide ? tc_launch<T, 256, true, true, false>(ma, mb, args, tiles, stream)
+                : tc_launch<T, 128, true, true, false>(ma, mb, args, tiles, stream);
 }
 
 }  // namespace rsx
