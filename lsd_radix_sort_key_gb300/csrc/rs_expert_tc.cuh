@@ -12,7 +12,9 @@
 //     past them; the surplus rows of D are computed and not stored.
 //   Ragged reduction (dw): the reduction runs over an expert's rows; the last
 //     slice's rows past the expert's end, which belong to the next expert, are
-//     overwritten with zeros in shared memory before they are used.
+//     overwritten with zeros in shared memory by warp 3 before the slice is
+//     handed on (the copy reports to warp 3, and warp 3 to the multiplying
+//     warp).
 // Either operand may have its reduction index or its row index adjacent in
 // memory (K-major / MN-major): both copy with rows of 128 bytes and both feed
 // the instruction directly, so nothing is transposed.
@@ -66,7 +68,7 @@ struct TcShape {
     static constexpr uint32_t kTileRows = PAIR ? 2 * kTcRows : kTcRows;
     static constexpr size_t smem(size_t experts)
     {
-        return 1024 + (size_t)kStages * kStage + kTcEpilogueWarps * kStaging + (2 * kStages + 4) * 8 + 16 +
+        return 1024 + (size_t)kStages * kStage + kTcEpilogueWarps * kStaging + (3 * kStages + 4) * 8 + 16 +
                Groups::words(experts) * 4;
     }
 };
@@ -142,30 +144,37 @@ __device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)
     __syncwarp();
 }
 
-// The reverse: this lane's row of a 32 x 16 piece (zeros outside).
+// The reverse, in two steps: the piece's vectors as memory holds them (zeros
+// outside), fetched ahead of their use, and then this lane's row of it.
 template <typename T>
-__device__ __forceinline__ void load_piece(uint4* stage, uint32_t (&mine)[8], const T* d, size_t d_i, uint32_t i0,
-                                           uint32_t i_end, uint32_t j0, uint32_t cols, bool vec)
+__device__ __forceinline__ void fetch_piece(uint4 (&v)[2], const T* d, size_t d_i, uint32_t i0, uint32_t i_end,
+                                            uint32_t j0, uint32_t cols, bool vec)
 {
     const uint32_t lane = threadIdx.x % 32;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const uint32_t row = n * 16 + lane / 2, q = lane % 2, i = i0 + row, j = j0 + q * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
+        v[n] = make_uint4(0, 0, 0, 0);
         if (i < i_end && j < cols) {
             const T* from = d + i * d_i + j;
             if (vec && j + 8 <= cols) {
-                v = __ldg(reinterpret_cast<const uint4*>(from));
+                v[n] = __ldg(reinterpret_cast<const uint4*>(from));
             } else {
                 uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     if (j + c < cols) w[c / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from)[c] << (c & 1) * 16;
-                v = make_uint4(w[0], w[1], w[2], w[3]);
+                v[n] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        stage[stage_slot(row, q)] = v;
     }
+}
+
+__device__ __forceinline__ void spread_piece(uint4* stage, uint32_t (&mine)[8], const uint4 (&v)[2])
+{
+    const uint32_t lane = threadIdx.x % 32;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) stage[stage_slot(n * 16 + lane / 2, lane % 2)] = v[n];
     __syncwarp();
     const uint4 lo = stage[stage_slot(lane, 0)], hi = stage[stage_slot(lane, 1)];
     mine[0] = lo.x, mine[1] = lo.y, mine[2] = lo.z, mine[3] = lo.w;
@@ -223,13 +232,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     using S = TcShape<BN, PAIR>;
     constexpr bool A_MN = RAGGED_K;
     static_assert(!RAGGED_K || B_MN, "both operands of a ragged reduction are MN-major");
-    static_assert(!RAGGED_K || !PAIR, "a ragged reduction's slices are mended by the block that multiplies them");
     extern __shared__ unsigned char raw[];
     unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
     unsigned char* staging = ring + S::kStages * S::kStage;
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + kTcEpilogueWarps * S::kStaging);
     uint64_t* empty = full + S::kStages;
-    uint64_t* acc_full = empty + S::kStages;
+    uint64_t* tail = empty + S::kStages;  // of slices that warp 3 mends
+    uint64_t* acc_full = tail + S::kStages;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     uint32_t* failed = slot + 1;
@@ -241,8 +250,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
         for (int s = 0; s < S::kStages; ++s) {
-            bar_init(full + s, 1);   // the leader's: bytes of both blocks
+            // the leader's: one arrival with the bytes of both blocks, or (ragged
+            // reduction) one of each block, from its copying or mending warp
+            bar_init(full + s, RAGGED_K ? blocks : 1);
             bar_init(empty + s, 1);  // each block's own
+            bar_init(tail + s, 1);   // each block's own
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(acc_full + s, 1);                            // each block's own
@@ -276,8 +288,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 unsigned char* a = ring + s * S::kStage;
                 unsigned char* b = a + S::kA;
                 if (elect_one()) {
-                    if (rank == 0) bar_expect(full + s, S::kStage * blocks);
-                    const uint32_t bar = PAIR ? cluster_addr(full + s, 0) : smem_addr(full + s);
+                    uint32_t bar = PAIR ? cluster_addr(full + s, 0) : smem_addr(full + s);
+                    if constexpr (RAGGED_K) {
+                        if (t.k_end - k < kTcDepth) {
+                            bar = PAIR ? cluster_addr(tail + s, rank) : smem_addr(tail + s);
+                            bar_expect(tail + s, S::kStage);
+                        } else if (rank != 0) {
+                            bar_expect_cluster(bar, S::kStage);
+                        } else {
+                            bar_expect(full + s, S::kStage);
+                        }
+                    } else if (rank == 0) {
+                        bar_expect(full + s, S::kStage * blocks);
+                    }
                     if constexpr (RAGGED_K) {
 #pragma unroll
                         for (int i = 0; i < kTcRows / 64; ++i)
@@ -319,23 +342,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++n;
             uint32_t more = 0;  // nothing accumulated yet
             for (uint32_t k = t.k0; k < t.k_end; k += kTcDepth) {
-                ok = bar_wait_warp(full + s, round & 1);
+                ok = PAIR && RAGGED_K ? bar_wait_cluster_warp(full + s, round & 1) : bar_wait_warp(full + s, round & 1);
                 if (!ok) break;
-                uint32_t steps = kTcDepth / 16;
-                if constexpr (RAGGED_K) {
-                    const uint32_t left = t.k_end - k;
-                    if (left < kTcDepth) {  // rows [left, 16 * steps) are another expert's
-                        steps = (left + 15) / 16;
-                        const uint32_t vecs = (steps * 16 - left) * 8;  // 16-byte vectors per box of 64 columns
-                        unsigned char* a = ring + s * S::kStage + left * 128;
-                        for (uint32_t v = lane; v < vecs; v += 32)
-#pragma unroll
-                            for (int i = 0; i < (kTcRows + BN) / 64; ++i)
-                                reinterpret_cast<uint4*>(a + i * 8192)[v] = make_uint4(0, 0, 0, 0);
-                        fence_async_smem();
-                        __syncwarp();
-                    }
-                }
+                const uint32_t steps = RAGGED_K ? min((t.k_end - k + 15) / 16, kTcDepth / 16u) : kTcDepth / 16;
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t da = desc_a + s * (S::kStage >> 4), db = desc_b + s * (S::kStage >> 4);
@@ -357,6 +366,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
         if (!ok) *failed = 1;
+    } else if (RAGGED_K && warp == 3) {
+        uint32_t used = 0, phases = 0;  // slices so far; bit s: the next phase of tail[s]
+        for (uint32_t tile = first_tile; tile < tiles; tile += tile_step) {
+            const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
+            used += (t.k_end - t.k0 + kTcDepth - 1) / kTcDepth;
+            const uint32_t left = (t.k_end - t.k0) % kTcDepth;
+            if (left == 0) continue;
+            const uint32_t s = (used - 1) % S::kStages;
+            if (!bar_wait_warp(tail + s, phases >> s & 1)) {
+                *failed = 1;
+                break;
+            }
+            phases ^= 1u << s;
+            // rows [left, next multiple of 16) of every box of 64 columns; the
+            // steps of 16 after that are not multiplied
+            const uint32_t vecs = ((left + 15) / 16 * 16 - left) * 8;
+            unsigned char* at = ring + s * S::kStage + left * 128;
+            for (uint32_t v = lane; v < vecs; v += 32)
+#pragma unroll
+                for (uint32_t i = 0; i < S::kStage / 8192; ++i)
+                    reinterpret_cast<uint4*>(at + i * 8192)[v] = make_uint4(0, 0, 0, 0);
+            fence_async();
+            __syncwarp();
+            if (elect_one()) {
+                if constexpr (PAIR) bar_arrive_cluster<true>(cluster_addr(full + s, 0));
+                else bar_arrive(full + s);
+            }
+            __syncwarp();
+        }
     } else if (warp >= kTcFirstEpilogueWarp) {
         constexpr uint32_t kPer = BN / (kTcEpilogueWarps / 4);  // columns per warp
         const uint32_t w = warp - kTcFirstEpilogueWarp;
@@ -382,38 +420,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             T* d = p.d + (RAGGED_K ? t.e * p.d_e : 0);
             // a piece with no rows or columns to store is not read either
             const uint32_t c_end = i0 >= t.i_end || t.j0 + c0 >= p.cols ? c0 : min(c0 + kPer, p.cols - t.j0);
-            for (uint32_t c = c0; c < c_end; c += 16) {
-                const uint32_t j = t.j0 + c;
-                uint32_t z[16], out[8] = {};
-                if (some) {
-                    tmem_load16(z, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter in the high half
-                    uint32_t res[8] = {};
+            if (some) {
+                // One piece ahead: the next piece's accumulators and residual are
+                // on their way while this one is finished (a load from tensor
+                // memory takes about 1000 cycles beside a busy tensor pipe).
+                uint32_t z[2][16];
+                uint4 res[2][2];
+                auto fetch = [&](uint32_t c, uint32_t (&zz)[16], uint4 (&rr)[2]) {
+                    tmem_load16(zz, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter in the high half
                     if (p.residual)
-                        load_piece<T>(stage, res, p.residual, p.residual_i, i0, t.i_end, j, p.cols, vec_res);
-                    tmem_load_wait(z);
-                    if (p.bias) add_bias<T>(z, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
+                        fetch_piece<T>(rr, p.residual, p.residual_i, i0, t.i_end, t.j0 + c, p.cols, vec_res);
+                };
+                if (c0 < c_end) fetch(c0, z[0], res[0]);
+#pragma unroll
+                for (uint32_t q = 0; q < kPer / 16; ++q) {
+                    const uint32_t c = c0 + q * 16, j = t.j0 + c;
+                    if (c >= c_end) break;
+                    uint32_t(&zz)[16] = z[q & 1];
+                    tmem_load_wait(zz);
+                    if (c + 16 < c_end) fetch(c + 16, z[(q & 1) ^ 1], res[(q & 1) ^ 1]);
+                    uint32_t out[8], add[8] = {};
+                    if (p.bias) add_bias<T>(zz, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
                     if (p.pre) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            out[i] = pack2<T>(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+                            out[i] = pack2<T>(__uint_as_float(zz[2 * i]), __uint_as_float(zz[2 * i + 1]));
                         store_piece<T>(stage, out, p.pre, p.pre_i, i0, t.i_end, j, p.cols, vec_pre);
                     }
+                    if (p.residual) spread_piece(stage, add, res[q & 1]);
                     switch (p.act) {
-                    case RS_ACT_NONE: finish<T, RS_ACT_NONE>(out, z, res); break;
-                    case RS_ACT_RELU: finish<T, RS_ACT_RELU>(out, z, res); break;
-                    case RS_ACT_GELU: finish<T, RS_ACT_GELU>(out, z, res); break;
-                    default: finish<T, RS_ACT_SILU>(out, z, res); break;
+                    case RS_ACT_NONE: finish<T, RS_ACT_NONE>(out, zz, add); break;
+                    case RS_ACT_RELU: finish<T, RS_ACT_RELU>(out, zz, add); break;
+                    case RS_ACT_GELU: finish<T, RS_ACT_GELU>(out, zz, add); break;
+                    default: finish<T, RS_ACT_SILU>(out, zz, add); break;
                     }
-                } else if (p.pre) {
-                    store_piece<T>(stage, out, p.pre, p.pre_i, i0, t.i_end, j, p.cols, vec_pre);
+                    store_piece<T>(stage, out, d, p.d_i, i0, t.i_end, j, p.cols, vec_d);
                 }
-                store_piece<T>(stage, out, d, p.d_i, i0, t.i_end, j, p.cols, vec_d);
+            } else {  // unused rows, or an expert without rows
+                const uint32_t out[8] = {};
+                for (uint32_t c = c0; c < c_end; c += 16) {
+                    if (p.pre) store_piece<T>(stage, out, p.pre, p.pre_i, i0, t.i_end, t.j0 + c, p.cols, vec_pre);
+                    store_piece<T>(stage, out, d, p.d_i, i0, t.i_end, t.j0 + c, p.cols, vec_d);
+                }
             }
             if (some) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) bar_arrive_cluster(cluster_addr(acc_empty + h, 0));
+                    if constexpr (PAIR) bar_arrive_cluster<false>(cluster_addr(acc_empty + h, 0));
                     else bar_arrive(acc_empty + h);
                 }
             }

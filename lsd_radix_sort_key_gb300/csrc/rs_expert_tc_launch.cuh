@@ -81,13 +81,15 @@ template <typename T>
 rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
 {
     constexpr bool kBf16 = !__is_same(T, __half);
-    const bool wide = args.cols > 128;
+    const bool wide = args.cols > 128, pair = wide && args.out_rows > 128;
     CUtensorMap ma, mb;
     const uint64_t da[2] = {args.out_rows, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
     const uint64_t db[2] = {args.cols, args.rows}, sb[1] = {(uint64_t)b.row_stride * 2};
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, 64) || !rstc::encode_map(&mb, kBf16, 2, b.p, db, sb, 64))
         return RS_ERR_UNSUPPORTED;
-    const size_t tiles = ceil_div(args.out_rows, kTcRows) * args.experts * ceil_div(args.cols, wide ? 256 : 128);
+    const size_t tiles =
+        ceil_div(args.out_rows, pair ? 2 * kTcRows : kTcRows) * args.experts * ceil_div(args.cols, wide ? 256 : 128);
+    if (pair) return tc_launch<T, 256, true, true, true>(ma, mb, args, tiles, stream);
     return wide ? tc_launch<T, 256, true, true, false>(ma, mb, args, tiles, stream)
                 : tc_launch<T, 128, true, true, false>(ma, mb, args, tiles, stream);
 }

@@ -97,9 +97,9 @@ __device__ __forceinline__ bool bar_wait_cluster_warp(uint64_t* bar, uint32_t pa
     return __all_sync(0xFFFFFFFFu, bar_wait_cluster(bar, parity));
 }
 
-// This thread's ordinary writes to shared memory before later reads of it by
-// the async proxy (tensor cores, bulk copies).
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// This thread's ordinary writes before later accesses of the async proxy
+// (tensor cores, bulk copies), from either block of a pair.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // ---- pairs of blocks (clusters of two)
 
@@ -118,9 +118,24 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
     return a;
 }
 
+// An arrival on a barrier of either block.  RELEASE: this thread's writes are
+// visible to the other block first, which waits for every store it has in
+// flight; without, the arrival only says that what the thread waited for
+// itself (loads from tensor memory) is done.
+template <bool RELEASE>
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    if constexpr (!RELEASE)
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect_cluster(uint32_t cluster_bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
+                 "r"(bytes)
+                 : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync()

@@ -91,7 +91,8 @@ def test_epilogues(dt, act, bias, residual):
 @pytest.mark.parametrize("counts,inner,outer", [([1] * 64, 512, 384), ([0] * 31 + [7], 1024, 256),
                                                 ([3, 0, 9, 17, 33, 1, 5, 2], 2048, 1032), ([16] * 300, 64, 72),
                                                 ([1000, 500, 0, 1548], 1000, 1160), ([4096], 1024, 512),
-                                                ([129] * 13, 72, 1024)])
+                                                ([129] * 13, 72, 1024), ([700, 1, 0, 15, 64, 63, 65, 17], 264, 520),
+                                                ([2000, 3], 136, 776)])
 def test_larger(dt, counts, inner, outer):
     dtype = TYPES[dt]
     a = make(counts, 11, inner, outer, dtype, 7)
@@ -277,13 +278,14 @@ def test_same_call_same_bits():
             assert torch.equal(p, q)
 
 
-def test_a_wait_that_runs_out_is_reported():
-    a = make([300, 200], 0, 256, 512, torch.bfloat16, 27)
+@pytest.mark.parametrize("rows", [250, 800])  # single blocks, pairs of blocks
+def test_a_wait_that_runs_out_is_reported(rows):
+    a = make([rows + 50, rows - 50], 0, 256, 512, torch.bfloat16, 27)
     temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     y = rs.expert_matmul(a["x"], a["w"], a["offsets"], temp=temp)
     assert rs.rs_expert_matmul_status(temp) == 0
     out = torch.empty_like(y)
-    d = rs.ExpertMatmulDesc(2, 0, 2, 500, 256, 512, a["offsets"].data_ptr(), a["x"].data_ptr(), 256, a["w"].data_ptr(),
+    d = rs.ExpertMatmulDesc(2, 0, 2, 2 * rows, 256, 512, a["offsets"].data_ptr(), a["x"].data_ptr(), 256, a["w"].data_ptr(),
                             256 * 512, 256, 1)
     d.y, d.y_stride, d.temp, d.temp_bytes = out.data_ptr(), 512, temp.data_ptr(), temp.numel()
     d.stream, d.stall_tile = torch.cuda.current_stream().cuda_stream, 4
