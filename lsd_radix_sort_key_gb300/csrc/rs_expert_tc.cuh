@@ -110,18 +110,37 @@ __device__ __forceinline__ float2 unpack2(uint32_t u)
     else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
-// One warp's 32 x 16 piece of D goes through shared memory, so that the lane
-// that holds a row in tensor memory need not store it: `mine` is this lane's
-// row as 2 vectors of 8 elements, and memory sees 2 lanes (a whole sector) per
-// row.  The vectors are permuted by the row so that neither side has bank
+// How a warp's 32 x 16 piece of a matrix meets memory.  A lane holds a row of
+// it as 16 elements: one whole 32-byte sector, which it loads or stores itself
+// where the rows are 32-byte aligned and the piece is whole (`direct`).
+// Otherwise the piece goes through shared memory, 2 lanes per row, so that
+// memory sees 16-byte vectors where the rows allow those, and elements where
+// not; the vectors are permuted by the row so that neither side has bank
 // conflicts.
+template <typename T>
+struct Rows {
+    T* p;
+    size_t stride;
+    bool direct, vec;
+    __device__ __forceinline__ Rows(T* p, size_t stride, size_t expert_stride) : p(p), stride(stride)
+    {
+        const uintptr_t bits = (uintptr_t)p | stride * sizeof(T) | expert_stride * sizeof(T);
+        direct = bits % 32 == 0;
+        vec = bits % 16 == 0;
+    }
+};
+
 __device__ __forceinline__ uint32_t stage_slot(uint32_t row, uint32_t vec) { return row * 2 + (vec ^ ((row >> 2) & 1)); }
 
 template <typename T>
-__device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)[8], T* d, size_t d_i, uint32_t i0,
-                                            uint32_t i_end, uint32_t j0, uint32_t cols, bool vec)
+__device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)[8], const Rows<T>& d, uint32_t i0,
+                                            uint32_t i_end, uint32_t j0, uint32_t cols)
 {
     const uint32_t lane = threadIdx.x % 32;
+    if (d.direct && j0 + 16 <= cols) {
+        if (i0 + lane < i_end) rstc::store_sector(d.p + (i0 + lane) * d.stride + j0, mine);
+        return;
+    }
     stage[stage_slot(lane, 0)] = make_uint4(mine[0], mine[1], mine[2], mine[3]);
     stage[stage_slot(lane, 1)] = make_uint4(mine[4], mine[5], mine[6], mine[7]);
     __syncwarp();
@@ -130,8 +149,8 @@ __device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)
         const uint32_t row = n * 16 + lane / 2, q = lane % 2, i = i0 + row, j = j0 + q * 8;
         if (i < i_end && j < cols) {
             const uint4 v = stage[stage_slot(row, q)];
-            T* to = d + i * d_i + j;
-            if (vec && j + 8 <= cols) {
+            T* to = d.p + i * d.stride + j;
+            if (d.vec && j + 8 <= cols) {
                 *reinterpret_cast<uint4*>(to) = v;
             } else {
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -144,60 +163,78 @@ __device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)
     __syncwarp();
 }
 
-// The reverse, in two steps: the piece's vectors as memory holds them (zeros
-// outside), fetched ahead of their use, and then this lane's row of it.
+// The reverse, in two steps: the piece as the accesses bring it (zeros
+// outside), fetched ahead of its use, and then this lane's row of it.
 template <typename T>
-__device__ __forceinline__ void fetch_piece(uint4 (&v)[2], const T* d, size_t d_i, uint32_t i0, uint32_t i_end,
-                                            uint32_t j0, uint32_t cols, bool vec)
+__device__ __forceinline__ void fetch_piece(uint32_t (&v)[8], const Rows<const T>& d, uint32_t i0, uint32_t i_end,
+                                            uint32_t j0, uint32_t cols)
 {
     const uint32_t lane = threadIdx.x % 32;
 #pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = 0;
+    if (d.direct && j0 + 16 <= cols) {
+        if (i0 + lane < i_end) rstc::load_sector(v, d.p + (i0 + lane) * d.stride + j0);
+        return;
+    }
+#pragma unroll
     for (int n = 0; n < 2; ++n) {
         const uint32_t row = n * 16 + lane / 2, q = lane % 2, i = i0 + row, j = j0 + q * 8;
-        v[n] = make_uint4(0, 0, 0, 0);
         if (i < i_end && j < cols) {
-            const T* from = d + i * d_i + j;
-            if (vec && j + 8 <= cols) {
-                v[n] = __ldg(reinterpret_cast<const uint4*>(from));
+            const T* from = d.p + i * d.stride + j;
+            if (d.vec && j + 8 <= cols) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(from));
+                v[4 * n] = u.x, v[4 * n + 1] = u.y, v[4 * n + 2] = u.z, v[4 * n + 3] = u.w;
             } else {
-                uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    if (j + c < cols) w[c / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from)[c] << (c & 1) * 16;
-                v[n] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (j + c < cols)
+                        v[4 * n + c / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(from)[c] << (c & 1) * 16;
             }
         }
     }
 }
 
-__device__ __forceinline__ void spread_piece(uint4* stage, uint32_t (&mine)[8], const uint4 (&v)[2])
+template <typename T>
+__device__ __forceinline__ void spread_piece(uint4* stage, uint32_t (&v)[8], const Rows<const T>& d, uint32_t j0,
+                                             uint32_t cols)
 {
+    if (d.direct && j0 + 16 <= cols) return;
     const uint32_t lane = threadIdx.x % 32;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) stage[stage_slot(n * 16 + lane / 2, lane % 2)] = v[n];
+    for (int n = 0; n < 2; ++n)
+        stage[stage_slot(n * 16 + lane / 2, lane % 2)] = make_uint4(v[4 * n], v[4 * n + 1], v[4 * n + 2], v[4 * n + 3]);
     __syncwarp();
     const uint4 lo = stage[stage_slot(lane, 0)], hi = stage[stage_slot(lane, 1)];
-    mine[0] = lo.x, mine[1] = lo.y, mine[2] = lo.z, mine[3] = lo.w;
-    mine[4] = hi.x, mine[5] = hi.y, mine[6] = hi.z, mine[7] = hi.w;
+    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+    v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
     __syncwarp();
 }
 
-template <typename T>
-__device__ __forceinline__ bool rows_aligned(const T* p, size_t stride)
+// z = act(z)
+template <int ACT>
+__device__ __forceinline__ void activate_all(uint32_t (&z)[16])
 {
-    return ((uintptr_t)p | (stride * sizeof(T))) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(activate<ACT, true>(__uint_as_float(z[i])));
 }
 
-// out = act(z) + residual, rounded.
-template <typename T, int ACT>
-__device__ __forceinline__ void finish(uint32_t (&out)[8], const uint32_t (&z)[16], const uint32_t (&res)[8])
+// z += v (16 elements)
+template <typename T>
+__device__ __forceinline__ void add_all(uint32_t (&z)[16], const uint32_t (&v)[8])
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 r = unpack2<T>(res[i]);
-        out[i] = pack2<T>(activate<ACT, true>(__uint_as_float(z[2 * i])) + r.x,
-                          activate<ACT, true>(__uint_as_float(z[2 * i + 1])) + r.y);
+        const float2 f = unpack2<T>(v[i]);
+        z[2 * i] = __float_as_uint(__uint_as_float(z[2 * i]) + f.x);
+        z[2 * i + 1] = __float_as_uint(__uint_as_float(z[2 * i + 1]) + f.y);
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void round_all(uint32_t (&out)[8], const uint32_t (&z)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = pack2<T>(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
 }
 
 template <typename T>
@@ -213,12 +250,7 @@ __device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint3
         for (int i = 0; i < 16; ++i)
             if (i < left) w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(bias)[i] << (i & 1) * 16;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = unpack2<T>(w[i]);
-        z[2 * i] = __float_as_uint(__uint_as_float(z[2 * i]) + f.x);
-        z[2 * i + 1] = __float_as_uint(__uint_as_float(z[2 * i + 1]) + f.y);
-    }
+    add_all<T>(z, w);
 }
 
 // Ragged rows: A is K-major rows of map_a (2-d), B is per expert (map_b, 3-d),
@@ -401,8 +433,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t quarter = warp % 4;  // the 32 tensor-memory lanes this warp can read
         const uint32_t c0 = w / 4 * kPer;   // and its share of the columns
         uint4* stage = reinterpret_cast<uint4*>(staging + w * S::kStaging);
-        const bool vec_d = rows_aligned(p.d, p.d_i | (RAGGED_K ? p.d_e : 0)), vec_pre = rows_aligned(p.pre, p.pre_i);
-        const bool vec_res = rows_aligned(p.residual, p.residual_i), vec_bias = rows_aligned(p.bias, p.bias_e);
+        Rows<T> d(p.d, p.d_i, RAGGED_K ? p.d_e : 0);
+        const Rows<T> pre(p.pre, p.pre_i, 0);
+        const Rows<const T> residual(p.residual, p.residual_i, 0);
+        const bool vec_bias = ((uintptr_t)p.bias | p.bias_e * sizeof(T)) % 16 == 0;
         uint32_t n = 0;
         for (uint32_t tile = first_tile; tile < tiles; tile += tile_step) {
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
@@ -417,50 +451,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++n;
             }
             const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32;
-            T* d = p.d + (RAGGED_K ? t.e * p.d_e : 0);
+            if constexpr (RAGGED_K) d.p = p.d + t.e * p.d_e;
             // a piece with no rows or columns to store is not read either
             const uint32_t c_end = i0 >= t.i_end || t.j0 + c0 >= p.cols ? c0 : min(c0 + kPer, p.cols - t.j0);
             if (some) {
                 // One piece ahead: the next piece's accumulators and residual are
                 // on their way while this one is finished (a load from tensor
                 // memory takes about 1000 cycles beside a busy tensor pipe).
-                uint32_t z[2][16];
-                uint4 res[2][2];
-                auto fetch = [&](uint32_t c, uint32_t (&zz)[16], uint4 (&rr)[2]) {
+                uint32_t z[2][16], add[2][8];
+                auto fetch = [&](uint32_t c, uint32_t (&zz)[16], uint32_t (&r)[8]) {
                     tmem_load16(zz, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter in the high half
-                    if (p.residual)
-                        fetch_piece<T>(rr, p.residual, p.residual_i, i0, t.i_end, t.j0 + c, p.cols, vec_res);
+                    if (p.residual) fetch_piece<T>(r, residual, i0, t.i_end, t.j0 + c, p.cols);
                 };
-                if (c0 < c_end) fetch(c0, z[0], res[0]);
+                if (c0 < c_end) fetch(c0, z[0], add[0]);
 #pragma unroll
                 for (uint32_t q = 0; q < kPer / 16; ++q) {
                     const uint32_t c = c0 + q * 16, j = t.j0 + c;
                     if (c >= c_end) break;
                     uint32_t(&zz)[16] = z[q & 1];
                     tmem_load_wait(zz);
-                    if (c + 16 < c_end) fetch(c + 16, z[(q & 1) ^ 1], res[(q & 1) ^ 1]);
-                    uint32_t out[8], add[8] = {};
+                    if (c + 16 < c_end) fetch(c + 16, z[(q & 1) ^ 1], add[(q & 1) ^ 1]);
+                    uint32_t out[8];
                     if (p.bias) add_bias<T>(zz, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
                     if (p.pre) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            out[i] = pack2<T>(__uint_as_float(zz[2 * i]), __uint_as_float(zz[2 * i + 1]));
-                        store_piece<T>(stage, out, p.pre, p.pre_i, i0, t.i_end, j, p.cols, vec_pre);
+                        round_all<T>(out, zz);
+                        store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                     }
-                    if (p.residual) spread_piece(stage, add, res[q & 1]);
-                    switch (p.act) {
-                    case RS_ACT_NONE: finish<T, RS_ACT_NONE>(out, zz, add); break;
-                    case RS_ACT_RELU: finish<T, RS_ACT_RELU>(out, zz, add); break;
-                    case RS_ACT_GELU: finish<T, RS_ACT_GELU>(out, zz, add); break;
-                    default: finish<T, RS_ACT_SILU>(out, zz, add); break;
+                    if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(zz);
+                    else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(zz);
+                    else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(zz);
+                    if (p.residual) {
+                        spread_piece<T>(stage, add[q & 1], residual, j, p.cols);
+                        add_all<T>(zz, add[q & 1]);
                     }
-                    store_piece<T>(stage, out, d, p.d_i, i0, t.i_end, j, p.cols, vec_d);
+                    round_all<T>(out, zz);
+                    store_piece<T>(stage, out, d, i0, t.i_end, j, p.cols);
                 }
             } else {  // unused rows, or an expert without rows
                 const uint32_t out[8] = {};
                 for (uint32_t c = c0; c < c_end; c += 16) {
-                    if (p.pre) store_piece<T>(stage, out, p.pre, p.pre_i, i0, t.i_end, t.j0 + c, p.cols, vec_pre);
-                    store_piece<T>(stage, out, d, p.d_i, i0, t.i_end, t.j0 + c, p.cols, vec_d);
+                    if (p.pre) store_piece<T>(stage, out, pre, i0, t.i_end, t.j0 + c, p.cols);
+                    store_piece<T>(stage, out, d, i0, t.i_end, t.j0 + c, p.cols);
                 }
             }
             if (some) {

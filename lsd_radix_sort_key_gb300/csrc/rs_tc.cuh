@@ -48,13 +48,16 @@ __device__ __forceinline__ void bar_arrive(uint64_t* bar)
 // still ends.
 constexpr long long kWaitClocks = 1ll << 32;
 
+// The thread may sleep this long (ns) in one try.
+constexpr uint32_t kTryNs = 1000000;
+
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity)
 {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kTryNs)
         : "memory");
     return done != 0;
 }
@@ -76,10 +79,10 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity)
     do {
         uint32_t done;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
             " selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(kTryNs)
             : "memory");
         if (done) return true;
     } while (clock64() - start < kWaitClocks);
@@ -183,6 +186,22 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
             "%4}], [%5];" ::"r"(smem_addr(dst)),
             "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
+}
+
+// ---- 32 bytes of global memory, 32-byte aligned: one sector in one access
+
+__device__ __forceinline__ void load_sector(uint32_t (&r)[8], const void* p)
+{
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
+
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&r)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // ---- tensor memory
