@@ -10,14 +10,20 @@
 // kTileSlots, a tile into one run of consecutive slots per warp.  Then
 // #{s' < s, same expert} = slots of e in earlier chunks + in earlier tiles +
 // in earlier warps of this tile + in earlier slots of this warp; the last two
-// come from __match_any_sync and one counter per (warp, expert) in shared
-// memory.  The whole sort is ONE kernel: up to kOneBlockSlots one block, above
-// that a cooperative launch of at most one block per SM in which every block
-// publishes its counts, the grid meets once, and every block then sums the
-// counts before its own (blocks * experts words, from L2).
+// come from one counter per (warp, expert) in shared memory and from the lanes
+// of equal expert, found with one ballot per bit of the expert number
+// (__match_any_sync took 70 cycles a time on an SM: 9 of the 23 us that 2^20
+// slots of 256 experts took).  The whole sort is ONE kernel: up to
+// kOneBlockSlots one block, above that a cooperative launch of at most one
+// block per SM: every block publishes its counts, one warp per expert scans
+// them over the blocks, and every block reads back its own.  (Every block
+// summing all counts before its own needs one meeting of the grid less, 1.3 us,
+// but reads blocks * experts words: 6.7 us.)  A block of such a grid puts a
+// tile's slots in expert order in shared memory first, so that `order` is
+// written in runs and not in single words (4.6 us).
 //
 // The bytes are few (12 or 16 per slot), so the time is launches and
-// dependent round trips.
+// dependent round trips: see the figures at the entry point.
 #include <cooperative_groups.h>
 
 #include "rs_expert_common.cuh"
@@ -40,7 +46,8 @@ struct SortParams {
     int32_t* order;
     int32_t* position;
     int32_t* offsets;
-    uint32_t* counts;  // [blocks][experts + 1], unused by a single block
+    int bits;          // of an expert number, the one past the dropped slots' included
+    uint32_t* counts;  // [blocks][experts + 1], then [experts + 1] totals; unused by a single block
 };
 
 // The slot's expert, or `experts` for a dropped slot.
@@ -54,18 +61,23 @@ __device__ __forceinline__ uint32_t load_expert(const SortParams& p, uint32_t s)
     return v < p.experts ? v : p.experts;
 }
 
-// A block's shared memory: per expert the first free row (base) and two
-// working sums, and per (warp, expert) a counter.
+// A block's shared memory: per expert the first row of its next slots (base),
+// the tile's count (total) and the sum of the tile's counts of lower experts
+// (local); per (warp, expert) a counter; and in a grid the tile's slots in
+// expert order.
 struct Shared {
-    uint32_t *base, *total, *before;
+    uint32_t *base, *total, *local, *sorted;
     uint16_t* counter;
     uint32_t bins;
-    __device__ __forceinline__ Shared(uint32_t* mem, uint32_t bins)
-        : base(mem), total(mem + bins), before(mem + 2 * bins), counter(reinterpret_cast<uint16_t*>(mem + 3 * bins)),
-          bins(bins)
+    __device__ __forceinline__ Shared(uint32_t* mem, uint32_t bins, bool grid)
+        : base(mem), total(mem + bins), local(mem + 2 * bins), sorted(mem + 3 * bins),
+          counter(reinterpret_cast<uint16_t*>(mem + 3 * bins + (grid ? kTileSlots : 0))), bins(bins)
     {
     }
-    static size_t bytes(size_t bins, size_t warps) { return 12 * bins + 2 * rsx::align_up(bins * warps, 2); }
+    static size_t bytes(size_t bins, size_t warps, bool grid)
+    {
+        return 12 * bins + (grid ? 4 * kTileSlots : 0) + 2 * rsx::align_up(bins * warps, 2);
+    }
 };
 
 // Where a thread's slots of a tile are: slots first + 32 * i, below end.
@@ -99,7 +111,11 @@ __device__ __forceinline__ void rank_tile(const SortParams& p, const Shared& sh,
     for (int i = 0; i < kItems; ++i) {
         const uint32_t e = expert[i];
         if (__all_sync(0xFFFFFFFFu, e == sh.bins)) break;  // the run ended (the ranks of the rest are not used)
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
+        uint32_t peers = 0xFFFFFFFFu;
+        for (int b = 0; b < p.bits; ++b) {
+            const uint32_t set = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
+            peers &= e >> b & 1 ? set : ~set;
+        }
         const uint32_t earlier = __popc(peers & ((1u << lane) - 1));
         const uint32_t before = e < sh.bins ? mine[e] : 0u;
         __syncwarp();
@@ -128,15 +144,15 @@ __device__ __forceinline__ void scan_warps(const Shared& sh)
     __syncthreads();
 }
 
-// base[e] = sum of total over the experts below e, + before[e].
-__device__ __forceinline__ void scan_experts(const SortParams& p, const Shared& sh)
+// out[e] = the sum of in[0 .. e), for all bins.
+__device__ __forceinline__ void scan_bins(uint32_t bins, const uint32_t* in, uint32_t* out)
 {
     __shared__ uint32_t warp_sum[kMaxThreads / 32];
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, warps = blockDim.x / 32;
     uint32_t carry = 0;
-    for (uint32_t e0 = 0; e0 < sh.bins; e0 += blockDim.x) {
+    for (uint32_t e0 = 0; e0 < bins; e0 += blockDim.x) {
         const uint32_t e = e0 + tid;
-        const uint32_t c = e < sh.bins ? sh.total[e] : 0u;
+        const uint32_t c = e < bins ? in[e] : 0u;
         uint32_t inc = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -155,28 +171,36 @@ __device__ __forceinline__ void scan_experts(const SortParams& p, const Shared& 
             if (lane >= d) sums += up;
         }
         const uint32_t earlier = __shfl_sync(0xFFFFFFFFu, sums - own, warp);
-        if (e < sh.bins) {
-            const uint32_t first = carry + earlier + inc - c;
-            sh.base[e] = first + sh.before[e];
-            if (blockIdx.x == 0) p.offsets[e] = (int32_t)first;
-        }
+        if (e < bins) out[e] = carry + earlier + inc - c;
         carry += __shfl_sync(0xFFFFFFFFu, sums, 31);
     }
     __syncthreads();
 }
 
-__device__ __forceinline__ void place_tile(const SortParams& p, const Shared& sh, const Run& run,
-                                           const uint32_t (&rank)[kItems])
+// Writes a ranked tile's positions and orders.  In a grid the orders go
+// through shared memory: sorted[i] = expert << 16 | slot - begin, i the slot's
+// place in the tile by expert.
+__device__ __forceinline__ void place_tile(const SortParams& p, const Shared& sh, const Run& run, uint32_t begin,
+                                           uint32_t len, const uint32_t (&rank)[kItems])
 {
     const uint16_t* mine = sh.counter + threadIdx.x / 32 * sh.bins;
+    const bool staged = gridDim.x > 1;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const uint32_t s = run.first + 32 * i;
         if (s < run.end) {
-            const uint32_t e = rank[i] >> 16, at = sh.base[e] + mine[e] + (rank[i] & 0xFFFFu);
+            const uint32_t e = rank[i] >> 16, nth = mine[e] + (rank[i] & 0xFFFFu), at = sh.base[e] + nth;
             p.position[s] = (int32_t)at;
-            if (at < p.n) p.order[at] = (int32_t)s;
+            if (staged) sh.sorted[sh.local[e] + nth] = e << 16 | (s - begin);
+            else if (at < p.n) p.order[at] = (int32_t)s;
         }
+    }
+    if (!staged) return;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < len; i += blockDim.x) {
+        const uint32_t v = sh.sorted[i], e = v >> 16;
+        const uint32_t at = sh.base[e] + (i - sh.local[e]);
+        if (at < p.n) p.order[at] = (int32_t)(begin + (v & 0xFFFFu));
     }
 }
 
@@ -184,8 +208,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
 {
     extern __shared__ uint32_t mem[];
     const uint32_t bins = p.experts + 1, tid = threadIdx.x;
-    const Shared sh(mem, bins);
-    const uint32_t begin = blockIdx.x * p.chunk, end = min(p.n, begin + p.chunk);  // begin <= n by the grid's size
+    const bool grid = gridDim.x > 1;
+    const Shared sh(mem, bins, grid);
+    const uint32_t begin = blockIdx.x * p.chunk, end = min(p.n, begin + p.chunk);  // begin < n by the grid's size
     uint32_t rank[kItems];
 
     // This block's counts; a chunk of one tile is ranked on the way.
@@ -201,48 +226,61 @@ __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
         __syncthreads();
     }
 
-    // Every block's counts -> the first row of this block's slots of each expert.
-    if (gridDim.x > 1) {
-        for (uint32_t e = tid; e < bins; e += blockDim.x) {
-            p.counts[(size_t)blockIdx.x * bins + e] = sh.total[e];
-            sh.total[e] = 0;
-            sh.before[e] = 0;
-        }
+    if (grid) {
+        // every block's counts -> the counts of the blocks before it, and the totals
+        uint32_t* mine = p.counts + (size_t)blockIdx.x * bins;
+        uint32_t* totals = p.counts + (size_t)gridDim.x * bins;
+        for (uint32_t e = tid; e < bins; e += blockDim.x) mine[e] = sh.total[e];
         cooperative_groups::this_grid().sync();
-        // neighbouring threads take neighbouring experts, thread groups every groups-th block
-        const uint32_t lanes = (bins + 31) / 32 * 32, groups = max(1u, blockDim.x / lanes);
-        const uint32_t group = tid / lanes;
-        for (uint32_t e = groups > 1 ? tid % lanes : tid; group < groups && e < bins; e += groups > 1 ? lanes : blockDim.x) {
-            uint32_t sum = 0, early = 0;
-#pragma unroll 8
-            for (uint32_t b = groups > 1 ? group : 0; b < gridDim.x; b += groups) {
-                const uint32_t c = __ldcg(p.counts + (size_t)b * bins + e);
-                sum += c;
-                early += b < blockIdx.x ? c : 0u;
+        const uint32_t lane = tid % 32, warps = blockDim.x / 32;
+        for (uint32_t e = blockIdx.x + gridDim.x * (tid / 32); e < bins; e += gridDim.x * warps) {
+            uint32_t c[kMaxBlocks / 32], carry = 0;
+#pragma unroll
+            for (uint32_t i = 0; i < kMaxBlocks / 32; ++i) {
+                const uint32_t b = i * 32 + lane;
+                c[i] = b < gridDim.x ? __ldcg(p.counts + (size_t)b * bins + e) : 0u;
             }
-            if (groups > 1) {
-                atomicAdd(&sh.total[e], sum);
-                atomicAdd(&sh.before[e], early);
-            } else {
-                sh.total[e] = sum;
-                sh.before[e] = early;
+#pragma unroll
+            for (uint32_t i = 0; i < kMaxBlocks / 32; ++i) {
+                if (i * 32 >= gridDim.x) break;
+                uint32_t inc = c[i];
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                    if (lane >= d) inc += up;
+                }
+                const uint32_t b = i * 32 + lane;
+                if (b < gridDim.x) p.counts[(size_t)b * bins + e] = carry + inc - c[i];
+                carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
             }
+            if (lane == 0) totals[e] = carry;
+        }
+        if (one_tile) scan_bins(bins, sh.total, sh.local);
+        cooperative_groups::this_grid().sync();
+        for (uint32_t e = tid; e < bins; e += blockDim.x) sh.total[e] = __ldcg(totals + e);
+        __syncthreads();
+        scan_bins(bins, sh.total, sh.base);
+        for (uint32_t e = tid; e < bins; e += blockDim.x) {
+            if (blockIdx.x == 0) p.offsets[e] = (int32_t)sh.base[e];
+            sh.base[e] += __ldcg(mine + e);
         }
     } else {
-        for (uint32_t e = tid; e < bins; e += blockDim.x) sh.before[e] = 0;
+        scan_bins(bins, sh.total, sh.base);
+        for (uint32_t e = tid; e < bins; e += blockDim.x) p.offsets[e] = (int32_t)sh.base[e];
     }
     __syncthreads();
-    scan_experts(p, sh);
 
     if (one_tile) {
-        place_tile(p, sh, run, rank);
+        place_tile(p, sh, run, begin, end - begin, rank);
         return;
     }
     for (uint32_t at = begin; at < end; at += kTileSlots) {
-        const Run r(at, min(end - at, kTileSlots));
+        const uint32_t len = min(end - at, kTileSlots);
+        const Run r(at, len);
         rank_tile(p, sh, r, rank);
         scan_warps(sh);
-        place_tile(p, sh, r, rank);
+        scan_bins(bins, sh.total, sh.local);
+        place_tile(p, sh, r, at, len, rank);
         __syncthreads();
         for (uint32_t e = tid; e < bins; e += blockDim.x) sh.base[e] += sh.total[e];
         // (rank_tile's barriers come before the next use of base)
@@ -258,7 +296,7 @@ size_t rs_expert_sort_temp_bytes(size_t n, int num_experts)
     if (n > RS_EXPERT_SLOTS_MAX || num_experts < 1 || num_experts > RS_EXPERTS_MAX) return (size_t)-1;
     if (n <= kOneBlockSlots) return 0;
     const size_t blocks = rsx::ceil_div(n, kChunkSlots);
-    return rsx::align_up((blocks < kMaxBlocks ? blocks : kMaxBlocks) * ((size_t)num_experts + 1) * 4, 256);
+    return rsx::align_up(((blocks < kMaxBlocks ? blocks : kMaxBlocks) + 1) * ((size_t)num_experts + 1) * 4, 256);
 }
 
 rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_experts, int32_t* order,
@@ -287,14 +325,15 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
     p.position = position;
     p.offsets = offsets;
     p.counts = static_cast<uint32_t*>(temp);
-    const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32);
+    p.bits = 32 - __builtin_clz((uint32_t)bins);  // of the largest value ranked, bins
+    const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32, n > kOneBlockSlots);
     if (most_smem > 48 * 1024 - 256 &&
         cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
         return RS_ERR_CUDA;
     if (n <= kOneBlockSlots) {
         p.chunk = (uint32_t)n;
         const unsigned threads = (unsigned)(n < kMaxThreads ? rsx::align_up(n, 32) : kMaxThreads);
-        k_expert_sort<<<1, threads, Shared::bytes(bins, threads / 32), s>>>(p);
+        k_expert_sort<<<1, threads, Shared::bytes(bins, threads / 32, false), s>>>(p);
     } else {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -23,11 +23,22 @@ import struct
 import sys
 
 _pkg = sys.modules[__package__]
+torch = None  # imported by the first call that needs it (importing the package does not)
+
+
+def _torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+        FTYPES.update({getattr(torch, name): code for name, code in FLOAT_TYPES.items()})
+
 
 FLOAT_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 EXPERTS_MAX = 1024  # RS_EXPERTS_MAX
 
+FTYPES = {}  # torch dtype -> rs_float_type
 _MATMUL_TEMP = 2048  # rs_expert_matmul_temp_bytes of every descriptor it accepts
 _SIZE_ERROR = ctypes.c_size_t(-1).value
 
@@ -124,14 +135,8 @@ def rs_expert_matmul_status(temp, stream=None) -> int:
 
 # --------------------------------------------------------------- convenience
 
-_NAMES = {}  # torch dtype -> rs_float_type
-
-
 def _ftype(t, what):
-    if not _NAMES:
-        import torch
-        _NAMES.update({getattr(torch, name): code for name, code in FLOAT_TYPES.items()})
-    code = _NAMES.get(t.dtype)
+    code = FTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{what}: float32, float16 or bfloat16 wanted, got {t.dtype}")
     return code
@@ -166,7 +171,6 @@ def _rows(what, t):
 
 def _plan(position, offsets, device):
     """(tokens, slots, address of the number of rows in use) of a sort's result."""
-    import torch
     for what, t, dims in (("position", position, 2), ("offsets", offsets, 1)):
         if t.dtype != torch.int32:
             raise TypeError(f"{what}: torch.int32 wanted, got {t.dtype}")
@@ -184,7 +188,6 @@ def _plan(position, offsets, device):
 
 
 def _weights(weights, y, shape):
-    import torch
     if weights.dtype != torch.float32 and weights.dtype != y.dtype:
         raise TypeError(f"weights: float32 or {y.dtype} wanted, got {weights.dtype}")
     if weights.shape != shape:
@@ -196,7 +199,6 @@ def _weights(weights, y, shape):
 def _current(device, stream):
     """The current stream's handle in the usual case: no stream is asked for
     and the tensors are on the current device; else None."""
-    import torch
     i = device.index
     if stream is None and i == torch._C._cuda_getDevice():
         return torch._C._cuda_getCurrentRawStream(i)
@@ -208,7 +210,6 @@ def _other(device, stream, inputs):
     """Allocate on, and launch into, `stream` (None: the current one) of
     `device`; the inputs' memory is then not handed out again before `stream`
     has passed."""
-    import torch
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.device(device):
         if s is None:
@@ -236,7 +237,8 @@ def expert_sort(ids, num_experts: int, *, stream=None):
     number lies outside [0, num_experts) is dropped: such slots come last, in
     rows offsets[num_experts] and on.
     """
-    import torch
+    if torch is None:
+        _torch()
     if ids.dtype != torch.int64 and ids.dtype != torch.int32:
         raise TypeError(f"ids: int32 or int64 wanted, got {ids.dtype}")
     if not ids.is_cuda or not ids.is_contiguous():
@@ -250,7 +252,6 @@ def expert_sort(ids, num_experts: int, *, stream=None):
 
 
 def _sort(ids, num_experts, dev, s):
-    import torch
     n, i32, h = ids.numel(), torch.int32, _rs()
     tb = h.rs_expert_sort_temp_bytes(n, num_experts)
     if tb == _SIZE_ERROR:
@@ -267,6 +268,8 @@ def _sort(ids, num_experts, dev, s):
 def expert_dispatch(x, position, offsets, *, stream=None):
     """x [T, H] laid out by expert: [T*K, H], row position[t, k] = x[t];
     the rows of dropped slots are zero."""
+    if torch is None:
+        _torch()
     ft, dev = _ftype(x, "x"), x.device
     rows, width, xs = _rows("x", x)
     t, k, routed = _plan(position, offsets, dev)
@@ -281,7 +284,6 @@ def expert_dispatch(x, position, offsets, *, stream=None):
 
 
 def _dispatch(ft, x, xs, position, routed, t, k, width, s):
-    import torch
     out = torch.empty((t * k, width), dtype=x.dtype, device=x.device)
     _check(_rs().rs_expert_dispatch(ft, x.data_ptr(), xs, position.data_ptr(), routed, t, k, width, out.data_ptr(),
                                     width or 1, s), "rs_expert_dispatch")
@@ -289,6 +291,8 @@ def _dispatch(ft, x, xs, position, routed, t, k, width, s):
 
 
 def _combine(y, weights, position, offsets, stream):
+    if torch is None:
+        _torch()
     ft, dev = _ftype(y, "y"), y.device
     rows, width, ys = _rows("y", y)
     t, k, routed = _plan(position, offsets, dev)
@@ -305,11 +309,10 @@ def _combine(y, weights, position, offsets, stream):
 
 
 def _combine_on(ft, y, ys, weights, position, routed, t, k, width, s):
-    import torch
     w, wt = None, 0
     if weights is not None:
         weights = weights.contiguous()
-        w, wt = weights.data_ptr(), _NAMES[weights.dtype]
+        w, wt = weights.data_ptr(), FTYPES[weights.dtype]
     out = torch.empty((t, width), dtype=y.dtype, device=y.device)
     _check(_rs().rs_expert_combine(ft, y.data_ptr(), ys, w, wt, position.data_ptr(), routed, t, k, width,
                                    out.data_ptr(), width or 1, s), "rs_expert_combine")
@@ -333,6 +336,8 @@ def expert_combine(y, weights, position, offsets, *, stream=None):
 def expert_combine_grad(dout, y, weights, position, offsets, *, stream=None):
     """The gradient of expert_combine for dout [T, H]: (dy [T*K, H] like y,
     dweights [T, K] like weights); zero for dropped slots."""
+    if torch is None:
+        _torch()
     ft, dev = _ftype(y, "y"), y.device
     rows, width, ys = _rows("y", y)
     t, k, routed = _plan(position, offsets, dev)
@@ -350,11 +355,10 @@ def expert_combine_grad(dout, y, weights, position, offsets, *, stream=None):
 
 
 def _combine_grad(ft, dout, ds, y, ys, weights, position, routed, t, k, width, s):
-    import torch
     w = weights.contiguous()
     dy = torch.empty((t * k, width), dtype=y.dtype, device=y.device)
     dweights = torch.empty((t, k), dtype=w.dtype, device=y.device)
-    _check(_rs().rs_expert_combine_grad(ft, dout.data_ptr(), ds, y.data_ptr(), ys, w.data_ptr(), _NAMES[w.dtype],
+    _check(_rs().rs_expert_combine_grad(ft, dout.data_ptr(), ds, y.data_ptr(), ys, w.data_ptr(), FTYPES[w.dtype],
                                         position.data_ptr(), routed, t, k, width, dy.data_ptr(), width or 1,
                                         dweights.data_ptr(), s), "rs_expert_combine_grad")
     return dy, dweights
@@ -363,7 +367,8 @@ def _combine_grad(ft, dout, ds, y, ys, weights, position, routed, t, k, width, s
 def _products(x, w, offsets, activation):
     """The head of the descriptor (up to w's strides) after the checks that
     both products share, and (rows, inner, outer, experts)."""
-    import torch
+    if torch is None:
+        _torch()
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: one of {', '.join(ACTIVATIONS)} wanted, got {activation!r}")
@@ -419,7 +424,6 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
 
 
 def _matmul(head, extra, x, rows, outer, return_pre, temp, s):
-    import torch
     y = torch.empty((rows, outer), dtype=x.dtype, device=x.device)
     pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device) if return_pre else None
     if temp is None:
@@ -454,7 +458,6 @@ def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=T
 
 
 def _matmul_grad(head, grads, x, rows, inner, outer, experts, need_dx, need_dw, bias, temp, s):
-    import torch
     dt, dev, h = x.dtype, x.device, _rs()
     dx = torch.empty((rows, inner), dtype=dt, device=dev) if need_dx else None
     dw = torch.empty((experts, outer, inner), dtype=dt, device=dev) if need_dw else None
