@@ -24,6 +24,16 @@ __device__ __forceinline__ T from_float(float v)
     else return __float2bfloat16_rn(v);
 }
 
+// Programmatic dependent launch, used between the kernels of one call.  A
+// kernel launched as the dependent of the one before it may start while that
+// one still runs, once all its blocks have called start_next_grid() or ended;
+// wait_prior_grid() returns when it has ended and its writes are visible (at
+// once after a plain launch).  Every kernel that may be a dependent calls
+// wait_prior_grid() before it ends, so that the end of a call's last kernel is
+// the end of all.
+__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // N adjacent elements: 16 bytes.
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);
@@ -205,6 +215,37 @@ __device__ __forceinline__ void store_partial(T* row, int i, int width, const Ve
 }
 
 // ---- host side
+
+template <typename... P, typename... A>
+rs_status launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                        bool dependent, const A&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (dependent) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return RS_ERR_CUDA;
+    }
+    return RS_OK;
+}
 
 // A number carried as a type, for generic lambdas.
 template <int N>

@@ -144,9 +144,9 @@ rs_status launch_any_reduce(const AnyArgs<T>& p, cudaStream_t s)
 
 // ------------------------------------------- dz = dy * act'(pre), and dbias
 
-constexpr int kDzRows = 64, kDzThreads = 256, kDzWarps = kDzThreads / 32;
+constexpr int kDzRows = 128, kDzThreads = 256, kDzWarps = kDzThreads / 32;
 
-// One block takes a tile of at most 64 rows of one expert and 32 vectors of
+// One block takes a tile of at most 128 rows of one expert and 32 vectors of
 // columns; each warp every eighth row.  part (if given) receives the tile's
 // column sums, [row tile][cols].
 template <typename T, int ACT, int N>
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ d
 {
     extern __shared__ uint32_t mem[];
     __shared__ float sums[kDzWarps][32 * N];
+    start_next_grid();
     const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
     if (blockIdx.x >= g.tiles()) return;
     const uint32_t e = g.find(blockIdx.x), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -172,12 +173,21 @@ __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ d
             Vec<T, N> z{};
             if constexpr (ACT != RS_ACT_NONE) z = load_vec<T, N>(pre + r * pre_i + c);
             Vec<T, N> o;
+            float g[N], y[N];
+            if constexpr (N > 1) {
+                to_floats<T>(g, d);
+                to_floats<T>(y, z);
+            } else {
+                g[0] = to_float(d.v[0]);
+                y[0] = to_float(z.v[0]);
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float v = to_float(d.v[i]) * activate_grad<ACT, sizeof(T) == 2>(to_float(z.v[i]));
-                sum[i] += v;
-                o.v[i] = from_float<T>(v);
+                g[i] *= activate_grad<ACT, sizeof(T) == 2>(y[i]);
+                sum[i] += g[i];
             }
+            if constexpr (N > 1) o = from_floats<T>(g);
+            else o.v[0] = from_float<T>(g[0]);
             if (dz) store_vec<T, N>(dz + r * dz_i + c, o);
         }
     if (!part) return;
@@ -193,19 +203,27 @@ __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ d
     }
 }
 
-// dbias[e] = the sum of its row tiles' sums, in order.
+// dbias[e] = the sum of its row tiles' sums, in order.  Blocks of 128 threads and
+// 32 registers fit beside a block of the tensor-core kernels, and with
+// wait_first off (k_act_grad is known to have ended) run there unnoticed.
+constexpr int kBiasThreads = 128;
+
 template <typename T>
-__global__ void __launch_bounds__(kDzThreads) k_bias_grad(const float* __restrict__ part, T* __restrict__ dbias,
-                                                          const int32_t* __restrict__ offsets, uint32_t experts,
-                                                          uint32_t rows, uint32_t cols)
+__global__ void __launch_bounds__(kBiasThreads, 16) k_bias_grad(const float* __restrict__ part, T* __restrict__ dbias,
+                                                                const int32_t* __restrict__ offsets, uint32_t experts,
+                                                                uint32_t rows, uint32_t cols, bool wait_first)
 {
     extern __shared__ uint32_t mem[];
+    if (wait_first) wait_prior_grid();
     const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
-    const uint32_t e = blockIdx.x, c = blockIdx.y * kDzThreads + threadIdx.x;
-    if (c >= cols) return;
-    float s = 0.0f;
-    for (uint32_t t = g.tile[e]; t < g.tile[e + 1]; ++t) s += part[(size_t)t * cols + c];
-    dbias[(size_t)e * cols + c] = from_float<T>(s);
+    const uint32_t e = blockIdx.x, c = blockIdx.y * kBiasThreads + threadIdx.x;
+    if (c < cols) {
+        float s = 0.0f;
+#pragma unroll 4
+        for (uint32_t t = g.tile[e]; t < g.tile[e + 1]; ++t) s += part[(size_t)t * cols + c];
+        dbias[(size_t)e * cols + c] = from_float<T>(s);
+    }
+    wait_prior_grid();
 }
 
 // ------------------------------------------------------------- host side
@@ -389,13 +407,9 @@ rs_status gradient(const rs_expert_matmul_desc* d)
         });
         if (st != RS_OK) return st;
     }
-    if (part && cols) {
-        k_bias_grad<T><<<dim3(experts, (unsigned)ceil_div(cols, kDzThreads)), kDzThreads, groups, s>>>(
-            part, static_cast<T*>(d->dbias), d->offsets, experts, rows, cols);
-        if (cudaGetLastError() != cudaSuccess) return RS_ERR_CUDA;
-    }
     // dx and dw share the status words; what takes none of them leaves them clear.
     const bool want_dx = d->dx && rows && d->inner, want_dw = d->dw && d->inner && cols;
+    const bool formed = (dz || part) && cols;  // k_act_grad was launched
     bool tc_dx = false, tc_dw = false;
     if constexpr (sizeof(T) == 2) {
         TcOperand<T> b;
@@ -405,6 +419,7 @@ rs_status gradient(const rs_expert_matmul_desc* d)
             p.reduce = cols;
             p.d = static_cast<T*>(d->dx);
             p.d_i = d->dx_stride;
+            p.dependent = p.wait_first = formed;
             const rs_status st = tc_ragged_rows<T>({g, g_stride, 0, false}, b, p, s);
             if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
             tc_dx = st == RS_OK;
@@ -416,11 +431,21 @@ rs_status gradient(const rs_expert_matmul_desc* d)
             p.d = static_cast<T*>(d->dw);
             p.d_e = d->outer * d->inner;
             p.d_i = d->inner;
+            // beside dx's kernel it need not wait for that one: dz is complete
+            // before any block of it starts
+            p.dependent = formed || tc_dx;
+            p.wait_first = !tc_dx;
             const rs_status st =
                 tc_ragged_reduce<T>({g, g_stride, 0, true}, {static_cast<const T*>(d->x), d->x_stride, 0, true}, p, s);
             if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
             tc_dw = st == RS_OK;
         }
+    }
+    if (part && cols) {
+        const rs_status st = launch_kernel(k_bias_grad<T>, dim3(experts, (unsigned)ceil_div(cols, kBiasThreads)), kBiasThreads,
+                                           groups, s, 1, true, (const float*)part, static_cast<T*>(d->dbias), d->offsets,
+                                           experts, rows, cols, !tc_dx && !tc_dw);
+        if (st != RS_OK) return st;
     }
     if (!tc_dx && (!want_dw || want_dx)) {
         const size_t bytes = want_dx && want_dw ? kStatusBytes / 2 : kStatusBytes;

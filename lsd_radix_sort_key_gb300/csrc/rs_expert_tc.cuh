@@ -56,6 +56,8 @@ struct TcArgs {
     size_t pre_i;
     uint32_t* status;  // one word per block: 0, or 1 if a wait ran out; the rest of the area is cleared
     uint32_t status_words;
+    uint32_t dependent;   // launched as the dependent of the kernel before it
+    uint32_t wait_first;  // and needs what that one writes
     uint32_t stall;    // testing hook: tile stall - 1 is never copied
 };
 
@@ -299,6 +301,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     // (the barrier inside make() orders all of the above)
     const Groups g = Groups::make(slot + 4, p.offsets, p.experts, p.rows, S::kTileRows, !RAGGED_K);
+    if (p.wait_first) wait_prior_grid();
+    start_next_grid();
     if constexpr (PAIR) cluster_sync();  // the other block's barriers are ready too
     tc_fence_after();
     const uint32_t tmem = *slot;
@@ -522,6 +526,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     if constexpr (PAIR) cluster_sync();
     if (warp == 2) tmem_free<PAIR>(tmem, 512);
+    wait_prior_grid();
 }
 
 // Launches one product; RS_ERR_UNSUPPORTED if the operands cannot be copied
