@@ -2,16 +2,21 @@
 
 One translation unit per key type plus the C-ABI unit, compiled in parallel
 with nvcc, then linked into a shared library with the CUDA runtime linked
-statically.  Nothing here runs at import time of the package except the
-check that the library exists.
+statically.  Beside it, csrc/rs_torch.cpp becomes a CPython extension for the
+installed torch (the expert operators' calls without the interpreter's cost;
+skipped where torch has no CUDA).  Nothing here runs at import time of the
+package except the check that the library exists.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -33,6 +38,39 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def torch_dir() -> str | None:
+    """The installed torch's folder if it has CUDA (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    root = spec and spec.submodule_search_locations and list(spec.submodule_search_locations)[0]
+    return root if root and os.path.exists(os.path.join(root, "lib", "libc10_cuda.so")) else None
+
+
+def torch_ext() -> str | None:
+    """Path of the extension for the installed torch (built or not)."""
+    return os.path.join(LIBDIR, f"rs_torch_{importlib.metadata.version('torch')}.so") if torch_dir() else None
+
+
+def build_torch_ext(force: bool = False) -> str | None:
+    out, src = torch_ext(), os.path.join(CSRC, "rs_torch.cpp")
+    if out is None:
+        return None
+    deps = [src, *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(map(os.path.getmtime, deps)):
+        return out
+    os.makedirs(LIBDIR, exist_ok=True)
+    root, tmp = torch_dir(), out + f".{os.getpid()}.tmp"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", os.path.join(root, "include"), "-I",
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", cuda, "-I",
+           sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-L", os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -50,6 +88,7 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False, libdir: st
     out_dir = libdir or LIBDIR
     out_lib = os.path.join(out_dir, "librs.so")
     if not force and libdir is None and not _stale():
+        build_torch_ext()
         return LIB
     os.makedirs(out_dir, exist_ok=True)
     objdir = os.path.join(out_dir, "obj")
@@ -67,8 +106,11 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False, libdir: st
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
+        ext = ex.submit(build_torch_ext, force) if libdir is None else None
         objs = list(ex.map(compile_one, sources()))
+        if ext:
+            ext.result()
     tmp = out_lib + f".{os.getpid()}.tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

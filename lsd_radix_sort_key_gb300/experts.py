@@ -19,6 +19,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 import sys
 
@@ -26,12 +29,29 @@ _pkg = sys.modules[__package__]
 torch = None  # imported by the first call that needs it (importing the package does not)
 
 
+# The calls below in their ordinary form, as a CPython extension (csrc/rs_torch.cpp):
+# each gives its outputs, or None for a call that is out of the ordinary or
+# refused, which then goes the way written here.  None where it is not built
+# for the installed torch.
+_fast = None
+
+
 def _torch():
-    global torch
-    if torch is None:
-        import torch as module
-        torch = module
-        FTYPES.update({getattr(torch, name): code for name, code in FLOAT_TYPES.items()})
+    global torch, _fast
+    if torch is not None:
+        return
+    import torch as module
+    FTYPES.update({getattr(module, name): code for name, code in FLOAT_TYPES.items()})
+    path = _pkg._build.torch_ext()
+    if path and os.path.exists(path):
+        loader = importlib.machinery.ExtensionFileLoader("rs_torch", path)
+        ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("rs_torch", loader))
+        loader.exec_module(ext)
+        names = ("sort_temp_bytes", "sort", "dispatch", "combine", "combine_grad", "matmul_temp_bytes", "matmul",
+                 "matmul_grad_temp_bytes", "matmul_grad")  # the order of Entry there
+        ext.bind(*(ctypes.cast(getattr(_rs(), "rs_expert_" + n), ctypes.c_void_p).value for n in names))
+        _fast = ext
+    torch = module
 
 
 FLOAT_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
@@ -239,6 +259,10 @@ def expert_sort(ids, num_experts: int, *, stream=None):
     """
     if torch is None:
         _torch()
+    if stream is None and _fast is not None:
+        out = _fast.sort(ids, num_experts)
+        if out is not None:
+            return out
     if ids.dtype != torch.int64 and ids.dtype != torch.int32:
         raise TypeError(f"ids: int32 or int64 wanted, got {ids.dtype}")
     if not ids.is_cuda or not ids.is_contiguous():
@@ -270,6 +294,10 @@ def expert_dispatch(x, position, offsets, *, stream=None):
     the rows of dropped slots are zero."""
     if torch is None:
         _torch()
+    if stream is None and _fast is not None:
+        out = _fast.dispatch(x, position, offsets)
+        if out is not None:
+            return out
     ft, dev = _ftype(x, "x"), x.device
     rows, width, xs = _rows("x", x)
     t, k, routed = _plan(position, offsets, dev)
@@ -293,6 +321,10 @@ def _dispatch(ft, x, xs, position, routed, t, k, width, s):
 def _combine(y, weights, position, offsets, stream):
     if torch is None:
         _torch()
+    if stream is None and _fast is not None:
+        out = _fast.combine(y, weights, position, offsets)
+        if out is not None:
+            return out
     ft, dev = _ftype(y, "y"), y.device
     rows, width, ys = _rows("y", y)
     t, k, routed = _plan(position, offsets, dev)
@@ -338,6 +370,10 @@ def expert_combine_grad(dout, y, weights, position, offsets, *, stream=None):
     dweights [T, K] like weights); zero for dropped slots."""
     if torch is None:
         _torch()
+    if stream is None and _fast is not None:
+        out = _fast.combine_grad(dout, y, weights, position, offsets)
+        if out is not None:
+            return out
     ft, dev = _ftype(y, "y"), y.device
     rows, width, ys = _rows("y", y)
     t, k, routed = _plan(position, offsets, dev)
@@ -367,8 +403,6 @@ def _combine_grad(ft, dout, ds, y, ys, weights, position, routed, t, k, width, s
 def _products(x, w, offsets, activation):
     """The head of the descriptor (up to w's strides) after the checks that
     both products share, and (rows, inner, outer, experts)."""
-    if torch is None:
-        _torch()
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation: one of {', '.join(ACTIVATIONS)} wanted, got {activation!r}")
@@ -407,6 +441,12 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
     expert_matmul_grad needs.  temp: scratch of the caller's (uint8, at least
     rs_expert_matmul_temp_bytes), for rs_expert_matmul_status.
     """
+    if torch is None:
+        _torch()
+    if stream is None and temp is None and _fast is not None:
+        out = _fast.matmul(x, w, offsets, bias, ACTIVATIONS.get(activation), residual, return_pre)
+        if out is not None:
+            return out
     head, rows, inner, outer, experts = _products(x, w, offsets, activation)
     extra = [None, 0, None, 0]
     if bias is not None:
@@ -441,6 +481,12 @@ def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=T
     wanted (need_dx, need_dw, bias).  `pre` is what return_pre gave; not
     needed for activation "none".  The residual's gradient is dy.
     """
+    if torch is None:
+        _torch()
+    if stream is None and temp is None and _fast is not None:
+        out = _fast.matmul_grad(dy, x, w, offsets, pre, ACTIVATIONS.get(activation), bias, need_dx, need_dw)
+        if out is not None:
+            return out
     head, rows, inner, outer, experts = _products(x, w, offsets, activation)
     _like("dy", dy, x, (rows, outer))
     grads = [dy.data_ptr(), _rows("dy", dy)[2], 0, 0]

@@ -3,6 +3,7 @@
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
+from lsd_radix_sort_key_gb300 import experts
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +21,15 @@ ACTS = ["none", "relu", "gelu", "silu"]
 def built():
     rs.build()
     rs.lib()
+    experts._torch()
+    assert experts._fast is not None  # the extension is part of the build
+
+
+@pytest.fixture(params=["extension", "python"])
+def way(request, monkeypatch):
+    """Both forms of a call: the extension's, and the one in Python."""
+    if request.param == "python":
+        monkeypatch.setattr(experts, "_fast", None)
 
 
 def make(counts, unused, inner, outer, dtype, seed, bias=True, residual=False):
@@ -80,7 +90,7 @@ def test_forward_and_gradient(dt, inner, outer, case):
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True), (True, True)])
-def test_epilogues(dt, act, bias, residual):
+def test_epilogues(way, dt, act, bias, residual):
     dtype = TYPES[dt]
     a = make([70, 0, 200, 3], 9, 192, 320, dtype, 5, bias, residual)
     check_forward(a, act, dtype)
@@ -102,7 +112,7 @@ def test_larger(dt, counts, inner, outer):
 
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("inner,outer", [(128, 256), (130, 72)])
-def test_layouts(dt, inner, outer):
+def test_layouts(way, dt, inner, outer):
     """Rows with a stride, unaligned bases, weights stored transposed, shared by all experts, or in a wider array."""
     dtype, g = TYPES[dt], gen(31)
     a = make([100, 0, 61, 7], 4, inner, outer, dtype, 9, residual=True)
@@ -180,7 +190,7 @@ def test_wrong_offsets_stay_inside_the_arrays(dt):
 
 
 @pytest.mark.parametrize("dt", TYPES)
-def test_empty(dt):
+def test_empty(way, dt):
     dtype = TYPES[dt]
     a = make([0, 0], 0, 64, 96, dtype, 17)
     assert rs.expert_matmul(a["x"], a["w"], a["offsets"]).shape == (0, 96)
@@ -199,7 +209,7 @@ def test_empty(dt):
     assert dx.shape == (8, 64) and not dx.any() and dw.shape == (2, 0, 64)
 
 
-def test_parts_of_the_gradient():
+def test_parts_of_the_gradient(way):
     a = make([50, 60], 5, 128, 136, torch.bfloat16, 21)
     dy, pre, full = check_grad(a, "silu", torch.bfloat16, 22)
     for want in range(8):
@@ -241,7 +251,7 @@ def test_gradients_against_differences(dt, act):
     assert abs(found - slope) <= allow + 1e-6 * max(1.0, abs(slope))
 
 
-def test_another_stream_and_graph():
+def test_another_stream_and_graph(way):
     a = make([50, 60, 1], 5, 128, 136, torch.bfloat16, 25)
     args = (a["x"], a["w"], a["offsets"])
     dy = torch.randn(116, 136, device=DEV).bfloat16()
@@ -294,3 +304,31 @@ def test_a_wait_that_runs_out_is_reported(rows):
     d.stall_tile = 0  # the next call works
     assert rs.rs_expert_matmul(d) == 0
     assert rs.rs_expert_matmul_status(temp) == 0 and torch.equal(out, y)
+
+
+def test_refusals_are_worded_whatever_the_way(way):
+    a = make([3, 4], 1, 64, 96, torch.bfloat16, 30)
+    x, w, off = a["x"], a["w"], a["offsets"]
+    for kw, error in ((dict(activation="tanh"), ValueError), (dict(bias=a["bias"].float()), TypeError),
+                      (dict(bias=a["bias"][:1]), ValueError), (dict(residual=x), ValueError)):
+        with pytest.raises(error):
+            rs.expert_matmul(x, w, off, **kw)
+    with pytest.raises(ValueError):
+        rs.expert_matmul(x, w, off[:-1])
+    with pytest.raises(TypeError):
+        rs.expert_matmul(x, w, off.long())
+    with pytest.raises(TypeError):
+        rs.expert_matmul_grad(x.new_zeros(8, 96), x, w, off, activation="silu")
+    with pytest.raises(rs.RadixSortError):
+        rs.expert_sort(torch.zeros(3, dtype=torch.int64, device=DEV), 2000)
+    with pytest.raises(ValueError):
+        rs.expert_dispatch(x.t(), torch.zeros(64, 1, dtype=torch.int32, device=DEV), off)
+    with pytest.raises(TypeError):
+        rs.expert_combine(x, None, torch.zeros(8, 1, dtype=torch.int32, device=DEV), off)
+
+
+def test_a_gradient_being_recorded_is_no_obstacle(way):
+    # the calls compute values only; tensors that require a gradient are as good as others
+    a = make([30, 40], 0, 64, 96, torch.bfloat16, 31)
+    want = rs.expert_matmul(a["x"], a["w"], a["offsets"])
+    assert torch.equal(rs.expert_matmul(a["x"].requires_grad_(), torch.nn.Parameter(a["w"]), a["offsets"]), want)

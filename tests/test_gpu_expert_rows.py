@@ -4,6 +4,7 @@ expert_util)."""
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
+from lsd_radix_sort_key_gb300 import experts
 
 pytestmark = pytest.mark.gpu
 
@@ -19,6 +20,15 @@ from expert_util import (ADD, DEV, TYPES, gen, held, make_plan, plain_combine, p
 def built():
     rs.build()
     rs.lib()
+    experts._torch()
+    assert experts._fast is not None  # the extension is part of the build
+
+
+@pytest.fixture(params=["extension", "python"])
+def way(request, monkeypatch):
+    """Both forms of a call: the extension's, and the one in Python."""
+    if request.param == "python":
+        monkeypatch.setattr(experts, "_fast", None)
 
 
 def check_sort(ids, experts):
@@ -39,7 +49,7 @@ def test_sort_sizes(n, experts):
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("tokens,slots,experts", [(1, 1, 1), (1, 8, 128), (64, 8, 1024), (777, 6, 1023), (5003, 4, 512),
                                                   (40_000, 8, 1024)])
-def test_sort_types_and_dropped(dtype, tokens, slots, experts):
+def test_sort_types_and_dropped(way, dtype, tokens, slots, experts):
     g = gen(tokens)
     ids = torch.randint(0, experts, (tokens, slots), device=DEV, generator=g)
     ids[torch.rand(tokens, slots, device=DEV, generator=g) < 0.3] = -1
@@ -63,7 +73,7 @@ def test_sort_one_expert_takes_all_or_nothing_is_kept(n):
     check_sort((n - 1 - torch.arange(n, device=DEV)) * 8 // n, 8)
 
 
-def test_sort_nothing():
+def test_sort_nothing(way):
     order, position, offsets = rs.expert_sort(torch.empty(0, 4, dtype=torch.int64, device=DEV), 6)
     assert order.shape == (0,) and position.shape == (0, 4) and offsets.tolist() == [0] * 7
 
@@ -97,7 +107,7 @@ def test_rows(dt, width, tokens, slots, drop):
 
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("width", [1000, 1001])
-def test_rows_strided_and_offset(dt, width):
+def test_rows_strided_and_offset(way, dt, width):
     # rows inside a wider matrix, at an offset that is not 16-byte aligned, and one row for all
     dtype, g = TYPES[dt], gen(3)
     tokens, slots = 129, 4
@@ -136,7 +146,7 @@ def test_infinities_and_nan_stay_in_their_tokens(width):
     held(rs.expert_combine(y, weights, position, offsets), want, torch.nan_to_num(4 * ADD * mag, 0, 0) + 1e-30)
 
 
-def test_all_slots_dropped_and_no_tokens():
+def test_all_slots_dropped_and_no_tokens(way):
     ids = torch.full((9, 4), -1, device=DEV)
     _, position, offsets = rs.expert_sort(ids, 5)
     x = torch.randn(9, 100, device=DEV)
@@ -192,7 +202,7 @@ def test_gradients_against_differences():
     assert abs(left - right) <= 5 * ADD * float(x.abs().double().sum() * 4 * d.abs().max())
 
 
-def test_another_stream_and_graph():
+def test_another_stream_and_graph(way):
     position, offsets = make_plan(500, 4, 8, 21, 0.1)
     x = torch.randn(500, 264, device=DEV)
     w = torch.rand(500, 4, device=DEV)
