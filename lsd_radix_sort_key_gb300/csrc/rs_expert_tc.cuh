@@ -257,8 +257,9 @@ __device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint3
 
 // Ragged rows: A is K-major rows of map_a (2-d), B is per expert (map_b, 3-d),
 // its row index adjacent in memory (B_MN) or its reduction index.  Ragged
-// reduction: both are MN-major columns of 2-d maps.
-template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR>
+// reduction: both are MN-major columns of 2-d maps.  FEW: A is copied in boxes
+// of 16 rows, as many as the tile has rows for.
+template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR, bool FEW>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_product_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, TcArgs<T> p)
 {
@@ -318,6 +319,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
             if (tile + 1 == p.stall) break;
             const int i0 = (int)(t.i0 + rank * kTcRows), j0 = (int)(t.j0 + rank * S::kCols);
+            // Rows past the expert's end are not stored, so whole boxes of them are
+            // not copied: what the stage held before stands in for them.
+            const uint32_t rows = RAGGED_K ? 0 : t.i_end - t.i0;  // of the tile, and more
+            const uint32_t a_boxes = FEW ? min((rows + 15) / 16, kTcRows / 16u) : 1;
+            const bool second = PAIR && !RAGGED_K && rows > kTcRows;  // the pair's second block has rows
+            const uint32_t tile_bytes = RAGGED_K ? S::kStage
+                                        : PAIR   ? 2 * S::kB + (second ? 2 : 1) * S::kA
+                                        : FEW    ? S::kB + a_boxes * 2048
+                                                 : S::kStage;
             for (uint32_t k = t.k0; k < t.k_end; k += kTcDepth, ++issued) {
                 ok = bar_wait_warp(empty + s, (round & 1) ^ 1);
                 if (!ok) break;
@@ -335,7 +345,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             bar_expect(full + s, S::kStage);
                         }
                     } else if (rank == 0) {
-                        bar_expect(full + s, S::kStage * blocks);
+                        bar_expect(full + s, tile_bytes);
                     }
                     if constexpr (RAGGED_K) {
 #pragma unroll
@@ -346,7 +356,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tma_load_2d<PAIR>(b + i * 8192, &map_b, j0 + i * 64, (int)k, bar);
                     } else {
                         const int e = (int)(t.e * p.b_expert);
-                        tma_load_2d<PAIR>(a, &map_a, (int)k, i0, bar);
+                        if constexpr (FEW) {
+                            for (uint32_t i = 0; i < a_boxes; ++i)
+                                tma_load_2d<PAIR>(a + i * 2048, &map_a, (int)k, i0 + (int)i * 16, bar);
+                        } else if (!PAIR || rank == 0 || second) {
+                            tma_load_2d<PAIR>(a, &map_a, (int)k, i0, bar);
+                        }
                         if constexpr (B_MN) {
 #pragma unroll
                             for (int i = 0; i < S::kCols / 64; ++i)

@@ -17,10 +17,10 @@ inline int sm_count()
     return sms;
 }
 
-template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR>
+template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR, bool FEW = false>
 rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T>& args, size_t tiles, cudaStream_t s)
 {
-    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN, PAIR>;
+    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN, PAIR, FEW>;
     const size_t smem = TcShape<BN, PAIR>::smem(args.experts);
     const int sms = sm_count();
     if (sms < 2) return RS_ERR_CUDA;
@@ -56,7 +56,7 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
     const uint64_t db[3] = {b.mn ? args.cols : args.reduce, b.mn ? args.reduce : args.cols, experts};
     const uint64_t sb[2] = {(uint64_t)b.row_stride * 2,
                             experts > 1 ? (uint64_t)b.expert_stride * 2 : (uint64_t)b.row_stride * 2};
-    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, kTcRows) ||
+    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, few ? 16 : kTcRows) ||
         !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : wide && !pair ? 256 : 128))
         return RS_ERR_UNSUPPORTED;
     const size_t tiles =
@@ -67,6 +67,9 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
     if (wide)
         return b.mn ? tc_launch<T, 256, false, true, false>(ma, mb, args, tiles, stream)
                     : tc_launch<T, 256, false, false, false>(ma, mb, args, tiles, stream);
+    if (few)
+        return b.mn ? tc_launch<T, 128, false, true, false, true>(ma, mb, args, tiles, stream)
+                    : tc_launch<T, 128, false, false, false, true>(ma, mb, args, tiles, stream);
     return b.mn ? tc_launch<T, 128, false, true, false>(ma, mb, args, tiles, stream)
                 : tc_launch<T, 128, false, false, false>(ma, mb, args, tiles, stream);
 }
