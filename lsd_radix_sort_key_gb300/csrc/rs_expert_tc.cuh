@@ -255,17 +255,32 @@ __device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint3
     add_all<T>(z, w);
 }
 
+// Zeros over rows [left, next multiple of 16) of every box of 64 columns in a
+// stage (the steps of 16 after that are not multiplied); a whole warp.
+template <uint32_t STAGE>
+__device__ __forceinline__ void mend_slice(unsigned char* stage, uint32_t left)
+{
+    const uint32_t vecs = ((left + 15) / 16 * 16 - left) * 8;
+    for (uint32_t v = threadIdx.x % 32; v < vecs; v += 32)
+#pragma unroll
+        for (uint32_t i = 0; i < STAGE / 8192; ++i)
+            reinterpret_cast<uint4*>(stage + i * 8192 + left * 128)[v] = make_uint4(0, 0, 0, 0);
+    rstc::fence_async();
+    __syncwarp();
+}
+
 // Ragged rows: A is K-major rows of map_a (2-d), B is per expert (map_b, 3-d),
 // its row index adjacent in memory (B_MN) or its reduction index.  Ragged
-// reduction: both are MN-major columns of 2-d maps.  FEW: A is copied in boxes
-// of 16 rows, as many as the tile has rows for.
-template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR, bool FEW>
+// reduction: both are MN-major columns of 2-d maps.  With 128
+// columns the tiles of ragged rows are often far from full, and A is copied in
+// boxes of 16 rows, as many as the tile has rows for.
+template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_product_tc(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, TcArgs<T> p)
 {
     using namespace rstc;
     using S = TcShape<BN, PAIR>;
-    constexpr bool A_MN = RAGGED_K;
+    constexpr bool A_MN = RAGGED_K, FEW = BN == 128 && !RAGGED_K;
     static_assert(!RAGGED_K || B_MN, "both operands of a ragged reduction are MN-major");
     extern __shared__ unsigned char raw[];
     unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
@@ -430,16 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             phases ^= 1u << s;
-            // rows [left, next multiple of 16) of every box of 64 columns; the
-            // steps of 16 after that are not multiplied
-            const uint32_t vecs = ((left + 15) / 16 * 16 - left) * 8;
-            unsigned char* at = ring + s * S::kStage + left * 128;
-            for (uint32_t v = lane; v < vecs; v += 32)
-#pragma unroll
-                for (uint32_t i = 0; i < S::kStage / 8192; ++i)
-                    reinterpret_cast<uint4*>(at + i * 8192)[v] = make_uint4(0, 0, 0, 0);
-            fence_async();
-            __syncwarp();
+            mend_slice<S::kStage>(ring + s * S::kStage, left);
             if (elect_one()) {
                 if constexpr (PAIR) bar_arrive_cluster<true>(cluster_addr(full + s, 0));
                 else bar_arrive(full + s);

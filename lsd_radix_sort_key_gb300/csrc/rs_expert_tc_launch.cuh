@@ -2,6 +2,9 @@
 // and launches.  Included by one translation unit per element type.
 #pragma once
 
+#include <atomic>
+
+#include "rs_expert_split.cuh"
 #include "rs_expert_tc.cuh"
 
 namespace rsx {
@@ -17,10 +20,10 @@ inline int sm_count()
     return sms;
 }
 
-template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR, bool FEW = false>
+template <typename T, int BN, bool RAGGED_K, bool B_MN, bool PAIR>
 rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T>& args, size_t tiles, cudaStream_t s)
 {
-    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN, PAIR, FEW>;
+    const auto kernel = k_product_tc<T, BN, RAGGED_K, B_MN, PAIR>;
     const size_t smem = TcShape<BN, PAIR>::smem(args.experts);
     const int sms = sm_count();
     if (sms < 2) return RS_ERR_CUDA;
@@ -33,62 +36,167 @@ rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T
                          args);
 }
 
-// Up to this many rows per expert (on average) the weights' bytes bound the
-// product, and 128-column tiles spread them more evenly over the SMs: 128 rows,
-// 64 experts of 2048 x 2048 83.6 us against 86.6 with 256 columns, 64 rows of
-// one expert of 4096 x 4096 21.1 against 29.2, 64 rows each of 128 experts of
-// 1536 x 2048 143.5 against 147.3; at 256 rows each 224 against 203.
-constexpr size_t kFewRows = 64;
+template <typename T, bool RAGGED_K, bool B_MN>
+rs_status split_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T>& args, size_t tiles, int blocks,
+                       int sms, cudaStream_t s)
+{
+    const auto kernel = k_product_split<T, RAGGED_K, B_MN>;
+    const size_t smem = SplitShape::smem(args.experts);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return RS_ERR_CUDA;
+    size_t clusters = (size_t)(sms < kTcMaxBlocks ? sms : kTcMaxBlocks) / blocks;
+    if (tiles < clusters) clusters = tiles;
+    return launch_kernel(kernel, dim3((unsigned)(clusters * blocks)), kTcThreads, smem, s, blocks, args.dependent != 0,
+                         ma, mb, args);
+}
 
-// Pairs of blocks from this many rows per expert on (on average).
-constexpr size_t kPairRows = 512;
+// Which kernel runs a product.  All tile the same work, so the choice is made
+// by a model of the time: a block's slices of 64 times the waves of tiles over
+// the SMs, in us,
+//   narrow  128 x 128 tiles, one block each       0.27 per slice
+//   wide    128 x 256, one block each             0.39 (shared memory bounds it)
+//   pair    256 x 256, two blocks each            0.30, and 3 to start
+//   split   128 x 128, 2, 4 or 8 blocks each, one wave only: 0.27 per slice of
+//           a block, and 2.5 to join.
+// The constants are a fit to timings on GB300 of 200 products (1 to 16 experts, 8
+// to 2048 rows each, inner x outer from 512 x 2048 to 4096 x 4096) by every
+// kernel: the choice was on average 2.5% above the best of them where they were
+// fitted and 4.6% on another box, at worst 1.6 times.
+// Some of them, narrow / wide / pair / split by 2 / 4 / 8, us:
+//   1 expert,      8 rows, 4096 x 1024   18.0  22.1  23.6  13.0  10.0   8.7
+//   1 expert,    128 rows, 4096 x 4096   23.4  23.6  25.3  17.4  13.4
+//   1 expert,    400 rows, 2048 x 2048   14.4  15.4  16.7  13.1  20.4
+//   8 experts,   100 rows, 2048 x 2048   15.0  18.3  18.1
+//   8 experts,   128 rows, 2048 x 2048   24.6  16.4  18.3
+//   4 experts,  2048 rows, 2048 x 2048   73.8  53.4  47.0
+// (A split that needs a second wave is the 20.4: the others then do better.)
+enum class Form { kNarrow, kWide, kPair, kSplit };
+
+struct Choice {
+    Form form;
+    int blocks;  // kSplit
+};
+
+// Clusters of `blocks` of the split kernel that the device holds at once.
+template <typename K>
+size_t resident_clusters(K kernel, int blocks, size_t smem)
+{
+    static std::atomic<int> known[kMaxDevices][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    std::atomic<int>& n = known[dev][blocks == 2 ? 0 : blocks == 4 ? 1 : 2];
+    int v = n.load(std::memory_order_relaxed);
+    if (v == 0) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kTcThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess)
+            return 0;
+        n.store(v, std::memory_order_relaxed);
+    }
+    return (size_t)v;
+}
+
+// narrow, wide, pair: tiles of each form (expected); most: 128 x 128 tiles that
+// there can be; slices: of the reduction; clusters(c): resident clusters of c.
+template <typename F>
+Choice choose(size_t narrow, size_t wide, size_t pair, size_t most, size_t slices, int sms, F clusters)
+{
+    const double n = (double)slices;
+    Choice best{Form::kNarrow, 1};
+    double time = 0.27 * n * (double)ceil_div(narrow, sms);
+    auto offer = [&](Form form, int blocks, double t) {
+        if (t < time) time = t, best = Choice{form, blocks};
+    };
+    if (wide) offer(Form::kWide, 1, 0.39 * n * (double)ceil_div(wide, sms));
+    if (pair) offer(Form::kPair, 2, 0.30 * n * (double)ceil_div(pair, sms / 2) + 3.0);
+    for (int c = 2; c <= 8 && slices >= (size_t)(2 * c) && most * c <= (size_t)sms; c *= 2)
+        if (most <= clusters(c)) offer(Form::kSplit, c, 0.27 * (double)ceil_div(slices, c) + 2.5);
+    return best;
+}
 
 template <typename T>
 rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
 {
     constexpr bool kBf16 = !__is_same(T, __half);
-    const bool few = args.rows <= kFewRows * args.experts;
-    const bool wide = args.cols > 128 && !few, pair = wide && args.rows >= kPairRows * args.experts;
+    const int sms = sm_count();
+    if (sms < 2) return RS_ERR_CUDA;
     const uint64_t experts = b.expert_stride ? args.experts : 1;
     args.b_expert = b.expert_stride ? 1 : 0;
+    // The offsets are on the device: with `owners` experts that can have rows,
+    // half of them are taken to end in a partly filled tile.
+    const size_t owners = args.rows < args.experts ? args.rows : args.experts;
+    auto down = [&](size_t tile_rows) {
+        const size_t t = args.rows / tile_rows + owners / 2;
+        return t > owners ? t : owners;
+    };
+    const size_t by128 = ceil_div(args.cols, 128), by256 = ceil_div(args.cols, 256);
+    const Choice c = choose(down(kTcRows) * by128, args.cols > 128 ? down(kTcRows) * by256 : 0,
+                            args.cols > 128 ? down(2 * kTcRows) * by256 : 0, (owners + args.rows / kTcRows) * by128,
+                            ceil_div(args.reduce, kTcDepth), sms, [&](int n) {
+                                return resident_clusters(k_product_split<T, false, false>, n,
+                                                         SplitShape::smem(RS_EXPERTS_MAX));
+                            });
+    const bool narrow = c.form == Form::kNarrow || c.form == Form::kSplit, pair = c.form == Form::kPair;
     CUtensorMap ma, mb;
     const uint64_t da[2] = {args.reduce, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
     const uint64_t db[3] = {b.mn ? args.cols : args.reduce, b.mn ? args.reduce : args.cols, experts};
     const uint64_t sb[2] = {(uint64_t)b.row_stride * 2,
                             experts > 1 ? (uint64_t)b.expert_stride * 2 : (uint64_t)b.row_stride * 2};
-    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, few ? 16 : kTcRows) ||
-        !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : wide && !pair ? 256 : 128))
+    if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, narrow ? 16 : kTcRows) ||
+        !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : narrow || pair ? 128 : 256))
         return RS_ERR_UNSUPPORTED;
-    const size_t tiles =
-        max_tiles(args.rows, args.experts, pair ? 2 * kTcRows : kTcRows) * ceil_div(args.cols, wide ? 256 : 128);
-    if (pair)
+    const size_t tiles = max_tiles(args.rows, args.experts, pair ? 2 * kTcRows : kTcRows) * (narrow ? by128 : by256);
+    switch (c.form) {
+    case Form::kSplit:
+        return b.mn ? split_launch<T, false, true>(ma, mb, args, tiles, c.blocks, sms, stream)
+                    : split_launch<T, false, false>(ma, mb, args, tiles, c.blocks, sms, stream);
+    case Form::kPair:
         return b.mn ? tc_launch<T, 256, false, true, true>(ma, mb, args, tiles, stream)
                     : tc_launch<T, 256, false, false, true>(ma, mb, args, tiles, stream);
-    if (wide)
+    case Form::kWide:
         return b.mn ? tc_launch<T, 256, false, true, false>(ma, mb, args, tiles, stream)
                     : tc_launch<T, 256, false, false, false>(ma, mb, args, tiles, stream);
-    if (few)
-        return b.mn ? tc_launch<T, 128, false, true, false, true>(ma, mb, args, tiles, stream)
-                    : tc_launch<T, 128, false, false, false, true>(ma, mb, args, tiles, stream);
-    return b.mn ? tc_launch<T, 128, false, true, false>(ma, mb, args, tiles, stream)
-                : tc_launch<T, 128, false, false, false>(ma, mb, args, tiles, stream);
+    default:
+        return b.mn ? tc_launch<T, 128, false, true, false>(ma, mb, args, tiles, stream)
+                    : tc_launch<T, 128, false, false, false>(ma, mb, args, tiles, stream);
+    }
 }
 
 template <typename T>
 rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T> args, cudaStream_t stream)
 {
     constexpr bool kBf16 = !__is_same(T, __half);
-    const bool wide = args.cols > 128, pair = wide && args.out_rows > 128;
+    const int sms = sm_count();
+    if (sms < 2) return RS_ERR_CUDA;
+    const size_t down = ceil_div(args.out_rows, kTcRows) * args.experts, by128 = ceil_div(args.cols, 128);
+    const size_t by256 = ceil_div(args.cols, 256);
+    const size_t down256 = ceil_div(args.out_rows, 2 * kTcRows) * args.experts;
+    const bool wide = args.cols > 128;
+    const Choice c = choose(down * by128, wide ? down * by256 : 0, wide && args.out_rows > 128 ? down256 * by256 : 0,
+                            down * by128, ceil_div(args.rows, args.experts * (size_t)kTcDepth), sms, [&](int n) {
+                                return resident_clusters(k_product_split<T, true, true>, n,
+                                                         SplitShape::smem(RS_EXPERTS_MAX));
+                            });
     CUtensorMap ma, mb;
     const uint64_t da[2] = {args.out_rows, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
     const uint64_t db[2] = {args.cols, args.rows}, sb[1] = {(uint64_t)b.row_stride * 2};
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, 64) || !rstc::encode_map(&mb, kBf16, 2, b.p, db, sb, 64))
         return RS_ERR_UNSUPPORTED;
-    const size_t tiles =
-        ceil_div(args.out_rows, pair ? 2 * kTcRows : kTcRows) * args.experts * ceil_div(args.cols, wide ? 256 : 128);
-    if (pair) return tc_launch<T, 256, true, true, true>(ma, mb, args, tiles, stream);
-    return wide ? tc_launch<T, 256, true, true, false>(ma, mb, args, tiles, stream)
-                : tc_launch<T, 128, true, true, false>(ma, mb, args, tiles, stream);
+    switch (c.form) {
+    case Form::kSplit: return split_launch<T, true, true>(ma, mb, args, down * by128, c.blocks, sms, stream);
+    case Form::kPair: return tc_launch<T, 256, true, true, true>(ma, mb, args, down256 * by256, stream);
+    case Form::kWide: return tc_launch<T, 256, true, true, false>(ma, mb, args, down * by256, stream);
+    default: return tc_launch<T, 128, true, true, false>(ma, mb, args, down * by128, stream);
+    }
 }
 
 }  // namespace rsx

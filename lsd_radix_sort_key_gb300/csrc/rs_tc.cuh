@@ -104,12 +104,19 @@ __device__ __forceinline__ bool bar_wait_cluster_warp(uint64_t* bar, uint32_t pa
 // (tensor cores, bulk copies), from either block of a pair.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// ---- pairs of blocks (clusters of two)
+// ---- clusters of blocks
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 
@@ -121,8 +128,8 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
     return a;
 }
 
-// An arrival on a barrier of either block.  RELEASE: this thread's writes are
-// visible to the other block first, which waits for every store it has in
+// An arrival on a barrier of any block of the cluster.  RELEASE: this thread's
+// writes are visible to that block first, which waits for every store it has in
 // flight; without, the arrival only says that what the thread waited for
 // itself (loads from tensor memory) is done.
 template <bool RELEASE>

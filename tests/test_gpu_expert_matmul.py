@@ -102,7 +102,9 @@ def test_epilogues(way, dt, act, bias, residual):
                                                 ([3, 0, 9, 17, 33, 1, 5, 2], 2048, 1032), ([16] * 300, 64, 72),
                                                 ([1000, 500, 0, 1548], 1000, 1160), ([4096], 1024, 512),
                                                 ([129] * 13, 72, 1024), ([700, 1, 0, 15, 64, 63, 65, 17], 264, 520),
-                                                ([2000, 3], 136, 776)])
+                                                ([2000, 3], 136, 776), ([3000, 70], 128, 256), ([5001], 64, 128),
+                                                ([777, 0, 1500, 64], 256, 136), ([9], 4096, 512), ([40, 2], 2048, 300),
+                                                ([1, 0, 200, 31, 5], 1024, 128), ([6000, 2500], 512, 1032)])
 def test_larger(dt, counts, inner, outer):
     dtype = TYPES[dt]
     a = make(counts, 11, inner, outer, dtype, 7)
@@ -288,16 +290,17 @@ def test_same_call_same_bits():
             assert torch.equal(p, q)
 
 
-@pytest.mark.parametrize("rows", [250, 800])  # single blocks, pairs of blocks
-def test_a_wait_that_runs_out_is_reported(rows):
-    a = make([rows + 50, rows - 50], 0, 256, 512, torch.bfloat16, 27)
+# a reduction cut over a cluster, tiles of one block (128 and 256 columns), pairs of blocks
+@pytest.mark.parametrize("rows,inner,outer", [(70, 1024, 512), (250, 256, 512), (900, 256, 4096), (6000, 1024, 1024)])
+def test_a_wait_that_runs_out_is_reported(rows, inner, outer):
+    a = make([rows + 50, rows - 50], 0, inner, outer, torch.bfloat16, 27)
     temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
     y = rs.expert_matmul(a["x"], a["w"], a["offsets"], temp=temp)
     assert rs.rs_expert_matmul_status(temp) == 0
     out = torch.empty_like(y)
-    d = rs.ExpertMatmulDesc(2, 0, 2, 2 * rows, 256, 512, a["offsets"].data_ptr(), a["x"].data_ptr(), 256, a["w"].data_ptr(),
-                            256 * 512, 256, 1)
-    d.y, d.y_stride, d.temp, d.temp_bytes = out.data_ptr(), 512, temp.data_ptr(), temp.numel()
+    d = rs.ExpertMatmulDesc(2, 0, 2, 2 * rows, inner, outer, a["offsets"].data_ptr(), a["x"].data_ptr(), inner,
+                            a["w"].data_ptr(), inner * outer, inner, 1)
+    d.y, d.y_stride, d.temp, d.temp_bytes = out.data_ptr(), outer, temp.data_ptr(), temp.numel()
     d.stream, d.stall_tile = torch.cuda.current_stream().cuda_stream, 4
     assert rs.rs_expert_matmul(d) == 0
     assert rs.rs_expert_matmul_status(temp) == 5  # RS_ERR_DEVICE_TIMEOUT
