@@ -14,9 +14,11 @@
 // of equal expert, found with one ballot per bit of the expert number
 // (__match_any_sync took 70 cycles a time on an SM: 9 of the 23 us that 2^20
 // slots of 256 experts took).  The whole sort is ONE kernel: up to
-// kOneBlockSlots one block, above that a cooperative launch of at most one
-// block per SM: every block publishes its counts, one warp per expert scans
-// them over the blocks, and every block reads back its own.  (Every block
+// kOneBlockSlots one block; up to kClusterSlots a cluster of 8, whose blocks
+// read each other's counts over the cluster's network; above that a
+// cooperative launch of at most one block per SM: every block publishes its
+// counts, one warp per expert scans them over the blocks, and every block reads
+// back its own.  (Every block
 // summing all counts before its own needs one meeting of the grid less, 1.3 us,
 // but reads blocks * experts words: 6.7 us.)  A block of such a grid puts a
 // tile's slots in expert order in shared memory first, so that `order` is
@@ -33,7 +35,9 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr int kItems = 8;  // slots per thread of a tile
 constexpr uint32_t kTileSlots = kMaxThreads * kItems;
-constexpr uint32_t kOneBlockSlots = kTileSlots;
+constexpr uint32_t kOneBlockSlots = 2048;
+constexpr uint32_t kClusterBlocks = 8;
+constexpr uint32_t kClusterSlots = kClusterBlocks * 4096;  // 30018 slots: 8.7 us, in a grid 9.4; 65536: 11.6, 9.1
 constexpr uint32_t kChunkSlots = 2048;  // least slots per block of a cooperative launch
 constexpr uint32_t kMaxBlocks = 256;
 
@@ -46,6 +50,7 @@ struct SortParams {
     int32_t* order;
     int32_t* position;
     int32_t* offsets;
+    bool cluster;      // the blocks are one cluster
     int bits;          // of an expert number, the one past the dropped slots' included
     uint32_t* counts;  // [blocks][experts + 1], then [experts + 1] totals; unused by a single block
 };
@@ -226,7 +231,30 @@ __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
         __syncthreads();
     }
 
-    if (grid) {
+    if (p.cluster) {
+        auto cluster = cooperative_groups::this_cluster();
+        scan_bins(bins, sh.total, sh.local);
+        cluster.sync();
+        uint32_t *sum = sh.sorted, *first = sh.sorted + bins;  // until the tile is placed
+        for (uint32_t e = tid; e < bins; e += blockDim.x) {
+            uint32_t all = 0, before = 0;
+#pragma unroll
+            for (uint32_t b = 0; b < kClusterBlocks; ++b) {
+                const uint32_t c = b < gridDim.x ? *cluster.map_shared_rank(sh.total + e, b) : 0u;
+                all += c;
+                before += b < blockIdx.x ? c : 0u;
+            }
+            sum[e] = all;
+            sh.base[e] = before;
+        }
+        __syncthreads();
+        scan_bins(bins, sum, first);
+        for (uint32_t e = tid; e < bins; e += blockDim.x) {
+            if (blockIdx.x == 0) p.offsets[e] = (int32_t)first[e];
+            sh.base[e] += first[e];
+        }
+        cluster.sync();  // every block has read the counts of the others
+    } else if (grid) {
         // every block's counts -> the counts of the blocks before it, and the totals
         uint32_t* mine = p.counts + (size_t)blockIdx.x * bins;
         uint32_t* totals = p.counts + (size_t)gridDim.x * bins;
@@ -294,7 +322,7 @@ extern "C" {
 size_t rs_expert_sort_temp_bytes(size_t n, int num_experts)
 {
     if (n > RS_EXPERT_SLOTS_MAX || num_experts < 1 || num_experts > RS_EXPERTS_MAX) return (size_t)-1;
-    if (n <= kOneBlockSlots) return 0;
+    if (n <= kClusterSlots) return 0;
     const size_t blocks = rsx::ceil_div(n, kChunkSlots);
     return rsx::align_up(((blocks < kMaxBlocks ? blocks : kMaxBlocks) + 1) * ((size_t)num_experts + 1) * 4, 256);
 }
@@ -334,6 +362,12 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
         p.chunk = (uint32_t)n;
         const unsigned threads = (unsigned)(n < kMaxThreads ? rsx::align_up(n, 32) : kMaxThreads);
         k_expert_sort<<<1, threads, Shared::bytes(bins, threads / 32, false), s>>>(p);
+    } else if (n <= kClusterSlots) {
+        p.chunk = (uint32_t)rsx::ceil_div(n, kClusterBlocks);
+        p.cluster = true;
+        const int threads = p.chunk < kMaxThreads ? (int)rsx::align_up(p.chunk, 32) : kMaxThreads;
+        return rsx::launch_kernel(k_expert_sort, dim3(kClusterBlocks), threads,
+                                  Shared::bytes(bins, threads / 32, true), s, kClusterBlocks, false, p);
     } else {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||

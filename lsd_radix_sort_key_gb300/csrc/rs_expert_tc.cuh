@@ -467,35 +467,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
             const bool some = t.k0 < t.k_end;
             const uint32_t h = n & 1;
+            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32;
+            if constexpr (RAGGED_K) d.p = p.d + t.e * p.d_e;
+            // a piece with no rows or columns to store is not read either
+            const uint32_t c_end = i0 >= t.i_end || t.j0 + c0 >= p.cols ? c0 : min(c0 + kPer, p.cols - t.j0);
+            // One piece ahead: the next piece's accumulators and residual are on
+            // their way while this one is finished (a load from tensor memory takes
+            // about 1000 cycles beside a busy tensor pipe), the first piece's
+            // residual while the tile is still being multiplied.
+            uint32_t z[2][16], add[2][8];
+            auto fetch_residual = [&](uint32_t c, uint32_t (&r)[8]) {
+                if (p.residual && c < c_end) fetch_piece<T>(r, residual, i0, t.i_end, t.j0 + c, p.cols);
+            };
+            auto fetch_acc = [&](uint32_t c, uint32_t (&zz)[16]) {
+                if (c < c_end) tmem_load16(zz, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter on top
+            };
+            // this warp's part of the accumulator has been read: it may be multiplied into again
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) bar_arrive_cluster<false>(cluster_addr(acc_empty + h, 0));
+                    else bar_arrive(acc_empty + h);
+                }
+            };
             if (some) {
+                fetch_residual(c0, add[0]);
                 if (!bar_wait_warp(acc_full + h, (n >> 1) & 1)) {
                     *failed = 1;
                     break;
                 }
                 tc_fence_after();
                 ++n;
-            }
-            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32;
-            if constexpr (RAGGED_K) d.p = p.d + t.e * p.d_e;
-            // a piece with no rows or columns to store is not read either
-            const uint32_t c_end = i0 >= t.i_end || t.j0 + c0 >= p.cols ? c0 : min(c0 + kPer, p.cols - t.j0);
-            if (some) {
-                // One piece ahead: the next piece's accumulators and residual are
-                // on their way while this one is finished (a load from tensor
-                // memory takes about 1000 cycles beside a busy tensor pipe).
-                uint32_t z[2][16], add[2][8];
-                auto fetch = [&](uint32_t c, uint32_t (&zz)[16], uint32_t (&r)[8]) {
-                    tmem_load16(zz, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter in the high half
-                    if (p.residual) fetch_piece<T>(r, residual, i0, t.i_end, t.j0 + c, p.cols);
-                };
-                if (c0 < c_end) fetch(c0, z[0], add[0]);
+                if (c0 >= c_end) release();
+                fetch_acc(c0, z[0]);
 #pragma unroll
                 for (uint32_t q = 0; q < kPer / 16; ++q) {
                     const uint32_t c = c0 + q * 16, j = t.j0 + c;
                     if (c >= c_end) break;
                     uint32_t(&zz)[16] = z[q & 1];
                     tmem_load_wait(zz);
-                    if (c + 16 < c_end) fetch(c + 16, z[(q & 1) ^ 1], add[(q & 1) ^ 1]);
+                    if (c + 16 >= c_end) release();
+                    fetch_acc(c + 16, z[(q & 1) ^ 1]);
+                    fetch_residual(c + 16, add[(q & 1) ^ 1]);
                     uint32_t out[8];
                     if (p.bias) add_bias<T>(zz, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
                     if (p.pre) {
@@ -517,14 +531,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (uint32_t c = c0; c < c_end; c += 16) {
                     if (p.pre) store_piece<T>(stage, out, pre, i0, t.i_end, t.j0 + c, p.cols);
                     store_piece<T>(stage, out, d, i0, t.i_end, t.j0 + c, p.cols);
-                }
-            }
-            if (some) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) bar_arrive_cluster<false>(cluster_addr(acc_empty + h, 0));
-                    else bar_arrive(acc_empty + h);
                 }
             }
         }

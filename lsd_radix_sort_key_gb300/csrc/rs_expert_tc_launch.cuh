@@ -58,6 +58,9 @@ rs_status split_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArg
 //   pair    256 x 256, two blocks each            0.30, and 3 to start
 //   split   128 x 128, 2, 4 or 8 blocks each, one wave only: 0.27 per slice of
 //           a block, and 2.5 to join.
+// but a slice that brings weights nobody has read yet takes as long as device
+// memory needs for it when every SM asks at once, 0.38 per 128 columns (6.5 TB/s;
+// 128 rows of 64 experts of 2048 x 2048: narrow 77, wide 87).
 // The constants are a fit to timings on GB300 of 200 products (1 to 16 experts, 8
 // to 2048 rows each, inner x outer from 512 x 2048 to 4096 x 4096) by every
 // kernel: the choice was on average 2.5% above the best of them where they were
@@ -106,18 +109,22 @@ size_t resident_clusters(K kernel, int blocks, size_t smem)
 }
 
 // narrow, wide, pair: tiles of each form (expected); most: 128 x 128 tiles that
-// there can be; slices: of the reduction; clusters(c): resident clusters of c.
+// there can be; slices: of the reduction; first, first_pair: the share of
+// tiles that are the first to read their weights; clusters(c): resident
+// clusters of c.
 template <typename F>
-Choice choose(size_t narrow, size_t wide, size_t pair, size_t most, size_t slices, int sms, F clusters)
+Choice choose(size_t narrow, size_t wide, size_t pair, size_t most, size_t slices, double first, double first_pair,
+              int sms, F clusters)
 {
-    const double n = (double)slices;
+    const double n = (double)slices, memory = 0.38;
+    auto larger = [](double a, double b) { return a > b ? a : b; };
     Choice best{Form::kNarrow, 1};
-    double time = 0.27 * n * (double)ceil_div(narrow, sms);
+    double time = larger(0.27, memory * first) * n * (double)ceil_div(narrow, sms);
     auto offer = [&](Form form, int blocks, double t) {
         if (t < time) time = t, best = Choice{form, blocks};
     };
-    if (wide) offer(Form::kWide, 1, 0.39 * n * (double)ceil_div(wide, sms));
-    if (pair) offer(Form::kPair, 2, 0.30 * n * (double)ceil_div(pair, sms / 2) + 3.0);
+    if (wide) offer(Form::kWide, 1, larger(0.39, 2 * memory * first) * n * (double)ceil_div(wide, sms));
+    if (pair) offer(Form::kPair, 2, larger(0.30, memory * first_pair) * n * (double)ceil_div(pair, sms / 2) + 3.0);
     for (int c = 2; c <= 8 && slices >= (size_t)(2 * c) && most * c <= (size_t)sms; c *= 2)
         if (most <= clusters(c)) offer(Form::kSplit, c, 0.27 * (double)ceil_div(slices, c) + 2.5);
     return best;
@@ -141,7 +148,8 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
     const size_t by128 = ceil_div(args.cols, 128), by256 = ceil_div(args.cols, 256);
     const Choice c = choose(down(kTcRows) * by128, args.cols > 128 ? down(kTcRows) * by256 : 0,
                             args.cols > 128 ? down(2 * kTcRows) * by256 : 0, (owners + args.rows / kTcRows) * by128,
-                            ceil_div(args.reduce, kTcDepth), sms, [&](int n) {
+                            ceil_div(args.reduce, kTcDepth), (double)owners / (double)down(kTcRows),
+                            (double)owners / (double)down(2 * kTcRows), sms, [&](int n) {
                                 return resident_clusters(k_product_split<T, false, false>, n,
                                                          SplitShape::smem(RS_EXPERTS_MAX));
                             });
@@ -182,7 +190,7 @@ rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<
     const size_t down256 = ceil_div(args.out_rows, 2 * kTcRows) * args.experts;
     const bool wide = args.cols > 128;
     const Choice c = choose(down * by128, wide ? down * by256 : 0, wide && args.out_rows > 128 ? down256 * by256 : 0,
-                            down * by128, ceil_div(args.rows, args.experts * (size_t)kTcDepth), sms, [&](int n) {
+                            down * by128, ceil_div(args.rows, args.experts * (size_t)kTcDepth), 0.0, 0.0, sms, [&](int n) {
                                 return resident_clusters(k_product_split<T, true, true>, n,
                                                          SplitShape::smem(RS_EXPERTS_MAX));
                             });
