@@ -11,9 +11,11 @@
 // #{s' < s, same expert} = slots of e in earlier chunks + in earlier tiles +
 // in earlier warps of this tile + in earlier slots of this warp; the last two
 // come from one counter per (warp, expert) in shared memory and from the lanes
-// of equal expert, found with one ballot per bit of the expert number
-// (__match_any_sync took 70 cycles a time on an SM: 9 of the 23 us that 2^20
-// slots of 256 experts took).  The whole sort is ONE kernel: up to
+// of equal expert: every lane sets its bit in its expert's mask (one word per
+// (warp, expert), atomicOr) and reads it back.  An SM takes 70 cycles for
+// __match_any_sync, 9 of the 23 us that 2^20 slots of 256 experts took with it,
+// and 4.6 for each of the ballots that would do; ballots are left to the sorts
+// of more than 511 experts, whose masks would not fit.  The whole sort is ONE kernel: up to
 // kOneBlockSlots one block; up to kClusterSlots a cluster of 8, whose blocks
 // read each other's counts over the cluster's network; above that a
 // cooperative launch of at most one block per SM: every block publishes its
@@ -40,6 +42,7 @@ constexpr uint32_t kClusterBlocks = 8;
 constexpr uint32_t kClusterSlots = kClusterBlocks * 4096;  // 30018 slots: 8.7 us, in a grid 9.4; 65536: 11.6, 9.1
 constexpr uint32_t kChunkSlots = 2048;  // least slots per block of a cooperative launch
 constexpr uint32_t kMaxBlocks = 256;
+constexpr size_t kMaskBins = 512;  // masks for so many experts and the dropped slots
 
 struct SortParams {
     const void* ids;
@@ -51,7 +54,6 @@ struct SortParams {
     int32_t* position;
     int32_t* offsets;
     bool cluster;      // the blocks are one cluster
-    int bits;          // of an expert number, the one past the dropped slots' included
     uint32_t* counts;  // [blocks][experts + 1], then [experts + 1] totals; unused by a single block
 };
 
@@ -69,19 +71,21 @@ __device__ __forceinline__ uint32_t load_expert(const SortParams& p, uint32_t s)
 // A block's shared memory: per expert the first row of its next slots (base),
 // the tile's count (total) and the sum of the tile's counts of lower experts
 // (local); per (warp, expert) a counter; and in a grid the tile's slots in
-// expert order.
+// expert order.  masks: and per (warp, expert) a mask of lanes, zero between uses.
 struct Shared {
-    uint32_t *base, *total, *local, *sorted;
+    uint32_t *base, *total, *local, *sorted, *mask;
     uint16_t* counter;
     uint32_t bins;
-    __device__ __forceinline__ Shared(uint32_t* mem, uint32_t bins, bool grid)
+    __device__ __forceinline__ Shared(uint32_t* mem, uint32_t bins, bool grid, bool masks)
         : base(mem), total(mem + bins), local(mem + 2 * bins), sorted(mem + 3 * bins),
-          counter(reinterpret_cast<uint16_t*>(mem + 3 * bins + (grid ? kTileSlots : 0))), bins(bins)
+          mask(mem + 3 * bins + (grid ? kTileSlots : 0)),
+          counter(reinterpret_cast<uint16_t*>(mask + (masks ? bins * (blockDim.x / 32) : 0))), bins(bins)
     {
     }
-    static size_t bytes(size_t bins, size_t warps, bool grid)
+    static size_t bytes(size_t bins, size_t warps, bool grid, bool masks)
     {
-        return 12 * bins + (grid ? 4 * kTileSlots : 0) + 2 * rsx::align_up(bins * warps, 2);
+        return 12 * bins + (grid ? 4 * kTileSlots : 0) + (masks ? 4 * bins * warps : 0) +
+               2 * rsx::align_up(bins * warps, 2);
     }
 };
 
@@ -99,10 +103,14 @@ struct Run {
 
 // Ranks a tile's slots: rank[i] = expert << 16 | slots of that expert before
 // this one in the warp's run; the counters end up as the warps' counts.
+template <bool MASKS>
 __device__ __forceinline__ void rank_tile(const SortParams& p, const Shared& sh, const Run& run,
                                           uint32_t (&rank)[kItems])
 {
-    for (uint32_t i = threadIdx.x; i < sh.bins * (blockDim.x / 32); i += blockDim.x) sh.counter[i] = 0;
+    if constexpr (MASKS)
+        for (uint32_t i = threadIdx.x; i < sh.bins * (blockDim.x / 32); i += blockDim.x) sh.mask[i] = 0;
+    uint32_t* pairs = reinterpret_cast<uint32_t*>(sh.counter);  // (a last odd counter is padded)
+    for (uint32_t i = threadIdx.x; i < (sh.bins * (blockDim.x / 32) + 1) / 2; i += blockDim.x) pairs[i] = 0;
     uint32_t expert[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
@@ -112,19 +120,32 @@ __device__ __forceinline__ void rank_tile(const SortParams& p, const Shared& sh,
     __syncthreads();
     const uint32_t lane = threadIdx.x % 32;
     uint16_t* mine = sh.counter + threadIdx.x / 32 * sh.bins;
+    uint32_t* mask = sh.mask + threadIdx.x / 32 * sh.bins;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const uint32_t e = expert[i];
         if (__all_sync(0xFFFFFFFFu, e == sh.bins)) break;  // the run ended (the ranks of the rest are not used)
+        const bool real = e < sh.bins;
         uint32_t peers = 0xFFFFFFFFu;
-        for (int b = 0; b < p.bits; ++b) {
-            const uint32_t set = __ballot_sync(0xFFFFFFFFu, e >> b & 1);
-            peers &= e >> b & 1 ? set : ~set;
+        if constexpr (MASKS) {
+            if (real) atomicOr(mask + e, 1u << lane);
+            __syncwarp();
+            peers = real ? mask[e] : 0u;
+        } else {
+#pragma unroll
+            for (int b = 0; b < 11; ++b) {  // of the largest number ranked, at most RS_EXPERTS_MAX + 1
+                const bool bit = e & (1u << b);
+                const uint32_t set = __ballot_sync(0xFFFFFFFFu, bit);
+                peers &= bit ? set : ~set;
+            }
         }
         const uint32_t earlier = __popc(peers & ((1u << lane) - 1));
-        const uint32_t before = e < sh.bins ? mine[e] : 0u;
+        const uint32_t before = real ? mine[e] : 0u;
         __syncwarp();
-        if (e < sh.bins && earlier == 0) mine[e] = (uint16_t)(before + __popc(peers));
+        if (real && earlier == 0) {
+            mine[e] = (uint16_t)(before + __popc(peers));
+            if constexpr (MASKS) mask[e] = 0;
+        }
         __syncwarp();
         rank[i] = e << 16 | (before + earlier);
     }
@@ -209,12 +230,13 @@ __device__ __forceinline__ void place_tile(const SortParams& p, const Shared& sh
     }
 }
 
+template <bool MASKS>
 __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
 {
     extern __shared__ uint32_t mem[];
     const uint32_t bins = p.experts + 1, tid = threadIdx.x;
     const bool grid = gridDim.x > 1;
-    const Shared sh(mem, bins, grid);
+    const Shared sh(mem, bins, grid, MASKS);
     const uint32_t begin = blockIdx.x * p.chunk, end = min(p.n, begin + p.chunk);  // begin < n by the grid's size
     uint32_t rank[kItems];
 
@@ -222,7 +244,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
     const bool one_tile = end - begin <= kTileSlots;
     const Run run(begin, min(end - begin, kTileSlots));
     if (one_tile) {
-        rank_tile(p, sh, run, rank);
+        rank_tile<MASKS>(p, sh, run, rank);
         scan_warps(sh);
     } else {
         for (uint32_t e = tid; e < bins; e += blockDim.x) sh.total[e] = 0;
@@ -305,7 +327,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_expert_sort(SortParams p)
     for (uint32_t at = begin; at < end; at += kTileSlots) {
         const uint32_t len = min(end - at, kTileSlots);
         const Run r(at, len);
-        rank_tile(p, sh, r, rank);
+        rank_tile<MASKS>(p, sh, r, rank);
         scan_warps(sh);
         scan_bins(bins, sh.total, sh.local);
         place_tile(p, sh, r, at, len, rank);
@@ -353,21 +375,22 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
     p.position = position;
     p.offsets = offsets;
     p.counts = static_cast<uint32_t*>(temp);
-    p.bits = 32 - __builtin_clz((uint32_t)bins);  // of the largest value ranked, bins
-    const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32, n > kOneBlockSlots);
+    const bool masks = bins <= kMaskBins;
+    const auto kernel = masks ? k_expert_sort<true> : k_expert_sort<false>;
+    const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32, n > kOneBlockSlots, masks);
     if (most_smem > 48 * 1024 - 256 &&
-        cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
         return RS_ERR_CUDA;
     if (n <= kOneBlockSlots) {
         p.chunk = (uint32_t)n;
         const unsigned threads = (unsigned)(n < kMaxThreads ? rsx::align_up(n, 32) : kMaxThreads);
-        k_expert_sort<<<1, threads, Shared::bytes(bins, threads / 32, false), s>>>(p);
+        kernel<<<1, threads, Shared::bytes(bins, threads / 32, false, masks), s>>>(p);
     } else if (n <= kClusterSlots) {
         p.chunk = (uint32_t)rsx::ceil_div(n, kClusterBlocks);
         p.cluster = true;
         const int threads = p.chunk < kMaxThreads ? (int)rsx::align_up(p.chunk, 32) : kMaxThreads;
-        return rsx::launch_kernel(k_expert_sort, dim3(kClusterBlocks), threads,
-                                  Shared::bytes(bins, threads / 32, true), s, kClusterBlocks, false, p);
+        return rsx::launch_kernel(kernel, dim3(kClusterBlocks), threads,
+                                  Shared::bytes(bins, threads / 32, true, masks), s, kClusterBlocks, false, p);
     } else {
         int dev = 0, sms = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -379,7 +402,7 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
         p.chunk = (uint32_t)rsx::ceil_div(n, blocks);
         blocks = rsx::ceil_div(n, p.chunk);
         void* args[] = {&p};
-        if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(k_expert_sort), dim3((unsigned)blocks),
+        if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)blocks),
                                         dim3(kMaxThreads), args, most_smem, s) != cudaSuccess) {
             cudaGetLastError();
             return RS_ERR_CUDA;
