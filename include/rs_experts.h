@@ -35,8 +35,9 @@
  *     way out.  Positions, orders and offsets are int32.
  *   Layout.   A matrix of rows is given with its row stride in ELEMENTS; the
  *     elements of a row are adjacent.  Any stride >= the row's width and any
- *     element-aligned base are accepted; 16-byte-aligned rows take the
- *     vector path.  An input's row stride may also be 0 (one row for all).
+ *     element-aligned base are accepted; 16-byte-aligned rows are the fast
+ *     ones (a product first copies 16-bit operands with other rows into
+ *     temp).  An input's row stride may also be 0 (one row for all).
  *   Dropped slots and unused rows.  A dropped slot adds nothing to a
  *     combined row (its y row is not read, so NaN there does not spread), its
  *     dispatched row, its dy row and its dweights are zero.  Rows of a

@@ -6,8 +6,9 @@
 //   dx       D = dx [rows, inner],  A = dz,   B = w[e]^T,  reduces over outer
 //   dw       D = dw[e] [outer, inner], A = dz^T, B = x^T,  reduces over the expert's rows
 // The first two are ragged in D's rows, the third in the reduction.  16-bit
-// operands whose rows are 16-byte aligned take the tensor cores
-// (rs_expert_tc.cuh); float32 and every other layout the kernel below.
+// operands take the tensor cores (rs_expert_tc.cuh), after a copy with aligned
+// rows into temp where their rows are not 16-byte aligned or are one row for
+// all; float32, and products of nothing, take the multiply-add kernels below.
 #include "rs_expert_groups.cuh"
 #include "rs_expert_tc.cuh"
 
@@ -29,7 +30,7 @@ namespace {
 
 using namespace rsx;
 
-// ------------------------------------------------- products with any strides
+// -------------------------------------------- products by multiply-adds
 
 // Element (i, k) of A in range e is a[e*a_e + i*a_i + k*a_k]; likewise B(j, k).
 template <typename T>
@@ -53,66 +54,108 @@ struct AnyArgs {
     size_t pre_i;
 };
 
-constexpr int kAnyTile = 64, kAnyK = 16, kAnyThreads = 256;
+constexpr int kAnyThreads = 256;
 
-// One 64 x 64 tile of D per block, 4 x 4 per thread, float32 multiply-adds.
-template <typename T, int ACT, bool RAGGED_K>
+// One TILE x TILE tile of D per block, float32 multiply-adds.  With TILE = 128 a
+// thread has 8 x 8 elements in four 4 x 4 squares 64 apart, so that a step of the
+// reduction reads four 16-byte vectors for 64 multiply-adds (32768 x 2048 x 4096
+// float32: 36 TFLOP/s, 23 with tiles of 64); the next slab of the reduction is
+// fetched into registers meanwhile.  TILE = 64 (4 x 4 per thread, rows 16 apart)
+// is for ranges of few rows, where the round trips of the slabs bound it: its
+// slabs are four times as deep, and the rows of 16 that a tile does not have
+// are not computed.
+template <typename T, int ACT, bool RAGGED_K, int TILE>
 __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
 {
+    constexpr int R = TILE / 16;                      // rows and columns of a thread
+    constexpr int kAnyK = TILE == 128 ? 16 : 64;      // depth of a slab
+    constexpr int kPer = TILE * kAnyK / kAnyThreads;  // elements of each operand a thread fetches per slab
+    constexpr int kPitch = TILE + 4;
     extern __shared__ uint32_t mem[];
-    __shared__ float as[kAnyK][kAnyTile + 4], bs[kAnyK][kAnyTile + 4];
-    const Groups g = Groups::make(mem, p.offsets, p.experts, p.rows, kAnyTile, !RAGGED_K);
+    __shared__ __align__(16) float as[kAnyK][kPitch], bs[kAnyK][kPitch];
+    const Groups g = Groups::make(mem, p.offsets, p.experts, p.rows, TILE, !RAGGED_K);
     uint32_t e, i0, i_end, k0, k_end;  // rows of D in [i0, i_end), reduction over [k0, k_end)
     if constexpr (RAGGED_K) {
-        const uint32_t per = (p.out_rows + kAnyTile - 1) / kAnyTile;
+        const uint32_t per = (p.out_rows + TILE - 1) / TILE;
         e = blockIdx.x / per;
-        i0 = (blockIdx.x - e * per) * kAnyTile;
+        i0 = (blockIdx.x - e * per) * TILE;
         i_end = p.out_rows;
         k0 = g.off[e];
         k_end = g.off[e + 1];
     } else {
         if (blockIdx.x >= g.tiles()) return;
         e = g.find(blockIdx.x);
-        i0 = g.off[e] + (blockIdx.x - g.tile[e]) * kAnyTile;
+        i0 = g.off[e] + (blockIdx.x - g.tile[e]) * TILE;
         i_end = g.off[e + 1];
         k0 = 0;
         k_end = e < p.experts ? p.reduce : 0;
     }
-    const uint32_t j0 = blockIdx.y * kAnyTile, tid = threadIdx.x;
+    const uint32_t j0 = blockIdx.y * TILE, tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const T* a = p.a + e * p.a_e;
     const T* b = p.b + (e < p.experts ? e * p.b_e : 0);
-    float acc[4][4] = {};
+    // what this thread fetches: neighbouring threads read neighbouring elements
+    const bool a_rows = p.a_k != 1, b_rows = p.b_k != 1;
+    auto row_of = [&](bool by_rows, int q) { return by_rows ? (tid + q * kAnyThreads) % TILE : (tid + q * kAnyThreads) / kAnyK; };
+    auto k_of = [&](bool by_rows, int q) { return by_rows ? (tid + q * kAnyThreads) / TILE : (tid + q * kAnyThreads) % kAnyK; };
+    float fa[kPer], fb[kPer];
+    auto fetch = [&](uint32_t k) {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const uint32_t ai = i0 + row_of(a_rows, q), ak = k + k_of(a_rows, q);
+            fa[q] = ai < i_end && ak < k_end ? to_float(a[ai * p.a_i + ak * p.a_k]) : 0.0f;
+            const uint32_t bj = j0 + row_of(b_rows, q), bk = k + k_of(b_rows, q);
+            fb[q] = bj < p.cols && bk < k_end ? to_float(b[bj * p.b_j + bk * p.b_k]) : 0.0f;
+        }
+    };
+    // row and column of a thread's element r, c
+    auto row = [&](int r) { return TILE == 128 ? (r / 4) * 64 + (int)ty * 4 + r % 4 : (int)ty + 16 * r; };
+    auto col = [&](int c) { return TILE == 128 ? (c / 4) * 64 + (int)tx * 4 + c % 4 : (int)tx + 16 * c; };
+    const int rows = TILE == 128 ? R : (int)min((i_end - i0 + 15) / 16, (uint32_t)R);
+    float acc[R][R] = {};
+    if (k0 < k_end) fetch(k0);
     for (uint32_t k = k0; k < k_end; k += kAnyK) {
-        for (int l = tid; l < kAnyTile * kAnyK; l += kAnyThreads) {
-            // neighbouring threads read neighbouring elements
-            const uint32_t ai = p.a_k == 1 ? l / kAnyK : l % kAnyTile, ak = p.a_k == 1 ? l % kAnyK : l / kAnyTile;
-            as[ak][ai] = i0 + ai < i_end && k + ak < k_end ? to_float(a[(i0 + ai) * p.a_i + (k + ak) * p.a_k]) : 0.0f;
-            const uint32_t bj = p.b_k == 1 ? l / kAnyK : l % kAnyTile, bk = p.b_k == 1 ? l % kAnyK : l / kAnyTile;
-            bs[bk][bj] = j0 + bj < p.cols && k + bk < k_end ? to_float(b[(j0 + bj) * p.b_j + (k + bk) * p.b_k]) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            as[k_of(a_rows, q)][row_of(a_rows, q)] = fa[q];
+            bs[k_of(b_rows, q)][row_of(b_rows, q)] = fb[q];
         }
         __syncthreads();
+        if (k + kAnyK < k_end) fetch(k + kAnyK);
 #pragma unroll
         for (int kk = 0; kk < kAnyK; ++kk) {
-            float av[4], bv[4];
+            float av[R], bv[R];
+            if constexpr (TILE == 128) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                av[q] = as[kk][tid / 16 + 16 * q];
-                bv[q] = bs[kk][tid % 16 + 16 * q];
+                for (int h = 0; h < 2; ++h) {
+                    const float4 u = *reinterpret_cast<const float4*>(&as[kk][h * 64 + ty * 4]);
+                    const float4 v = *reinterpret_cast<const float4*>(&bs[kk][h * 64 + tx * 4]);
+                    av[4 * h] = u.x, av[4 * h + 1] = u.y, av[4 * h + 2] = u.z, av[4 * h + 3] = u.w;
+                    bv[4 * h] = v.x, bv[4 * h + 1] = v.y, bv[4 * h + 2] = v.z, bv[4 * h + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    av[q] = as[kk][ty + 16 * q];
+                    bv[q] = bs[kk][tx + 16 * q];
+                }
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < R; ++r) {
+                if (r < rows) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
+                    for (int c = 0; c < R; ++c) acc[r][c] = fmaf(av[r], bv[c], acc[r][c]);
+                }
+            }
         }
         __syncthreads();
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint32_t i = i0 + tid / 16 + 16 * r;
+    for (int r = 0; r < R; ++r) {
+        const uint32_t i = i0 + row(r);
         if (i >= i_end) continue;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t j = j0 + tid % 16 + 16 * c;
+        for (int c = 0; c < R; ++c) {
+            const uint32_t j = j0 + col(c);
             if (j >= p.cols) continue;
             float z = acc[r][c], y = 0.0f;
             if (e < p.experts) {
@@ -126,19 +169,88 @@ __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
     }
 }
 
+// From this many rows per expert (on average) on, ragged rows take tiles of 128.
+constexpr size_t kAnyRows = 64;
+
 template <typename T, int ACT>
 rs_status launch_any_rows(const AnyArgs<T>& p, cudaStream_t s)
 {
-    const dim3 grid((unsigned)max_tiles(p.rows, p.experts, kAnyTile), (unsigned)ceil_div(p.cols, kAnyTile));
-    k_product_any<T, ACT, false><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+    auto run = [&](auto kernel, size_t tile) {
+        const dim3 grid((unsigned)max_tiles(p.rows, p.experts, tile), (unsigned)ceil_div(p.cols, tile));
+        kernel<<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    };
+    if constexpr (sizeof(T) == 4)
+        if (p.rows >= kAnyRows * p.experts && p.reduce) return run(k_product_any<T, ACT, false, 128>, 128);
+    return run(k_product_any<T, ACT, false, 64>, 64);
+}
+
+rs_status launch_any_reduce(const AnyArgs<float>& p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)(ceil_div(p.out_rows, 128) * p.experts), (unsigned)ceil_div(p.cols, 128));
+    k_product_any<float, RS_ACT_NONE, true, 128><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
+// ------------------------------------------------- copies with aligned rows
+
+// `matrices` matrices of `rows` rows of `width` elements, at any strides, to
+// rows of `stride` elements (a multiple of 16 bytes, at least width) one after
+// the other; one warp per row.  Elements between width and stride may receive
+// anything.
 template <typename T>
-rs_status launch_any_reduce(const AnyArgs<T>& p, cudaStream_t s)
+__global__ void __launch_bounds__(256) k_align_rows(const T* __restrict__ from, size_t from_matrix, size_t from_row,
+                                                    uint32_t matrices, uint32_t rows, uint32_t width,
+                                                    T* __restrict__ to, size_t stride)
 {
-    const dim3 grid((unsigned)(ceil_div(p.out_rows, kAnyTile) * p.experts), (unsigned)ceil_div(p.cols, kAnyTile));
-    k_product_any<T, RS_ACT_NONE, true><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+    const uint64_t n = (uint64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (n >= (uint64_t)matrices * rows) return;
+    const uint32_t m = (uint32_t)(n / rows), r = (uint32_t)(n - (uint64_t)m * rows);
+    const T* first = from + m * from_matrix;
+    const T* last = first + (rows - 1) * from_row + width;
+    const T* src = first + r * from_row;
+    T* dst = to + n * stride;
+    for (uint32_t v = threadIdx.x % 32; v * kVec<T> < width; v += 32) {
+        Shifted<T> w;
+        w.load(src + v * kVec<T>, first, last);
+        store_vec<T, kVec<T>>(dst + v * kVec<T>, w.get(src, (int)(v * kVec<T>), (int)width));
+    }
+}
+
+// A matrix of 16-bit rows as the tensor-core kernels take it, and where its
+// aligned copy goes if it has to be copied.
+struct Operand {
+    const void* p;
+    size_t row_stride, matrix_stride;
+    size_t matrices, rows, width;
+    bool copy;
+    size_t at, bytes;  // in temp
+
+    size_t copy_stride() const { return align_up(width, 8); }
+};
+
+Operand operand(const void* p, size_t row_stride, size_t matrix_stride, size_t matrices, size_t rows, size_t width)
+{
+    Operand o{p, row_stride, matrix_stride, matrix_stride ? matrices : 1, rows, width, false, 0, 0};
+    if (rows <= 1) o.row_stride = o.copy_stride();  // a single row's stride is not used
+    if (o.matrices <= 1) o.matrix_stride = 0;
+    o.copy = (uintptr_t)p % 16 || o.row_stride * 2 % 16 || o.row_stride < width || o.matrix_stride * 2 % 16;
+    if (o.copy) o.bytes = align_up(o.matrices * rows * o.copy_stride() * 2, 256);
+    return o;
+}
+
+// Makes the copy if there is to be one; p and the strides are then the copy's.
+template <typename T>
+rs_status settle(Operand* o, void* temp, cudaStream_t s)
+{
+    if (!o->copy) return RS_OK;
+    T* to = reinterpret_cast<T*>(static_cast<char*>(temp) + o->at);
+    k_align_rows<T><<<(unsigned)ceil_div(o->matrices * o->rows, 8), 256, 0, s>>>(
+        static_cast<const T*>(o->p), o->matrix_stride, o->row_stride, (uint32_t)o->matrices, (uint32_t)o->rows,
+        (uint32_t)o->width, to, o->copy_stride());
+    o->p = to;
+    o->row_stride = o->copy_stride();
+    o->matrix_stride = o->matrices > 1 ? o->rows * o->copy_stride() : 0;
     return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
@@ -231,25 +343,49 @@ __global__ void __launch_bounds__(kBiasThreads, 16) k_bias_grad(const float* __r
 // temp starts with the status words of the tensor-core kernels.
 constexpr size_t kStatusBytes = kStatusWords * 4;
 
-struct GradLayout {
-    size_t dz;  // byte offsets in temp; dz rows are padded to 16 bytes
-    size_t dz_stride;
-    size_t part;
+Operand rows_operand(const void* p, size_t stride, size_t rows, size_t width)
+{
+    return operand(p, stride, 0, 1, rows, width);
+}
+
+Operand weights_operand(const rs_expert_matmul_desc* d)
+{
+    const bool inner_adjacent = d->w_inner_stride == 1;
+    return operand(d->w, inner_adjacent ? d->w_outer_stride : d->w_inner_stride, d->w_expert_stride, d->num_experts,
+                   inner_adjacent ? d->outer : d->inner, inner_adjacent ? d->inner : d->outer);
+}
+
+// What temp holds after the status words; offsets in bytes.
+struct Layout {
+    size_t dz, dz_stride, part;
+    Operand x, w, g;  // g: dy itself, where it is the products' operand
     size_t total;
 };
 
-GradLayout grad_layout(const rs_expert_matmul_desc* d)
+Layout layout(const rs_expert_matmul_desc* d, bool grad)
 {
     const size_t eb = type_bytes(d->type);
-    GradLayout l{};
+    const bool dx = grad && d->dx && d->rows && d->inner && d->outer;
+    const bool dw = grad && d->dw && d->rows && d->inner && d->outer;
+    Layout l{};
     size_t at = kStatusBytes;
-    if (d->activation != RS_ACT_NONE && (d->dx || d->dw)) {
-        l.dz = at;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, 256);
+        return here;
+    };
+    if (grad && d->activation != RS_ACT_NONE && (d->dx || d->dw)) {
         l.dz_stride = align_up(d->outer, 16 / eb);
-        at += align_up(d->rows * l.dz_stride * eb, 256);
+        l.dz = take(d->rows * l.dz_stride * eb);
     }
-    l.part = at;
-    if (d->dbias) at += align_up(max_tiles(d->rows, d->num_experts, kDzRows) * d->outer * 4, 256);
+    if (grad && d->dbias) l.part = take(max_tiles(d->rows, d->num_experts, kDzRows) * d->outer * 4);
+    if (eb == 2) {
+        if (dw || (!grad && d->rows && d->inner && d->outer)) l.x = rows_operand(d->x, d->x_stride, d->rows, d->inner);
+        if (dx || (!grad && d->rows && d->inner && d->outer)) l.w = weights_operand(d);
+        if ((dx || dw) && d->activation == RS_ACT_NONE) l.g = rows_operand(d->y, d->y_stride, d->rows, d->outer);
+        for (Operand* o : {&l.x, &l.w, &l.g})
+            if (o->copy) o->at = take(o->bytes);
+    }
     l.total = at;
     return l;
 }
@@ -304,18 +440,12 @@ TcArgs<T> tc_args(const rs_expert_matmul_desc* d, size_t first_word, size_t word
     return p;
 }
 
-// The weights as an operand whose rows run over outer (forward) or inner (dx);
-// false if neither of the matrix's sides is adjacent.
+// The weights as B of a product whose columns run over outer (forward) or inner (dx).
 template <typename T>
-bool weight_operand(const rs_expert_matmul_desc* d, bool rows_are_outer, TcOperand<T>* b)
+TcOperand<T> weight_tc(const rs_expert_matmul_desc* d, const Operand& w, bool cols_are_outer)
 {
-    const bool k_adjacent = rows_are_outer ? d->w_inner_stride == 1 : d->w_outer_stride == 1;
-    const bool mn_adjacent = rows_are_outer ? d->w_outer_stride == 1 : d->w_inner_stride == 1;
-    const size_t other = d->w_inner_stride == 1 ? d->w_outer_stride : d->w_inner_stride;
-    const size_t width = d->w_inner_stride == 1 ? d->inner : d->outer;
-    if ((!k_adjacent && !mn_adjacent) || other < width) return false;
-    *b = TcOperand<T>{static_cast<const T*>(d->w), other, d->num_experts > 1 ? d->w_expert_stride : 0, !k_adjacent};
-    return true;
+    const bool inner_adjacent = d->w_inner_stride == 1;
+    return TcOperand<T>{static_cast<const T*>(w.p), w.row_stride, w.matrix_stride, inner_adjacent != cols_are_outer};
 }
 
 template <typename T>
@@ -333,8 +463,11 @@ rs_status forward(const rs_expert_matmul_desc* d)
 {
     cudaStream_t s = static_cast<cudaStream_t>(d->stream);
     if constexpr (sizeof(T) == 2) {
-        TcOperand<T> b;
-        if (d->inner && weight_operand<T>(d, true, &b)) {
+        if (d->inner) {
+            Layout l = layout(d, false);
+            rs_status st = settle<T>(&l.x, d->temp, s);
+            if (st == RS_OK) st = settle<T>(&l.w, d->temp, s);
+            if (st != RS_OK) return st;
             TcArgs<T> p = tc_args<T>(d, 0, kStatusWords);
             p.cols = (uint32_t)d->outer;
             p.reduce = (uint32_t)d->inner;
@@ -347,8 +480,8 @@ rs_status forward(const rs_expert_matmul_desc* d)
             p.residual_i = d->residual_stride;
             p.pre = static_cast<T*>(d->pre);
             p.pre_i = d->pre_stride;
-            const rs_status st = tc_ragged_rows<T>({static_cast<const T*>(d->x), d->x_stride, 0, false}, b, p, s);
-            if (st != RS_ERR_UNSUPPORTED) return st;
+            return tc_ragged_rows<T>({static_cast<const T*>(l.x.p), l.x.row_stride, 0, false},
+                                     weight_tc<T>(d, l.w, true), p, s);
         }
     }
     if (cudaMemsetAsync(d->temp, 0, kStatusBytes, s) != cudaSuccess) return RS_ERR_CUDA;
@@ -381,15 +514,21 @@ rs_status gradient(const rs_expert_matmul_desc* d)
     cudaStream_t s = static_cast<cudaStream_t>(d->stream);
     const size_t eb = sizeof(T), groups = Groups::words(d->num_experts) * 4;
     const uint32_t experts = (uint32_t)d->num_experts, rows = (uint32_t)d->rows, cols = (uint32_t)d->outer;
-    const GradLayout l = grad_layout(d);
+    Layout l = layout(d, true);
     char* temp = static_cast<char*>(d->temp);
     const bool act = d->activation != RS_ACT_NONE;
     const T* dy = static_cast<const T*>(d->y);
     const T* pre = static_cast<const T*>(d->pre);
     T* dz = act && (d->dx || d->dw) ? reinterpret_cast<T*>(temp + l.dz) : nullptr;
-    const T* g = act ? dz : dy;
-    const size_t g_stride = act ? l.dz_stride : d->y_stride;
     float* part = d->dbias ? reinterpret_cast<float*>(temp + l.part) : nullptr;
+    if constexpr (sizeof(T) == 2)
+        for (Operand* o : {&l.x, &l.w, &l.g}) {
+            const rs_status st = settle<T>(o, temp, s);
+            if (st != RS_OK) return st;
+        }
+    // the products' operand: dz, or dy where there is no activation
+    const T* g = act ? dz : sizeof(T) == 2 ? static_cast<const T*>(l.g.p) : dy;
+    const size_t g_stride = act ? l.dz_stride : sizeof(T) == 2 ? l.g.row_stride : d->y_stride;
     if ((dz || part) && cols) {
         constexpr int kVec = 16 / sizeof(T);
         const bool vec = aligned16(dy, d->y_stride, eb) && (!act || aligned16(pre, d->pre_stride, eb)) &&
@@ -412,17 +551,16 @@ rs_status gradient(const rs_expert_matmul_desc* d)
     const bool formed = (dz || part) && cols;  // k_act_grad was launched
     bool tc_dx = false, tc_dw = false;
     if constexpr (sizeof(T) == 2) {
-        TcOperand<T> b;
-        if (want_dx && cols && weight_operand<T>(d, false, &b)) {
+        if (want_dx && cols) {
             TcArgs<T> p = tc_args<T>(d, 0, want_dw ? kStatusWords / 2 : kStatusWords);
             p.cols = (uint32_t)d->inner;
             p.reduce = cols;
             p.d = static_cast<T*>(d->dx);
             p.d_i = d->dx_stride;
             p.dependent = p.wait_first = formed;
-            const rs_status st = tc_ragged_rows<T>({g, g_stride, 0, false}, b, p, s);
-            if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
-            tc_dx = st == RS_OK;
+            const rs_status st = tc_ragged_rows<T>({g, g_stride, 0, false}, weight_tc<T>(d, l.w, false), p, s);
+            if (st != RS_OK) return st;
+            tc_dx = true;
         }
         if (want_dw && rows) {
             TcArgs<T> p = tc_args<T>(d, want_dx ? kStatusWords / 2 : 0, want_dx ? kStatusWords / 2 : kStatusWords);
@@ -435,10 +573,10 @@ rs_status gradient(const rs_expert_matmul_desc* d)
             // before any block of it starts
             p.dependent = formed || tc_dx;
             p.wait_first = !tc_dx;
-            const rs_status st =
-                tc_ragged_reduce<T>({g, g_stride, 0, true}, {static_cast<const T*>(d->x), d->x_stride, 0, true}, p, s);
-            if (st != RS_OK && st != RS_ERR_UNSUPPORTED) return st;
-            tc_dw = st == RS_OK;
+            const rs_status st = tc_ragged_reduce<T>(
+                {g, g_stride, 0, true}, {static_cast<const T*>(l.x.p), l.x.row_stride, 0, true}, p, s);
+            if (st != RS_OK) return st;
+            tc_dw = true;
         }
     }
     if (part && cols) {
@@ -472,20 +610,23 @@ rs_status gradient(const rs_expert_matmul_desc* d)
         if (st != RS_OK) return st;
     }
     if (want_dw && !tc_dw) {
-        AnyArgs<T> p = any_args<T>(d);
-        p.a = g;
-        p.a_i = 1;
-        p.a_k = g_stride;
-        p.b = static_cast<const T*>(d->x);
-        p.b_j = 1;
-        p.b_k = d->x_stride;
-        p.d = static_cast<T*>(d->dw);
-        p.d_e = d->outer * d->inner;
-        p.d_i = d->inner;
-        p.cols = (uint32_t)d->inner;
-        p.out_rows = cols;
-        const rs_status st = launch_any_reduce<T>(p, s);
-        if (st != RS_OK) return st;
+        if (rows == 0)
+            return cudaMemsetAsync(d->dw, 0, d->outer * d->inner * experts * eb, s) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+        if constexpr (sizeof(T) == 4) {
+            AnyArgs<T> p = any_args<T>(d);
+            p.a = g;
+            p.a_i = 1;
+            p.a_k = g_stride;
+            p.b = static_cast<const T*>(d->x);
+            p.b_j = 1;
+            p.b_k = d->x_stride;
+            p.d = static_cast<T*>(d->dw);
+            p.d_e = d->outer * d->inner;
+            p.d_i = d->inner;
+            p.cols = (uint32_t)d->inner;
+            p.out_rows = cols;
+            return launch_any_reduce(p, s);
+        }
     }
     return RS_OK;
 }
@@ -506,7 +647,7 @@ extern "C" {
 
 size_t rs_expert_matmul_temp_bytes(const rs_expert_matmul_desc* d)
 {
-    return check_common(d) == RS_OK ? kStatusBytes : (size_t)-1;
+    return check_common(d) == RS_OK ? layout(d, false).total : (size_t)-1;
 }
 
 rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
@@ -516,8 +657,6 @@ rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
     if (d->rows == 0 || d->outer == 0) return RS_OK;
     const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows;
     if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
-    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
-    if (d->temp_bytes < kStatusBytes) return RS_ERR_TEMP_TOO_SMALL;
     if (!valid_rows(d->y, eb, yw, d->y_stride, false)) return RS_ERR_INVALID_ARG;
     if (d->pre && !valid_rows(d->pre, eb, yw, d->pre_stride, false)) return RS_ERR_INVALID_ARG;
     if (d->bias && !valid_rows(d->bias, eb, yw, d->bias_stride, true)) return RS_ERR_INVALID_ARG;
@@ -526,9 +665,12 @@ rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
         if (!valid_rows(d->x, eb, xw, d->x_stride, true)) return RS_ERR_INVALID_ARG;
         if ((st = check_weights(d)) != RS_OK) return st;
     }
+    const size_t need = layout(d, false).total;
+    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
+    if (d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
     const Range r[] = {{d->y, span_bytes(n, yw, d->y_stride, eb)},
                        {d->pre, d->pre ? span_bytes(n, yw, d->pre_stride, eb) : 0},
-                       {d->temp, kStatusBytes},
+                       {d->temp, need},
                        {d->x, span_bytes(n, xw, d->x_stride, eb)},
                        {d->w, xw ? weight_span(d) * eb : 0},
                        {d->bias, d->bias ? span_bytes(d->num_experts, yw, d->bias_stride, eb) : 0},
@@ -540,7 +682,7 @@ rs_status rs_expert_matmul(const rs_expert_matmul_desc* d)
 
 size_t rs_expert_matmul_grad_temp_bytes(const rs_expert_matmul_desc* d)
 {
-    return check_common(d) == RS_OK ? grad_layout(d).total : (size_t)-1;
+    return check_common(d) == RS_OK ? layout(d, true).total : (size_t)-1;
 }
 
 rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
@@ -548,11 +690,9 @@ rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
     rs_status st = check_common(d);
     if (st != RS_OK) return st;
     if (!d->dx && !d->dw && !d->dbias) return RS_OK;
-    const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows, need = grad_layout(d).total;
+    const size_t eb = type_bytes(d->type), xw = d->inner, yw = d->outer, n = d->rows;
     const bool act = d->activation != RS_ACT_NONE;
     if (!d->offsets || (uintptr_t)d->offsets % 4) return RS_ERR_INVALID_ARG;
-    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
-    if (d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
     if ((uintptr_t)d->dw % eb || (uintptr_t)d->dbias % eb) return RS_ERR_INVALID_ARG;
     if (n && yw) {
         if (!valid_rows(d->y, eb, yw, d->y_stride, true)) return RS_ERR_INVALID_ARG;
@@ -563,6 +703,9 @@ rs_status rs_expert_matmul_grad(const rs_expert_matmul_desc* d)
         if (!valid_rows(d->dx, eb, xw, d->dx_stride, false)) return RS_ERR_INVALID_ARG;
         if (yw && (st = check_weights(d)) != RS_OK) return st;
     }
+    const size_t need = layout(d, true).total;
+    if (!d->temp || (uintptr_t)d->temp % 256) return RS_ERR_INVALID_ARG;
+    if (d->temp_bytes < need) return RS_ERR_TEMP_TOO_SMALL;
     const Range r[] = {{d->dx, d->dx ? span_bytes(n, xw, d->dx_stride, eb) : 0},
                        {d->dw, d->dw ? (size_t)d->num_experts * xw * yw * eb : 0},
                        {d->dbias, d->dbias ? (size_t)d->num_experts * yw * eb : 0},

@@ -146,20 +146,18 @@ __device__ __forceinline__ void store_piece(uint4* stage, const uint32_t (&mine)
     stage[stage_slot(lane, 0)] = make_uint4(mine[0], mine[1], mine[2], mine[3]);
     stage[stage_slot(lane, 1)] = make_uint4(mine[4], mine[5], mine[6], mine[7]);
     __syncwarp();
+    if (d.vec && j0 + 16 <= cols) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const uint32_t row = n * 16 + lane / 2, q = lane % 2, i = i0 + row, j = j0 + q * 8;
-        if (i < i_end && j < cols) {
-            const uint4 v = stage[stage_slot(row, q)];
-            T* to = d.p + i * d.stride + j;
-            if (d.vec && j + 8 <= cols) {
-                *reinterpret_cast<uint4*>(to) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (j + c < cols) reinterpret_cast<uint16_t*>(to)[c] = (uint16_t)(w[c / 2] >> (c & 1) * 16);
-            }
+        for (int n = 0; n < 2; ++n) {
+            const uint32_t row = n * 16 + lane / 2, q = lane % 2, i = i0 + row;
+            if (i < i_end) *reinterpret_cast<uint4*>(d.p + i * d.stride + j0 + q * 8) = stage[stage_slot(row, q)];
+        }
+    } else {  // element by element, 16 lanes to a row
+#pragma unroll 1
+        for (int n = 0; n < 16; ++n) {
+            const uint32_t row = n * 2 + lane / 16, c = lane % 16, i = i0 + row;
+            const uint16_t v = reinterpret_cast<const uint16_t*>(stage)[stage_slot(row, c / 8) * 8 + c % 8];
+            if (i < i_end && j0 + c < cols) reinterpret_cast<uint16_t*>(d.p)[i * d.stride + j0 + c] = v;
         }
     }
     __syncwarp();

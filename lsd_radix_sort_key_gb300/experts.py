@@ -59,7 +59,6 @@ ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 EXPERTS_MAX = 1024  # RS_EXPERTS_MAX
 
 FTYPES = {}  # torch dtype -> rs_float_type
-_MATMUL_TEMP = 2048  # rs_expert_matmul_temp_bytes of every descriptor it accepts
 _SIZE_ERROR = ctypes.c_size_t(-1).value
 
 
@@ -466,11 +465,15 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
 def _matmul(head, extra, x, rows, outer, return_pre, temp, s):
     y = torch.empty((rows, outer), dtype=x.dtype, device=x.device)
     pre = torch.empty((rows, outer), dtype=x.dtype, device=x.device) if return_pre else None
+    h = _rs()
+    body = (*head, *[v or 0 for v in extra], y.data_ptr(), outer or 1, pre.data_ptr() if return_pre else 0, outer or 1,
+            0, 0, 0, 0)
     if temp is None:
-        temp = torch.empty(_MATMUL_TEMP, dtype=torch.uint8, device=x.device)
-    desc = _DESC.pack(*head, *[v or 0 for v in extra], y.data_ptr(), outer or 1, pre.data_ptr() if return_pre else 0,
-                      outer or 1, 0, 0, 0, 0, temp.data_ptr(), temp.numel(), s, 0)
-    _check(_rs().rs_expert_matmul(desc), "rs_expert_matmul")
+        tb = h.rs_expert_matmul_temp_bytes(_DESC.pack(*body, 0, 0, 0, 0))
+        if tb == _SIZE_ERROR:
+            _check(1, "rs_expert_matmul")
+        temp = torch.empty(tb, dtype=torch.uint8, device=x.device)
+    _check(h.rs_expert_matmul(_DESC.pack(*body, temp.data_ptr(), temp.numel(), s, 0)), "rs_expert_matmul")
     return (y, pre) if return_pre else y
 
 

@@ -40,7 +40,6 @@ def test_the_packed_descriptor_is_the_structure():
     assert experts._DESC.size == ctypes.sizeof(rs.ExpertMatmulDesc)
     values = [3 + i for i in range(len(rs.ExpertMatmulDesc._fields_))]
     assert experts._DESC.pack(*values) == bytes(rs.ExpertMatmulDesc(*values))
-    assert experts._MATMUL_TEMP == rs.rs_expert_matmul_temp_bytes(desc())
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -149,6 +148,13 @@ def test_matmul_temp_bytes():
     assert rs.rs_expert_matmul_grad_temp_bytes(desc(activation=0)) < both
     assert rs.rs_expert_matmul_grad_temp_bytes(desc(activation=0, dbias=None)) == rs.rs_expert_matmul_temp_bytes(desc())
     assert rs.rs_expert_matmul_status(None, 0) == 1
+    # rows that are not 16-byte aligned are copied into temp
+    plain = rs.rs_expert_matmul_temp_bytes(desc())
+    assert rs.rs_expert_matmul_temp_bytes(desc(x=2 * F + 2)) >= plain + 100 * 64 * 2
+    assert rs.rs_expert_matmul_temp_bytes(desc(w=3 * F + 2)) >= plain + 4 * 128 * 64 * 2
+    assert rs.rs_expert_matmul_temp_bytes(desc(x_stride=0)) >= plain + 100 * 64 * 2
+    assert rs.rs_expert_matmul_temp_bytes(desc(type=0, x=2 * F + 4)) == plain
+    assert rs.rs_expert_matmul_grad_temp_bytes(desc(x=2 * F + 2)) >= both + 100 * 64 * 2
 
 
 def test_the_binding_checks_its_tensors():
