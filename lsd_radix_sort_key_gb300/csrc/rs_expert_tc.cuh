@@ -253,6 +253,14 @@ __device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint3
     add_all<T>(z, w);
 }
 
+// A pair's tile of at most 128 rows is multiplied as one of 128 rows, 64 to a
+// block, in half the time (an expert's last tile, every second time).
+template <bool PAIR, bool RAGGED_K>
+__device__ __forceinline__ bool half_tile(const TcTile& t)
+{
+    return PAIR && !RAGGED_K && t.i_end - t.i0 <= kTcRows;
+}
+
 // Zeros over rows [left, next multiple of 16) of every box of 64 columns in a
 // stage (the steps of 16 after that are not multiplied); a whole warp.
 template <uint32_t STAGE>
@@ -331,12 +339,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
             if (tile + 1 == p.stall) break;
-            const int i0 = (int)(t.i0 + rank * kTcRows), j0 = (int)(t.j0 + rank * S::kCols);
+            const bool half = half_tile<PAIR, RAGGED_K>(t);
+            const uint32_t own = half ? kTcRows / 2 : kTcRows;  // rows of a block
+            const int i0 = (int)(t.i0 + rank * own), j0 = (int)(t.j0 + rank * S::kCols);
             // Rows past the expert's end are not stored, so whole boxes of them are
             // not copied: what the stage held before stands in for them.
             const uint32_t rows = RAGGED_K ? 0 : t.i_end - t.i0;  // of the tile, and more
             const uint32_t a_boxes = FEW ? min((rows + 15) / 16, kTcRows / 16u) : 1;
-            const bool second = PAIR && !RAGGED_K && rows > kTcRows;  // the pair's second block has rows
+            const bool second = PAIR && !RAGGED_K && rows > own;  // the pair's second block has rows
             const uint32_t tile_bytes = RAGGED_K ? S::kStage
                                         : PAIR   ? 2 * S::kB + (second ? 2 : 1) * S::kA
                                         : FEW    ? S::kB + a_boxes * 2048
@@ -390,7 +400,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!ok) *failed = 1;
     } else if (warp == 1 && rank == 0) {
-        constexpr uint32_t kDesc = mma_desc(!__is_same(T, __half), A_MN, B_MN, S::kTileRows, BN);
+        constexpr uint32_t kWhole = mma_desc(!__is_same(T, __half), A_MN, B_MN, S::kTileRows, BN);
+        constexpr uint32_t kHalf = mma_desc(!__is_same(T, __half), A_MN, B_MN, S::kTileRows / 2, BN);
         constexpr uint32_t kAStep = A_MN ? 2048 : 32, kBStep = B_MN ? 2048 : 32;
         const uint64_t desc_a = smem_desc(smem_addr(ring), A_MN ? 8192 : 16);
         const uint64_t desc_b = smem_desc(smem_addr(ring) + S::kA, B_MN ? 8192 : 16);
@@ -404,6 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!ok) break;
             tc_fence_after();
             ++n;
+            const uint32_t desc = half_tile<PAIR, RAGGED_K>(t) ? kHalf : kWhole;
             uint32_t more = 0;  // nothing accumulated yet
             for (uint32_t k = t.k0; k < t.k_end; k += kTcDepth) {
                 ok = PAIR && RAGGED_K ? bar_wait_cluster_warp(full + s, round & 1) : bar_wait_warp(full + s, round & 1);
@@ -415,10 +427,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (steps == kTcDepth / 16) {
 #pragma unroll
                         for (uint32_t i = 0; i < kTcDepth / 16; ++i)
-                            mma_f16<PAIR>(acc, da + i * (kAStep >> 4), db + i * (kBStep >> 4), kDesc, more | i);
+                            mma_f16<PAIR>(acc, da + i * (kAStep >> 4), db + i * (kBStep >> 4), desc, more | i);
                     } else {
                         for (uint32_t i = 0; i < steps; ++i)
-                            mma_f16<PAIR>(acc, da + i * (kAStep >> 4), db + i * (kBStep >> 4), kDesc, more | i);
+                            mma_f16<PAIR>(acc, da + i * (kAStep >> 4), db + i * (kBStep >> 4), desc, more | i);
                     }
                     mma_commit<PAIR>(empty + s);
                 }
@@ -454,7 +466,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         constexpr uint32_t kPer = BN / (kTcEpilogueWarps / 4);  // columns per warp
         const uint32_t w = warp - kTcFirstEpilogueWarp;
         const uint32_t quarter = warp % 4;  // the 32 tensor-memory lanes this warp can read
-        const uint32_t c0 = w / 4 * kPer;   // and its share of the columns
         uint4* stage = reinterpret_cast<uint4*>(staging + w * S::kStaging);
         Rows<T> d(p.d, p.d_i, RAGGED_K ? p.d_e : 0);
         const Rows<T> pre(p.pre, p.pre_i, 0);
@@ -465,17 +476,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
             const bool some = t.k0 < t.k_end;
             const uint32_t h = n & 1;
-            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32;
+            // A half tile's rows are 64 to a block: tensor memory holds columns 0..127
+            // of D in lanes 0..63 and columns 128..255 in lanes 64..127.
+            const bool half = half_tile<PAIR, RAGGED_K>(t);
+            const uint32_t per = half ? kPer / 2 : kPer, c0 = w / 4 * per;  // this warp's columns in tensor memory
+            const uint32_t i0 = t.i0 + rank * (half ? 64 : kTcRows) + (half ? quarter % 2 : quarter) * 32;
+            const uint32_t j_first = t.j0 + (half ? quarter / 2 * (BN / 2) : 0);  // D's column of column 0 there
             if constexpr (RAGGED_K) d.p = p.d + t.e * p.d_e;
             // a piece with no rows or columns to store is not read either
-            const uint32_t c_end = i0 >= t.i_end || t.j0 + c0 >= p.cols ? c0 : min(c0 + kPer, p.cols - t.j0);
+            const uint32_t c_end = i0 >= t.i_end || j_first + c0 >= p.cols ? c0 : min(c0 + per, p.cols - j_first);
             // One piece ahead: the next piece's accumulators and residual are on
             // their way while this one is finished (a load from tensor memory takes
             // about 1000 cycles beside a busy tensor pipe), the first piece's
             // residual while the tile is still being multiplied.
             uint32_t z[2][16], add[2][8];
             auto fetch_residual = [&](uint32_t c, uint32_t (&r)[8]) {
-                if (p.residual && c < c_end) fetch_piece<T>(r, residual, i0, t.i_end, t.j0 + c, p.cols);
+                if (p.residual && c < c_end) fetch_piece<T>(r, residual, i0, t.i_end, j_first + c, p.cols);
             };
             auto fetch_acc = [&](uint32_t c, uint32_t (&zz)[16]) {
                 if (c < c_end) tmem_load16(zz, tmem + h * 256 + c + (quarter << 21));  // lane 32 * quarter on top
@@ -501,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 fetch_acc(c0, z[0]);
 #pragma unroll
                 for (uint32_t q = 0; q < kPer / 16; ++q) {
-                    const uint32_t c = c0 + q * 16, j = t.j0 + c;
+                    const uint32_t c = c0 + q * 16, j = j_first + c;
                     if (c >= c_end) break;
                     uint32_t(&zz)[16] = z[q & 1];
                     tmem_load_wait(zz);
@@ -527,8 +543,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else {  // unused rows, or an expert without rows
                 const uint32_t out[8] = {};
                 for (uint32_t c = c0; c < c_end; c += 16) {
-                    if (p.pre) store_piece<T>(stage, out, pre, i0, t.i_end, t.j0 + c, p.cols);
-                    store_piece<T>(stage, out, d, i0, t.i_end, t.j0 + c, p.cols);
+                    if (p.pre) store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c, p.cols);
+                    store_piece<T>(stage, out, d, i0, t.i_end, j_first + c, p.cols);
                 }
             }
         }

@@ -104,7 +104,8 @@ def test_epilogues(way, dt, act, bias, residual):
                                                 ([129] * 13, 72, 1024), ([700, 1, 0, 15, 64, 63, 65, 17], 264, 520),
                                                 ([2000, 3], 136, 776), ([3000, 70], 128, 256), ([5001], 64, 128),
                                                 ([777, 0, 1500, 64], 256, 136), ([9], 4096, 512), ([40, 2], 2048, 300),
-                                                ([1, 0, 200, 31, 5], 1024, 128), ([6000, 2500], 512, 1032)])
+                                                ([1, 0, 200, 31, 5], 1024, 128), ([6000, 2500], 512, 1032),
+                                                ([1100, 129, 700, 640, 64, 900], 2048, 2056)])
 def test_larger(dt, counts, inner, outer):
     dtype = TYPES[dt]
     a = make(counts, 11, inner, outer, dtype, 7)

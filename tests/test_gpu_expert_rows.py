@@ -245,3 +245,27 @@ def test_positions_past_32_bit_offsets():
     w = torch.zeros(tokens, slots, device=DEV)
     w[:, -1] = 1.0
     assert torch.equal(rs.expert_combine(out, w, position, offsets), x)
+
+
+@pytest.mark.parametrize("n", [1000, 20_000, 32_768, 32_769, 200_000])
+def test_sort_in_a_graph_and_beside_other_work(n):
+    # one block, a cluster, a grid: captured, replayed on new numbers, and on two streams at once
+    ids = torch.randint(-1, 60, (n,), device=DEV, generator=gen(n))
+    rs.expert_sort(ids, 60)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = rs.expert_sort(ids, 60)
+    for seed in (1, 2):
+        ids.copy_(torch.randint(-1, 61, (n,), device=DEV, generator=gen(n + seed)))
+        graph.replay()
+        for g, w in zip(got, plain_order(ids, 60)):
+            assert torch.equal(g.cpu(), w)
+    other = torch.randint(0, 60, (n,), device=DEV, generator=gen(n + 3))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [(rs.expert_sort(ids, 60), rs.expert_sort(other, 60, stream=side)) for _ in range(20)]
+    torch.cuda.synchronize()
+    want = plain_order(ids, 60), plain_order(other, 60)
+    for pair in outs:
+        for got, w in zip(pair, want):
+            assert all(torch.equal(g.cpu(), v) for g, v in zip(got, w))
