@@ -38,28 +38,36 @@ __device__ __forceinline__ uint32_t row_vecs(uint32_t width)
     return (width + N - 1) / N + (SHIFT ? 1 : 0);  // a lead adds at most one
 }
 
-// A warp's slots of one token, up to 32: a slot per lane, handed around by
-// shuffles.
-template <typename W>
+// GL lanes take one token (32, or 16 or 8 where a row has no more vectors, so
+// that a warp takes 2 or 4 tokens); its slots are loaded GL at a time, one per
+// lane, and handed around by shuffles, in which the whole warp takes part.
+template <typename W, int GL>
 struct Slots {
     uint32_t row = 0xFFFFFFFFu;
     float weight = 1.0f;
     __device__ __forceinline__ void load(const int32_t* position, const W* weights, size_t first, uint32_t count)
     {
-        const uint32_t lane = threadIdx.x % 32;
+        const uint32_t lane = threadIdx.x % GL;
+        row = 0xFFFFFFFFu;
         if (lane < count) {
             row = (uint32_t)__ldg(position + first + lane);
             if (weights) weight = to_float(weights[first + lane]);
         }
     }
-    __device__ __forceinline__ uint32_t row_of(uint32_t k) const { return __shfl_sync(0xFFFFFFFFu, row, k & 31); }
-    __device__ __forceinline__ float weight_of(uint32_t k) const { return __shfl_sync(0xFFFFFFFFu, weight, k & 31); }
+    __device__ __forceinline__ uint32_t row_of(uint32_t k) const
+    {
+        return __shfl_sync(0xFFFFFFFFu, row, k & (GL - 1), GL);
+    }
+    __device__ __forceinline__ float weight_of(uint32_t k) const
+    {
+        return __shfl_sync(0xFFFFFFFFu, weight, k & (GL - 1), GL);
+    }
 };
 
 // One warp moves one piece of a token's row to its K places.  Written bytes
 // bound it: 16384 x 8 rows of 4 KB move at 6.5 TB/s with V = 2, 5.4 when each
 // slot's position was loaded on its own.
-template <typename T, bool SHIFT>
+template <typename T, bool SHIFT, int GL, int V>
 __global__ void __launch_bounds__(kThreads) k_dispatch(const T* __restrict__ x, size_t x_stride,
                                                        const int32_t* __restrict__ position,
                                                        const int32_t* __restrict__ routed, uint32_t slots_total,
@@ -68,43 +76,45 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const T* __restrict__ x, 
                                                        const T* __restrict__ x_end, T* __restrict__ out,
                                                        size_t out_stride)
 {
-    constexpr int N = kVec<T>, V = 2;
-    const uint32_t item = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t t = item / pieces;
-    if (t >= tokens) return;
-    const uint32_t v0 = (item - t * pieces) * (32 * V) + lane, vecs = row_vecs<T, SHIFT>(width);
+    constexpr int N = kVec<T>;
+    const uint32_t item = blockIdx.x * (kThreads / GL) + threadIdx.x / GL, lane = threadIdx.x % GL;
+    uint32_t t = item / pieces;
+    const bool live = t < tokens;
+    if (GL == 32 && !live) return;
+    const uint32_t v0 = (item - t * pieces) * (GL * V) + lane, vecs = live ? row_vecs<T, SHIFT>(width) : 0;
+    if (!live) t = 0;  // beside live tokens, for the shuffles
     const uint32_t limit = routed_rows(routed, slots_total);
     const T* row = x + t * x_stride;
     Vec<T, N> r[V];
     if constexpr (!SHIFT) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (v0 + i * 32 < vecs) r[i] = load_vec<T, N>(row + (size_t)(v0 + i * 32) * N);
+            if (v0 + i * GL < vecs) r[i] = load_vec<T, N>(row + (size_t)(v0 + i * GL) * N);
     }
-    for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
-        const uint32_t here = min(slots - k0, 32u);
-        Slots<float> sl;
+    for (uint32_t k0 = 0; k0 < slots; k0 += GL) {
+        const uint32_t here = min(slots - k0, (uint32_t)GL);
+        Slots<float, GL> sl;
         sl.load(position, nullptr, (size_t)t * slots + k0, here);
         for (uint32_t k = 0; k < here; ++k) {
             const uint32_t p = sl.row_of(k);
-            if (p >= slots_total) continue;
+            if (!live || p >= slots_total) continue;
             T* to = out + p * out_stride;
             const bool kept = p < limit;
             if constexpr (SHIFT) {
                 const int skip = lead(to);
                 Shifted<T> w[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) w[i].load(row + ((int)((v0 + i * 32) * N) - skip), x_begin, x_end);
+                for (int i = 0; i < V; ++i) w[i].load(row + ((int)((v0 + i * GL) * N) - skip), x_begin, x_end);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int at = (int)((v0 + i * 32) * N) - skip;
+                    const int at = (int)((v0 + i * GL) * N) - skip;
                     if (at < (int)width)
                         store_partial<T>(to, at, (int)width, keep_if(kept, w[i].get(row, at, (int)width)));
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (v0 + i * 32 < vecs) store_vec<T, N>(to + (size_t)(v0 + i * 32) * N, keep_if(kept, r[i]));
+                    if (v0 + i * GL < vecs) store_vec<T, N>(to + (size_t)(v0 + i * GL) * N, keep_if(kept, r[i]));
             }
         }
     }
@@ -117,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) k_dispatch(const T* __restrict__ x, 
 // 4x1 5.2, 4x2 6.6, 2x2 6.5, 2x8 5.7; 65536 x 1 rows of 8 KB: 2x2 4.8 with
 // span 1, 6.1 with span 4, 1x4 6.6 with span 4; 8192 x 2 of 16 KB: 2x2 5.6,
 // 6.2, 6.4 with span 1, 2, 4.
-template <typename T, typename W, bool SHIFT, int G, int V>
+template <typename T, typename W, bool SHIFT, int G, int V, int GL>
 __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, size_t y_stride,
                                                       const W* __restrict__ weights,
                                                       const int32_t* __restrict__ position,
@@ -127,20 +137,23 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
                                                       size_t out_stride)
 {
     constexpr int N = kVec<T>;
-    const uint32_t item = blockIdx.x * kWarps + threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t t = item / parts;
-    if (t >= tokens) return;
-    const uint32_t limit = routed_rows(routed, slots_total), vecs = row_vecs<T, SHIFT>(width);
+    const uint32_t item = blockIdx.x * (kThreads / GL) + threadIdx.x / GL, lane = threadIdx.x % GL;
+    uint32_t t = item / parts;
+    const bool live = t < tokens;
+    if (GL == 32 && !live) return;
+    const uint32_t part = item - t * parts;
+    if (!live) t = 0;  // beside live tokens, for the shuffles
+    const uint32_t limit = live ? routed_rows(routed, slots_total) : 0, vecs = row_vecs<T, SHIFT>(width);
     T* to = out + t * out_stride;
     const int skip = SHIFT ? lead(to) : 0;
-    const uint32_t first = (item - t * parts) * span * (32 * V), last = min(vecs, first + span * (32 * V));
-    Slots<W> sl;
-    sl.load(position, weights, (size_t)t * slots, min(slots, 32u));
-    for (uint32_t v0 = first; v0 < last; v0 += 32 * V) {
+    const uint32_t first = part * span * (GL * V), last = min(vecs, first + span * (GL * V));
+    Slots<W, GL> sl;
+    sl.load(position, weights, (size_t)t * slots, min(slots, (uint32_t)GL));
+    for (uint32_t v0 = first; v0 < last; v0 += GL * V) {
         float acc[V][N] = {};
-        for (uint32_t k0 = 0; k0 < slots; k0 += 32) {
-            const uint32_t here = min(slots - k0, 32u);
-            if (slots > 32) sl.load(position, weights, (size_t)t * slots + k0, here);
+        for (uint32_t k0 = 0; k0 < slots; k0 += GL) {
+            const uint32_t here = min(slots - k0, (uint32_t)GL);
+            if (slots > GL) sl.load(position, weights, (size_t)t * slots + k0, here);
             for (uint32_t k = 0; k < here; k += G) {
                 using Loaded = std::conditional_t<SHIFT, Shifted<T>, Vec<T, N>>;
                 Loaded r[G][V];
@@ -154,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
                     const T* from = y + p[j] * y_stride;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const uint32_t v = v0 + i * 32 + lane;
+                        const uint32_t v = v0 + i * GL + lane;
                         if constexpr (SHIFT) r[j][i].load(from + ((int)(v * N) - skip), y, y_end);
                         else if (v < vecs) r[j][i] = load_vec<T, N>(from + (size_t)v * N);
                     }
@@ -167,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
                     for (int i = 0; i < V; ++i) {
                         float f[N];
                         if constexpr (SHIFT)
-                            to_floats<T>(f, r[j][i].get(y + p[j] * y_stride, (int)((v0 + i * 32 + lane) * N) - skip,
+                            to_floats<T>(f, r[j][i].get(y + p[j] * y_stride, (int)((v0 + i * GL + lane) * N) - skip,
                                                         (int)width));
                         else to_floats<T>(f, r[j][i]);
 #pragma unroll
@@ -178,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t v = v0 + i * 32 + lane;
-            if (v >= vecs) continue;
+            const uint32_t v = v0 + i * GL + lane;
+            if (!live || v >= vecs) continue;
             const Vec<T, N> o = from_floats<T>(acc[i]);
             if constexpr (SHIFT) store_partial<T>(to, (int)(v * N) - skip, (int)width, o);
             else store_vec<T, N>(to + (size_t)v * N, o);
@@ -194,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
 // within 3% of it from 1 to 8 slots (16384 x 8 rows of 4 KB 6.6 TB/s; 65536 x 1
 // of 8 KB 6.4 against 3.5 with G x V = 8x1); rows of at most 32 vectors leave
 // half of V = 2 idle and take 4x1 (131072 x 8 rows of 512 bytes 6.6 against 5.7).
-template <typename T, typename W, bool SHIFT, int G, int V, int WT>
+template <typename T, typename W, bool SHIFT, int G, int V, int WT, int GL>
 __global__ void __launch_bounds__(kThreads) k_combine_grad(
     const T* __restrict__ dout, size_t dout_stride, const T* __restrict__ y, size_t y_stride,
     const W* __restrict__ weights, const int32_t* __restrict__ position, const int32_t* __restrict__ routed,
@@ -204,26 +217,27 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
 {
     constexpr int N = kVec<T>, kSlots = 8;
     __shared__ float part[kWarps][kSlots];
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t t = blockIdx.x * (kWarps / WT) + warp / WT;
+    static_assert(WT == 1 || GL == 32, "several warps or part of one");
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % GL;
+    const uint32_t t = WT > 1 ? blockIdx.x * (kWarps / WT) + warp / WT : blockIdx.x * (kThreads / GL) + threadIdx.x / GL;
     const bool live = t < tokens;  // no early return: the block has barriers when WT > 1
     const uint32_t limit = routed_rows(routed, slots_total), vecs = live ? row_vecs<T, SHIFT>(width) : 0;
     const T* grad = dout + (live ? t : 0) * dout_stride;
     for (uint32_t k0 = 0; k0 < slots; k0 += kSlots) {
-        const uint32_t here = live ? min(slots - k0, (uint32_t)kSlots) : 0;
-        Slots<W> sl;
+        const uint32_t here = live ? min(slots - k0, (uint32_t)kSlots) : 0, most = min(slots - k0, (uint32_t)kSlots);
+        Slots<W, GL> sl;
         sl.load(position, weights, (size_t)t * slots + k0, here);
         float dot[kSlots] = {};
-        for (uint32_t v0 = (warp % WT) * (32 * V); v0 < vecs; v0 += 32 * V * WT) {
+        for (uint32_t v0 = WT > 1 ? (warp % WT) * (GL * V) : 0; v0 < row_vecs<T, SHIFT>(width); v0 += GL * V * WT) {
             Vec<T, N> d[V];
             if constexpr (!SHIFT) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (v0 + i * 32 + lane < vecs) d[i] = load_vec<T, N>(grad + (size_t)(v0 + i * 32 + lane) * N);
+                    if (v0 + i * GL + lane < vecs) d[i] = load_vec<T, N>(grad + (size_t)(v0 + i * GL + lane) * N);
             }
 #pragma unroll
             for (int k = 0; k < kSlots; k += G) {
-                if (k >= here) break;
+                if (k >= most) break;
                 using Loaded = std::conditional_t<SHIFT, Shifted<T>, Vec<T, N>>;
                 Loaded r[G][V], g[SHIFT ? G : 1][V];
                 uint32_t p[G];
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
                     const int skip = SHIFT ? lead(dy + p[j] * dy_stride) : 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const uint32_t v = v0 + i * 32 + lane;
+                        const uint32_t v = v0 + i * GL + lane;
                         if constexpr (SHIFT) {
                             r[j][i].load(from + ((int)(v * N) - skip), y, y_end);
                             g[j][i].load(grad + ((int)(v * N) - skip), dout, dout_end);
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
                     const int skip = SHIFT ? lead(to) : 0;
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const uint32_t v = v0 + i * 32 + lane;
+                        const uint32_t v = v0 + i * GL + lane;
                         if (v >= vecs) continue;
                         Vec<T, N> o{};
                         if (p[j] < limit) {
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
 #pragma unroll
-            for (int d = 16; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+            for (int d = GL / 2; d; d >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
         float sum = 0.0f;  // lane j: slot j's
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
@@ -323,35 +337,47 @@ rs_status check_rows(const RowArgs& a, int type)
 
 rs_status launched() { return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA; }
 
+// Lanes per token for rows of so many vectors (97483 x 6 rows of 105 bf16, 15
+// vectors: combine 59.6 us with 16, 98 with 32).
+inline int lanes_for(uint32_t vecs) { return vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32; }
+
 template <typename T, bool SHIFT>
 rs_status run_dispatch(const RowArgs& a, const T* x, size_t x_stride, T* out, size_t out_stride)
 {
-    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT, pieces = (uint32_t)ceil_div(vecs, 64);
-    const size_t step = tokens_per_launch(pieces);
-    for (size_t t = 0; t < a.tokens; t += step) {
-        const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
-        k_dispatch<T, SHIFT><<<(unsigned)ceil_div((size_t)here * pieces, kWarps), kThreads, 0, a.stream>>>(
-            x + t * x_stride, x_stride, a.position + t * a.slots, a.routed, a.slots_total(), here, a.slots,
-            (uint32_t)a.width, pieces, x, x + (a.tokens - 1) * x_stride + a.width, out, out_stride);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT;
+    auto run = [&](auto kernel, int lanes, int v) {
+        const uint32_t pieces = (uint32_t)ceil_div(vecs, lanes * v);
+        const size_t step = tokens_per_launch(pieces);
+        for (size_t t = 0; t < a.tokens; t += step) {
+            const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
+            kernel<<<(unsigned)ceil_div((size_t)here * pieces, kThreads / lanes), kThreads, 0, a.stream>>>(
+                x + t * x_stride, x_stride, a.position + t * a.slots, a.routed, a.slots_total(), here, a.slots,
+                (uint32_t)a.width, pieces, x, x + (a.tokens - 1) * x_stride + a.width, out, out_stride);
+        }
+        return launched();
+    };
+    switch (lanes_for(vecs)) {
+    case 8: return run(k_dispatch<T, SHIFT, 8, 1>, 8, 1);
+    case 16: return run(k_dispatch<T, SHIFT, 16, 1>, 16, 1);
+    default: return run(k_dispatch<T, SHIFT, 32, 2>, 32, 2);
     }
-    return launched();
 }
 
 // Warps that keep every SM's memory pipeline full several times over; below
 // this the spans of k_combine are cut to spread the work.
 constexpr size_t kManyWarps = 16384;
 
-template <typename T, typename W, bool SHIFT, int G, int V>
+template <typename T, typename W, bool SHIFT, int G, int V, int GL>
 rs_status launch_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride,
                          uint32_t span)
 {
-    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT, pieces = (uint32_t)ceil_div(vecs, 32 * V);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT, pieces = (uint32_t)ceil_div(vecs, GL * V);
     while (span > 1 && a.tokens * ceil_div(pieces, span) < kManyWarps) span /= 2;
     const uint32_t parts = (uint32_t)ceil_div(pieces, span);
     const size_t step = tokens_per_launch(parts);
     for (size_t t = 0; t < a.tokens; t += step) {
         const uint32_t here = (uint32_t)(a.tokens - t < step ? a.tokens - t : step);
-        k_combine<T, W, SHIFT, G, V><<<(unsigned)ceil_div((size_t)here * parts, kWarps), kThreads, 0, a.stream>>>(
+        k_combine<T, W, SHIFT, G, V, GL><<<(unsigned)ceil_div((size_t)here * parts, kThreads / GL), kThreads, 0, a.stream>>>(
             y, y_stride, weights ? weights + t * a.slots : nullptr, a.position + t * a.slots, a.routed,
             a.slots_total(), here, a.slots, (uint32_t)a.width, parts, span,
             y + ((size_t)a.slots_total() - 1) * y_stride + a.width, out + t * out_stride, out_stride);
@@ -362,9 +388,12 @@ rs_status launch_combine(const RowArgs& a, const T* y, size_t y_stride, const W*
 template <typename T, typename W, bool SHIFT>
 rs_status run_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
 {
-    if (a.width <= 32 * kVec<T>) return launch_combine<T, W, SHIFT, 4, 1>(a, y, y_stride, weights, out, out_stride, 1);
-    if (a.slots == 1) return launch_combine<T, W, SHIFT, 1, 4>(a, y, y_stride, weights, out, out_stride, 4);
-    return launch_combine<T, W, SHIFT, 2, 2>(a, y, y_stride, weights, out, out_stride, 2);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT;
+    if (vecs <= 8) return launch_combine<T, W, SHIFT, 4, 1, 8>(a, y, y_stride, weights, out, out_stride, 1);
+    if (vecs <= 16) return launch_combine<T, W, SHIFT, 4, 1, 16>(a, y, y_stride, weights, out, out_stride, 1);
+    if (vecs <= 32) return launch_combine<T, W, SHIFT, 4, 1, 32>(a, y, y_stride, weights, out, out_stride, 1);
+    if (a.slots == 1) return launch_combine<T, W, SHIFT, 1, 4, 32>(a, y, y_stride, weights, out, out_stride, 4);
+    return launch_combine<T, W, SHIFT, 2, 2, 32>(a, y, y_stride, weights, out, out_stride, 2);
 }
 
 template <typename T, typename W, bool SHIFT>
@@ -378,12 +407,15 @@ rs_status run_combine_grad(const RowArgs& a, const T* dout, size_t dout_stride, 
             y + ((size_t)a.slots_total() - 1) * y_stride + a.width, dy, dy_stride, dweights);
         return launched();
     };
-    if (a.width <= 32 * kVec<T>) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1>, kWarps);
+    const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT;
+    if (vecs <= 8) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 8>, kThreads / 8);
+    if (vecs <= 16) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 16>, kThreads / 16);
+    if (vecs <= 32) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 32>, kWarps);
     // Shifted vectors take twice the registers.
     constexpr int G = 2, V = SHIFT ? 1 : 2;
     // Few tokens: a whole block each, so that a row is spread over 256 lanes.
-    if (a.tokens < 2048) return run(k_combine_grad<T, W, SHIFT, G, V, kWarps>, 1);
-    return run(k_combine_grad<T, W, SHIFT, G, V, 1>, kWarps);
+    if (a.tokens < 2048) return run(k_combine_grad<T, W, SHIFT, G, V, kWarps, 32>, 1);
+    return run(k_combine_grad<T, W, SHIFT, G, V, 1, 32>, kWarps);
 }
 
 // f(T{}, Int<SHIFT>{}) for the type and alignment at hand.

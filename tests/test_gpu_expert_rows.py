@@ -78,7 +78,7 @@ def test_sort_nothing(way):
     assert order.shape == (0,) and position.shape == (0, 4) and offsets.tolist() == [0] * 7
 
 
-WIDTHS = [1, 7, 8, 33, 256, 1000, 1032, 2048, 4097]
+WIDTHS = [1, 7, 8, 33, 64, 71, 105, 128, 129, 256, 1000, 1032, 2048, 4097]
 
 
 @pytest.mark.parametrize("dt", TYPES)
