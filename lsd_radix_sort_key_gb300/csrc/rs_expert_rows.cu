@@ -207,6 +207,11 @@ __global__ void __launch_bounds__(kThreads) k_combine(const T* __restrict__ y, s
 // within 3% of it from 1 to 8 slots (16384 x 8 rows of 4 KB 6.6 TB/s; 65536 x 1
 // of 8 KB 6.4 against 3.5 with G x V = 8x1); rows of at most 32 vectors leave
 // half of V = 2 idle and take 4x1 (131072 x 8 rows of 512 bytes 6.6 against 5.7).
+// Unaligned rows: each slot's row has a lead of its own, so dout is read once
+// per slot, from L1 after the first.  Rows of 16-bit types read it where it is
+// used, which leaves the registers for more rows in flight (16384 x 8 rows of
+// 2047 bf16 363 us against 409, 131072 x 8 of 129 408 against 486); 32-bit rows
+// along with y's (8191 x 2 of 4095 162 us against 195).
 template <typename T, typename W, bool SHIFT, int G, int V, int WT, int GL>
 __global__ void __launch_bounds__(kThreads) k_combine_grad(
     const T* __restrict__ dout, size_t dout_stride, const T* __restrict__ y, size_t y_stride,
@@ -216,6 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
     W* __restrict__ dweights)
 {
     constexpr int N = kVec<T>, kSlots = 8;
+    constexpr bool early = SHIFT && sizeof(T) == 4;
     __shared__ float part[kWarps][kSlots];
     static_assert(WT == 1 || GL == 32, "several warps or part of one");
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % GL;
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
             for (int k = 0; k < kSlots; k += G) {
                 if (k >= most) break;
                 using Loaded = std::conditional_t<SHIFT, Shifted<T>, Vec<T, N>>;
-                Loaded r[G][V], g[SHIFT ? G : 1][V];
+                Loaded r[G][V], g[early ? G : 1][V];
                 uint32_t p[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
                         const uint32_t v = v0 + i * GL + lane;
                         if constexpr (SHIFT) {
                             r[j][i].load(from + ((int)(v * N) - skip), y, y_end);
-                            g[j][i].load(grad + ((int)(v * N) - skip), dout, dout_end);
+                            if constexpr (early) g[j][i].load(grad + ((int)(v * N) - skip), dout, dout_end);
                         } else if (v < vecs) {
                             r[j][i] = load_vec<T, N>(from + (size_t)v * N);
                         }
@@ -274,7 +280,9 @@ __global__ void __launch_bounds__(kThreads) k_combine_grad(
                             float q[N], f[N], e[N];
                             if constexpr (SHIFT) {
                                 const int at = (int)(v * N) - skip;
-                                to_floats<T>(q, g[j][i].get(grad, at, (int)width));
+                                Loaded late;
+                                if constexpr (!early) late.load(grad + at, dout, dout_end);
+                                to_floats<T>(q, (early ? g[j][i] : late).get(grad, at, (int)width));
                                 to_floats<T>(f, r[j][i].get(y + p[j] * y_stride, at, (int)width));
                                 clear_outside<T>(q, at, (int)width);
                                 clear_outside<T>(f, at, (int)width);
