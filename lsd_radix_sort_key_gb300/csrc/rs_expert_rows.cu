@@ -346,8 +346,15 @@ rs_status check_rows(const RowArgs& a, int type)
 rs_status launched() { return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA; }
 
 // Lanes per token for rows of so many vectors (97483 x 6 rows of 105 bf16, 15
-// vectors: combine 59.6 us with 16, 98 with 32).
-inline int lanes_for(uint32_t vecs) { return vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32; }
+// vectors: combine 59.6 us with 16, 98 with 32).  17 to 24 vectors take three
+// steps of 8 lanes rather than one of 32 (131072 x 8 rows of 129 bf16: dispatch
+// 130 us against 200, combine 127 against 160, its gradient 275 against 409; of
+// 192 74, 84, 144 against 74, 89, 162; only combine of unaligned 32-bit rows
+// loses, 40348 x 8 of 71 60 against 54).
+inline int lanes_for(uint32_t vecs)
+{
+    return vecs <= 8 || (vecs > 16 && vecs <= 24) ? 8 : vecs <= 16 ? 16 : 32;
+}
 
 template <typename T, bool SHIFT>
 rs_status run_dispatch(const RowArgs& a, const T* x, size_t x_stride, T* out, size_t out_stride)
@@ -397,7 +404,7 @@ template <typename T, typename W, bool SHIFT>
 rs_status run_combine(const RowArgs& a, const T* y, size_t y_stride, const W* weights, T* out, size_t out_stride)
 {
     const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT;
-    if (vecs <= 8) return launch_combine<T, W, SHIFT, 4, 1, 8>(a, y, y_stride, weights, out, out_stride, 1);
+    if (lanes_for(vecs) == 8) return launch_combine<T, W, SHIFT, 4, 1, 8>(a, y, y_stride, weights, out, out_stride, 1);
     if (vecs <= 16) return launch_combine<T, W, SHIFT, 4, 1, 16>(a, y, y_stride, weights, out, out_stride, 1);
     if (vecs <= 32) return launch_combine<T, W, SHIFT, 4, 1, 32>(a, y, y_stride, weights, out, out_stride, 1);
     if (a.slots == 1) return launch_combine<T, W, SHIFT, 1, 4, 32>(a, y, y_stride, weights, out, out_stride, 4);
@@ -416,13 +423,16 @@ rs_status run_combine_grad(const RowArgs& a, const T* dout, size_t dout_stride, 
         return launched();
     };
     const uint32_t vecs = (uint32_t)ceil_div(a.width, kVec<T>) + SHIFT;
-    if (vecs <= 8) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 8>, kThreads / 8);
+    // With few tokens a row's steps are what lasts (1000 x 8 rows of 192 bf16:
+    // 5.7 us in one step, 8.1 in three).
+    const bool few = a.tokens < 2048;
+    if (vecs <= 8 || (!few && lanes_for(vecs) == 8)) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 8>, kThreads / 8);
     if (vecs <= 16) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 16>, kThreads / 16);
     if (vecs <= 32) return run(k_combine_grad<T, W, SHIFT, 4, 1, 1, 32>, kWarps);
     // Shifted vectors take twice the registers.
     constexpr int G = 2, V = SHIFT ? 1 : 2;
     // Few tokens: a whole block each, so that a row is spread over 256 lanes.
-    if (a.tokens < 2048) return run(k_combine_grad<T, W, SHIFT, G, V, kWarps, 32>, 1);
+    if (few) return run(k_combine_grad<T, W, SHIFT, G, V, kWarps, 32>, 1);
     return run(k_combine_grad<T, W, SHIFT, G, V, 1, 32>, kWarps);
 }
 

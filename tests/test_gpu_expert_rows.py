@@ -104,6 +104,12 @@ def test_rows(dt, width, tokens, slots, drop):
         held(dy, want, want.abs() * ADD + rounded(want, dtype))
         held(dw, want_w, (width + 1) * ADD * mag + rounded(want_w, wtype))
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("width", [1, 63, 64, 65, 71, 96, 129, 136, 160, 185, 192, 193, 255, 257, 777])
+@pytest.mark.parametrize("tokens,slots", [(2047, 3), (2049, 2), (2111, 9)])
+def test_rows_of_many_tokens(dt, width, tokens, slots):
+    test_rows(dt, width, tokens, slots, 0.1)
+
 
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("width", [1000, 1001])
