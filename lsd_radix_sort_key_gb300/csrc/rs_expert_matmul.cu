@@ -256,7 +256,7 @@ rs_status settle(Operand* o, void* temp, cudaStream_t s)
 
 // ------------------------------------------- dz = dy * act'(pre), and dbias
 
-constexpr int kDzRows = 128, kDzThreads = 256, kDzWarps = kDzThreads / 32;
+constexpr int kDzThreads = 256, kDzWarps = kDzThreads / 32;
 
 // Vectors of a row that a lane takes: whole rows should pass through memory at
 // once, so a block spans DZV * 32 vectors and neighbouring blocks neighbouring
@@ -265,26 +265,40 @@ constexpr int kDzRows = 128, kDzThreads = 256, kDzWarps = kDzThreads / 32;
 template <int N>
 constexpr int kDzVecs = N > 1 ? 2 : 1;
 
-// One block takes a tile of at most 128 rows of one expert and kDzVecs * 32
-// vectors of columns; each warp every eighth row.  part (if given) receives the
-// tile's column sums, [row tile][cols].
+// Rows of a tile: 128, fewer while those would not make kDzBlocks blocks: a
+// warp's rows one after the other are what lasts then (gradients of silu in
+// bf16, always 128 rows -> so: 3001 rows, 8 experts of 1000 x 1160 55.6 -> 39.4 us,
+// 2048, 16 of 1024 x 2048 67.7 -> 49.4, 4096, 8 of 2048 x 2048 87.7 -> 73.6).
+constexpr size_t kDzBlocks = 608;  // four for each of 152 SMs
+
+size_t dz_tile_rows(size_t rows, size_t cols, size_t elem_bytes)
+{
+    const size_t across = ceil_div(cols * elem_bytes, 1024);
+    size_t tile = 128;
+    while (tile > 16 && ceil_div(rows, tile) * across < kDzBlocks) tile /= 2;
+    return tile;
+}
+
+// One block takes a tile of at most tile_rows rows of one expert and kDzVecs *
+// 32 vectors of columns; each warp every eighth row.  part (if given) receives
+// the tile's column sums, [row tile][cols].
 template <typename T, int ACT, int N>
 __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ dy, size_t dy_i,
                                                          const T* __restrict__ pre, size_t pre_i, T* __restrict__ dz,
                                                          size_t dz_i, float* __restrict__ part,
                                                          const int32_t* __restrict__ offsets, uint32_t experts,
-                                                         uint32_t rows, uint32_t cols)
+                                                         uint32_t rows, uint32_t cols, uint32_t tile_rows)
 {
     constexpr int V = kDzVecs<N>, kCols = 32 * V * N;
     extern __shared__ uint32_t mem[];
     __shared__ float sums[kDzWarps][kCols];
     start_next_grid();
-    const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
+    const Groups g = Groups::make(mem, offsets, experts, rows, tile_rows, false);
     const uint32_t across = (cols + kCols - 1) / kCols, tile = blockIdx.x / across;
     if (tile >= g.tiles()) return;
     const uint32_t e = g.find(tile), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t r0 = g.off[e] + (tile - g.tile[e]) * kDzRows;
-    const uint32_t r_end = min(r0 + kDzRows, g.off[e + 1]);
+    const uint32_t r0 = g.off[e] + (tile - g.tile[e]) * tile_rows;
+    const uint32_t r_end = min(r0 + tile_rows, g.off[e + 1]);
     const uint32_t c0 = (blockIdx.x - tile * across) * kCols + lane * N;
     float sum[V][N] = {};
 #pragma unroll 2
@@ -344,15 +358,16 @@ constexpr int kBiasThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kBiasThreads, 16) k_bias_grad(const float* __restrict__ part, T* __restrict__ dbias,
                                                                 const int32_t* __restrict__ offsets, uint32_t experts,
-                                                                uint32_t rows, uint32_t cols, bool wait_first)
+                                                                uint32_t rows, uint32_t cols, uint32_t tile_rows,
+                                                                bool wait_first)
 {
     extern __shared__ uint32_t mem[];
     if (wait_first) wait_prior_grid();
-    const Groups g = Groups::make(mem, offsets, experts, rows, kDzRows, false);
+    const Groups g = Groups::make(mem, offsets, experts, rows, tile_rows, false);
     const uint32_t e = blockIdx.x, c = blockIdx.y * kBiasThreads + threadIdx.x;
     if (c < cols) {
         float s = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t t = g.tile[e]; t < g.tile[e + 1]; ++t) s += part[(size_t)t * cols + c];
         dbias[(size_t)e * cols + c] = from_float<T>(s);
     }
@@ -399,7 +414,7 @@ Layout layout(const rs_expert_matmul_desc* d, bool grad)
         l.dz_stride = align_up(d->outer, 16 / eb);
         l.dz = take(d->rows * l.dz_stride * eb);
     }
-    if (grad && d->dbias) l.part = take(max_tiles(d->rows, d->num_experts, kDzRows) * d->outer * 4);
+    if (grad && d->dbias) l.part = take(max_tiles(d->rows, d->num_experts, dz_tile_rows(d->rows, d->outer, eb)) * d->outer * 4);
     if (eb == 2) {
         if (dw || (!grad && d->rows && d->inner && d->outer)) l.x = rows_operand(d->x, d->x_stride, d->rows, d->inner);
         if (dx || (!grad && d->rows && d->inner && d->outer)) l.w = weights_operand(d);
@@ -550,20 +565,22 @@ rs_status gradient(const rs_expert_matmul_desc* d)
     // the products' operand: dz, or dy where there is no activation
     const T* g = act ? dz : sizeof(T) == 2 ? static_cast<const T*>(l.g.p) : dy;
     const size_t g_stride = act ? l.dz_stride : sizeof(T) == 2 ? l.g.row_stride : d->y_stride;
+    const uint32_t tile_rows = (uint32_t)dz_tile_rows(rows, cols, eb);
     if ((dz || part) && cols) {
         constexpr int kVec = 16 / sizeof(T);
         const bool vec = aligned16(dy, d->y_stride, eb) && (!act || aligned16(pre, d->pre_stride, eb)) &&
                          d->outer % kVec == 0;
         const rs_status st = by_act(d->activation, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-            const size_t tiles = max_tiles(rows, experts, kDzRows);
+            const size_t tiles = max_tiles(rows, experts, tile_rows);
             if (vec)
                 k_act_grad<T, ACT, kVec><<<(unsigned)(tiles * ceil_div(cols, 32 * kDzVecs<kVec> * kVec)), kDzThreads,
                                            groups, s>>>(dy, d->y_stride, pre, d->pre_stride, dz, l.dz_stride, part,
-                                                        d->offsets, experts, rows, cols);
+                                                        d->offsets, experts, rows, cols, tile_rows);
             else
                 k_act_grad<T, ACT, 1><<<(unsigned)(tiles * ceil_div(cols, 32)), kDzThreads, groups, s>>>(
-                    dy, d->y_stride, pre, d->pre_stride, dz, l.dz_stride, part, d->offsets, experts, rows, cols);
+                    dy, d->y_stride, pre, d->pre_stride, dz, l.dz_stride, part, d->offsets, experts, rows, cols,
+                    tile_rows);
             return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
         });
         if (st != RS_OK) return st;
@@ -604,7 +621,7 @@ rs_status gradient(const rs_expert_matmul_desc* d)
     if (part && cols) {
         const rs_status st = launch_kernel(k_bias_grad<T>, dim3(experts, (unsigned)ceil_div(cols, kBiasThreads)), kBiasThreads,
                                            groups, s, 1, true, (const float*)part, static_cast<T*>(d->dbias), d->offsets,
-                                           experts, rows, cols, !tc_dx && !tc_dw);
+                                           experts, rows, cols, tile_rows, !tc_dx && !tc_dw);
         if (st != RS_OK) return st;
     }
     if (!tc_dx && (!want_dw || want_dx)) {
