@@ -169,8 +169,15 @@ __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
     }
 }
 
-// From this many rows per expert (on average) on, ragged rows take tiles of 128.
-constexpr size_t kAnyRows = 64;
+// Tiles of 128 for ranges of 64 rows or more (on average), if tiles of 64 would
+// not fit in two per SM: one of those takes half a tile of 128's time, which
+// wins while SMs are idle (64 rows of 1024 x 1024 float32 133 -> 70 us; dw of 2432
+// rows and 512 x 1024 292 -> 125) and loses at three per SM (1500 rows, 2 experts
+// of 2048 x 1024: 382 us against 268).
+bool any_wide(size_t rows, size_t cols, size_t experts)
+{
+    return rows >= 64 && experts * ceil_div(rows, 64) * ceil_div(cols, 64) > 2 * 152;
+}
 
 template <typename T, int ACT>
 rs_status launch_any_rows(const AnyArgs<T>& p, cudaStream_t s)
@@ -181,15 +188,20 @@ rs_status launch_any_rows(const AnyArgs<T>& p, cudaStream_t s)
         return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
     };
     if constexpr (sizeof(T) == 4)
-        if (p.rows >= kAnyRows * p.experts && p.reduce) return run(k_product_any<T, ACT, false, 128>, 128);
+        if (any_wide(p.rows / p.experts, p.cols, p.experts) && p.reduce) return run(k_product_any<T, ACT, false, 128>, 128);
     return run(k_product_any<T, ACT, false, 64>, 64);
 }
 
 rs_status launch_any_reduce(const AnyArgs<float>& p, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(ceil_div(p.out_rows, 128) * p.experts), (unsigned)ceil_div(p.cols, 128));
-    k_product_any<float, RS_ACT_NONE, true, 128><<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    auto run = [&](auto kernel, size_t tile) {
+        const dim3 grid((unsigned)(ceil_div(p.out_rows, tile) * p.experts), (unsigned)ceil_div(p.cols, tile));
+        kernel<<<grid, kAnyThreads, Groups::words(p.experts) * 4, s>>>(p);
+        return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    };
+    if (any_wide(p.out_rows, p.cols, p.experts))
+        return run(k_product_any<float, RS_ACT_NONE, true, 128>, 128);
+    return run(k_product_any<float, RS_ACT_NONE, true, 64>, 64);
 }
 
 // ------------------------------------------------- copies with aligned rows

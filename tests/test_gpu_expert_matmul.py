@@ -113,6 +113,23 @@ def test_larger(dt, counts, inner, outer):
     check_grad(a, "gelu", dtype, 8)
 
 
+@pytest.mark.parametrize("counts,inner,outer", [([300, 257, 0, 400], 1000, 1160), ([2000], 1000, 1032),
+                                                ([700, 1, 0, 150, 64, 63, 65, 17], 520, 1000), ([64], 1030, 999),
+                                                ([63], 1030, 999), ([64] * 40, 65, 193)])
+def test_larger_float32(counts, inner, outer):
+    a = make(counts, 11, inner, outer, torch.float32, 41)
+    check_forward(a, "gelu", torch.float32)
+    check_grad(a, "gelu", torch.float32, 42)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows", [2600, 5200, 10400, 20000])
+@pytest.mark.parametrize("outer", [2056, 2055])
+def test_gradient_of_many_rows(dt, rows, outer):
+    a = make([rows // 2 - 7, 0, 7, rows // 2 - 40], 40, 8, outer, TYPES[dt], 43)
+    check_grad(a, "silu", TYPES[dt], 44)
+
+
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("inner,outer", [(128, 256), (130, 72)])
 def test_layouts(way, dt, inner, outer):
