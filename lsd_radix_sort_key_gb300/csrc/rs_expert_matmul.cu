@@ -280,8 +280,10 @@ constexpr int kDzVecs = N > 1 ? 2 : 1;
 // Rows of a tile: 128, fewer while those would not make kDzBlocks blocks: a
 // warp's rows one after the other are what lasts then (gradients of silu in
 // bf16, always 128 rows -> so: 3001 rows, 8 experts of 1000 x 1160 55.6 -> 39.4 us,
-// 2048, 16 of 1024 x 2048 67.7 -> 49.4, 4096, 8 of 2048 x 2048 87.7 -> 73.6).
-constexpr size_t kDzBlocks = 608;  // four for each of 152 SMs
+// 2048, 16 of 1024 x 2048 67.7 -> 49.3, 4096, 8 of 2048 x 2048 87.7 -> 72.7).
+// Two for each of 152 SMs; four cost dbias longer sums and gain nothing (16384 x
+// 2048 bf16, silu, sums only: 36.9 us with 304, 38.4 with 608, 42.6 with 1216).
+constexpr size_t kDzBlocks = 304;
 
 size_t dz_tile_rows(size_t rows, size_t cols, size_t elem_bytes)
 {
