@@ -215,6 +215,17 @@ def _weights(weights, y, shape):
         raise ValueError(f"weights: a tensor on {y.device} is wanted, got one on {weights.device}")
 
 
+def _scratch(temp, x):
+    """The caller's scratch is memory that x's device can be handed: all of its
+    bytes are its own."""
+    if not isinstance(temp, torch.Tensor) or temp.dtype != torch.uint8:
+        raise TypeError(f"temp: a torch.uint8 tensor is wanted, got {getattr(temp, 'dtype', type(temp).__name__)}")
+    if temp.device != x.device:
+        raise ValueError(f"temp: a tensor on {x.device} is wanted, got one on {temp.device}")
+    if not temp.is_contiguous():
+        raise ValueError("temp: a contiguous tensor is wanted")
+
+
 def _current(device, stream):
     """The current stream's handle in the usual case: no stream is asked for
     and the tensors are on the current device; else None."""
@@ -227,8 +238,8 @@ def _current(device, stream):
 @contextlib.contextmanager
 def _other(device, stream, inputs):
     """Allocate on, and launch into, `stream` (None: the current one) of
-    `device`; the inputs' memory is then not handed out again before `stream`
-    has passed."""
+    `device`; the memory of the caller's tensors (inputs, scratch) is then not
+    handed out again before `stream` has passed."""
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.device(device):
         if s is None:
@@ -437,8 +448,9 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
     adjacent in memory; bias [experts, outer]; residual [rows, outer]; all of
     x's type.  activation: none, relu, gelu (erf) or silu.  Returns y [rows,
     outer], or (y, pre) with the values before the activation, which
-    expert_matmul_grad needs.  temp: scratch of the caller's (uint8, at least
-    rs_expert_matmul_temp_bytes), for rs_expert_matmul_status.
+    expert_matmul_grad needs.  temp: scratch of the caller's (uint8 on x's
+    device, contiguous, 256-byte aligned, at least rs_expert_matmul_temp_bytes),
+    for rs_expert_matmul_status.
     """
     if torch is None:
         _torch()
@@ -454,10 +466,12 @@ def expert_matmul(x, w, offsets, *, bias=None, activation="none", residual=None,
     if residual is not None:
         _like("residual", residual, x, (rows, outer))
         extra[2:4] = residual.data_ptr(), _rows("residual", residual)[2]
+    if temp is not None:
+        _scratch(temp, x)
     args = (head, extra, x, rows, outer, return_pre, temp)
     s = _current(x.device, stream)
     if s is None:
-        with _other(x.device, stream, (x, w, offsets, bias, residual)) as s:
+        with _other(x.device, stream, (x, w, offsets, bias, residual, temp)) as s:
             return _matmul(*args, s)
     return _matmul(*args, s)
 
@@ -498,10 +512,12 @@ def expert_matmul_grad(dy, x, w, offsets, *, pre=None, activation="none", bias=T
             raise TypeError(f"pre: needed for activation {activation!r}")
         _like("pre", pre, x, (rows, outer))
         grads[2:4] = pre.data_ptr(), _rows("pre", pre)[2]
+    if temp is not None:
+        _scratch(temp, x)
     args = (head, grads, x, rows, inner, outer, experts, need_dx, need_dw, bias, temp)
     s = _current(x.device, stream)
     if s is None:
-        with _other(x.device, stream, (dy, x, w, offsets, pre)) as s:
+        with _other(x.device, stream, (dy, x, w, offsets, pre, temp)) as s:
             return _matmul_grad(*args, s)
     return _matmul_grad(*args, s)
 

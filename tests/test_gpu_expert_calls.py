@@ -1,0 +1,74 @@
+"""The expert operators' calls at their edges: the caller's scratch."""
+import pytest
+
+import lsd_radix_sort_key_gb300 as rs
+from lsd_radix_sort_key_gb300 import experts
+
+pytestmark = pytest.mark.gpu
+
+np = pytest.importorskip("numpy")
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from expert_util import DEV, gen  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    rs.build()
+    rs.lib()
+    experts._torch()
+    assert experts._fast is not None  # the extension is part of the build
+
+
+def product(counts, inner, outer, dtype=torch.bfloat16, seed=1):
+    g = gen(seed)
+    off = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32, device=DEV)
+    x = torch.randn(sum(counts), inner, device=DEV, generator=g).to(dtype)
+    w = torch.randn(len(counts), outer, inner, device=DEV, generator=g).to(dtype)
+    return x, w, off
+
+
+# --------------------------------------------------------- caller's scratch
+
+def calls(x, w, off, dy):
+    """Both products, as functions of temp and the other keywords."""
+    return (lambda **kw: (rs.expert_matmul(x, w, off, **kw),),
+            lambda **kw: rs.expert_matmul_grad(dy, x, w, off, **kw))
+
+
+def test_scratch_that_is_not_ours_to_use_is_refused():
+    # refused on the host, before anything is enqueued
+    x, w, off = product([30, 41], 64, 96)
+    for call in calls(x, w, off, torch.randn(71, 96, device=DEV).bfloat16()):
+        for temp, error in ((torch.empty(1 << 20, dtype=torch.uint8), ValueError),  # the host's
+                            (torch.empty(1 << 20, dtype=torch.uint8, device="meta"), ValueError),
+                            (torch.empty(1, dtype=torch.uint8, device=DEV).expand(1 << 20), ValueError),
+                            (torch.empty(1 << 21, dtype=torch.uint8, device=DEV)[::2], ValueError),
+                            (torch.empty(1 << 18, device=DEV), TypeError), (1 << 40, TypeError),
+                            (torch.empty(100, dtype=torch.uint8, device=DEV), rs.RadixSortError),
+                            (torch.empty(1 << 20, dtype=torch.uint8, device=DEV)[16:], rs.RadixSortError)):
+            with pytest.raises(error):
+                call(temp=temp)
+        temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+        for got, want in zip(call(temp=temp), call()):
+            assert torch.equal(got, want)
+
+
+def test_scratch_of_another_stream_is_kept_until_that_stream_has_passed():
+    x, w, off = product([30, 41], 64, 96)
+    size = 33 << 20  # a block of its own in torch's allocator
+    for call in calls(x, w, off, torch.randn(71, 96, device=DEV).bfloat16()):
+        want, side = call(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        temp = torch.empty(size, dtype=torch.uint8, device=DEV)
+        where = temp.data_ptr()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000_000)  # half a second: the call is still to come when temp goes
+        got = call(temp=temp, stream=side)
+        del temp
+        again = torch.empty(size, dtype=torch.uint8, device=DEV)
+        assert not side.query() and again.data_ptr() != where
+        side.synchronize()
+        assert all(torch.equal(g, v) for g, v in zip(got, want))
