@@ -39,6 +39,13 @@ struct Entry {
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// A flag is True or False; any other object's truth is Python's to find.
+bool flag(PyObject* o, bool* value)
+{
+    *value = o == Py_True;
+    return o == Py_True || o == Py_False;
+}
+
 // A plain tensor (not a subclass with ideas of its own), or nullptr.
 const at::Tensor* tensor(PyObject* o)
 {
@@ -256,7 +263,9 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (n != 7) return none();
     const at::Tensor *x = tensor(a[0]), *w = tensor(a[1]), *offsets = tensor(a[2]);
     const at::Tensor *bias = a[3] == Py_None ? nullptr : tensor(a[3]), *res = a[5] == Py_None ? nullptr : tensor(a[5]);
-    if (!x || !w || !offsets || (!bias && a[3] != Py_None) || (!res && a[5] != Py_None) || !PyLong_CheckExact(a[4]))
+    bool want_pre;
+    if (!x || !w || !offsets || (!bias && a[3] != Py_None) || (!res && a[5] != Py_None) || !PyLong_CheckExact(a[4]) ||
+        !flag(a[6], &want_pre))
         return none();
     rs_expert_matmul_desc d{};
     if (!products(*x, *w, *offsets, PyLong_AsLong(a[4]), &d)) return none();
@@ -272,7 +281,6 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n)
     at::Tensor y = like(*x, {rows, outer}), pre;
     d.y = y.mutable_data_ptr();
     d.y_stride = d.pre_stride = (size_t)outer;
-    const bool want_pre = a[6] == Py_True;
     if (want_pre) {
         pre = like(*x, {rows, outer});
         d.pre = pre.mutable_data_ptr();
@@ -295,7 +303,10 @@ PyObject* matmul_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (n != 9) return none();
     const at::Tensor *dy = tensor(a[0]), *x = tensor(a[1]), *w = tensor(a[2]), *offsets = tensor(a[3]);
     const at::Tensor* pre = a[4] == Py_None ? nullptr : tensor(a[4]);
-    if (!dy || !x || !w || !offsets || (!pre && a[4] != Py_None) || !PyLong_CheckExact(a[5])) return none();
+    bool want_bias, want_dx, want_dw;
+    if (!dy || !x || !w || !offsets || (!pre && a[4] != Py_None) || !PyLong_CheckExact(a[5]) ||
+        !flag(a[6], &want_bias) || !flag(a[7], &want_dx) || !flag(a[8], &want_dw))
+        return none();
     rs_expert_matmul_desc d{};
     const long act = PyLong_AsLong(a[5]);
     if (!products(*x, *w, *offsets, act, &d)) return none();
@@ -307,16 +318,16 @@ PyObject* matmul_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
         d.pre = const_cast<void*>(pre->const_data_ptr());
     }
     at::Tensor dx, dw, dbias;
-    if (a[7] == Py_True) {
+    if (want_dx) {
         dx = like(*x, {rows, inner});
         d.dx = dx.mutable_data_ptr();
         d.dx_stride = (size_t)inner;
     }
-    if (a[8] == Py_True) {
+    if (want_dw) {
         dw = like(*x, {w->size(0), outer, inner});
         d.dw = dw.mutable_data_ptr();
     }
-    if (a[6] == Py_True) {
+    if (want_bias) {
         dbias = like(*x, {w->size(0), outer});
         d.dbias = dbias.mutable_data_ptr();
     }

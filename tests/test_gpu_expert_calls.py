@@ -1,4 +1,5 @@
-"""The expert operators' calls at their edges: the caller's scratch."""
+"""The expert operators' calls at their edges: the caller's scratch and flags
+that are not bools."""
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
@@ -20,6 +21,13 @@ def built():
     rs.lib()
     experts._torch()
     assert experts._fast is not None  # the extension is part of the build
+
+
+@pytest.fixture(params=["extension", "python"])
+def way(request, monkeypatch):
+    """Both forms of a call: the extension's, and the one in Python."""
+    if request.param == "python":
+        monkeypatch.setattr(experts, "_fast", None)
 
 
 def product(counts, inner, outer, dtype=torch.bfloat16, seed=1):
@@ -72,3 +80,30 @@ def test_scratch_of_another_stream_is_kept_until_that_stream_has_passed():
         assert not side.query() and again.data_ptr() != where
         side.synchronize()
         assert all(torch.equal(g, v) for g, v in zip(got, want))
+
+
+# ------------------------------------------------------------------- flags
+
+@pytest.mark.parametrize("yes,no", [(1, 0), (np.True_, np.False_), ("yes", ""), (True, None)])
+def test_flags_are_taken_by_their_truth(way, yes, no):
+    x, w, off = product([30, 0, 41], 64, 96)
+    dy = torch.randn(71, 96, device=DEV, generator=gen(2)).bfloat16()
+    y, pre = rs.expert_matmul(x, w, off, activation="silu", return_pre=True)
+    got = rs.expert_matmul(x, w, off, activation="silu", return_pre=yes)
+    assert isinstance(got, tuple) and torch.equal(got[0], y) and torch.equal(got[1], pre)
+    assert torch.equal(rs.expert_matmul(x, w, off, activation="silu", return_pre=no), y)
+    full = rs.expert_matmul_grad(dy, x, w, off, pre=pre, activation="silu")
+    for want in range(8):
+        need = [bool(want >> i & 1) for i in range(3)]
+        flags = [yes if n else no for n in need]
+        got = rs.expert_matmul_grad(dy, x, w, off, pre=pre, activation="silu", need_dx=flags[0], need_dw=flags[1],
+                                    bias=flags[2])
+        for g, f, n in zip(got, full, need):
+            assert (g is None) if not n else torch.equal(g, f)
+
+
+def test_a_flag_without_a_truth_is_refused(way):
+    x, w, off = product([30, 41], 64, 96)
+    dy = torch.randn(71, 96, device=DEV).bfloat16()
+    with pytest.raises(RuntimeError):  # torch's own: a tensor of many values is neither
+        rs.expert_matmul_grad(dy, x, w, off, bias=torch.zeros(2, 96, device=DEV))
