@@ -398,11 +398,20 @@ Operand rows_operand(const void* p, size_t stride, size_t rows, size_t width)
     return operand(p, stride, 0, 1, rows, width);
 }
 
+// Which side of an expert's matrix is adjacent in memory: inner or outer.  The
+// inner stride of a single column says nothing, so a column whose outer stride
+// is not 1 either is rows of one element.  (A single row with an inner stride
+// is the same by its outer side.)
+bool inner_adjacent(const rs_expert_matmul_desc* d)
+{
+    return d->w_inner_stride == 1 || (d->inner == 1 && d->w_outer_stride != 1);
+}
+
 Operand weights_operand(const rs_expert_matmul_desc* d)
 {
-    const bool inner_adjacent = d->w_inner_stride == 1;
-    return operand(d->w, inner_adjacent ? d->w_outer_stride : d->w_inner_stride, d->w_expert_stride, d->num_experts,
-                   inner_adjacent ? d->outer : d->inner, inner_adjacent ? d->inner : d->outer);
+    const bool by_inner = inner_adjacent(d);
+    return operand(d->w, by_inner ? d->w_outer_stride : d->w_inner_stride, d->w_expert_stride, d->num_experts,
+                   by_inner ? d->outer : d->inner, by_inner ? d->inner : d->outer);
 }
 
 // What temp holds after the status words; offsets in bytes.
@@ -494,8 +503,7 @@ TcArgs<T> tc_args(const rs_expert_matmul_desc* d, size_t first_word, size_t word
 template <typename T>
 TcOperand<T> weight_tc(const rs_expert_matmul_desc* d, const Operand& w, bool cols_are_outer)
 {
-    const bool inner_adjacent = d->w_inner_stride == 1;
-    return TcOperand<T>{static_cast<const T*>(w.p), w.row_stride, w.matrix_stride, inner_adjacent != cols_are_outer};
+    return TcOperand<T>{static_cast<const T*>(w.p), w.row_stride, w.matrix_stride, inner_adjacent(d) != cols_are_outer};
 }
 
 template <typename T>

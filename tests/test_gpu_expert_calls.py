@@ -1,5 +1,5 @@
-"""The expert operators' calls at their edges: the caller's scratch and flags
-that are not bools."""
+"""The expert operators' calls at their edges: the caller's scratch, flags
+that are not bools, and layouts that only the C interface can name."""
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
@@ -12,7 +12,8 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from expert_util import DEV, gen  # noqa: E402
+from expert_util import (DEV, TYPES, gen, grad_bounds, held, matmul_bounds, plain_matmul,  # noqa: E402
+                         plain_matmul_grad)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -107,3 +108,38 @@ def test_a_flag_without_a_truth_is_refused(way):
     dy = torch.randn(71, 96, device=DEV).bfloat16()
     with pytest.raises(RuntimeError):  # torch's own: a tensor of many values is neither
         rs.expert_matmul_grad(dy, x, w, off, bias=torch.zeros(2, 96, device=DEV))
+
+
+# ------------------------------------------ layouts of the C interface alone
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("inner,outer,so,si", [(1, 40, 6, 9), (1, 40, 6, 1), (1, 40, 1, 9), (1, 40, 8, 16), (24, 1, 9, 5),
+                                               (24, 1, 9, 1), (24, 1, 1, 5), (1, 1, 9, 5)])
+def test_weights_of_one_column_or_row_at_any_strides(dt, act, inner, outer, so, si):
+    dtype, count = TYPES[dt], 3
+    g, span = gen(inner + so), (outer - 1) * so + (inner - 1) * si + 1
+    base = torch.randn(count, span + 11, device=DEV, generator=g).to(dtype)
+    at = torch.arange(outer, device=DEV)[:, None] * so + torch.arange(inner, device=DEV) * si
+    w = base[:, at]  # what the call has to read
+    counts = [17, 0, 30]
+    x, _, off = product(counts, inner, outer, dtype, 5)
+    rows = sum(counts)
+    dy = torch.randn(rows, outer, device=DEV, generator=g).to(dtype)
+    y, pre = (torch.empty(rows, outer, dtype=dtype, device=DEV) for _ in range(2))
+    temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    d = rs.ExpertMatmulDesc(list(TYPES).index(dt), rs.ACTIVATIONS[act], count, rows, inner, outer, off.data_ptr(),
+                            x.data_ptr(), inner, base.data_ptr(), base.stride(0), so, si)
+    d.y, d.y_stride, d.pre, d.pre_stride = y.data_ptr(), outer, pre.data_ptr(), outer
+    d.temp, d.temp_bytes, d.stream = temp.data_ptr(), temp.numel(), torch.cuda.current_stream().cuda_stream
+    assert rs.rs_expert_matmul_temp_bytes(d) <= temp.numel() and rs.rs_expert_matmul(d) == 0
+    want, z, mag = plain_matmul(x, w, off, None, act)
+    by, bz = matmul_bounds(want, z, mag, inner, dtype)
+    held(y, want, by)
+    held(pre, z, bz)
+    dx, dw = torch.empty_like(x), torch.empty(count, outer, inner, dtype=dtype, device=DEV)
+    d.y, d.dx, d.dx_stride, d.dw = dy.data_ptr(), dx.data_ptr(), inner, dw.data_ptr()
+    assert rs.rs_expert_matmul_grad_temp_bytes(d) <= temp.numel() and rs.rs_expert_matmul_grad(d) == 0
+    want, mags, errs = plain_matmul_grad(dy, x, w, off, pre, act)
+    for got, v, b in zip((dx, dw), want, grad_bounds(want, mags, errs, (outer, 30, 30), dtype)):
+        held(got, v, b)
