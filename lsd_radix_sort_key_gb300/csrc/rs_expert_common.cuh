@@ -216,6 +216,20 @@ __device__ __forceinline__ void store_partial(T* row, int i, int width, const Ve
 
 // ---- host side
 
+constexpr size_t kBlockSmem = 227 * 1024;  // that a block can have
+
+// Lets a kernel be launched with up to `most` bytes of dynamic shared memory.
+// The limit belongs to the kernel on the device, not to the calling thread, so
+// `most` is what the kernel may ever need and no call lowers it under another
+// thread's launch.
+template <typename K>
+bool allow_smem(K kernel, size_t most)
+{
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
 template <typename... P, typename... A>
 rs_status launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
                         bool dependent, const A&... args)

@@ -379,7 +379,7 @@ rs_status rs_expert_sort(const void* ids, int id_bytes, size_t n, int num_expert
     const auto kernel = masks ? k_expert_sort<true> : k_expert_sort<false>;
     const size_t most_smem = Shared::bytes(bins, kMaxThreads / 32, n > kOneBlockSlots, masks);
     if (most_smem > 48 * 1024 - 256 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem) != cudaSuccess)
+        !rsx::allow_smem(kernel, Shared::bytes(masks ? kMaskBins : RS_EXPERTS_MAX + 1, kMaxThreads / 32, true, masks)))
         return RS_ERR_CUDA;
     if (n <= kOneBlockSlots) {
         p.chunk = (uint32_t)n;

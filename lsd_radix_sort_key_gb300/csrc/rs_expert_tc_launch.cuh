@@ -27,8 +27,9 @@ rs_status tc_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArgs<T
     const size_t smem = TcShape<BN, PAIR>::smem(args.experts);
     const int sms = sm_count();
     if (sms < 2) return RS_ERR_CUDA;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return RS_ERR_CUDA;
+    constexpr size_t most = TcShape<BN, PAIR>::smem(RS_EXPERTS_MAX);
+    static_assert(most <= kBlockSmem);
+    if (!allow_smem(kernel, most)) return RS_ERR_CUDA;
     size_t grid = (size_t)sms < kTcMaxBlocks ? (size_t)sms : kTcMaxBlocks;
     if constexpr (PAIR) grid = grid / 2 * 2 < tiles * 2 ? grid / 2 * 2 : tiles * 2;
     else grid = grid < tiles ? grid : tiles;
@@ -42,8 +43,9 @@ rs_status split_launch(const CUtensorMap& ma, const CUtensorMap& mb, const TcArg
 {
     const auto kernel = k_product_split<T, RAGGED_K, B_MN>;
     const size_t smem = SplitShape::smem(args.experts);
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return RS_ERR_CUDA;
+    constexpr size_t most = SplitShape::smem(RS_EXPERTS_MAX);
+    static_assert(most <= kBlockSmem);
+    if (!allow_smem(kernel, most)) return RS_ERR_CUDA;
     size_t clusters = (size_t)(sms < kTcMaxBlocks ? sms : kTcMaxBlocks) / blocks;
     if (tiles < clusters) clusters = tiles;
     return launch_kernel(kernel, dim3((unsigned)(clusters * blocks)), kTcThreads, smem, s, blocks, args.dependent != 0,
@@ -100,9 +102,7 @@ size_t resident_clusters(K kernel, int blocks, size_t smem)
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess)
-            return 0;
+        if (!allow_smem(kernel, smem) || cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess) return 0;
         n.store(v, std::memory_order_relaxed);
     }
     return (size_t)v;

@@ -1,5 +1,8 @@
 """The expert operators' calls at their edges: the caller's scratch, flags
-that are not bools, and layouts that only the C interface can name."""
+that are not bools, layouts that only the C interface can name, and calls from
+several host threads."""
+import threading
+
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
@@ -13,7 +16,7 @@ if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
 from expert_util import (DEV, TYPES, gen, grad_bounds, held, matmul_bounds, plain_matmul,  # noqa: E402
-                         plain_matmul_grad)
+                         plain_matmul_grad, plain_order)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -143,3 +146,66 @@ def test_weights_of_one_column_or_row_at_any_strides(dt, act, inner, outer, so, 
     want, mags, errs = plain_matmul_grad(dy, x, w, off, pre, act)
     for got, v, b in zip((dx, dw), want, grad_bounds(want, mags, errs, (outer, 30, 30), dtype)):
         held(got, v, b)
+
+
+# ------------------------------------------------------------ host threads
+
+def in_threads(*calls):
+    """Runs the calls at once, one thread and stream each; the first error of any is raised here."""
+    errors, start = [], threading.Barrier(len(calls))
+
+    def run(call):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait()
+            call(stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if errors:
+        raise errors[0]
+
+
+@pytest.mark.parametrize("n,few,many", [(1500, 400, 500), (20_000, 100, 500), (20_000, 600, 1024), (60_000, 300, 511)])
+def test_sorts_of_two_threads(n, few, many):
+    # the kernels' shared memory goes by the number of experts; the C calls run without the interpreter's lock
+    def sorts(count, seed):
+        ids = torch.randint(-1, count, (n,), device=DEV, generator=gen(seed))
+        got = [torch.empty(k, dtype=torch.int32, device=DEV) for k in (n, n, count + 1)]
+        tb = rs.rs_expert_sort_temp_bytes(n, count)
+        temp = torch.empty(max(tb, 1), dtype=torch.uint8, device=DEV)
+        want = plain_order(ids, count)
+        torch.cuda.synchronize()
+
+        def call(stream):
+            s = stream.cuda_stream
+            assert not any(rs.rs_expert_sort(ids, 8, n, count, *got, temp, tb, s) for _ in range(20_000))
+            stream.synchronize()
+            assert all(torch.equal(g.cpu(), w.flatten()) for g, w in zip(got, want))
+        return call
+
+    in_threads(sorts(few, 1), sorts(many, 2))
+
+
+@pytest.mark.parametrize("inner,outer", [(64, 64), (1024, 128)])
+def test_products_of_two_threads(inner, outer):
+    def products(count, seed):
+        x, w, off = product([1] * count, inner, outer, seed=seed)
+        dy = torch.randn(count, outer, device=DEV, generator=gen(seed)).bfloat16()
+        want = (rs.expert_matmul(x, w, off), *rs.expert_matmul_grad(dy, x, w, off))
+        torch.cuda.synchronize()
+
+        def call(stream):
+            for _ in range(1500):
+                got = (rs.expert_matmul(x, w, off, stream=stream), *rs.expert_matmul_grad(dy, x, w, off, stream=stream))
+            stream.synchronize()
+            assert all(torch.equal(g, v) for g, v in zip(got, want))
+        return call
+
+    in_threads(products(8, 3), products(1024, 4))
