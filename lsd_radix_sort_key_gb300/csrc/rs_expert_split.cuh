@@ -200,6 +200,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (ok && elect_one()) mma_commit<false>(acc_full);
             __syncwarp();
         }
+        // as in k_product_tc: what was issued is done before anything it uses is given up
+        if (s || round) ok &= bar_wait_warp(empty + (s ? s : S::kStages) - 1, (s ? round : round - 1) & 1);
         if (!ok) *failed = 1;
     } else if (RAGGED_K && warp == 3) {
         uint32_t used = 0, phases = 0;  // slices so far; bit s: the next phase of tail[s]

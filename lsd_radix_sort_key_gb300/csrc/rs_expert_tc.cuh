@@ -441,6 +441,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (ok && elect_one()) mma_commit<PAIR>(acc_full + h);
             __syncwarp();
         }
+        // What was issued is done before anything it uses is given up, also when
+        // the epilogue's wait for it has run out.
+        if (s || round) ok &= bar_wait_warp(empty + (s ? s : S::kStages) - 1, (s ? round : round - 1) & 1);
         if (!ok) *failed = 1;
     } else if (RAGGED_K && warp == 3) {
         uint32_t used = 0, phases = 0;  // slices so far; bit s: the next phase of tail[s]
