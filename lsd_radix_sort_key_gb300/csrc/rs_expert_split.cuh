@@ -59,10 +59,11 @@ struct Share {
     uint32_t begin, end;
     __device__ __forceinline__ Share(const TcTile& t, uint32_t rank, uint32_t blocks)
     {
-        const uint32_t slices = (t.k_end - t.k0 + kTcDepth - 1) / kTcDepth;
+        const uint32_t slices = t.slices();
         begin = t.k0 + (uint32_t)((uint64_t)slices * rank / blocks) * kTcDepth;
         end = min(t.k0 + (uint32_t)((uint64_t)slices * (rank + 1) / blocks) * kTcDepth, t.k_end);
     }
+    __device__ __forceinline__ uint32_t slices() const { return (end - begin + kTcDepth - 1) / kTcDepth; }
 };
 
 // RAGGED_K and B_MN as in k_product_tc.
@@ -205,19 +206,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) *failed = 1;
     } else if (RAGGED_K && warp == 3) {
         uint32_t used = 0, phases = 0;  // slices so far; bit s: the next phase of tail[s]
+        uint32_t skipped = 0;           // of `used`, those since the last wait
         for (uint32_t tile = first_tile; tile < tiles; tile += tile_step) {
             const TcTile t = tc_tile<S::kBN, kTcRows, RAGGED_K>(p, g, tile);
             if (t.k0 >= t.k_end) continue;
             const Share share(t, rank, blocks);
             if (share.begin >= share.end) continue;
-            used += (share.end - share.begin + kTcDepth - 1) / kTcDepth;
+            used += share.slices();
+            skipped += share.slices();
             const uint32_t left = (share.end - share.begin) % kTcDepth;
             if (left == 0) continue;
             const uint32_t s = (used - 1) % S::kStages;
-            if (!bar_wait_warp(tail + s, phases >> s & 1)) {
+            if (!bar_wait_warp(tail + s, phases >> s & 1, skipped)) {
                 *failed = 1;
                 break;
             }
+            skipped = 0;
             phases ^= 1u << s;
             mend_slice<S::kStage>(ring + s * S::kStage, left);
             if (elect_one()) bar_arrive(full + s);
@@ -243,12 +247,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 continue;
             }
-            if (!bar_wait_warp(acc_full, n & 1) || !bar_wait_cluster_warp(part_empty, (n & 1) ^ 1)) {
+            const Share share(t, rank, blocks);
+            if (!bar_wait_warp(acc_full, n & 1, share.slices()) || !bar_wait_cluster_warp(part_empty, (n & 1) ^ 1)) {
                 *failed = 1;
                 break;
             }
             tc_fence_after();
-            const Share share(t, rank, blocks);
             if (quarter * 32 < rows) {
                 const uint32_t row = quarter * 32 + lane;
 #pragma unroll
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(acc_empty);
             if (lane < blocks) bar_arrive_cluster<true>(told_full);
-            if (!bar_wait_cluster_warp(part_full, n & 1)) {
+            if (!bar_wait_cluster_warp(part_full, n & 1, share.slices())) {
                 *failed = 1;
                 break;
             }

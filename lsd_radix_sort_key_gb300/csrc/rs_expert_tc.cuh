@@ -79,6 +79,7 @@ struct TcShape {
 // the reduction [k0, k_end).
 struct TcTile {
     uint32_t e, i0, i_end, j0, k0, k_end;
+    __device__ __forceinline__ uint32_t slices() const { return (k_end - k0 + kTcDepth - 1) / kTcDepth; }
 };
 
 template <int BN, uint32_t ROWS, bool RAGGED_K, typename T>
@@ -447,16 +448,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) *failed = 1;
     } else if (RAGGED_K && warp == 3) {
         uint32_t used = 0, phases = 0;  // slices so far; bit s: the next phase of tail[s]
+        uint32_t skipped = 0;           // of `used`, those since the last wait
         for (uint32_t tile = first_tile; tile < tiles; tile += tile_step) {
             const TcTile t = tc_tile<BN, S::kTileRows, RAGGED_K>(p, g, tile);
-            used += (t.k_end - t.k0 + kTcDepth - 1) / kTcDepth;
+            used += t.slices();
+            skipped += t.slices();
             const uint32_t left = (t.k_end - t.k0) % kTcDepth;
             if (left == 0) continue;
             const uint32_t s = (used - 1) % S::kStages;
-            if (!bar_wait_warp(tail + s, phases >> s & 1)) {
+            if (!bar_wait_warp(tail + s, phases >> s & 1, skipped)) {
                 *failed = 1;
                 break;
             }
+            skipped = 0;
             phases ^= 1u << s;
             mend_slice<S::kStage>(ring + s * S::kStage, left);
             if (elect_one()) {
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (some) {
                 fetch_residual(c0, add[0]);
                 if (!rehearsal) {
-                    if (!bar_wait_warp(acc_full + h, (n >> 1) & 1)) {
+                    if (!bar_wait_warp(acc_full + h, (n >> 1) & 1, t.slices())) {
                         *failed = 1;
                         break;
                     }

@@ -43,10 +43,12 @@ __device__ __forceinline__ void bar_arrive(uint64_t* bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// A wait gives up after this many SM clocks (about two seconds): far longer
-// than any wait of a working kernel, short enough that a call with a fault
-// still ends.
-constexpr long long kWaitClocks = 1ll << 32;
+// A wait gives up after this many SM clocks (about two seconds), short enough
+// that a call with a fault still ends, and far longer than a working kernel
+// waits for a copy, a free stage or another block.  A wait for a whole
+// reduction has kSliceClocks more (4 us) for each of the reduction's 64-deep
+// slices, which take 0.2 to 0.8 us: 2^30 rows in one tile take four seconds.
+constexpr long long kWaitClocks = 1ll << 32, kSliceClocks = 1 << 13;
 
 // The thread may sleep this long (ns) in one try.
 constexpr uint32_t kTryNs = 1000000;
@@ -62,18 +64,19 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity)
     return done != 0;
 }
 
-// Waits for phase `parity` of bar to complete; false if the time ran out.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity)
+// Waits for phase `parity` of bar to complete, which may take as long as
+// `slices` of a reduction; false if the time ran out.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, uint32_t slices = 0)
 {
     if (bar_try(bar, parity)) return true;
     const long long start = clock64();
-    while (clock64() - start < kWaitClocks)
+    while (clock64() - start < kWaitClocks + slices * kSliceClocks)
         if (bar_try(bar, parity)) return true;
     return false;
 }
 
 // The same for arrivals from the other block of a pair.
-__device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity, uint32_t slices = 0)
 {
     const long long start = clock64();
     do {
@@ -85,19 +88,19 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity)
             : "r"(smem_addr(bar)), "r"(parity), "r"(kTryNs)
             : "memory");
         if (done) return true;
-    } while (clock64() - start < kWaitClocks);
+    } while (clock64() - start < kWaitClocks + slices * kSliceClocks);
     return false;
 }
 
 // The same for a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t slices = 0)
 {
-    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity));
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, slices));
 }
 
-__device__ __forceinline__ bool bar_wait_cluster_warp(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool bar_wait_cluster_warp(uint64_t* bar, uint32_t parity, uint32_t slices = 0)
 {
-    return __all_sync(0xFFFFFFFFu, bar_wait_cluster(bar, parity));
+    return __all_sync(0xFFFFFFFFu, bar_wait_cluster(bar, parity, slices));
 }
 
 // This thread's ordinary writes before later accesses of the async proxy

@@ -1,6 +1,5 @@
-"""The expert operators on inputs as long as their interface takes: sorts whose
-blocks go through several tiles, reductions that last longer than any wait of a
-kernel's own, and element offsets past 32 bits."""
+"""The expert operators on inputs as long as their interface takes: reductions
+that last longer than any other wait of a kernel's own."""
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
@@ -11,7 +10,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
-from expert_util import DEV, gen, plain_order  # noqa: E402
+from expert_util import DEV, gen  # noqa: E402
 
 SMS = torch.cuda.get_device_properties(0).multi_processor_count
 
@@ -20,31 +19,6 @@ SMS = torch.cuda.get_device_properties(0).multi_processor_count
 def built():
     rs.build()
     rs.lib()
-
-
-# ------------------------------------------------------------------- sorts
-
-def check_sort(ids, count):
-    for name, got, want in zip(("order", "position", "offsets"), rs.expert_sort(ids, count), plain_order(ids, count)):
-        assert torch.equal(got.cpu(), want), name
-
-
-# a block has one tile of 8192 slots up to SMS * 8192 slots, several above
-@pytest.mark.parametrize("n", [SMS * 8192, SMS * 8192 + 1, 1_300_003, 5_000_011])
-@pytest.mark.parametrize("count", [7, 257, 511, 512, 1024])
-def test_sorts_of_several_tiles_per_block(n, count):
-    g = gen(n + count)
-    ids = torch.randint(0, count, (n,), device=DEV, generator=g)
-    ids[torch.rand(n, device=DEV, generator=g) < 0.1] = -1
-    check_sort(ids, count)
-
-
-@pytest.mark.parametrize("n", [SMS * 8192 + 1, 3_000_001])
-@pytest.mark.parametrize("count", [8, 1024])
-def test_sorts_of_several_tiles_one_expert_takes_all_or_none(n, count):
-    check_sort(torch.full((n,), count - 1, device=DEV, dtype=torch.int32), count)
-    check_sort(torch.full((n,), -1, device=DEV), count)
-    check_sort((n - 1 - torch.arange(n, device=DEV)) * count // n, count)
 
 
 # -------------------------------------------------------------- reductions
@@ -66,6 +40,10 @@ def test_a_long_reduction_runs_to_its_end():
     x[last + 5:] = float("nan")  # unused rows
     w = torch.zeros(count, 8, 8, dtype=torch.bfloat16, device=DEV)
     temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
     dw = rs.expert_matmul_grad(dy, x, w, off, bias=False, need_dx=False, temp=temp)[1]
+    end.record()
     assert rs.rs_expert_matmul_status(temp) == 0
+    assert begin.elapsed_time(end) > 2500  # ms: past the 2^32 clocks of the other waits
     assert torch.equal(dw.float(), want)
