@@ -82,9 +82,10 @@ struct Choice {
     int blocks;  // kSplit
 };
 
-// Clusters of `blocks` of the split kernel that the device holds at once.
-template <typename K>
-size_t resident_clusters(K kernel, int blocks, size_t smem)
+// Clusters of `blocks` of a split kernel that the device holds at once, with
+// shared memory for any number of experts.
+template <auto kernel>
+size_t resident_clusters(int blocks)
 {
     static std::atomic<int> known[kMaxDevices][4];
     int dev = 0;
@@ -95,14 +96,18 @@ size_t resident_clusters(K kernel, int blocks, size_t smem)
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)blocks);
         cfg.blockDim = dim3(kTcThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = SplitShape::smem(RS_EXPERTS_MAX);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)blocks;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (!allow_smem(kernel, smem) || cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess) return 0;
+        if (!allow_smem(kernel, cfg.dynamicSmemBytes)) return 0;
+        if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
         n.store(v, std::memory_order_relaxed);
     }
     return (size_t)v;
@@ -150,8 +155,8 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
                             args.cols > 128 ? down(2 * kTcRows) * by256 : 0, (owners + args.rows / kTcRows) * by128,
                             ceil_div(args.reduce, kTcDepth), (double)owners / (double)down(kTcRows),
                             (double)owners / (double)down(2 * kTcRows), sms, [&](int n) {
-                                return resident_clusters(k_product_split<T, false, false>, n,
-                                                         SplitShape::smem(RS_EXPERTS_MAX));
+                                return b.mn ? resident_clusters<k_product_split<T, false, true>>(n)
+                                            : resident_clusters<k_product_split<T, false, false>>(n);
                             });
     const bool narrow = c.form == Form::kNarrow || c.form == Form::kSplit, pair = c.form == Form::kPair;
     CUtensorMap ma, mb;
@@ -191,8 +196,7 @@ rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<
     const bool wide = args.cols > 128;
     const Choice c = choose(down * by128, wide ? down * by256 : 0, wide && args.out_rows > 128 ? down256 * by256 : 0,
                             down * by128, ceil_div(args.rows, args.experts * (size_t)kTcDepth), 0.0, 0.0, sms, [&](int n) {
-                                return resident_clusters(k_product_split<T, true, true>, n,
-                                                         SplitShape::smem(RS_EXPERTS_MAX));
+                                return resident_clusters<k_product_split<T, true, true>>(n);
                             });
     CUtensorMap ma, mb;
     const uint64_t da[2] = {args.out_rows, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
