@@ -115,7 +115,9 @@ rs_status rs_expert_combine_grad(rs_float_type type, const void* dout, size_t do
  * The experts' products.  x: rows x inner; w: one outer x inner matrix per
  * expert, element (e, n, k) at w[e*w_expert_stride + n*w_outer_stride +
  * k*w_inner_stride]; one of the last two strides is 1 (either layout of the
- * matrix runs at full speed) unless inner or outer is 1.  bias: outer
+ * matrix runs at full speed) unless inner or outer is 1, and all are below
+ * 2^40 bytes (the stride of a single expert, row or column is not used).
+ * Row strides are at most 2^32 elements everywhere.  bias: outer
  * values per expert, row stride bias_stride (0: one bias for every expert), or
  * NULL.  residual: rows x outer, or NULL.  num_experts == 1 with offsets
  * {0, rows} is the plain dense product.

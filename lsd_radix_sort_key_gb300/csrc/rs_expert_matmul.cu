@@ -459,7 +459,7 @@ rs_status check_common(const rs_expert_matmul_desc* d)
     return RS_OK;
 }
 
-// The last weight's element offset plus one, checked against 2^62 bytes.
+// The last weight's element offset plus one (below 2^61 bytes by check_weights).
 size_t weight_span(const rs_expert_matmul_desc* d)
 {
     return (size_t)(d->num_experts - 1) * d->w_expert_stride + (d->outer - 1) * d->w_outer_stride +
@@ -468,9 +468,13 @@ size_t weight_span(const rs_expert_matmul_desc* d)
 
 rs_status check_weights(const rs_expert_matmul_desc* d)
 {
-    const size_t most = (size_t)1 << 40, eb = type_bytes(d->type);
+    const size_t eb = type_bytes(d->type);
     if (!d->w || (uintptr_t)d->w % eb) return RS_ERR_INVALID_ARG;
-    if (d->w_expert_stride > most || d->w_outer_stride > most || d->w_inner_stride > most) return RS_ERR_INVALID_ARG;
+    // strides that are used: below 2^40 bytes, what a tensor map can hold
+    auto fits = [&](size_t count, size_t stride) { return count <= 1 || stride < ((size_t)1 << 40) / eb; };
+    if (!fits((size_t)d->num_experts, d->w_expert_stride) || !fits(d->outer, d->w_outer_stride) ||
+        !fits(d->inner, d->w_inner_stride))
+        return RS_ERR_INVALID_ARG;
     if (d->w_inner_stride != 1 && d->w_outer_stride != 1 && d->inner != 1 && d->outer != 1) return RS_ERR_INVALID_ARG;
     return RS_OK;
 }

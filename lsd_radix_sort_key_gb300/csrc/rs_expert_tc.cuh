@@ -589,9 +589,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     wait_prior_grid();
 }
 
-// Launches one product; RS_ERR_UNSUPPORTED if the operands cannot be copied
-// this way (alignment, strides), so that the caller takes the general kernel.
-// Instantiated in rs_expert_tc_<type>.cu.
+// Launches one product.  Bases and strides are multiples of 16 bytes, strides
+// below 2^40 bytes (the caller's checks and copies see to it); RS_ERR_CUDA if
+// the driver makes no tensor map.  Instantiated in rs_expert_tc_<type>.cu.
 template <typename T>
 struct TcOperand {
     const T* p;

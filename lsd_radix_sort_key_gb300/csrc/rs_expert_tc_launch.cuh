@@ -166,7 +166,7 @@ rs_status tc_ragged_rows(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<T>
                             experts > 1 ? (uint64_t)b.expert_stride * 2 : (uint64_t)b.row_stride * 2};
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, narrow ? 16 : kTcRows) ||
         !rstc::encode_map(&mb, kBf16, 3, b.p, db, sb, b.mn ? 64 : narrow || pair ? 128 : 256))
-        return RS_ERR_UNSUPPORTED;
+        return RS_ERR_CUDA;
     const size_t tiles = max_tiles(args.rows, args.experts, pair ? 2 * kTcRows : kTcRows) * (narrow ? by128 : by256);
     switch (c.form) {
     case Form::kSplit:
@@ -202,7 +202,7 @@ rs_status tc_ragged_reduce(const TcOperand<T>& a, const TcOperand<T>& b, TcArgs<
     const uint64_t da[2] = {args.out_rows, args.rows}, sa[1] = {(uint64_t)a.row_stride * 2};
     const uint64_t db[2] = {args.cols, args.rows}, sb[1] = {(uint64_t)b.row_stride * 2};
     if (!rstc::encode_map(&ma, kBf16, 2, a.p, da, sa, 64) || !rstc::encode_map(&mb, kBf16, 2, b.p, db, sb, 64))
-        return RS_ERR_UNSUPPORTED;
+        return RS_ERR_CUDA;
     switch (c.form) {
     case Form::kSplit: return split_launch<T, true, true>(ma, mb, args, down * by128, c.blocks, sms, stream);
     case Form::kPair: return tc_launch<T, 256, true, true, true>(ma, mb, args, down256 * by256, stream);

@@ -6,6 +6,7 @@ import subprocess
 
 import pytest
 
+import lsd_radix_sort_key_gb300 as rs
 from lsd_radix_sort_key_gb300 import _build, experts
 
 torch = pytest.importorskip("torch")
@@ -35,3 +36,22 @@ def test_each_split_kernel_has_a_count_of_its_own():
     kernels = set(re.findall(r"rsx::k_product_split<(__\w+, \w+, \w+)>\(CUtensorMap_st, CUtensorMap_st", names))
     counts = set(re.findall(r"resident_clusters<.*k_product_split<(__\w+, \w+, \w+)>.*::known$", names, re.M))
     assert len(kernels) == 6 and counts == kernels
+
+
+F = 1 << 40  # 256-byte aligned addresses that are never dereferenced
+
+
+def desc(**kw):
+    d = rs.ExpertMatmulDesc(2, 3, 4, 100, 64, 128, F, 2 * F, 64, 3 * F, 64 * 128, 64, 1, 4 * F, 128, 5 * F, 128,
+                            6 * F, 128, 7 * F, 128, 8 * F, 64, 9 * F, 10 * F, 11 * F, 1 << 62, None)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+@pytest.mark.parametrize("kw", [dict(type=t, **{name: (1 << 40) // size}) for t, size in ((0, 4), (1, 2), (2, 2))
+                                for name in ("w_expert_stride", "w_outer_stride")] +
+                         [dict(w_outer_stride=1, w_inner_stride=1 << 39), dict(w_outer_stride=1 << 63)])
+def test_weight_strides_past_a_tensor_map_are_refused_first(kw):
+    assert rs.rs_expert_matmul(desc(**kw)) == 1
+    assert rs.rs_expert_matmul_grad(desc(**kw)) == 1
