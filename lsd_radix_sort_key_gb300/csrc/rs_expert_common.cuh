@@ -279,8 +279,8 @@ inline size_t span_bytes(size_t rows, size_t width, size_t stride, size_t elem)
     return rows == 0 || width == 0 ? 0 : ((rows - 1) * stride + width) * elem;
 }
 
-// A matrix of rows: base aligned to its element; strides no longer than 2^40
-// elements, so that no byte offset inside it passes 2^63.
+// A matrix of rows: base aligned to its element; strides no longer than 2^32
+// elements, so that with at most 2^30 rows span_bytes stays below 2^64.
 inline bool valid_rows(const void* p, size_t elem, size_t width, size_t stride, bool may_broadcast)
 {
     if (!p || (uintptr_t)p % elem) return false;
@@ -291,8 +291,8 @@ inline bool valid_rows(const void* p, size_t elem, size_t width, size_t stride, 
 inline bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes)
 {
     if (!a || !b || abytes == 0 || bbytes == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + bbytes && b0 < a0 + abytes;
+    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;  // (an end may pass 2^64: differences, not sums)
+    return a0 < b0 ? b0 - a0 < abytes : a0 - b0 < bbytes;
 }
 
 struct Range {

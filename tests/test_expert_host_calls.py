@@ -55,3 +55,11 @@ def desc(**kw):
 def test_weight_strides_past_a_tensor_map_are_refused_first(kw):
     assert rs.rs_expert_matmul(desc(**kw)) == 1
     assert rs.rs_expert_matmul_grad(desc(**kw)) == 1
+
+
+def test_overlap_is_seen_however_long_a_matrix_is():
+    # x spans all but 2^34 of the 2^64 bytes: its end lies past the last address
+    long = dict(type=0, rows=1 << 30, x_stride=1 << 32)
+    for name, at in (("y", 6), ("pre", 7), ("temp", 11)):
+        assert rs.rs_expert_matmul(desc(**long, **{name: at * F})) == 3
+    assert rs.rs_expert_matmul_grad(desc(**long)) == 3
