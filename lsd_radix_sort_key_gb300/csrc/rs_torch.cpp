@@ -95,7 +95,8 @@ bool plan(const at::Tensor& position, const at::Tensor& offsets, const at::Tenso
 {
     if (position.scalar_type() != at::kInt || offsets.scalar_type() != at::kInt || position.dim() != 2 ||
         offsets.dim() != 1 || position.device() != like.device() || offsets.device() != like.device() ||
-        !position.is_contiguous() || !offsets.is_contiguous() || position.size(1) < 1 || offsets.size(0) < 2)
+        !position.is_contiguous() || !offsets.is_contiguous() || position.size(1) < 1 ||
+        position.size(1) > RS_EXPERT_SLOTS_MAX || offsets.size(0) < 2)
         return false;
     *p = Plan{static_cast<const int32_t*>(position.const_data_ptr()),
               static_cast<const int32_t*>(offsets.const_data_ptr()) + offsets.size(0) - 1, position.size(0),

@@ -57,6 +57,7 @@ def _torch():
 FLOAT_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 EXPERTS_MAX = 1024  # RS_EXPERTS_MAX
+SLOTS_MAX = 1 << 30  # RS_EXPERT_SLOTS_MAX
 
 FTYPES = {}  # torch dtype -> rs_float_type
 _SIZE_ERROR = ctypes.c_size_t(-1).value
@@ -200,6 +201,8 @@ def _plan(position, offsets, device):
     tokens, slots = position.shape
     if slots < 1:
         raise ValueError("position: shape [tokens, slots] wanted")
+    if slots > SLOTS_MAX:  # C's int would hold its low 32 bits
+        _check(1, "position")
     edges = offsets.shape[0]
     if edges < 2:
         raise ValueError("offsets: shape [num_experts + 1] wanted")
@@ -287,6 +290,8 @@ def expert_sort(ids, num_experts: int, *, stream=None):
 
 def _sort(ids, num_experts, dev, s):
     n, i32, h = ids.numel(), torch.int32, _rs()
+    if not 1 <= num_experts <= EXPERTS_MAX:  # here, as C's int would hold its low 32 bits
+        _check(1, "rs_expert_sort")
     tb = h.rs_expert_sort_temp_bytes(n, num_experts)
     if tb == _SIZE_ERROR:
         _check(1, "rs_expert_sort")

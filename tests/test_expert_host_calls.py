@@ -1,5 +1,6 @@
 """What the Python forms of the expert operators check themselves, as far as it
 needs no GPU."""
+import os
 import re
 import shutil
 import subprocess
@@ -63,3 +64,13 @@ def test_overlap_is_seen_however_long_a_matrix_is():
     for name, at in (("y", 6), ("pre", 7), ("temp", 11)):
         assert rs.rs_expert_matmul(desc(**long, **{name: at * F})) == 3
     assert rs.rs_expert_matmul_grad(desc(**long)) == 3
+
+
+def test_more_slots_than_an_int_holds_are_refused():
+    # 2^32 + 1 would count as 1
+    offsets = torch.empty(3, dtype=torch.int32, device="meta")
+    with pytest.raises(rs.RadixSortError):
+        experts._plan(torch.empty(1, (1 << 32) + 1, dtype=torch.int32, device="meta"), offsets, offsets.device)
+    assert experts._plan(torch.empty(2, 5, dtype=torch.int32, device="meta"), offsets, offsets.device)[:2] == (2, 5)
+    text = open(os.path.join(_build.INCLUDE, "rs_experts.h")).read()
+    assert int(re.search(r"#define RS_EXPERT_SLOTS_MAX (\d+)u", text).group(1)) == experts.SLOTS_MAX

@@ -1,6 +1,6 @@
-"""The expert operators' calls at their edges: the caller's scratch, flags
-that are not bools, layouts that only the C interface can name, and calls from
-several host threads."""
+"""The expert operators' calls at their edges: the caller's scratch, flags that
+are not bools, numbers past 32 bits, layouts that only the C interface can name,
+and calls from several host threads."""
 import threading
 
 import pytest
@@ -111,6 +111,26 @@ def test_a_flag_without_a_truth_is_refused(way):
     dy = torch.randn(71, 96, device=DEV).bfloat16()
     with pytest.raises(RuntimeError):  # torch's own: a tensor of many values is neither
         rs.expert_matmul_grad(dy, x, w, off, bias=torch.zeros(2, 96, device=DEV))
+
+
+# ----------------------------------------------------------------- numbers
+
+def test_numbers_past_32_bits_are_refused(way):
+    # not taken by their low 32 bits: 2^32 + 1 is not 1
+    many = (1 << 32) + 1
+    ids = torch.zeros(6, dtype=torch.int64, device=DEV)
+    for count in (many, 1 << 32, -(1 << 32) + 1, 0, 1025):
+        with pytest.raises(rs.RadixSortError):
+            rs.expert_sort(ids, count)
+    position = torch.empty(1, many, dtype=torch.int32, device=DEV)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    one = torch.zeros(1, 1, dtype=torch.float16, device=DEV)
+    for call in (lambda: rs.expert_dispatch(one, position, off),
+                 lambda: rs.expert_dispatch_grad(one.expand(many, 1), position, off),
+                 lambda: rs.expert_combine(one.expand(many, 1), one.expand(1, many), position, off),
+                 lambda: rs.expert_combine_grad(one, one.expand(many, 1), one.expand(1, many), position, off)):
+        with pytest.raises(rs.RadixSortError):
+            call()
 
 
 # ------------------------------------------ layouts of the C interface alone
