@@ -4,7 +4,8 @@ One translation unit per key type plus the C-ABI unit, compiled in parallel
 with nvcc, then linked into a shared library with the CUDA runtime linked
 statically.  Beside it, csrc/rs_torch.cpp becomes a CPython extension for the
 installed torch (the expert operators' calls without the interpreter's cost;
-skipped where torch has no CUDA).  Nothing here runs at import time of the
+skipped where torch has no CUDA, and with a warning where it does not build:
+the calls then go through Python).  Nothing here runs at import time of the
 package except the check that the library exists.
 """
 from __future__ import annotations
@@ -17,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -46,11 +48,16 @@ def torch_dir() -> str | None:
 
 
 def torch_ext() -> str | None:
-    """Path of the extension for the installed torch (built or not)."""
-    return os.path.join(LIBDIR, f"rs_torch_{importlib.metadata.version('torch')}.so") if torch_dir() else None
+    """Path of the extension for this Python and the installed torch (built or not)."""
+    if not torch_dir():
+        return None
+    return os.path.join(LIBDIR, f"rs_torch_{importlib.metadata.version('torch')}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def build_torch_ext(force: bool = False) -> str | None:
+    """Build the extension if a source is newer than it; its path, or None
+    where there is none.  The library does not need it, so what keeps it from
+    being built is a warning."""
     out, src = torch_ext(), os.path.join(CSRC, "rs_torch.cpp")
     if out is None:
         return None
@@ -64,9 +71,17 @@ def build_torch_ext(force: bool = False) -> str | None:
            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", cuda, "-I",
            sysconfig.get_paths()["include"], "-I", INCLUDE, src, "-L", os.path.join(root, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = "" if r.returncode == 0 else f"{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        why = str(e)
+    if why:
+        if os.path.exists(out):  # of older sources: its structures may not be the library's
+            os.remove(out)
+        warnings.warn(f"the expert operators' extension was not built, their calls go through Python: g++ failed on "
+                      f"{src}:\n{why}", RuntimeWarning, stacklevel=2)
+        return None
     os.replace(tmp, out)
     return out
 

@@ -4,6 +4,7 @@ import os
 import re
 import shutil
 import subprocess
+import sysconfig
 
 import pytest
 
@@ -74,3 +75,27 @@ def test_more_slots_than_an_int_holds_are_refused():
     assert experts._plan(torch.empty(2, 5, dtype=torch.int32, device="meta"), offsets, offsets.device)[:2] == (2, 5)
     text = open(os.path.join(_build.INCLUDE, "rs_experts.h")).read()
     assert int(re.search(r"#define RS_EXPERT_SLOTS_MAX (\d+)u", text).group(1)) == experts.SLOTS_MAX
+
+
+@pytest.mark.skipif(not _build.torch_dir(), reason="torch without CUDA has no extension")
+@pytest.mark.parametrize("fails", ["headers", "no compiler"])
+def test_the_library_is_built_where_the_extension_is_not(tmp_path, monkeypatch, fails):
+    monkeypatch.setattr(_build, "LIBDIR", str(tmp_path))
+    assert sysconfig.get_config_var("SOABI") in _build.torch_ext()
+    run = subprocess.run
+
+    def broken(cmd, **kw):
+        if cmd[0] != "g++":
+            return run(cmd, **kw)
+        if fails == "no compiler":
+            raise FileNotFoundError("g++")
+        return subprocess.CompletedProcess(cmd, 1, "", "no such header")
+
+    with open(_build.torch_ext(), "w") as f:
+        f.write("of older sources")
+    monkeypatch.setattr(_build.subprocess, "run", broken)
+    monkeypatch.setattr(_build, "_stale", lambda: False)  # librs.so as it is
+    with pytest.warns(RuntimeWarning, match="go through Python"):
+        os.utime(_build.torch_ext(), (0, 0))
+        assert _build.build() == _build.LIB
+    assert not os.path.exists(_build.torch_ext())  # not the older one either
