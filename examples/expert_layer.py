@@ -43,8 +43,10 @@ class Matmul(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         x, w, offsets, pre = ctx.saved_tensors
-        dx, dw, dbias = rs.expert_matmul_grad(grad.contiguous(), x, w, offsets, pre=pre, activation=ctx.activation)
-        return dx, dw, dbias, None, None
+        dx, dw, dbias = ctx.needs_input_grad[:3]  # the ones wanted
+        grads = rs.expert_matmul_grad(grad.contiguous(), x, w, offsets, pre=pre, activation=ctx.activation, need_dx=dx,
+                                      need_dw=dw, bias=dbias)
+        return (*grads, None, None)
 
 
 class Combine(torch.autograd.Function):
