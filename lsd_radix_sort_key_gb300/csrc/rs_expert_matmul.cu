@@ -30,13 +30,18 @@ namespace {
 
 using namespace rsx;
 
+// SMs, for choices that temp's size or the order of additions go by: those are
+// the descriptor's alone, on whatever device the call is made.
+constexpr size_t kSms = 152;
+
 // -------------------------------------------- products by multiply-adds
 
-// Element (i, k) of A in range e is a[e*a_e + i*a_i + k*a_k]; likewise B(j, k).
+// Element (i, k) of A is a[i*a_i + k*a_k]; element (j, k) of B in range e is
+// b[e*b_e + j*b_j + k*b_k].
 template <typename T>
 struct AnyArgs {
     const T* a;
-    size_t a_e, a_i, a_k;
+    size_t a_i, a_k;
     const T* b;
     size_t b_e, b_j, b_k;
     T* d;
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
         k_end = e < p.experts ? p.reduce : 0;
     }
     const uint32_t j0 = blockIdx.y * TILE, tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const T* a = p.a + e * p.a_e;
+    const T* a = p.a;
     const T* b = p.b + (e < p.experts ? e * p.b_e : 0);
     // what this thread fetches: neighbouring threads read neighbouring elements
     const bool a_rows = p.a_k != 1, b_rows = p.b_k != 1;
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_product_any(AnyArgs<T> p)
 // of 2048 x 1024: 382 us against 268).
 bool any_wide(size_t rows, size_t cols, size_t experts)
 {
-    return rows >= 64 && experts * ceil_div(rows, 64) * ceil_div(cols, 64) > 2 * 152;
+    return rows >= 64 && experts * ceil_div(rows, 64) * ceil_div(cols, 64) > 2 * kSms;
 }
 
 template <typename T, int ACT>
@@ -281,9 +286,9 @@ constexpr int kDzVecs = N > 1 ? 2 : 1;
 // warp's rows one after the other are what lasts then (gradients of silu in
 // bf16, always 128 rows -> so: 3001 rows, 8 experts of 1000 x 1160 55.6 -> 39.4 us,
 // 2048, 16 of 1024 x 2048 67.7 -> 49.3, 4096, 8 of 2048 x 2048 87.7 -> 72.7).
-// Two for each of 152 SMs; four cost dbias longer sums and gain nothing (16384 x
-// 2048 bf16, silu, sums only: 36.9 us with 304, 38.4 with 608, 42.6 with 1216).
-constexpr size_t kDzBlocks = 304;
+// Two per SM; four cost dbias longer sums and gain nothing (16384 x 2048 bf16,
+// silu, sums only: 36.9 us with 304, 38.4 with 608, 42.6 with 1216).
+constexpr size_t kDzBlocks = 2 * kSms;
 
 size_t dz_tile_rows(size_t rows, size_t cols, size_t elem_bytes)
 {
