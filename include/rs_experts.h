@@ -130,7 +130,8 @@ rs_status rs_expert_combine_grad(rs_float_type type, const void* dout, size_t do
  * inner), dw (contiguous num_experts x outer x inner) and dbias (contiguous
  * num_experts x outer) that are not NULL, each in `type`.  dz = dy * act'(pre)
  * is formed in float32 and rounded to `type` as the products' operand, as x
- * and w are; dbias sums the unrounded values.
+ * and w are (so in binary16 a dz up to 2^-25 counts as 0 and one of 65520 or
+ * more as infinite); dbias sums the unrounded values.
  *
  * temp: 256-byte aligned scratch of at least rs_expert_matmul_temp_bytes /
  * rs_expert_matmul_grad_temp_bytes bytes, computed from the same descriptor;

@@ -30,8 +30,8 @@ namespace {
 
 using namespace rsx;
 
-// SMs, for choices that temp's size or the order of additions go by: those are
-// the descriptor's alone, on whatever device the call is made.
+// SMs, for the sizes of tiles below.  Not asked of the device: temp's size and the
+// order of dbias's additions go by them, and those are the descriptor's alone.
 constexpr size_t kSms = 152;
 
 // -------------------------------------------- products by multiply-adds
@@ -300,7 +300,11 @@ size_t dz_tile_rows(size_t rows, size_t cols, size_t elem_bytes)
 
 // One block takes a tile of at most tile_rows rows of one expert and kDzVecs *
 // 32 vectors of columns; each warp every eighth row.  part (if given) receives
-// the tile's column sums, [row tile][cols].
+// the tile's column sums, [row tile][cols], of the values before rounding.  dz
+// itself is rounded to T, the type the tensor cores take: that costs dx and dw a
+// factor of about sqrt 2 in error (bf16 2.3e-3 against 1.7e-3), and in binary16
+// a |dy act'| up to 2^-25 becomes 0 and one of 65520 or more infinite, as in any
+// dz that is stored between two calls.
 template <typename T, int ACT, int N>
 __global__ void __launch_bounds__(kDzThreads) k_act_grad(const T* __restrict__ dy, size_t dy_i,
                                                          const T* __restrict__ pre, size_t pre_i, T* __restrict__ dz,

@@ -27,7 +27,10 @@
 // written in runs and not in single words (4.6 us).
 //
 // The bytes are few (12 or 16 per slot), so the time is launches and
-// dependent round trips: see the figures at the entry point.
+// dependent round trips.  On the device alone (captured graph, int64 numbers):
+// 512 slots of 128 experts 3.1 us, 30018 of 160 8.1, 65536 of 64 9.0, 2^20 of
+// 256 17.7, of which 3.6 are the numbers' way from device memory (14.1 when the
+// same input is sorted again).
 #include <cooperative_groups.h>
 
 #include "rs_expert_common.cuh"

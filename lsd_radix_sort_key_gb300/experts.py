@@ -13,7 +13,9 @@ and the ``_grad`` functions give its gradients.  Functions named as in C
 (``rs_expert_*``) take torch tensors or raw addresses and return the status;
 the others check their tensors, allocate outputs and scratch with torch,
 enqueue on ``stream`` (default: the current stream), never synchronise, and
-raise on a refused call.
+raise on a refused call.  They compute values only: what they return is not
+part of autograd's graph, whatever their inputs require
+(``examples/expert_layer.py`` has autograd Functions made of them).
 """
 from __future__ import annotations
 
