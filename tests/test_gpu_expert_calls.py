@@ -1,6 +1,6 @@
 """The expert operators' calls at their edges: the caller's scratch, flags that
 are not bools, numbers past 32 bits, layouts that only the C interface can name,
-and calls from several host threads."""
+calls from several host threads, and waits of a gradient that run out."""
 import threading
 
 import pytest
@@ -229,3 +229,29 @@ def test_products_of_two_threads(inner, outer):
         return call
 
     in_threads(products(8, 3), products(1024, 4))
+
+
+# ------------------------------------------------------ waits that run out
+
+# dw cut over a cluster, by tiles of one block (128 and 256 columns), by pairs; then dx
+@pytest.mark.parametrize("which,rows,inner,outer", [("dw", 2000, 128, 128), ("dw", 250, 512, 256), ("dw", 1000, 4096, 384),
+                                                    ("dw", 8000, 4096, 384), ("dx", 70, 512, 1024), ("dx", 6000, 1024, 1024)])
+def test_a_wait_that_runs_out_in_a_gradient_is_reported(which, rows, inner, outer):
+    x, w, off = product([rows // 2 + 5, rows // 2 - 5], inner, outer)  # both end in a partial slice
+    dy = torch.randn(rows, outer, device=DEV, generator=gen(6)).bfloat16()
+    temp = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    want = rs.expert_matmul_grad(dy, x, w, off, bias=False, need_dx=which == "dx", need_dw=which == "dw", temp=temp)
+    want = want[0] if which == "dx" else want[1]
+    assert rs.rs_expert_matmul_status(temp) == 0
+    out = torch.empty_like(want)
+    d = rs.ExpertMatmulDesc(2, 0, 2, rows, inner, outer, off.data_ptr(), x.data_ptr(), inner, w.data_ptr(),
+                            inner * outer, inner, 1)
+    d.y, d.y_stride, d.dx_stride = dy.data_ptr(), outer, inner
+    setattr(d, which, out.data_ptr())
+    d.temp, d.temp_bytes, d.stream = temp.data_ptr(), temp.numel(), torch.cuda.current_stream().cuda_stream
+    d.stall_tile = 2
+    assert rs.rs_expert_matmul_grad(d) == 0
+    assert rs.rs_expert_matmul_status(temp) == 5  # RS_ERR_DEVICE_TIMEOUT
+    d.stall_tile = 0  # the next call works
+    assert rs.rs_expert_matmul_grad(d) == 0
+    assert rs.rs_expert_matmul_status(temp) == 0 and torch.equal(out, want)
