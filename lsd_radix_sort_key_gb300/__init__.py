@@ -9,7 +9,8 @@ Low-level functions carry the C names (``rs_sort_keys_u32``, ``rs_sort_pairs_f32
 ``rs_temp_bytes``, ``rs_sort``, ...) and accept torch tensors or raw integer
 addresses for pointers.  ``sort()`` is the convenience wrapper that allocates
 outputs and temp with torch.  The expert operators (include/rs_experts.h) are
-bound in ``experts.py`` and re-exported here.
+bound in ``experts.py``, the expert block in 8 bits and the norms around it
+(include/rs_expert_block.h) in ``expert_block.py``, and re-exported here.
 """
 from __future__ import annotations
 
@@ -83,6 +84,14 @@ for _t in ("rs_expert_matmul", "rs_expert_matmul_grad"):
     SIGNATURES[_t] = (_i, [_vp])
     SIGNATURES[_t + "_temp_bytes"] = (_sz, [_vp])
 SIGNATURES["rs_expert_matmul_status"] = (_i, [_vp, _vp])
+SIGNATURES["rs_expert_quantize"] = (_i, [_i, _vp, _sz, _sz, _sz, _vp, _sz, _vp, _sz, _vp])
+SIGNATURES["rs_expert_dispatch_quantized"] = (_i, [_i, _vp, _sz, _vp, _vp, _sz, _i, _sz, _vp, _sz, _vp, _sz, _vp])
+SIGNATURES["rs_expert_quantize_weights"] = (_i, [_i, _vp, _sz, _sz, _sz, _i, _sz, _sz, _vp, _sz, _vp, _vp])
+SIGNATURES["rs_expert_matmul_quantized_temp_bytes"] = (_sz, [_vp])
+SIGNATURES["rs_expert_matmul_quantized"] = (_i, [_vp])
+SIGNATURES["rs_expert_norm"] = (_i, [_vp])
+SIGNATURES["rs_expert_norm_grad_temp_bytes"] = (_sz, [_vp])
+SIGNATURES["rs_expert_norm_grad"] = (_i, [_vp])
 SIGNATURES["rs_lbvh_build"] = (_i, [_vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 LBVH_LEAF = 0x80000000
 NOALLOC_MAX_N = 1 << 22
@@ -369,3 +378,10 @@ from .experts import (ACTIVATIONS, EXPERTS_MAX, FLOAT_TYPES, ExpertMatmulDesc, e
                       rs_expert_dispatch, rs_expert_matmul, rs_expert_matmul_grad,
                       rs_expert_matmul_grad_temp_bytes, rs_expert_matmul_status, rs_expert_matmul_temp_bytes,
                       rs_expert_sort, rs_expert_sort_temp_bytes)
+# An expert block in 8 bits: quantised rows and weights, their products, and the norms around it.
+from .expert_block import (NORM_WIDTH_MAX, QUANT_BLOCK, ExpertMatmulQuantizedDesc, ExpertNormDesc,  # noqa: E402
+                           expert_dispatch_quantized, expert_matmul_quantized, expert_norm, expert_norm_grad,
+                           expert_quantize, expert_quantize_weights, rs_expert_dispatch_quantized,
+                           rs_expert_matmul_quantized, rs_expert_matmul_quantized_temp_bytes, rs_expert_norm,
+                           rs_expert_norm_grad, rs_expert_norm_grad_temp_bytes, rs_expert_quantize,
+                           rs_expert_quantize_weights)

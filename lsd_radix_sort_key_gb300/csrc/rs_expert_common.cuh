@@ -231,12 +231,12 @@ bool allow_smem(K kernel, size_t most)
 }
 
 template <typename... P, typename... A>
-rs_status launch_kernel(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+rs_status launch_kernel(void (*kernel)(P...), dim3 grid, dim3 threads, size_t smem, cudaStream_t stream, int cluster,
                         bool dependent, const A&... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -1,0 +1,487 @@
+// rs_expert_f8.cuh -- the experts' products of rows and weights in 8 bits with
+// block scales, on the tensor cores (definitions in rs_expert_block.h).
+//
+// D = A B^T, tiles of D per persistent block (128 x 128) or pair of blocks (PAIR:
+// 256 x 256, a cluster of two on neighbouring SMs).  Scales are powers of two,
+// which tcgen05.mma.kind::mxf8f6f4 applies itself to every 32 products that it
+// adds, exactly, so the sums stay in one float32 accumulator in tensor memory
+// and nothing is added up outside the tensor pipe.  Warp 0 copies 128-deep
+// slices of A and B, one scale block each, into a ring of shared-memory stages
+// (TMA, 128-byte swizzle); warp 3 gathers the scales of four slices at a time,
+// one 32-bit word per row, into a ring of its own; warp 1 has them copied to
+// tensor memory and issues the products; 8 epilogue warps, each with 32 rows of
+// 128 columns, read finished accumulators, apply the epilogue and store.
+//
+// Tensor memory (512 columns): two accumulators and two sets of scales.  A
+// pair's accumulators are 256 columns each and there is room for 480: they
+// overlap by 32 columns, which the epilogue reads first (`early`).
+#pragma once
+
+#include "rs_expert_e4m3.cuh"
+#include "rs_expert_tc.cuh"
+
+namespace rsx {
+
+constexpr int kF8Depth = 128;  // reduction elements per stage: one swizzled row of 128 bytes, one scale block
+constexpr int kF8EpilogueWarps = 8;
+constexpr int kF8Threads = 32 * (kTcFirstEpilogueWarp + kF8EpilogueWarps);
+
+template <typename T>
+struct F8Args {
+    const int32_t* offsets;
+    uint32_t experts, rows;
+    uint32_t cols;    // of D
+    uint32_t reduce;  // the reduction's length
+    int act;          // rs_activation
+    const uint8_t* a_scales;
+    size_t a_scales_i;
+    const uint8_t* b_scales;  // [experts][blocks of cols][blocks of reduce]
+    const T* bias;
+    size_t bias_e;
+    const T* residual;
+    size_t residual_i;
+    T* d;
+    size_t d_i;
+    uint8_t* q;  // or D quantised
+    size_t q_i;
+    uint8_t* q_scales;
+    size_t q_scales_i;
+    T* pre;
+    size_t pre_i;
+    uint32_t* status;  // as in TcArgs
+    uint32_t status_words;
+    uint32_t stall;    // testing hook: tile stall - 1 is never copied
+};
+
+template <bool PAIR>
+struct F8Shape {
+    static constexpr uint32_t kCols = PAIR ? 256 : 128, kRows = PAIR ? 2 * kTcRows : kTcRows;  // of a tile
+    static constexpr uint32_t kA = kTcRows * kF8Depth, kB = 128 * kF8Depth, kStage = kA + kB;   // of a block
+    static constexpr int kStages = 6;
+    static constexpr uint32_t kScales = 512 + kCols * 4;  // of four slices
+    static constexpr int kScaleStages = 4;
+    static constexpr uint32_t kStaging = 32 * 32;  // per epilogue warp: 32 rows of 16 elements
+    static constexpr uint32_t kOverlap = PAIR ? 32 : 0;
+    static constexpr uint32_t kAccStep = kCols - kOverlap;  // columns from one accumulator to the other
+    static constexpr uint32_t kScaleCols = PAIR ? 480 : 256, kScaleStep = 16;
+    static constexpr size_t smem(size_t experts)
+    {
+        return 1024 + (size_t)kStages * kStage + kScaleStages * kScales + kF8EpilogueWarps * kStaging +
+               (2 * kStages + 2 * kScaleStages + 6) * 8 + 16 + Groups::words(experts) * 4;
+    }
+};
+
+// Bytes [4 q, 4 q + 4) of a row of `n` scales; those past its end count as one.
+__device__ __forceinline__ uint32_t scales_word(const uint8_t* row, uint32_t q, uint32_t n, bool words)
+{
+    if (words && 4 * q + 4 <= n) return __ldg(reinterpret_cast<const uint32_t*>(row) + q);
+    uint32_t w = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) w |= (4 * q + i < n ? (uint32_t)__ldg(row + 4 * q + i) : kScaleOne) << 8 * i;
+    return w;
+}
+
+// This lane's row of 128 columns, from j0 on, rounded to 8 bits and stored with
+// its scale; all lanes of the warp.
+template <typename T>
+__device__ __forceinline__ void store_quantized(uint32_t (&z)[8][16], const F8Args<T>& p, uint32_t i, bool live, uint32_t j0)
+{
+    const uint32_t left = p.cols - j0;
+    uint32_t most = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < 128; ++c) {
+        if (c >= left) z[c / 16][c % 16] = 0;
+        most = max(most, z[c / 16][c % 16] & 0x7FFFFFFFu);
+    }
+    if (most >= kNotFinite) {
+        most = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < 128; ++c) {
+            const float f = __uint_as_float(z[c / 16][c % 16]);
+            most = max(most, magnitude(f) < kNotFinite ? magnitude(f) : 0u);
+            z[c / 16][c % 16] = __float_as_uint(finite_or_nan(f));
+        }
+    }
+    const uint32_t byte = scale_byte(most);
+    const float inverse = scale_inverse(byte);
+    if (!live) return;
+    uint8_t* to = p.q + i * p.q_i + j0;
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = to_e4m3x4(__uint_as_float(z[c][4 * k]) * inverse, __uint_as_float(z[c][4 * k + 1]) * inverse,
+                             __uint_as_float(z[c][4 * k + 2]) * inverse, __uint_as_float(z[c][4 * k + 3]) * inverse);
+        if (c * 16 < left) reinterpret_cast<uint4*>(to)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    p.q_scales[i * p.q_scales_i + j0 / RS_QUANT_BLOCK] = (uint8_t)byte;
+}
+
+// A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
+// have the reduction index adjacent.  QUANT: D leaves in 8 bits.
+template <typename T, bool PAIR, bool QUANT>
+__global__ void __launch_bounds__(kF8Threads, 1)
+    k_product_f8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, F8Args<T> p)
+{
+    using namespace rstc;
+    using S = F8Shape<PAIR>;
+    constexpr uint32_t BN = S::kCols;
+    extern __shared__ unsigned char raw[];
+    unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
+    unsigned char* scales = ring + S::kStages * S::kStage;
+    unsigned char* staging = scales + S::kScaleStages * S::kScales;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kF8EpilogueWarps * S::kStaging);
+    uint64_t* empty = full + S::kStages;
+    uint64_t* scales_full = empty + S::kStages;
+    uint64_t* scales_empty = scales_full + S::kScaleStages;
+    uint64_t* acc_full = scales_empty + S::kScaleStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* early = acc_empty + 2;  // what the next accumulator overlaps has been read
+    uint32_t* slot = reinterpret_cast<uint32_t*>(early + 2);
+    uint32_t* failed = slot + 1;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = PAIR ? cluster_rank() : 0, blocks = PAIR ? 2 : 1;
+    const uint32_t first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
+    // narrow: the two groups of four epilogue warps take turns; pair: half the columns each
+    constexpr uint32_t kReaders = PAIR ? 2 * kF8EpilogueWarps : kF8EpilogueWarps / 2;
+
+    if (threadIdx.x == 32) {
+        tma_prefetch(&map_a);
+        tma_prefetch(&map_b);
+        for (int s = 0; s < S::kStages; ++s) {
+            bar_init(full + s, 1);   // the leader's: one arrival with the bytes of both blocks
+            bar_init(empty + s, 1);  // each block's own
+        }
+        for (int s = 0; s < S::kScaleStages; ++s) {
+            bar_init(scales_full + s, blocks);  // the leader's
+            bar_init(scales_empty + s, 1);      // each block's own
+        }
+        for (int s = 0; s < 2; ++s) {
+            bar_init(acc_full + s, 1);           // each block's own
+            bar_init(acc_empty + s, kReaders);   // the leader's
+            bar_init(early + s, kReaders);       // the leader's
+        }
+        bar_init_fence();
+        *failed = 0;
+    }
+    if (warp == 2) tmem_alloc<PAIR>(slot, 512);
+    tc_fence_before();
+    // (the barrier inside make() orders all of the above)
+    const Groups g = Groups::make(slot + 4, p.offsets, p.experts, p.rows, S::kRows, true);
+    if constexpr (PAIR) cluster_sync();  // the other block's barriers are ready too
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const uint32_t across = (p.cols + BN - 1) / BN, tiles = g.tiles() * across;
+    const uint32_t slices = (p.reduce + kF8Depth - 1) / kF8Depth;
+    auto tile_at = [&](uint32_t tile) {
+        TcTile t;
+        const uint32_t down = tile / across;
+        t.j0 = (tile - down * across) * BN;
+        t.e = g.find(down);
+        t.i0 = g.off[t.e] + (down - g.tile[t.e]) * S::kRows;
+        t.i_end = g.off[t.e + 1];
+        t.k0 = 0;
+        t.k_end = t.e < p.experts ? p.reduce : 0;  // 0: the unused rows
+        return t;
+    };
+
+    uint32_t issued = 0;  // stages filled so far (the copying warp)
+    if (warp == 0) {
+        uint32_t s = 0, round = 0;
+        bool ok = true;
+        for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
+            const TcTile t = tile_at(tile);
+            if (tile + 1 == p.stall) break;
+            const int i0 = (int)(t.i0 + rank * kTcRows), w0 = (int)(t.e * p.cols + t.j0 + rank * 128);
+            // Rows past the expert's end are not stored, so whole boxes of them are
+            // not copied: what the stage held before stands in for them.
+            const uint32_t rows = t.i_end - t.i0;  // of the tile, and more
+            const uint32_t a_boxes = PAIR ? 1 : min((rows + 15) / 16, kTcRows / 16u);
+            const bool second = PAIR && rows > kTcRows;  // the pair's second block has rows
+            const uint32_t bytes = PAIR ? 2 * S::kB + (second ? 2 : 1) * S::kA : S::kB + a_boxes * 2048;
+            for (uint32_t k = 0; k < t.k_end; k += kF8Depth, ++issued) {
+                ok = bar_wait_warp(empty + s, (round & 1) ^ 1);
+                if (!ok) break;
+                unsigned char* a = ring + s * S::kStage;
+                if (elect_one()) {
+                    const uint32_t bar = PAIR ? cluster_addr(full + s, 0) : smem_addr(full + s);
+                    if (rank == 0) bar_expect(full + s, bytes);
+                    tma_load_2d<PAIR>(a + S::kA, &map_b, (int)k, w0, bar);
+                    if constexpr (!PAIR) {
+                        for (uint32_t i = 0; i < a_boxes; ++i)
+                            tma_load_2d<PAIR>(a + i * 2048, &map_a, (int)k, i0 + (int)i * 16, bar);
+                    } else if (rank == 0 || second) {
+                        tma_load_2d<PAIR>(a, &map_a, (int)k, i0, bar);
+                    }
+                }
+                __syncwarp();
+                if (++s == S::kStages) s = 0, ++round;
+            }
+        }
+        if (!ok) *failed = 1;
+    } else if (warp == 3) {
+        const uint32_t down = (p.cols + RS_QUANT_BLOCK - 1) / RS_QUANT_BLOCK;
+        const bool a_words = ((uintptr_t)p.a_scales | p.a_scales_i) % 4 == 0;
+        const bool b_words = ((uintptr_t)p.b_scales | slices) % 4 == 0;
+        uint32_t s = 0, round = 0;
+        bool ok = true;
+        for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
+            const TcTile t = tile_at(tile);
+            if (tile + 1 == p.stall) break;
+            if (t.k_end == 0) continue;
+            const uint8_t* a[4];
+            const uint8_t* b[BN / 128];
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+                a[c] = p.a_scales + min(t.i0 + rank * kTcRows + c * 32 + lane, p.rows - 1) * p.a_scales_i;
+#pragma unroll
+            for (uint32_t h = 0; h < BN / 128; ++h)
+                b[h] = p.b_scales + ((size_t)t.e * down + min(t.j0 / RS_QUANT_BLOCK + h, down - 1)) * slices;
+            for (uint32_t q = 0; q * 4 < slices; ++q) {
+                uint4 wa, wb[BN / 128];
+                wa.x = scales_word(a[0], q, slices, a_words), wa.y = scales_word(a[1], q, slices, a_words);
+                wa.z = scales_word(a[2], q, slices, a_words), wa.w = scales_word(a[3], q, slices, a_words);
+#pragma unroll
+                for (uint32_t h = 0; h < BN / 128; ++h) {
+                    const uint32_t w = scales_word(b[h], q, slices, b_words);
+                    wb[h] = make_uint4(w, w, w, w);
+                }
+                ok = bar_wait_warp(scales_empty + s, (round & 1) ^ 1);
+                if (!ok) break;
+                uint4* to = reinterpret_cast<uint4*>(scales + s * S::kScales) + lane;
+                to[0] = wa;
+#pragma unroll
+                for (uint32_t h = 0; h < BN / 128; ++h) to[32 + 32 * h] = wb[h];
+                fence_async();
+                __syncwarp();
+                if (elect_one()) {
+                    if constexpr (PAIR) bar_arrive_cluster<true>(cluster_addr(scales_full + s, 0));
+                    else bar_arrive(scales_full + s);
+                }
+                __syncwarp();
+                if (++s == S::kScaleStages) s = 0, ++round;
+            }
+        }
+        if (!ok) *failed = 1;
+    } else if (warp == 1 && rank == 0) {
+        constexpr uint32_t kDesc = mma_scaled_desc(S::kRows, BN);
+        const uint64_t desc_a = smem_desc(smem_addr(ring), 16), desc_b = smem_desc(smem_addr(ring) + S::kA, 16);
+        const uint64_t desc_s = scales_desc(smem_addr(scales));
+        uint32_t s = 0, round = 0, n = 0, ss = 0, scale_round = 0, set = 0;
+        bool ok = true;
+        for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
+            const TcTile t = tile_at(tile);
+            if (t.k_end == 0) continue;
+            const uint32_t h = n & 1, acc = tmem + h * S::kAccStep, free = ((n >> 1) & 1) ^ 1;
+            ok = PAIR ? bar_wait_cluster_warp(acc_empty + h, free) : bar_wait_warp(acc_empty + h, free);
+            if (PAIR && ok && n) ok = bar_wait_cluster_warp(early + (h ^ 1), ((n - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            ++n;
+            for (uint32_t i = 0; i < slices; ++i) {
+                if (i % 4 == 0) {
+                    ok = PAIR ? bar_wait_cluster_warp(scales_full + ss, scale_round & 1)
+                              : bar_wait_warp(scales_full + ss, scale_round & 1);
+                    if (!ok) break;
+                    set ^= 1;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t c = 0; c <= BN / 128; ++c)
+                            tmem_copy_scales<PAIR>(tmem + S::kScaleCols + set * S::kScaleStep + c * 4,
+                                                   desc_s + ((ss * S::kScales + c * 512) >> 4));
+                        mma_commit<PAIR>(scales_empty + ss);
+                    }
+                    __syncwarp();
+                    if (++ss == S::kScaleStages) ss = 0, ++scale_round;
+                }
+                ok = bar_wait_warp(full + s, round & 1);
+                if (!ok) break;
+                const uint32_t steps = min((p.reduce - i * kF8Depth + 31) / 32, kF8Depth / 32u);
+                const uint32_t sa = tmem + S::kScaleCols + set * S::kScaleStep, desc = kDesc | mma_scale_byte(i % 4);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t da = desc_a + s * (S::kStage >> 4), db = desc_b + s * (S::kStage >> 4);
+#pragma unroll
+                    for (uint32_t k = 0; k < kF8Depth / 32; ++k)
+                        if (k < steps) mma_e4m3_scaled<PAIR>(acc, da + k * 2, db + k * 2, desc, sa, sa + 4, i | k);
+                    mma_commit<PAIR>(empty + s);
+                }
+                __syncwarp();
+                if (++s == S::kStages) s = 0, ++round;
+            }
+            if (ok && elect_one()) mma_commit<PAIR>(acc_full + h);
+            __syncwarp();
+        }
+        // What was issued is done before anything it uses is given up, also when
+        // the epilogue's wait for it has run out.
+        if (s || round) ok &= bar_wait_warp(empty + (s ? s : S::kStages) - 1, (s ? round : round - 1) & 1);
+        if (ss || scale_round)
+            ok &= bar_wait_warp(scales_empty + (ss ? ss : S::kScaleStages) - 1, (ss ? scale_round : scale_round - 1) & 1);
+        if (!ok) *failed = 1;
+    } else if (warp >= kTcFirstEpilogueWarp) {
+        const uint32_t w = warp - kTcFirstEpilogueWarp, group = w / 4;
+        const uint32_t quarter = warp % 4;  // the 32 tensor-memory lanes this warp can read
+        uint4* stage = reinterpret_cast<uint4*>(staging + w * S::kStaging);
+        const Rows<T> d(p.d, p.d_i, 0);
+        const Rows<T> pre(p.pre, p.pre_i, 0);
+        const Rows<const T> residual(p.residual, p.residual_i, 0);
+        const bool vec_bias = ((uintptr_t)p.bias | p.bias_e * sizeof(T)) % 16 == 0;
+        uint32_t n = 0, seen = 0;
+        for (uint32_t tile = first_tile; tile < tiles; tile += tile_step, ++seen) {
+            const TcTile t = tile_at(tile);
+            const bool some = t.k_end != 0;
+            const uint32_t h = n & 1, phase = (n >> 1) & 1;
+            n += some;
+            if (!PAIR && (some ? h : seen & 1) != group) continue;
+            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32, i = i0 + lane;
+            const uint32_t j_first = t.j0 + (PAIR ? group * 128 : 0);
+            const uint32_t acc = tmem + h * S::kAccStep + (PAIR ? group * 128 : 0) + (quarter << 21);
+            const uint32_t cols = j_first >= p.cols || i0 >= t.i_end ? 0 : min(128u, p.cols - j_first);  // to be stored
+            // this warp's part of the accumulator, or of what the next one overlaps, has been read
+            auto release = [&](uint64_t* bar) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) bar_arrive_cluster<false>(cluster_addr(bar + h, 0));
+                    else bar_arrive(bar + h);
+                }
+            };
+            if constexpr (QUANT) {
+                uint32_t z[8][16];
+                if (some) {
+                    if (!bar_wait_warp(acc_full + h, phase, 2 * slices)) {
+                        *failed = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (cols) {
+#pragma unroll
+                        for (uint32_t c = 0; c < 8; ++c) tmem_load16(z[c], acc + c * 16);
+#pragma unroll
+                        for (uint32_t c = 0; c < 8; ++c) tmem_load_wait(z[c]);
+                    }
+                    if constexpr (PAIR) release(early);
+                    release(acc_empty);
+                    if (!cols) continue;
+                    if (p.bias) {
+#pragma unroll
+                        for (uint32_t c = 0; c < 8; ++c)
+                            if (c * 16 < cols)
+                                add_bias<T>(z[c], p.bias + t.e * p.bias_e + j_first + c * 16, cols - c * 16, vec_bias);
+                    }
+                } else {
+                    if (!cols) continue;
+#pragma unroll
+                    for (uint32_t c = 0; c < 128; ++c) z[c / 16][c % 16] = 0;
+                }
+                if (p.pre) {
+#pragma unroll
+                    for (uint32_t c = 0; c < 8; ++c) {
+                        uint32_t out[8];
+                        round_all<T>(out, z[c]);
+                        if (c * 16 < cols) store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c * 16, p.cols);
+                    }
+                }
+                // (an activation of zero is zero)
+#pragma unroll
+                for (uint32_t c = 0; c < 8; ++c) {
+                    if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(z[c]);
+                    else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(z[c]);
+                    else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(z[c]);
+                }
+                store_quantized<T>(z, p, i, i < t.i_end, j_first);
+            } else if (some) {
+                // One piece of 16 columns ahead: the next piece's accumulators and
+                // residual are on their way while this one is finished.  A pair's
+                // first accumulator is read from its end, which the second overlaps.
+                const bool down = PAIR && h == 0;
+                uint32_t z[2][16], add[2][8];
+                auto col = [&](uint32_t c) { return (down ? 7 - c : c) * 16; };
+                auto fetch_residual = [&](uint32_t c, uint32_t (&r)[8]) {
+                    if (p.residual && c < 8 && col(c) < cols)
+                        fetch_piece<T>(r, residual, i0, t.i_end, j_first + col(c), p.cols);
+                };
+                auto fetch_acc = [&](uint32_t c, uint32_t (&zz)[16]) {
+                    if (c < 8 && col(c) < cols) tmem_load16(zz, acc + col(c));
+                };
+                fetch_residual(0, add[0]);
+                if (!bar_wait_warp(acc_full + h, phase, 2 * slices)) {
+                    *failed = 1;
+                    break;
+                }
+                tc_fence_after();
+                fetch_acc(0, z[0]);
+#pragma unroll 1
+                for (uint32_t c2 = 0; c2 < 8; c2 += 2)
+#pragma unroll
+                    for (uint32_t o = 0; o < 2; ++o) {
+                        const uint32_t c = c2 + o, j = j_first + col(c);
+                        uint32_t(&zz)[16] = z[o];
+                        tmem_load_wait(zz);
+                        if (PAIR && c == S::kOverlap / 16 - 1) release(early);
+                        if (c == 7) release(acc_empty);
+                        fetch_acc(c + 1, z[o ^ 1]);
+                        fetch_residual(c + 1, add[o ^ 1]);
+                        if (col(c) >= cols) continue;
+                        uint32_t out[8];
+                        if (p.bias) add_bias<T>(zz, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
+                        if (p.pre) {
+                            round_all<T>(out, zz);
+                            store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
+                        }
+                        if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(zz);
+                        else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(zz);
+                        else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(zz);
+                        if (p.residual) {
+                            spread_piece<T>(stage, add[o], residual, j, p.cols);
+                            add_all<T>(zz, add[o]);
+                        }
+                        round_all<T>(out, zz);
+                        store_piece<T>(stage, out, d, i0, t.i_end, j, p.cols);
+                    }
+            } else {  // unused rows
+                const uint32_t out[8] = {};
+                for (uint32_t c = 0; c < cols; c += 16) {
+                    if (p.pre) store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c, p.cols);
+                    store_piece<T>(stage, out, d, i0, t.i_end, j_first + c, p.cols);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // neither block's memory goes while the other's work may reach it
+    tc_fence_after();
+    if (threadIdx.x == 0) {
+        if (*failed && rank == 0)  // a copy must not land in shared memory that its block no longer owns
+            for (uint32_t s = 0; s < S::kStages && s < issued; ++s) {
+                const uint32_t last = (issued - 1 - s) / S::kStages;
+                bar_wait(full + s, last & 1);
+            }
+        p.status[blockIdx.x] = *failed;
+    }
+    if (blockIdx.x == 0)
+        for (uint32_t i = gridDim.x + threadIdx.x; i < p.status_words; i += kF8Threads) p.status[i] = 0;
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 2) tmem_free<PAIR>(tmem, 512);
+}
+
+// x: rows x reduce, w: (experts * cols) x reduce, bytes; strides in bytes,
+// multiples of 16, as the bases are.
+struct F8Operands {
+    const void* x;
+    size_t x_stride;
+    const void* w;
+    size_t w_stride;
+};
+
+// Launches a product (the kernel by its sizes); RS_ERR_CUDA if the driver makes no
+// tensor map.  Instantiated in rs_expert_f8_<type>.cu.
+template <typename T>
+rs_status f8_product(const F8Operands& o, const F8Args<T>& args, cudaStream_t stream);
+
+}  // namespace rsx

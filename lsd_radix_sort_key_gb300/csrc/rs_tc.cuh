@@ -288,8 +288,44 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// An arrival on bar (PAIR: on that barrier of both blocks) once every mma this
-// thread issued so far is done.
+// The same for K = 32 of e4m3 elements with a scale (a power of two, e8m0) for
+// each row of A and of B: scales are in tensor memory, four to a 32-bit word, of
+// which `idesc` names the byte.  Row 32 c + l of an operand has its word in
+// column c of lane l, and again in the same columns 32, 64 and 96 lanes on.
+// PAIR: each block has the scales of its own rows of A and of all rows of B.
+template <bool PAIR>
+__device__ __forceinline__ void mma_e4m3_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t scale_a,
+                                                uint32_t scale_b, bool accumulate)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(scale_a), "r"(scale_b)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(scale_a), "r"(scale_b)
+            : "memory");
+}
+
+// Copies 32 rows of 16 bytes, 512 adjacent bytes of shared memory (scales_desc), to
+// the four columns from `addr` of lanes 0..31 and of each 32 lanes after them.
+// Matrix instructions that the thread issues later see them.  PAIR: issued by
+// the leader; each block's tensor memory receives its own shared memory's.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t addr, uint64_t desc)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(addr), "l"(desc) : "memory");
+}
+
+// An arrival on bar (PAIR: on that barrier of both blocks) once every mma and
+// copy to tensor memory that this thread issued so far is done.
 template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
@@ -314,6 +350,13 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
            ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// The same for mma_e4m3_scaled, both operands K-major; `byte` of the scales' words.
+__host__ __device__ constexpr uint32_t mma_scaled_desc(uint32_t m, uint32_t n)
+{
+    return ((n >> 3) << 17) | (1u << 23) | ((m >> 7) << 27);
+}
+__host__ __device__ constexpr uint32_t mma_scale_byte(uint32_t byte) { return (byte << 29) | (byte << 4); }
+
 // Shared-memory operand descriptor for tiles copied with the 128-byte
 // swizzle (rows of 128 bytes, groups of 8 rows = 1024 bytes, 1024-aligned).
 //   K-major:  a row holds 64 reduction elements of one operand row; the next
@@ -326,6 +369,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t mn_stride)
 {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// 512 bytes of scales, not swizzled: groups of 8 rows of 16 bytes, one after the
+// other.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
 }
 
 // ---- host side
@@ -346,15 +396,15 @@ inline decltype(&cuTensorMapEncodeTiled) tensor_map_encoder()
     return fn;
 }
 
-// A map of 16-bit elements with the 128-byte swizzle: dims[0] adjacent,
-// strides (bytes) of dims 1.., boxes of 64 x box1 (x 1).
-inline bool encode_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
-                       const uint64_t* strides, uint32_t box1)
+// A map with the 128-byte swizzle: dims[0] adjacent, strides (bytes) of dims
+// 1.., boxes of 128 bytes x box1 (x 1).
+inline bool encode_tiles(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem_bytes, int rank, const void* base,
+                         const uint64_t* dims, const uint64_t* strides, uint32_t box1)
 {
     const auto encode = tensor_map_encoder();
     if (!encode) return false;
     cuuint64_t d[3], s[2];
-    cuuint32_t box[3] = {64, box1, 1}, step[3] = {1, 1, 1};
+    cuuint32_t box[3] = {128 / elem_bytes, box1, 1}, step[3] = {1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         if (dims[i] == 0 || dims[i] > 0xFFFFFFFFull) return false;
         d[i] = dims[i];
@@ -364,10 +414,17 @@ inline bool encode_map(CUtensorMap* map, bool bf16, int rank, const void* base, 
         s[i] = strides[i];
     }
     if ((uintptr_t)base % 16) return false;
-    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-                  const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Of 16-bit elements.
+inline bool encode_map(CUtensorMap* map, bool bf16, int rank, const void* base, const uint64_t* dims,
+                       const uint64_t* strides, uint32_t box1)
+{
+    return encode_tiles(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rank, base, dims,
+                        strides, box1);
 }
 
 }  // namespace rstc

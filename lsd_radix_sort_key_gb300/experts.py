@@ -50,7 +50,9 @@ def _torch():
         ext = importlib.util.module_from_spec(importlib.util.spec_from_loader("rs_torch", loader))
         loader.exec_module(ext)
         names = ("sort_temp_bytes", "sort", "dispatch", "combine", "combine_grad", "matmul_temp_bytes", "matmul",
-                 "matmul_grad_temp_bytes", "matmul_grad")  # the order of Entry there
+                 "matmul_grad_temp_bytes", "matmul_grad", "quantize", "dispatch_quantized", "quantize_weights",
+                 "matmul_quantized_temp_bytes", "matmul_quantized", "norm", "norm_grad_temp_bytes",
+                 "norm_grad")  # the order of Entry there
         ext.bind(*(ctypes.cast(getattr(_rs(), "rs_expert_" + n), ctypes.c_void_p).value for n in names))
         _fast = ext
     torch = module
