@@ -7,9 +7,9 @@
 // adds, exactly, so the sums stay in one float32 accumulator in tensor memory
 // and nothing is added up outside the tensor pipe.  Warp 0 copies 128-deep
 // slices of A and B, one scale block each, into a ring of shared-memory stages
-// (TMA, 128-byte swizzle); warp 3 gathers the scales of four slices at a time,
-// one 32-bit word per row, into a ring of its own; warp 1 has them copied to
-// tensor memory and issues the products; 8 epilogue warps, each with 32 rows of
+// (TMA, 128-byte swizzle); warp 3 gathers the scales of eight slices at a time, a
+// 32-bit word for each four of a row, into a ring of its own; warp 1 has those
+// of four slices at a time copied to tensor memory and issues the products; 8 epilogue warps, each with 32 rows of
 // 128 columns, read finished accumulators, apply the epilogue and store.
 //
 // Tensor memory (512 columns): two accumulators and two sets of scales.  A
@@ -23,8 +23,6 @@
 namespace rsx {
 
 constexpr int kF8Depth = 128;  // reduction elements per stage: one swizzled row of 128 bytes, one scale block
-constexpr int kF8EpilogueWarps = 8;
-constexpr int kF8Threads = 32 * (kTcFirstEpilogueWarp + kF8EpilogueWarps);
 
 template <typename T>
 struct F8Args {
@@ -53,33 +51,70 @@ struct F8Args {
     uint32_t stall;    // testing hook: tile stall - 1 is never copied
 };
 
-template <bool PAIR>
+// QUANT: an epilogue thread holds a row's 128 columns, a scale block, at once, which
+// takes the registers of 12 warps.  Otherwise 16 epilogue warps of 64 columns
+// each, 16 at a time: with 8 the epilogue was what lasted (32768 x 2048 x 4096 with
+// gelu 250 us, 200 without an activation).
+template <bool PAIR, bool QUANT>
 struct F8Shape {
+    static constexpr int kWarps = QUANT ? 8 : 16, kThreads = 32 * (kTcFirstEpilogueWarp + kWarps);
+    static constexpr uint32_t kWarpCols = QUANT ? 128 : 64;  // of an epilogue warp
+    // a block's warps that read an accumulator: all, or those whose turn it is
+    static constexpr uint32_t kReaders = PAIR ? 2 * kWarps : kWarps / 2;
     static constexpr uint32_t kCols = PAIR ? 256 : 128, kRows = PAIR ? 2 * kTcRows : kTcRows;  // of a tile
     static constexpr uint32_t kA = kTcRows * kF8Depth, kB = 128 * kF8Depth, kStage = kA + kB;   // of a block
     static constexpr int kStages = 6;
     static constexpr uint32_t kScales = 512 + kCols * 4;  // of four slices
-    static constexpr int kScaleStages = 4;
+    static constexpr uint32_t kScaleStage = 2 * kScales;  // of eight
+    static constexpr int kScaleStages = 2;
     static constexpr uint32_t kStaging = 32 * 32;  // per epilogue warp: 32 rows of 16 elements
     static constexpr uint32_t kOverlap = PAIR ? 32 : 0;
     static constexpr uint32_t kAccStep = kCols - kOverlap;  // columns from one accumulator to the other
     static constexpr uint32_t kScaleCols = PAIR ? 480 : 256, kScaleStep = 16;
     static constexpr size_t smem(size_t experts)
     {
-        return 1024 + (size_t)kStages * kStage + kScaleStages * kScales + kF8EpilogueWarps * kStaging +
+        return 1024 + (size_t)kStages * kStage + kScaleStages * kScaleStage + kWarps * kStaging +
                (2 * kStages + 2 * kScaleStages + 6) * 8 + 16 + Groups::words(experts) * 4;
     }
 };
 
-// Bytes [4 q, 4 q + 4) of a row of `n` scales; those past its end count as one.
-__device__ __forceinline__ uint32_t scales_word(const uint8_t* row, uint32_t q, uint32_t n, bool words)
-{
-    if (words && 4 * q + 4 <= n) return __ldg(reinterpret_cast<const uint32_t*>(row) + q);
-    uint32_t w = 0;
+// Eight adjacent scales as two words: from the three aligned words around them, so
+// that any base and stride will do, loaded in one go (load) before the first is
+// looked at (get).  The words may hold other rows' scales, which are not used;
+// those that do not lie wholly inside the scales, [begin, end), are read byte by
+// byte.
+struct Scales8 {
+    uint32_t w[3];
+    __device__ __forceinline__ static bool inside(uintptr_t a, const uint8_t* begin, const uint8_t* end)
+    {
+        return a >= (uintptr_t)begin && a + 4 <= (uintptr_t)end;
+    }
+    __device__ __forceinline__ void load(const uint8_t* from, const uint8_t* begin, const uint8_t* end)
+    {
+        const uintptr_t a = (uintptr_t)from & ~(uintptr_t)3;
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) w |= (4 * q + i < n ? (uint32_t)__ldg(row + 4 * q + i) : kScaleOne) << 8 * i;
-    return w;
-}
+        for (int i = 0; i < 3; ++i) {
+            w[i] = 0;
+            if (inside(a + 4 * i, begin, end)) w[i] = __ldg(reinterpret_cast<const uint32_t*>(a + 4 * i));
+        }
+    }
+    __device__ __forceinline__ void get(uint32_t (&out)[2], const uint8_t* from, const uint8_t* begin, const uint8_t* end)
+    {
+        const uintptr_t a = (uintptr_t)from & ~(uintptr_t)3;
+        if (!inside(a, begin, end) || !inside(a + 8, begin, end)) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (!inside(a + 4 * i, begin, end))
+                    for (int c = 0; c < 4; ++c) {
+                        const uint8_t* at = reinterpret_cast<const uint8_t*>(a) + 4 * i + c;
+                        if (at >= begin && at < end) w[i] |= (uint32_t)__ldg(at) << 8 * c;
+                    }
+        }
+        const uint32_t bits = (uint32_t)((uintptr_t)from & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    }
+};
 
 // This lane's row of 128 columns, from j0 on, rounded to 8 bits and stored with
 // its scale; all lanes of the warp.
@@ -121,17 +156,17 @@ __device__ __forceinline__ void store_quantized(uint32_t (&z)[8][16], const F8Ar
 // A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
 // have the reduction index adjacent.  QUANT: D leaves in 8 bits.
 template <typename T, bool PAIR, bool QUANT>
-__global__ void __launch_bounds__(kF8Threads, 1)
+__global__ void __launch_bounds__(F8Shape<PAIR, QUANT>::kThreads, 1)
     k_product_f8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, F8Args<T> p)
 {
     using namespace rstc;
-    using S = F8Shape<PAIR>;
+    using S = F8Shape<PAIR, QUANT>;
     constexpr uint32_t BN = S::kCols;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
     unsigned char* scales = ring + S::kStages * S::kStage;
-    unsigned char* staging = scales + S::kScaleStages * S::kScales;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kF8EpilogueWarps * S::kStaging);
+    unsigned char* staging = scales + S::kScaleStages * S::kScaleStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + S::kWarps * S::kStaging);
     uint64_t* empty = full + S::kStages;
     uint64_t* scales_full = empty + S::kStages;
     uint64_t* scales_empty = scales_full + S::kScaleStages;
@@ -143,9 +178,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = PAIR ? cluster_rank() : 0, blocks = PAIR ? 2 : 1;
     const uint32_t first_tile = blockIdx.x / blocks, tile_step = gridDim.x / blocks;
-    // narrow: the two groups of four epilogue warps take turns; pair: half the columns each
-    constexpr uint32_t kReaders = PAIR ? 2 * kF8EpilogueWarps : kF8EpilogueWarps / 2;
-
     if (threadIdx.x == 32) {
         tma_prefetch(&map_a);
         tma_prefetch(&map_b);
@@ -159,8 +191,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(acc_full + s, 1);           // each block's own
-            bar_init(acc_empty + s, kReaders);   // the leader's
-            bar_init(early + s, kReaders);       // the leader's
+            bar_init(acc_empty + s, S::kReaders);   // the leader's
+            bar_init(early + s, S::kReaders);       // the leader's
         }
         bar_init_fence();
         *failed = 0;
@@ -222,8 +254,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (!ok) *failed = 1;
     } else if (warp == 3) {
         const uint32_t down = (p.cols + RS_QUANT_BLOCK - 1) / RS_QUANT_BLOCK;
-        const bool a_words = ((uintptr_t)p.a_scales | p.a_scales_i) % 4 == 0;
-        const bool b_words = ((uintptr_t)p.b_scales | slices) % 4 == 0;
+        const uint8_t* a_end = p.a_scales + (p.rows - 1) * p.a_scales_i + slices;
+        const uint8_t* b_end = p.b_scales + (size_t)p.experts * down * slices;
         uint32_t s = 0, round = 0;
         bool ok = true;
         for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
@@ -238,22 +270,30 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
             for (uint32_t h = 0; h < BN / 128; ++h)
                 b[h] = p.b_scales + ((size_t)t.e * down + min(t.j0 / RS_QUANT_BLOCK + h, down - 1)) * slices;
-            for (uint32_t q = 0; q * 4 < slices; ++q) {
-                uint4 wa, wb[BN / 128];
-                wa.x = scales_word(a[0], q, slices, a_words), wa.y = scales_word(a[1], q, slices, a_words);
-                wa.z = scales_word(a[2], q, slices, a_words), wa.w = scales_word(a[3], q, slices, a_words);
+            // The fences of a step wait for all that the warp has in flight, so loads for a
+            // later step would only hold them up; the ring is two steps deep.
+            for (uint32_t k = 0; k < slices; k += 8) {
+                Scales8 ra[4], rb[BN / 128];
 #pragma unroll
-                for (uint32_t h = 0; h < BN / 128; ++h) {
-                    const uint32_t w = scales_word(b[h], q, slices, b_words);
-                    wb[h] = make_uint4(w, w, w, w);
-                }
+                for (uint32_t c = 0; c < 4; ++c) ra[c].load(a[c] + k, p.a_scales, a_end);
+#pragma unroll
+                for (uint32_t h = 0; h < BN / 128; ++h) rb[h].load(b[h] + k, p.b_scales, b_end);
+                uint32_t wa[4][2], wb[BN / 128][2];
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) ra[c].get(wa[c], a[c] + k, p.a_scales, a_end);
+#pragma unroll
+                for (uint32_t h = 0; h < BN / 128; ++h) rb[h].get(wb[h], b[h] + k, p.b_scales, b_end);
                 ok = bar_wait_warp(scales_empty + s, (round & 1) ^ 1);
                 if (!ok) break;
-                uint4* to = reinterpret_cast<uint4*>(scales + s * S::kScales) + lane;
-                to[0] = wa;
+                uint4* to = reinterpret_cast<uint4*>(scales + s * S::kScaleStage) + lane;
 #pragma unroll
-                for (uint32_t h = 0; h < BN / 128; ++h) to[32 + 32 * h] = wb[h];
-                fence_async();
+                for (uint32_t i = 0; i < 2; ++i, to += S::kScales / 16) {
+                    to[0] = make_uint4(wa[0][i], wa[1][i], wa[2][i], wa[3][i]);
+#pragma unroll
+                    for (uint32_t h = 0; h < BN / 128; ++h)
+                        to[32 + 32 * h] = make_uint4(wb[h][i], wb[h][i], wb[h][i], wb[h][i]);
+                }
+                fence_async_shared();
                 __syncwarp();
                 if (elect_one()) {
                     if constexpr (PAIR) bar_arrive_cluster<true>(cluster_addr(scales_full + s, 0));
@@ -280,21 +320,24 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             tc_fence_after();
             ++n;
             for (uint32_t i = 0; i < slices; ++i) {
-                if (i % 4 == 0) {
+                if (i % 8 == 0) {
                     ok = PAIR ? bar_wait_cluster_warp(scales_full + ss, scale_round & 1)
                               : bar_wait_warp(scales_full + ss, scale_round & 1);
                     if (!ok) break;
+                }
+                if (i % 4 == 0) {
                     set ^= 1;
                     tc_fence_after();
+                    const bool last = i % 8 == 4 || i + 4 >= slices;  // of this stage
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t c = 0; c <= BN / 128; ++c)
                             tmem_copy_scales<PAIR>(tmem + S::kScaleCols + set * S::kScaleStep + c * 4,
-                                                   desc_s + ((ss * S::kScales + c * 512) >> 4));
-                        mma_commit<PAIR>(scales_empty + ss);
+                                                   desc_s + ((ss * S::kScaleStage + i / 4 % 2 * S::kScales + c * 512) >> 4));
+                        if (last) mma_commit<PAIR>(scales_empty + ss);
                     }
                     __syncwarp();
-                    if (++ss == S::kScaleStages) ss = 0, ++scale_round;
+                    if (last && ++ss == S::kScaleStages) ss = 0, ++scale_round;
                 }
                 ok = bar_wait_warp(full + s, round & 1);
                 if (!ok) break;
@@ -334,11 +377,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             const bool some = t.k_end != 0;
             const uint32_t h = n & 1, phase = (n >> 1) & 1;
             n += some;
-            if (!PAIR && (some ? h : seen & 1) != group) continue;
-            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32, i = i0 + lane;
-            const uint32_t j_first = t.j0 + (PAIR ? group * 128 : 0);
-            const uint32_t acc = tmem + h * S::kAccStep + (PAIR ? group * 128 : 0) + (quarter << 21);
-            const uint32_t cols = j_first >= p.cols || i0 >= t.i_end ? 0 : min(128u, p.cols - j_first);  // to be stored
+            const uint32_t turn = some ? h : seen & 1;
+            constexpr uint32_t W = S::kWarpCols, kOfTile = BN / W;  // groups that a tile takes
+            if (!PAIR && turn != group / kOfTile) continue;
+            const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32, i = i0 + lane, c_first = group % kOfTile * W;
+            const uint32_t j_first = t.j0 + c_first;
+            const uint32_t acc = tmem + h * S::kAccStep + c_first + (quarter << 21);
+            const uint32_t cols = j_first >= p.cols || i0 >= t.i_end ? 0 : min(W, p.cols - j_first);  // to be stored
             // this warp's part of the accumulator, or of what the next one overlaps, has been read
             auto release = [&](uint64_t* bar) {
                 tc_fence_before();
@@ -393,53 +438,65 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                 }
                 store_quantized<T>(z, p, i, i < t.i_end, j_first);
             } else if (some) {
-                // One piece of 16 columns ahead: the next piece's accumulators and
-                // residual are on their way while this one is finished.  A pair's
-                // first accumulator is read from its end, which the second overlaps.
+                // Two pieces of 16 columns at a time: one is on its way while the other is
+                // finished.  A pair's first accumulator is read from its end, which the
+                // second overlaps; both of its pieces there are loaded before anything
+                // else is done, as the tensor pipe waits for them.
                 const bool down = PAIR && h == 0;
-                uint32_t z[2][16], add[2][8];
-                auto col = [&](uint32_t c) { return (down ? 7 - c : c) * 16; };
+                uint32_t z[2][16], add[2][8], bias[8];
+                auto col = [&](uint32_t c) { return (down ? W / 16 - 1 - c : c) * 16; };
                 auto fetch_residual = [&](uint32_t c, uint32_t (&r)[8]) {
-                    if (p.residual && c < 8 && col(c) < cols)
+                    if (p.residual && c < W / 16 && col(c) < cols)
                         fetch_piece<T>(r, residual, i0, t.i_end, j_first + col(c), p.cols);
                 };
-                auto fetch_acc = [&](uint32_t c, uint32_t (&zz)[16]) {
-                    if (c < 8 && col(c) < cols) tmem_load16(zz, acc + col(c));
+                auto fetch_bias = [&](uint32_t c) {
+                    if (p.bias && c < W / 16 && col(c) < cols)
+                        load_bias<T>(bias, p.bias + t.e * p.bias_e + j_first + col(c), cols - col(c), vec_bias);
                 };
+                auto fetch_acc = [&](uint32_t c, uint32_t (&zz)[16]) {
+                    if (c < W / 16 && col(c) < cols) tmem_load16(zz, acc + col(c));
+                };
+                static_assert(S::kOverlap <= 32, "two pieces");
                 fetch_residual(0, add[0]);
+                fetch_bias(0);
                 if (!bar_wait_warp(acc_full + h, phase, 2 * slices)) {
                     *failed = 1;
                     break;
                 }
                 tc_fence_after();
                 fetch_acc(0, z[0]);
+                fetch_acc(1, z[1]);
+                if constexpr (PAIR) {
+                    tmem_load_wait(z[0]);
+                    tmem_load_wait(z[1]);
+                    release(early);
+                }
 #pragma unroll 1
-                for (uint32_t c2 = 0; c2 < 8; c2 += 2)
+                for (uint32_t c2 = 0; c2 < W / 16; c2 += 2)
 #pragma unroll
                     for (uint32_t o = 0; o < 2; ++o) {
                         const uint32_t c = c2 + o, j = j_first + col(c);
                         uint32_t(&zz)[16] = z[o];
                         tmem_load_wait(zz);
-                        if (PAIR && c == S::kOverlap / 16 - 1) release(early);
-                        if (c == 7) release(acc_empty);
-                        fetch_acc(c + 1, z[o ^ 1]);
+                        if (c == W / 16 - 1) release(acc_empty);
+                        if (p.bias && col(c) < cols) add_all<T>(zz, bias);
+                        fetch_bias(c + 1);
                         fetch_residual(c + 1, add[o ^ 1]);
-                        if (col(c) >= cols) continue;
                         uint32_t out[8];
-                        if (p.bias) add_bias<T>(zz, p.bias + t.e * p.bias_e + j, p.cols - j, vec_bias);
-                        if (p.pre) {
+                        if (p.pre && col(c) < cols) {
                             round_all<T>(out, zz);
                             store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                         }
                         if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(zz);
                         else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(zz);
                         else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(zz);
-                        if (p.residual) {
+                        if (p.residual && col(c) < cols) {
                             spread_piece<T>(stage, add[o], residual, j, p.cols);
                             add_all<T>(zz, add[o]);
                         }
                         round_all<T>(out, zz);
-                        store_piece<T>(stage, out, d, i0, t.i_end, j, p.cols);
+                        fetch_acc(c + 2, zz);
+                        if (col(c) < cols) store_piece<T>(stage, out, d, i0, t.i_end, j, p.cols);
                     }
             } else {  // unused rows
                 const uint32_t out[8] = {};
@@ -464,7 +521,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         p.status[blockIdx.x] = *failed;
     }
     if (blockIdx.x == 0)
-        for (uint32_t i = gridDim.x + threadIdx.x; i < p.status_words; i += kF8Threads) p.status[i] = 0;
+        for (uint32_t i = gridDim.x + threadIdx.x; i < p.status_words; i += S::kThreads) p.status[i] = 0;
     __syncthreads();
     if constexpr (PAIR) cluster_sync();
     if (warp == 2) tmem_free<PAIR>(tmem, 512);

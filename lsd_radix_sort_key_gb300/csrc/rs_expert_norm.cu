@@ -10,15 +10,6 @@ namespace rsx {
 RS_EXTERN_NORM(float)
 RS_EXTERN_NORM(__half)
 RS_EXTERN_NORM(__nv_bfloat16)
-
-uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem)
-{
-    // A block has one thread per 16 bytes of a row, 512 at most; 1024 threads
-    // per SM (152), and no more than 8 blocks.
-    const size_t threads = align_up(ceil_div(width * elem, 16), 32);
-    const size_t per = threads >= 512 ? 2 : threads <= 128 ? 8 : 1024 / threads, blocks = 152 * per;
-    return (uint32_t)(rows < blocks ? rows : blocks);
-}
 }  // namespace rsx
 
 namespace {
@@ -103,7 +94,7 @@ private:
 
 size_t grad_temp(const rs_expert_norm_desc* d)
 {
-    const size_t blocks = norm_grad_blocks(d->rows, d->width, type_bytes(d->type));
+    const size_t blocks = norm_grad_blocks(d->rows, d->width, type_bytes(d->type), d->block != nullptr);
     return align_up(kParts * blocks * d->width * 4, 256);
 }
 
@@ -208,7 +199,7 @@ rs_status rs_expert_norm_grad(const rs_expert_norm_desc* d)
         p.dblock_weight = d->dblock_weight;
         p.dgate = d->dgate;
         p.part = static_cast<float*>(d->temp);
-        return norm_gradient<T>(p, vectors, norm_grad_blocks(n, w, eb), s);
+        return norm_gradient<T>(p, vectors, norm_grad_blocks(n, w, eb, d->block != nullptr), s);
     });
 }
 

@@ -102,27 +102,38 @@ __device__ __forceinline__ void store_params(void* p, size_t i, const float (&f)
     }
 }
 
-// Sums over the threads of a row: blockDim.x of them, 32 or a whole block.
+// Sums over a block's threads.  mem: two halves of [K][32] floats, used in turn
+// (`turn` counts the calls), so that one barrier per call is enough: a half is
+// written again only after the barrier of the call between.
 template <int K>
-__device__ __forceinline__ void row_sums(float (&s)[K], float* mem)
+__device__ __forceinline__ void block_sums(float (&s)[K], float* mem, uint32_t& turn)
 {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int d = 16; d; d >>= 1)
 #pragma unroll
-        for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
-    if (blockDim.x == 32) return;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    __syncthreads();  // (the sums before have been read)
-    if (lane == 0)
+        for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
+    const uint32_t warps = blockDim.x / 32;
+    if (warps == 1) return;
+    float* half = mem + (turn++ & 1) * (3 * 32);
+    if (threadIdx.x % 32 == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) mem[k * 32 + warp] = s[k];
+        for (int k = 0; k < K; ++k) half[k * 32 + threadIdx.x / 32] = s[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        s[k] = lane < warps ? mem[k * 32 + lane] : 0.0f;
+    for (int k = 0; k < K; ++k) s[k] = 0.0f;
+    for (uint32_t w = 0; w < warps; w += 4) {  // (the ones past the last warp's are zero)
 #pragma unroll
-        for (int d = 16; d; d >>= 1) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], d);
+        for (int k = 0; k < K; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(half + k * 32 + w);
+            s[k] += (v.x + v.y) + (v.z + v.w);
+        }
     }
+}
+
+__device__ __forceinline__ void clear_sums(float* mem)
+{
+    for (uint32_t i = threadIdx.x; i < 2 * 3 * 32; i += blockDim.x) mem[i] = 0.0f;
+    __syncthreads();
 }
 
 template <typename T, int N, int V>
@@ -139,77 +150,31 @@ struct NormRow {
     }
 };
 
-// threadIdx.x walks a row, V accesses of N elements per thread; threadIdx.y
-// (with 32 threads to a row) takes rows of its own.
-template <typename T, int N, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) k_norm(NormArgs<T> p)
+// This thread's columns of a row of parameters; `none` where there is none.
+template <typename T, int N, int V>
+__device__ __forceinline__ void load_columns(float (&f)[V][N], const void* p, size_t at, bool wide, float none, uint32_t width)
 {
-    __shared__ float mem[32];
-    const uint32_t r = blockIdx.x * blockDim.y + threadIdx.y;
-    if (r >= p.rows) return;  // (a whole warp, or the block)
-    NormRow<T, N, V> x, b;
-    x.load(p.x + r * p.x_i, p.width);
-    if (p.block) {
-        b.load(p.block + r * p.block_i, p.width);
-        float rb = 1.0f;
-        if (p.block_weight) {
-            float s[1] = {};
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float f[N];
-                widen<T, N>(f, b.v[i]);
-#pragma unroll
-                for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
-            }
-            row_sums(s, mem);
-            rb = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
-        }
-        const size_t gate = p.gate_rows > 1 ? (size_t)(r / (p.rows / p.gate_rows)) * p.width : 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-            if (c0 >= p.width) continue;
-            float fx[N], u[N], w[N];
-            widen<T, N>(fx, x.v[i]);
-            widen<T, N>(u, b.v[i]);
-            if (p.block_weight) {
-                load_params<T, N>(w, p.block_weight, c0, p.wide_params);
-#pragma unroll
-                for (int c = 0; c < N; ++c) u[c] *= rb * w[c];
-            }
-            if (p.gate_rows) {
-                load_params<T, N>(w, p.gate, gate + c0, p.wide_params);
-#pragma unroll
-                for (int c = 0; c < N; ++c) u[c] *= w[c];
-            }
-#pragma unroll
-            for (int c = 0; c < N; ++c) u[c] = fmaf(p.scale, fx[c], u[c]);
-            x.v[i] = narrow<T, N>(u);  // y as it is held
-            store_vec<T, N>(p.y + r * p.y_i + c0, x.v[i]);
-        }
-        if (!p.weight) return;
-    }
-    float s[1] = {};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float f[N];
-        widen<T, N>(f, x.v[i]);
-#pragma unroll
-        for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
-    }
-    row_sums(s, mem);
-    const float rx = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-        if (c0 >= p.width) continue;
-        float f[N], w[N];
-        widen<T, N>(f, x.v[i]);
-        load_params<T, N>(w, p.weight, c0, p.wide_params);
 #pragma unroll
-        for (int c = 0; c < N; ++c) f[c] *= rx * w[c];
-        store_vec<T, N>(p.h + r * p.h_i + c0, narrow<T, N>(f));
+        for (int c = 0; c < N; ++c) f[i][c] = none;
+        if (p && c0 < width) load_params<T, N>(f[i], p, at + c0, wide);
     }
+}
+
+// The gate times the block's weight, this thread's columns.
+template <typename T, int N, int V>
+__device__ __forceinline__ void load_gate(float (&f)[V][N], const NormArgs<T>& p, uint32_t gate)
+{
+    load_columns<T, N, V>(f, p.gate_rows ? p.gate : nullptr, (size_t)gate * p.width, p.wide_params, 1.0f, p.width);
+    if (!p.block_weight) return;
+    float w[V][N];
+    load_columns<T, N, V>(w, p.block_weight, 0, p.wide_params, 1.0f, p.width);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int c = 0; c < N; ++c) f[i][c] *= w[i][c];
 }
 
 // A block's rows: [first(b), first(b + 1)).
@@ -218,155 +183,238 @@ __host__ __device__ inline uint32_t first_row(uint32_t block, uint32_t blocks, u
     return (uint32_t)((uint64_t)block * rows / blocks);
 }
 
-// Each block walks adjacent rows, the next one's loads in flight while it sums
-// over this one, and keeps its threads' columns of the summed gradients in
-// registers.
-template <typename T, int N, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) k_norm_grad(NormArgs<T> p)
+// Each block walks adjacent rows, V accesses of N elements per thread, the next
+// row's loads in flight while it sums over this one.  The parameters' columns
+// stay in registers (a gate's until it changes): reading them again for every
+// row, 24 KB beside a row's 16 of 2048 bf16, took 70 us where this takes NNN
+// (16384 x 2048 bf16 with everything, float32 parameters).
+template <typename T, int N, int V, int THREADS, bool BLOCK>
+__global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(NormArgs<T> p)
 {
-    __shared__ float mem[3 * 32];
-    start_next_grid();
+    __shared__ __align__(16) float mem[2 * 3 * 32];
+    clear_sums(mem);
     const uint32_t first = first_row(blockIdx.x, gridDim.x, p.rows), last = first_row(blockIdx.x + 1, gridDim.x, p.rows);
     const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
-    const uint32_t first_gate = first / per_gate;
-    float dw[V][N] = {}, db[V][N] = {}, dg[V][N] = {};
-    struct {
-        NormRow<T, N, V> y, dh, dy, b;
-    } next;
+    uint32_t turn = 0, gate = first / per_gate, gate_end = (gate + 1) * per_gate;
+    float w[V][N], gw[BLOCK ? V : 1][N];
+    NormRow<T, N, V> next_x, next_b;
     auto fetch = [&](uint32_t r) {
-        if (p.dh) {
-            next.y.load(p.x + r * p.x_i, p.width);
-            next.dh.load(p.dh + r * p.dh_i, p.width);
-        }
-        if (p.dy) next.dy.load(p.dy + r * p.dy_i, p.width);
-        if (p.block) next.b.load(p.block + r * p.block_i, p.width);
-    };
-    auto store_part = [&](int kind, const float (&f)[V][N]) {
-        float* to = p.part + ((size_t)kind * gridDim.x + blockIdx.x) * p.width;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-#pragma unroll
-            for (int c = 0; c < N; ++c)
-                if (c0 < p.width) to[c0 + c] = f[i][c];
-        }
+        next_x.load(p.x + r * p.x_i, p.width);
+        if constexpr (BLOCK) next_b.load(p.block + r * p.block_i, p.width);
     };
     fetch(first);
+    load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
+    if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
     for (uint32_t r = first; r < last; ++r) {
-        auto now = next;
+        NormRow<T, N, V> x = next_x, b;
+        if constexpr (BLOCK) b = next_b;
         if (r + 1 < last) fetch(r + 1);
-        const uint32_t gate = r / per_gate;
-        const size_t gate_at = p.gate_rows > 1 ? (size_t)gate * p.width : 0;
-        float sums[3] = {};  // y^2, <g, y>, block^2
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-            if (c0 >= p.width) continue;
-            float y[N], g[N], w[N];
-            if (p.dh) {
-                widen<T, N>(y, now.y.v[i]);
-                widen<T, N>(g, now.dh.v[i]);
-                load_params<T, N>(w, p.weight, c0, p.wide_params);
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    sums[0] = fmaf(y[c], y[c], sums[0]);
-                    sums[1] = fmaf(g[c] * w[c], y[c], sums[1]);
-                }
+        float s[1] = {};
+        if constexpr (BLOCK) {
+            if (r == gate_end) {
+                ++gate;
+                gate_end += per_gate;
+                load_gate<T, N, V>(gw, p, gate);
             }
+            float rb = 1.0f;
             if (p.block_weight) {
-                widen<T, N>(y, now.b.v[i]);
 #pragma unroll
-                for (int c = 0; c < N; ++c) sums[2] = fmaf(y[c], y[c], sums[2]);
-            }
-        }
-        row_sums(sums, mem);
-        const float rx = 1.0f / sqrtf(fmaf(sums[0], p.per_width, p.eps)), kx = rx * rx * rx * p.per_width * sums[1];
-        const float rb = p.block_weight ? 1.0f / sqrtf(fmaf(sums[2], p.per_width, p.eps)) : 1.0f;
-        float dot[1] = {};  // <du, block>
-        float du[V][N];
+                for (int i = 0; i < V; ++i) {
+                    float f[N];
+                    widen<T, N>(f, b.v[i]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-            if (c0 >= p.width) continue;
-            float d[N] = {}, y[N], g[N], w[N];
-            if (p.dh) {
-                widen<T, N>(y, now.y.v[i]);
-                widen<T, N>(g, now.dh.v[i]);
-                load_params<T, N>(w, p.weight, c0, p.wide_params);
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    d[c] = fmaf(rx * w[c], g[c], -kx * y[c]);
-                    dw[i][c] = fmaf(g[c], y[c] * rx, dw[i][c]);
+                    for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
                 }
+                block_sums(s, mem, turn);
+                rb = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
             }
-            if (p.dy) {
-                widen<T, N>(g, now.dy.v[i]);
-#pragma unroll
-                for (int c = 0; c < N; ++c) d[c] += g[c];
-            }
-            if (p.dx) {
-#pragma unroll
-                for (int c = 0; c < N; ++c) y[c] = p.scale * d[c];
-                store_vec<T, N>(p.dx + r * p.dx_i + c0, narrow<T, N>(y));
-            }
-            if (!p.block) continue;
-            float b[N];
-            widen<T, N>(b, now.b.v[i]);
-#pragma unroll
-            for (int c = 0; c < N; ++c) w[c] = 1.0f;
-            if (p.block_weight) load_params<T, N>(w, p.block_weight, c0, p.wide_params);
-            if (p.gate_rows) {
-                load_params<T, N>(g, p.gate, gate_at + c0, p.wide_params);
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    dg[i][c] = fmaf(d[c], b[c] * rb * w[c], dg[i][c]);
-                    d[c] *= g[c];
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                if (p.block_weight) db[i][c] = fmaf(d[c], b[c] * rb, db[i][c]);
-                du[i][c] = d[c] * w[c];
-                dot[0] = fmaf(du[i][c], b[c], dot[0]);
-            }
-        }
-        if (p.dblock) {
-            float kb = 0.0f;
-            if (p.block_weight) {
-                row_sums(dot, mem);
-                kb = rb * rb * rb * p.per_width * dot[0];
-            }
+            s[0] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-                if (c0 >= p.width) continue;
-                float b[N];
-                widen<T, N>(b, now.b.v[i]);
+                float f[N], u[N];
+                widen<T, N>(f, x.v[i]);
+                widen<T, N>(u, b.v[i]);
 #pragma unroll
-                for (int c = 0; c < N; ++c) b[c] = fmaf(rb, du[i][c], -kb * b[c]);
-                store_vec<T, N>(p.dblock + r * p.dblock_i + c0, narrow<T, N>(b));
+                for (int c = 0; c < N; ++c) u[c] = fmaf(p.scale, f[c], u[c] * rb * gw[i][c]);
+                x.v[i] = narrow<T, N>(u);  // y as it is held
+                if (c0 < p.width) store_vec<T, N>(p.y + r * p.y_i + c0, x.v[i]);
+            }
+            if (!p.weight) continue;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f[N];
+            widen<T, N>(f, x.v[i]);
+#pragma unroll
+            for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
+        }
+        block_sums(s, mem, turn);
+        const float rx = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
+            if (c0 >= p.width) continue;
+            float f[N];
+            widen<T, N>(f, x.v[i]);
+#pragma unroll
+            for (int c = 0; c < N; ++c) f[c] *= rx * w[i][c];
+            store_vec<T, N>(p.h + r * p.h_i + c0, narrow<T, N>(f));
+        }
+    }
+}
+
+// Each block walks adjacent rows as above and keeps its threads' columns of the
+// summed gradients in registers.  Within one gate row, with n = block r,
+//     dgate = block_weight S,  dblock_weight += gate S,  S = the sum of d n,
+// so one sum serves both until the gate changes.
+template <typename T, int N, int V, int THREADS, bool BLOCK>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(NormArgs<T> p)
+{
+    __shared__ __align__(16) float mem[2 * 3 * 32];
+    start_next_grid();
+    clear_sums(mem);
+    const uint32_t first = first_row(blockIdx.x, gridDim.x, p.rows), last = first_row(blockIdx.x + 1, gridDim.x, p.rows);
+    const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
+    uint32_t turn = 0, gate = first / per_gate, gate_end = (gate + 1) * per_gate;
+    constexpr int VB = BLOCK ? V : 1;
+    float w[V][N], gw[VB][N], dw[V][N] = {}, db[VB][N] = {}, sum[VB][N] = {};
+    NormRow<T, N, V> next_y, next_dh, next_dy, next_b;
+    auto fetch = [&](uint32_t r) {
+        if (p.dh) {
+            next_y.load(p.x + r * p.x_i, p.width);
+            next_dh.load(p.dh + r * p.dh_i, p.width);
+        }
+        if (p.dy) next_dy.load(p.dy + r * p.dy_i, p.width);
+        if constexpr (BLOCK) next_b.load(p.block + r * p.block_i, p.width);
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) next_y.v[i] = next_dh.v[i] = next_dy.v[i] = Vec<T, N>{};
+    fetch(first);
+    load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
+    if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
+    auto store_part = [&](int kind, int i, const float (&f)[N]) {
+        const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
+        if (c0 >= p.width) return;
+        float* to = p.part + ((size_t)kind * gridDim.x + blockIdx.x) * p.width + c0;
+        if constexpr (N == 1) {
+            *to = f[0];
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+        }
+    };
+    for (uint32_t r = first; r < last; ++r) {
+        const NormRow<T, N, V> y = next_y, dh = next_dh, dy = next_dy;
+        NormRow<T, N, V> b;
+        if constexpr (BLOCK) b = next_b;
+        if (r + 1 < last) fetch(r + 1);
+        float sums[3] = {};  // y^2, <g, y>, block^2
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f[N], g[N];
+            widen<T, N>(f, y.v[i]);
+            widen<T, N>(g, dh.v[i]);
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                sums[0] = fmaf(f[c], f[c], sums[0]);
+                sums[1] = fmaf(g[c] * w[i][c], f[c], sums[1]);
+            }
+            if constexpr (BLOCK) {
+                widen<T, N>(f, b.v[i]);
+#pragma unroll
+                for (int c = 0; c < N; ++c) sums[2] = fmaf(f[c], f[c], sums[2]);
             }
         }
-        if (p.dgate && (r + 1 == last || (r + 1) / per_gate != gate)) {
-            // this block's last row with this gate row: whole, or a part of it
-            const bool whole = gate * per_gate >= first && (gate + 1) * per_gate <= last;
-            if (whole) {
+        block_sums(sums, mem, turn);
+        const float rx = p.dh ? 1.0f / sqrtf(fmaf(sums[0], p.per_width, p.eps)) : 0.0f;
+        const float kx = rx * rx * rx * p.per_width * sums[1];
+        const float rb = BLOCK && p.block_weight ? 1.0f / sqrtf(fmaf(sums[2], p.per_width, p.eps)) : 1.0f;
+        float dot[1] = {};  // <du, block>
+        float du[VB][N];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
+            float f[N], g[N], d[N];
+            widen<T, N>(f, y.v[i]);
+            widen<T, N>(g, dh.v[i]);
+            widen<T, N>(d, dy.v[i]);
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                d[c] = fmaf(rx * w[i][c], g[c], fmaf(-kx, f[c], d[c]));
+                dw[i][c] = fmaf(g[c], f[c] * rx, dw[i][c]);
+                g[c] = p.scale * d[c];
+            }
+            if (p.dx && c0 < p.width) store_vec<T, N>(p.dx + r * p.dx_i + c0, narrow<T, N>(g));
+            if constexpr (BLOCK) {
+                widen<T, N>(f, b.v[i]);
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    sum[i][c] = fmaf(d[c], f[c] * rb, sum[i][c]);
+                    du[i][c] = d[c] * gw[i][c];
+                    dot[0] = fmaf(du[i][c], f[c], dot[0]);
+                }
+            }
+        }
+        if constexpr (BLOCK) {
+            if (p.dblock) {
+                float kb = 0.0f;
+                if (p.block_weight) {
+                    block_sums(dot, mem, turn);
+                    kb = rb * rb * rb * p.per_width * dot[0];
+                }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-                    if (c0 < p.width) store_params<T, N>(p.dgate, gate_at + c0, dg[i], p.wide_params);
+                    float f[N];
+                    widen<T, N>(f, b.v[i]);
+#pragma unroll
+                    for (int c = 0; c < N; ++c) f[c] = fmaf(rb, du[i][c], -kb * f[c]);
+                    if (c0 < p.width) store_vec<T, N>(p.dblock + r * p.dblock_i + c0, narrow<T, N>(f));
                 }
-            } else {
-                store_part(gate == first_gate ? kPartGateFirst : kPartGateLater, dg);
             }
+            if (r + 1 == last || r + 1 == gate_end) {
+                // this block's last row with this gate row: all of its rows, or a part
+                const uint32_t begin = gate_end - per_gate;
+                const bool whole = begin >= first && gate_end <= last;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
+                    if (c0 >= p.width) continue;
+                    float f[N];
+                    if (p.dblock_weight) {
 #pragma unroll
-                for (int c = 0; c < N; ++c) dg[i][c] = 0.0f;
+                        for (int c = 0; c < N; ++c) f[c] = 1.0f;
+                        if (p.gate_rows) load_params<T, N>(f, p.gate, (size_t)gate * p.width + c0, p.wide_params);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) db[i][c] = fmaf(f[c], sum[i][c], db[i][c]);
+                    }
+                    if (p.dgate) {
+#pragma unroll
+                        for (int c = 0; c < N; ++c) f[c] = 1.0f;
+                        if (p.block_weight) load_params<T, N>(f, p.block_weight, c0, p.wide_params);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) f[c] *= sum[i][c];
+                        if (whole) store_params<T, N>(p.dgate, (size_t)gate * p.width + c0, f, p.wide_params);
+                        else store_part(begin <= first ? kPartGateFirst : kPartGateLater, i, f);
+                    }
+#pragma unroll
+                    for (int c = 0; c < N; ++c) sum[i][c] = 0.0f;
+                }
+                if (r + 1 < last) {
+                    ++gate;
+                    gate_end += per_gate;
+                    load_gate<T, N, V>(gw, p, gate);
+                }
+            }
         }
     }
-    if (p.dweight) store_part(kPartWeight, dw);
-    if (p.dblock_weight) store_part(kPartBlockWeight, db);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (p.dweight) store_part(kPartWeight, i, dw[i]);
+        if constexpr (BLOCK)
+            if (p.dblock_weight) store_part(kPartBlockWeight, i, db[i]);
+    }
 }
 
 // The summed gradients from the blocks' parts, in the blocks' order: job 0
@@ -403,14 +451,15 @@ __global__ void __launch_bounds__(kFinishCols* kFinishRows) k_norm_finish(NormAr
         b_end = block_of((gate + 1) * per_gate - 1) + 1;
         if (b_end - b0 == 1) return;  // that block has stored it
     }
+    // (of the blocks that share a gate row only the first may have begun with another)
+    const uint32_t kind = job < 2 ? job : kPartGateFirst;
+    const bool later = job >= 2 && first_row(b0, blocks, p.rows) < gate * per_gate;
     float s = 0.0f;
     if (col < p.width) {
-#pragma unroll 4
-        for (uint32_t b = b0 + threadIdx.y; b < b_end; b += kFinishRows) {
-            int kind = (int)job;
-            if (job >= 2) kind = gate == first_row(b, blocks, p.rows) / per_gate ? kPartGateFirst : kPartGateLater;
-            s += p.part[((size_t)kind * blocks + b) * p.width + col];
-        }
+        const float* from = p.part + (size_t)kind * blocks * p.width + col;
+#pragma unroll 8
+        for (uint32_t b = b0 + threadIdx.y; b < b_end; b += kFinishRows)
+            s += from[((size_t)b + (later && b == b0 ? blocks : 0)) * p.width];
     }
     mem[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -429,7 +478,20 @@ rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s);
 template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s);
 
-// Blocks of a gradient: the sizes alone decide, as the order of its sums goes by them.
-uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem);
+// Blocks of `threads` per SM, of as many threads in all; at least one.
+inline size_t norm_blocks_per_sm(size_t threads, size_t of)
+{
+    return threads > of ? 1 : of / threads < 16 ? of / threads : 16;
+}
+
+// Blocks of a gradient: the sizes alone decide, as the order of its sums goes by
+// them.  As many as an SM holds at once, with 128 registers per thread (96
+// without a block).
+inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem, bool block)
+{
+    const size_t threads = align_up(ceil_div(width * elem, 16), 32);
+    const size_t blocks = 152 * norm_blocks_per_sm(threads, block ? 512 : 640);
+    return (uint32_t)(rows < blocks ? rows : blocks);
+}
 
 }  // namespace rsx

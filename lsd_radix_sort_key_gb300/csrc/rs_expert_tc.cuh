@@ -238,19 +238,28 @@ __device__ __forceinline__ void round_all(uint32_t (&out)[8], const uint32_t (&z
     for (int i = 0; i < 8; ++i) out[i] = pack2<T>(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
 }
 
+// 16 elements of a bias, zeros from `left` on.
 template <typename T>
-__device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint32_t left, bool vec)
+__device__ __forceinline__ void load_bias(uint32_t (&w)[8], const T* bias, uint32_t left, bool vec)
 {
-    uint32_t w[8] = {};
     if (vec && left >= 16) {
         const uint4 lo = __ldg(reinterpret_cast<const uint4*>(bias)), hi = __ldg(reinterpret_cast<const uint4*>(bias) + 1);
         w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
         w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
     } else {
 #pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0;
+#pragma unroll
         for (int i = 0; i < 16; ++i)
             if (i < left) w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(bias)[i] << (i & 1) * 16;
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void add_bias(uint32_t (&z)[16], const T* bias, uint32_t left, bool vec)
+{
+    uint32_t w[8];
+    load_bias<T>(w, bias, left, vec);
     add_all<T>(z, w);
 }
 

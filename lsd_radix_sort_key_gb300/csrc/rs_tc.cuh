@@ -107,6 +107,9 @@ __device__ __forceinline__ bool bar_wait_cluster_warp(uint64_t* bar, uint32_t pa
 // (tensor cores, bulk copies), from either block of a pair.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+// The same for writes to shared memory alone, which do not wait for the rest.
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ---- clusters of blocks
 
 __device__ __forceinline__ uint32_t cluster_rank()
