@@ -51,14 +51,12 @@ struct F8Args {
     uint32_t stall;    // testing hook: tile stall - 1 is never copied
 };
 
-// QUANT: an epilogue thread holds a row's 128 columns, a scale block, at once, which
-// takes the registers of 12 warps.  Otherwise 16 epilogue warps of 64 columns
-// each, 16 at a time: with 8 the epilogue was what lasted (32768 x 2048 x 4096 with
-// gelu 250 us, 200 without an activation).
-template <bool PAIR, bool QUANT>
+// 16 epilogue warps of 64 columns each: with 8 the epilogue was what lasted
+// (32768 x 2048 x 4096 with gelu 250 us, 200 without an activation).
+template <bool PAIR>
 struct F8Shape {
-    static constexpr int kWarps = QUANT ? 8 : 16, kThreads = 32 * (kTcFirstEpilogueWarp + kWarps);
-    static constexpr uint32_t kWarpCols = QUANT ? 128 : 64;  // of an epilogue warp
+    static constexpr int kWarps = 16, kThreads = 32 * (kTcFirstEpilogueWarp + kWarps);
+    static constexpr uint32_t kWarpCols = 64;  // of an epilogue warp
     // a block's warps that read an accumulator: all, or those whose turn it is
     static constexpr uint32_t kReaders = PAIR ? 2 * kWarps : kWarps / 2;
     static constexpr uint32_t kCols = PAIR ? 256 : 128, kRows = PAIR ? 2 * kTcRows : kTcRows;  // of a tile
@@ -116,33 +114,50 @@ struct Scales8 {
     }
 };
 
-// This lane's row of 128 columns, from j0 on, rounded to 8 bits and stored with
-// its scale; all lanes of the warp.
-template <typename T>
-__device__ __forceinline__ void store_quantized(uint32_t (&z)[8][16], const F8Args<T>& p, uint32_t i, bool live, uint32_t j0)
+// The larger of this lane's value and that of the same lane in the warp that has the
+// other half of its columns.  mine, other: shared memory of the two warps, 32
+// words each; both come here together (barrier `id`).
+__device__ __forceinline__ uint32_t max_of_both(uint32_t v, uint32_t* mine, const uint32_t* other, uint32_t id)
 {
-    const uint32_t left = p.cols - j0;
+    mine[threadIdx.x % 32] = v;
+    rstc::meet_two_warps(id, true);
+    v = max(v, other[threadIdx.x % 32]);
+    rstc::meet_two_warps(id, true);  // both have read: the memory may be used again
+    return v;
+}
+
+// This lane's row of 64 columns from j0 on, rounded to 8 bits and stored, the scale
+// by the warp of the block's first half; all lanes of both warps.
+template <typename T>
+__device__ __forceinline__ void store_quantized(uint32_t (&z)[4][16], const F8Args<T>& p, uint32_t i, bool live, uint32_t j0,
+                                                uint32_t* mine, const uint32_t* other, uint32_t id)
+{
+    const uint32_t left = j0 < p.cols ? p.cols - j0 : 0;
+    if (left < 64) {
+#pragma unroll
+        for (uint32_t c = 0; c < 64; ++c)
+            if (c >= left) z[c / 16][c % 16] = 0;
+    }
     uint32_t most = 0;
 #pragma unroll
-    for (uint32_t c = 0; c < 128; ++c) {
-        if (c >= left) z[c / 16][c % 16] = 0;
-        most = max(most, z[c / 16][c % 16] & 0x7FFFFFFFu);
-    }
-    if (most >= kNotFinite) {
+    for (uint32_t c = 0; c < 64; ++c) most = max(most, z[c / 16][c % 16] & 0x7FFFFFFFu);
+    most = max_of_both(most, mine, other, id);
+    if (__any_sync(0xFFFFFFFFu, most >= kNotFinite)) {
         most = 0;
 #pragma unroll
-        for (uint32_t c = 0; c < 128; ++c) {
+        for (uint32_t c = 0; c < 64; ++c) {
             const float f = __uint_as_float(z[c / 16][c % 16]);
             most = max(most, magnitude(f) < kNotFinite ? magnitude(f) : 0u);
             z[c / 16][c % 16] = __float_as_uint(finite_or_nan(f));
         }
+        most = max_of_both(most, mine, other, id);
     }
     const uint32_t byte = scale_byte(most);
     const float inverse = scale_inverse(byte);
-    if (!live) return;
+    if (!live || left == 0) return;
     uint8_t* to = p.q + i * p.q_i + j0;
 #pragma unroll
-    for (uint32_t c = 0; c < 8; ++c) {
+    for (uint32_t c = 0; c < 4; ++c) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -150,17 +165,17 @@ __device__ __forceinline__ void store_quantized(uint32_t (&z)[8][16], const F8Ar
                              __uint_as_float(z[c][4 * k + 2]) * inverse, __uint_as_float(z[c][4 * k + 3]) * inverse);
         if (c * 16 < left) reinterpret_cast<uint4*>(to)[c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    p.q_scales[i * p.q_scales_i + j0 / RS_QUANT_BLOCK] = (uint8_t)byte;
+    if (j0 % RS_QUANT_BLOCK == 0) p.q_scales[i * p.q_scales_i + j0 / RS_QUANT_BLOCK] = (uint8_t)byte;
 }
 
 // A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
 // have the reduction index adjacent.  QUANT: D leaves in 8 bits.
 template <typename T, bool PAIR, bool QUANT>
-__global__ void __launch_bounds__(F8Shape<PAIR, QUANT>::kThreads, 1)
+__global__ void __launch_bounds__(F8Shape<PAIR>::kThreads, 1)
     k_product_f8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, F8Args<T> p)
 {
     using namespace rstc;
-    using S = F8Shape<PAIR, QUANT>;
+    using S = F8Shape<PAIR>;
     constexpr uint32_t BN = S::kCols;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
@@ -305,64 +320,67 @@ __global__ void __launch_bounds__(F8Shape<PAIR, QUANT>::kThreads, 1)
         }
         if (!ok) *failed = 1;
     } else if (warp == 1 && rank == 0) {
-        constexpr uint32_t kDesc = mma_scaled_desc(S::kRows, BN);
-        const uint64_t desc_a = smem_desc(smem_addr(ring), 16), desc_b = smem_desc(smem_addr(ring) + S::kA, 16);
-        const uint64_t desc_s = scales_desc(smem_addr(scales));
-        uint32_t s = 0, round = 0, n = 0, ss = 0, scale_round = 0, set = 0;
-        bool ok = true;
-        for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
-            const TcTile t = tile_at(tile);
-            if (t.k_end == 0) continue;
-            const uint32_t h = n & 1, acc = tmem + h * S::kAccStep, free = ((n >> 1) & 1) ^ 1;
-            ok = PAIR ? bar_wait_cluster_warp(acc_empty + h, free) : bar_wait_warp(acc_empty + h, free);
-            if (PAIR && ok && n) ok = bar_wait_cluster_warp(early + (h ^ 1), ((n - 1) >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            ++n;
-            for (uint32_t i = 0; i < slices; ++i) {
-                if (i % 8 == 0) {
-                    ok = PAIR ? bar_wait_cluster_warp(scales_full + ss, scale_round & 1)
-                              : bar_wait_warp(scales_full + ss, scale_round & 1);
-                    if (!ok) break;
-                }
-                if (i % 4 == 0) {
-                    set ^= 1;
-                    tc_fence_after();
-                    const bool last = i % 8 == 4 || i + 4 >= slices;  // of this stage
-                    if (elect_one()) {
+        // One thread alone: what a slice takes besides its matrix instructions has to
+        // fit in their time (with votes and elections of the whole warp 630 cycles
+        // per slice, whose instructions take 512).
+        if (elect_one()) {
+            constexpr uint32_t kDesc = mma_scaled_desc(S::kRows, BN);
+            const uint64_t desc_a = smem_desc(smem_addr(ring), 16), desc_b = smem_desc(smem_addr(ring) + S::kA, 16);
+            const uint64_t desc_s = scales_desc(smem_addr(scales));
+            uint32_t s = 0, round = 0, n = 0, ss = 0, scale_round = 0, set = 0;
+            bool ok = true;
+            auto wait_for = [](uint64_t* bar, uint32_t parity) {
+                return PAIR ? bar_wait_cluster(bar, parity) : bar_wait(bar, parity);
+            };
+            for (uint32_t tile = first_tile; ok && tile < tiles; tile += tile_step) {
+                const TcTile t = tile_at(tile);
+                if (t.k_end == 0) continue;
+                const uint32_t h = n & 1, acc = tmem + h * S::kAccStep;
+                for (uint32_t i = 0; i < slices; ++i) {
+                    if (i % 8 == 0) {
+                        ok = wait_for(scales_full + ss, scale_round & 1);
+                        if (!ok) break;
+                    }
+                    if (i % 4 == 0) {
+                        set ^= 1;
+                        tc_fence_after();
 #pragma unroll
                         for (uint32_t c = 0; c <= BN / 128; ++c)
                             tmem_copy_scales<PAIR>(tmem + S::kScaleCols + set * S::kScaleStep + c * 4,
                                                    desc_s + ((ss * S::kScaleStage + i / 4 % 2 * S::kScales + c * 512) >> 4));
-                        if (last) mma_commit<PAIR>(scales_empty + ss);
+                        if (i % 8 == 4 || i + 4 >= slices) {  // the last of this stage
+                            mma_commit<PAIR>(scales_empty + ss);
+                            if (++ss == S::kScaleStages) ss = 0, ++scale_round;
+                        }
                     }
-                    __syncwarp();
-                    if (last && ++ss == S::kScaleStages) ss = 0, ++scale_round;
-                }
-                ok = bar_wait_warp(full + s, round & 1);
-                if (!ok) break;
-                const uint32_t steps = min((p.reduce - i * kF8Depth + 31) / 32, kF8Depth / 32u);
-                const uint32_t sa = tmem + S::kScaleCols + set * S::kScaleStep, desc = kDesc | mma_scale_byte(i % 4);
-                tc_fence_after();
-                if (elect_one()) {
+                    ok = bar_wait(full + s, round & 1);
+                    if (!ok) break;
+                    if (i == 0) {  // only now: all but the accumulator is there
+                        ok = wait_for(acc_empty + h, ((n >> 1) & 1) ^ 1);
+                        if (PAIR && ok && n) ok = wait_for(early + (h ^ 1), ((n - 1) >> 1) & 1);
+                        if (!ok) break;
+                        ++n;
+                    }
+                    const uint32_t steps = min((p.reduce - i * kF8Depth + 31) / 32, kF8Depth / 32u);
+                    const uint32_t sa = tmem + S::kScaleCols + set * S::kScaleStep, desc = kDesc | mma_scale_byte(i % 4);
                     const uint64_t da = desc_a + s * (S::kStage >> 4), db = desc_b + s * (S::kStage >> 4);
+                    tc_fence_after();
 #pragma unroll
                     for (uint32_t k = 0; k < kF8Depth / 32; ++k)
                         if (k < steps) mma_e4m3_scaled<PAIR>(acc, da + k * 2, db + k * 2, desc, sa, sa + 4, i | k);
                     mma_commit<PAIR>(empty + s);
+                    if (++s == S::kStages) s = 0, ++round;
                 }
-                __syncwarp();
-                if (++s == S::kStages) s = 0, ++round;
+                if (ok) mma_commit<PAIR>(acc_full + h);
             }
-            if (ok && elect_one()) mma_commit<PAIR>(acc_full + h);
-            __syncwarp();
+            // What was issued is done before anything it uses is given up, also when
+            // the epilogue's wait for it has run out.
+            if (s || round) ok &= bar_wait(empty + (s ? s : S::kStages) - 1, (s ? round : round - 1) & 1);
+            if (ss || scale_round)
+                ok &= bar_wait(scales_empty + (ss ? ss : S::kScaleStages) - 1, (ss ? scale_round : scale_round - 1) & 1);
+            if (!ok) *failed = 1;
         }
-        // What was issued is done before anything it uses is given up, also when
-        // the epilogue's wait for it has run out.
-        if (s || round) ok &= bar_wait_warp(empty + (s ? s : S::kStages) - 1, (s ? round : round - 1) & 1);
-        if (ss || scale_round)
-            ok &= bar_wait_warp(scales_empty + (ss ? ss : S::kScaleStages) - 1, (ss ? scale_round : scale_round - 1) & 1);
-        if (!ok) *failed = 1;
+        __syncwarp();
     } else if (warp >= kTcFirstEpilogueWarp) {
         const uint32_t w = warp - kTcFirstEpilogueWarp, group = w / 4;
         const uint32_t quarter = warp % 4;  // the 32 tensor-memory lanes this warp can read
@@ -394,49 +412,44 @@ __global__ void __launch_bounds__(F8Shape<PAIR, QUANT>::kThreads, 1)
                 }
             };
             if constexpr (QUANT) {
-                uint32_t z[8][16];
+                // A scale block's two warps go through every tile together.
+                const uint32_t id = 1 + quarter + 4 * (group / 2);
+                uint32_t* mine = reinterpret_cast<uint32_t*>(stage);
+                const uint32_t* other = reinterpret_cast<const uint32_t*>(staging + (w ^ 4) * S::kStaging);
+                const bool any = i0 < t.i_end && j_first / RS_QUANT_BLOCK * RS_QUANT_BLOCK < p.cols;
+                uint32_t z[4][16] = {};
                 if (some) {
-                    if (!bar_wait_warp(acc_full + h, phase, 2 * slices)) {
+                    if (!meet_two_warps(id, bar_wait_warp(acc_full + h, phase, 2 * slices))) {
                         *failed = 1;
                         break;
                     }
                     tc_fence_after();
                     if (cols) {
 #pragma unroll
-                        for (uint32_t c = 0; c < 8; ++c) tmem_load16(z[c], acc + c * 16);
+                        for (uint32_t c = 0; c < 4; ++c) tmem_load16(z[c], acc + c * 16);
 #pragma unroll
-                        for (uint32_t c = 0; c < 8; ++c) tmem_load_wait(z[c]);
+                        for (uint32_t c = 0; c < 4; ++c) tmem_load_wait(z[c]);
                     }
                     if constexpr (PAIR) release(early);
                     release(acc_empty);
-                    if (!cols) continue;
-                    if (p.bias) {
-#pragma unroll
-                        for (uint32_t c = 0; c < 8; ++c)
-                            if (c * 16 < cols)
-                                add_bias<T>(z[c], p.bias + t.e * p.bias_e + j_first + c * 16, cols - c * 16, vec_bias);
-                    }
-                } else {
-                    if (!cols) continue;
-#pragma unroll
-                    for (uint32_t c = 0; c < 128; ++c) z[c / 16][c % 16] = 0;
                 }
-                if (p.pre) {
+                if (!any) continue;
+                const T* bias = p.bias + t.e * p.bias_e + j_first;
 #pragma unroll
-                    for (uint32_t c = 0; c < 8; ++c) {
+                for (uint32_t c = 0; c < 4; ++c) {
+                    if (c * 16 >= cols) continue;
+                    if (p.bias && some) add_bias<T>(z[c], bias + c * 16, cols - c * 16, vec_bias);
+                    if (p.pre) {
                         uint32_t out[8];
                         round_all<T>(out, z[c]);
-                        if (c * 16 < cols) store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c * 16, p.cols);
+                        store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c * 16, p.cols);
                     }
-                }
-                // (an activation of zero is zero)
-#pragma unroll
-                for (uint32_t c = 0; c < 8; ++c) {
+                    // (an activation of zero is zero)
                     if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(z[c]);
                     else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(z[c]);
                     else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(z[c]);
                 }
-                store_quantized<T>(z, p, i, i < t.i_end, j_first);
+                store_quantized<T>(z, p, i, i < t.i_end, j_first, mine, other, id);
             } else if (some) {
                 // Two pieces of 16 columns at a time: one is on its way while the other is
                 // finished.  A pair's first accumulator is read from its end, which the

@@ -110,6 +110,19 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;
 // The same for writes to shared memory alone, which do not wait for the rest.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Two warps meet at barrier `id` (1 to 15): true if both bring true.
+__device__ __forceinline__ bool meet_two_warps(uint32_t id, bool ok)
+{
+    uint32_t both;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.and.pred q, %1, 64, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(both)
+        : "r"(id), "r"((uint32_t)ok)
+        : "memory");
+    return both != 0;
+}
+
 // ---- clusters of blocks
 
 __device__ __forceinline__ uint32_t cluster_rank()
