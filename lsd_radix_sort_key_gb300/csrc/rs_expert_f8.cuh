@@ -126,46 +126,33 @@ __device__ __forceinline__ uint32_t max_of_both(uint32_t v, uint32_t* mine, cons
     return v;
 }
 
-// This lane's row of 64 columns from j0 on, rounded to 8 bits and stored, the scale
-// by the warp of the block's first half; all lanes of both warps.
-template <typename T>
-__device__ __forceinline__ void store_quantized(uint32_t (&z)[4][16], const F8Args<T>& p, uint32_t i, bool live, uint32_t j0,
-                                                uint32_t* mine, const uint32_t* other, uint32_t id)
+// The largest magnitude of 16 values, or of the finite ones among them.
+__device__ __forceinline__ uint32_t largest16(const uint32_t (&z)[16], bool finite_only)
 {
-    const uint32_t left = j0 < p.cols ? p.cols - j0 : 0;
-    if (left < 64) {
-#pragma unroll
-        for (uint32_t c = 0; c < 64; ++c)
-            if (c >= left) z[c / 16][c % 16] = 0;
-    }
     uint32_t most = 0;
 #pragma unroll
-    for (uint32_t c = 0; c < 64; ++c) most = max(most, z[c / 16][c % 16] & 0x7FFFFFFFu);
-    most = max_of_both(most, mine, other, id);
-    if (__any_sync(0xFFFFFFFFu, most >= kNotFinite)) {
-        most = 0;
+    for (uint32_t c = 0; c < 16; ++c) {
+        const uint32_t m = z[c] & 0x7FFFFFFFu;
+        most = max(most, finite_only && m >= kNotFinite ? 0u : m);
+    }
+    return most;
+}
+
+// 16 values rounded to 8 bits.
+__device__ __forceinline__ uint4 quantized16(const uint32_t (&z)[16], float inverse, bool all_finite)
+{
+    uint32_t w[4];
 #pragma unroll
-        for (uint32_t c = 0; c < 64; ++c) {
-            const float f = __uint_as_float(z[c / 16][c % 16]);
-            most = max(most, magnitude(f) < kNotFinite ? magnitude(f) : 0u);
-            z[c / 16][c % 16] = __float_as_uint(finite_or_nan(f));
+    for (int k = 0; k < 4; ++k) {
+        float f[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            f[c] = __uint_as_float(z[4 * k + c]);
+            f[c] = (all_finite ? f[c] : finite_or_nan(f[c])) * inverse;
         }
-        most = max_of_both(most, mine, other, id);
+        w[k] = to_e4m3x4(f[0], f[1], f[2], f[3]);
     }
-    const uint32_t byte = scale_byte(most);
-    const float inverse = scale_inverse(byte);
-    if (!live || left == 0) return;
-    uint8_t* to = p.q + i * p.q_i + j0;
-#pragma unroll
-    for (uint32_t c = 0; c < 4; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = to_e4m3x4(__uint_as_float(z[c][4 * k]) * inverse, __uint_as_float(z[c][4 * k + 1]) * inverse,
-                             __uint_as_float(z[c][4 * k + 2]) * inverse, __uint_as_float(z[c][4 * k + 3]) * inverse);
-        if (c * 16 < left) reinterpret_cast<uint4*>(to)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (j0 % RS_QUANT_BLOCK == 0) p.q_scales[i * p.q_scales_i + j0 / RS_QUANT_BLOCK] = (uint8_t)byte;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
@@ -412,12 +399,18 @@ __global__ void __launch_bounds__(F8Shape<PAIR>::kThreads, 1)
                 }
             };
             if constexpr (QUANT) {
-                // A scale block's two warps go through every tile together.
+                // A scale block's two warps go through every tile together.  The values
+                // are gone through twice, first for the largest: two of a warp's four
+                // pieces (those that a pair's next accumulator overlaps) wait in registers
+                // and two in tensor memory.  With all four in registers some went to
+                // local memory, whose path the operands of the matrix instructions fill:
+                // 4000 cycles for the largest of 64 values.
                 const uint32_t id = 1 + quarter + 4 * (group / 2);
                 uint32_t* mine = reinterpret_cast<uint32_t*>(stage);
                 const uint32_t* other = reinterpret_cast<const uint32_t*>(staging + (w ^ 4) * S::kStaging);
-                const bool any = i0 < t.i_end && j_first / RS_QUANT_BLOCK * RS_QUANT_BLOCK < p.cols;
-                uint32_t z[4][16] = {};
+                const bool down = PAIR && h == 0;
+                auto col = [&](uint32_t c) { return (down ? 3 - c : c) * 16; };
+                uint32_t kept[2][16], z[16];
                 if (some) {
                     if (!meet_two_warps(id, bar_wait_warp(acc_full + h, phase, 2 * slices))) {
                         *failed = 1;
@@ -425,31 +418,90 @@ __global__ void __launch_bounds__(F8Shape<PAIR>::kThreads, 1)
                     }
                     tc_fence_after();
                     if (cols) {
-#pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c) tmem_load16(z[c], acc + c * 16);
-#pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c) tmem_load_wait(z[c]);
+                        tmem_load16(kept[0], acc + col(0));
+                        tmem_load16(kept[1], acc + col(1));
+                        tmem_load_wait(kept[0]);
+                        tmem_load_wait(kept[1]);
                     }
                     if constexpr (PAIR) release(early);
-                    release(acc_empty);
                 }
-                if (!any) continue;
-                const T* bias = p.bias + t.e * p.bias_e + j_first;
+                if (i0 >= t.i_end || j_first / RS_QUANT_BLOCK * RS_QUANT_BLOCK >= p.cols) {  // nothing for either warp
+                    if (some) release(acc_empty);
+                    continue;
+                }
+                // the epilogue of a piece; columns past the matrix count as zero
+                auto finish = [&](uint32_t c, uint32_t (&v)[16]) {
+                    if (col(c) >= cols || !some) {
 #pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) {
-                    if (c * 16 >= cols) continue;
-                    if (p.bias && some) add_bias<T>(z[c], bias + c * 16, cols - c * 16, vec_bias);
+                        for (uint32_t k = 0; k < 16; ++k) v[k] = 0;
+                        if (col(c) >= cols) return;
+                    }
+                    const uint32_t j = j_first + col(c), left = cols - col(c);
+                    if (p.bias && some) add_bias<T>(v, p.bias + t.e * p.bias_e + j, left, vec_bias);
                     if (p.pre) {
                         uint32_t out[8];
-                        round_all<T>(out, z[c]);
-                        store_piece<T>(stage, out, pre, i0, t.i_end, j_first + c * 16, p.cols);
+                        round_all<T>(out, v);
+                        store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                     }
                     // (an activation of zero is zero)
-                    if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(z[c]);
-                    else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(z[c]);
-                    else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(z[c]);
+                    if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(v);
+                    else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(v);
+                    else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(v);
+                    if (left < 16)
+#pragma unroll
+                        for (uint32_t k = 0; k < 16; ++k)
+                            if (k >= left) v[k] = 0;
+                };
+                uint32_t most = 0;
+#pragma unroll 1
+                for (uint32_t c = 2; c < 4; ++c) {
+                    if (some && cols) {
+                        tmem_load16(z, acc + col(c));
+                        tmem_load_wait(z);
+                    }
+                    finish(c, z);
+                    most = max(most, largest16(z, false));
+                    if (some && cols) tmem_store16(acc + col(c), z);
                 }
-                store_quantized<T>(z, p, i, i < t.i_end, j_first, mine, other, id);
+#pragma unroll
+                for (uint32_t c = 0; c < 2; ++c) {
+                    finish(c, kept[c]);
+                    most = max(most, largest16(kept[c], false));
+                }
+                tmem_store_wait();
+                most = max_of_both(most, mine, other, id);
+                const bool all_finite = !__any_sync(0xFFFFFFFFu, most >= kNotFinite);
+                auto again = [&](uint32_t c) {  // a piece from tensor memory
+                    if (some && cols) {
+                        tmem_load16(z, acc + col(c));
+                        tmem_load_wait(z);
+                    }
+                };
+                if (!all_finite) {
+                    most = max(largest16(kept[0], true), largest16(kept[1], true));
+#pragma unroll 1
+                    for (uint32_t c = 2; c < 4; ++c) {
+                        again(c);
+                        most = max(most, largest16(z, true));
+                    }
+                    most = max_of_both(most, mine, other, id);
+                }
+                const uint32_t byte = scale_byte(most);
+                const float inverse = scale_inverse(byte);
+                const bool live = i < t.i_end;
+                auto put = [&](uint32_t c, const uint32_t (&v)[16]) {
+                    const uint4 q = quantized16(v, inverse, all_finite);
+                    if (live && col(c) < cols) *reinterpret_cast<uint4*>(p.q + i * p.q_i + j_first + col(c)) = q;
+                };
+#pragma unroll 1
+                for (uint32_t c = 2; c < 4; ++c) {
+                    again(c);
+                    if (c == 3 && some) release(acc_empty);
+                    put(c, z);
+                }
+                put(0, kept[0]);
+                put(1, kept[1]);
+                if (live && j_first % RS_QUANT_BLOCK == 0) p.q_scales[i * p.q_scales_i + j_first / RS_QUANT_BLOCK] = (uint8_t)byte;
             } else if (some) {
                 // Two pieces of 16 columns at a time: one is on its way while the other is
                 // finished.  A pair's first accumulator is read from its end, which the

@@ -282,6 +282,19 @@ __device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[16])
                  : "memory");
 }
 
+// The reverse of tmem_load16; tmem_store_wait before the columns are read again.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---- the matrix instruction
 
 // D (tensor memory, float32) = or += A B^T for K = 16 of 16-bit elements.
