@@ -44,4 +44,80 @@ __device__ __forceinline__ float finite_or_nan(float f)
     return magnitude(f) == kNotFinite ? __uint_as_float(0x7FC00000u) : f;
 }
 
+// ---- values as they are loaded: 32-bit words of one float32 or two 16-bit elements
+
+// The larger of `most` and the magnitudes in a word, in the elements' own bits (which
+// are ordered as the magnitudes are); 16-bit ones by halves of the word.
+template <typename T>
+__device__ __forceinline__ uint32_t larger(uint32_t most, uint32_t word)
+{
+    if constexpr (sizeof(T) == 4) return max(most, word & 0x7FFFFFFFu);
+    else return __vmaxu2(most, word & 0x7FFF7FFFu);
+}
+
+// Such a maximum as float bits.
+template <typename T>
+__device__ __forceinline__ uint32_t largest_bits(uint32_t most)
+{
+    if constexpr (sizeof(T) == 4) {
+        return most;
+    } else {
+        const uint16_t m = (uint16_t)max(most & 0xFFFFu, most >> 16);
+        if constexpr (__is_same(T, __half)) return __float_as_uint(__half2float(__ushort_as_half(m)));
+        else return (uint32_t)m << 16;
+    }
+}
+
+// An element's bits: those from here on are infinite or NaN.
+template <typename T>
+constexpr uint32_t kNotFiniteBits = sizeof(T) == 4 ? kNotFinite : __is_same(T, __half) ? 0x7C00u : 0x7F80u;
+
+// `larger` over the finite elements alone.
+template <typename T>
+__device__ __forceinline__ uint32_t larger_finite(uint32_t most, uint32_t word)
+{
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t m = word & 0x7FFFFFFFu;
+        return m < kNotFinite ? max(most, m) : most;
+    } else {
+        const uint32_t lo = word & 0x7FFFu, hi = word >> 16 & 0x7FFFu;
+        return __vmaxu2(most, (lo < kNotFiniteBits<T> ? lo : 0u) | (hi < kNotFiniteBits<T> ? hi : 0u) << 16);
+    }
+}
+
+// The word with NaN in place of infinities.
+template <typename T>
+__device__ __forceinline__ uint32_t without_infinities(uint32_t word)
+{
+    if constexpr (sizeof(T) == 4) {
+        return __float_as_uint(finite_or_nan(__uint_as_float(word)));
+    } else {
+        if ((word & 0x7FFFu) == kNotFiniteBits<T>) word |= 1u;
+        if ((word >> 16 & 0x7FFFu) == kNotFiniteBits<T>) word |= 0x10000u;
+        return word;
+    }
+}
+
+// Four elements, scaled and rounded.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize4(const uint32_t* w, float inverse)
+{
+    if constexpr (sizeof(T) == 4) {
+        return to_e4m3x4(__uint_as_float(w[0]) * inverse, __uint_as_float(w[1]) * inverse, __uint_as_float(w[2]) * inverse,
+                         __uint_as_float(w[3]) * inverse);
+    } else {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (__is_same(T, __half)) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = v.x, f[2 * i + 1] = v.y;
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+        return to_e4m3x4(f[0] * inverse, f[1] * inverse, f[2] * inverse, f[3] * inverse);
+    }
+}
+
 }  // namespace rsx

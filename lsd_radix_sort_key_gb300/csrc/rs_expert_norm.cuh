@@ -136,17 +136,101 @@ __device__ __forceinline__ void clear_sums(float* mem)
     __syncthreads();
 }
 
-template <typename T, int N, int V>
-struct NormRow {
-    Vec<T, N> v[V];
-    __device__ __forceinline__ void load(const T* row, uint32_t width)
+// Asynchronous copies of 16 bytes to shared memory, waited for in groups.
+__device__ __forceinline__ void copy16(void* to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>  // all but the last LATER groups have arrived
+__device__ __forceinline__ void wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
+
+// This thread's columns of the rows that a block walks: STREAMS matrices, V accesses
+// of N elements each.  DEPTH > 0: rows are copied to shared memory DEPTH - 1 rows
+// ahead, each thread's part by itself and for itself, so no barrier is needed.
+// DEPTH 0 (single elements, or rows too wide): one row ahead, in registers.
+// With one row ahead the SMs had too few bytes in flight (16384 x 2048 bf16: forward
+// 63 us, gradient 182).
+template <typename T, int N, int V, int STREAMS, int DEPTH>
+struct Feed {
+    Vec<T, N> now[DEPTH ? 1 : STREAMS][V], next[DEPTH ? 1 : STREAMS][V];
+    unsigned char* ring;  // [DEPTH][STREAMS][V][threads] of 16 bytes
+    uint32_t slot;
+
+    static constexpr size_t smem(size_t threads) { return (size_t)DEPTH * STREAMS * V * threads * 16; }
+
+    __device__ __forceinline__ void* at(uint32_t s, int stream, int i) const
+    {
+        return ring + ((((s * STREAMS + stream) * V + i) * blockDim.x) + threadIdx.x) * 16;
+    }
+    __device__ __forceinline__ void clear(unsigned char* mem)
+    {
+        ring = mem;
+        slot = 0;
+        if constexpr (DEPTH > 0) {
+            for (uint32_t s = 0; s < DEPTH; ++s)
+#pragma unroll
+                for (int k = 0; k < STREAMS; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) *static_cast<uint4*>(at(s, k, i)) = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int k = 0; k < STREAMS; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) next[k][i] = Vec<T, N>{};
+        }
+    }
+    // source(k, r): row r of matrix k, or nullptr if there is none (it reads as zero).
+    template <typename F>
+    __device__ __forceinline__ void fetch(F source, uint32_t r, uint32_t to, uint32_t width)
     {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t c = (i * blockDim.x + threadIdx.x) * N;
-            v[i] = Vec<T, N>{};
-            if (c < width) v[i] = load_vec<T, N>(row + c);
+        for (int k = 0; k < STREAMS; ++k) {
+            const T* row = source(k, r);
+            if (!row) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t c = (i * blockDim.x + threadIdx.x) * N;
+                if (c >= width) continue;
+                if constexpr (DEPTH > 0) copy16(at(to, k, i), row + c);
+                else next[k][i] = load_vec<T, N>(row + c);
+            }
         }
+    }
+    template <typename F>
+    __device__ __forceinline__ void start(F source, uint32_t first, uint32_t last, uint32_t width)
+    {
+        if constexpr (DEPTH > 0) {
+#pragma unroll
+            for (uint32_t d = 0; d + 1 < DEPTH; ++d) {
+                if (first + d < last) fetch(source, first + d, d, width);
+                end_group();
+            }
+        } else {
+            fetch(source, first, 0, width);
+        }
+    }
+    // Row r is there afterwards.
+    template <typename F>
+    __device__ __forceinline__ void turn_to(F source, uint32_t r, uint32_t first, uint32_t last, uint32_t width)
+    {
+        if constexpr (DEPTH > 0) {
+            slot = r == first ? 0 : slot + 1 == DEPTH ? 0 : slot + 1;
+            if (r + DEPTH - 1 < last) fetch(source, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, width);
+            end_group();
+            wait_groups<DEPTH - 1>();
+        } else {
+#pragma unroll
+            for (int k = 0; k < STREAMS; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) now[k][i] = next[k][i];
+            if (r + 1 < last) fetch(source, r + 1, 0, width);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[N], int stream, int i) const
+    {
+        if constexpr (DEPTH > 0) widen<T, N>(f, *static_cast<const Vec<T, N>*>(at(slot, stream, i)));
+        else widen<T, N>(f, now[stream][i]);
     }
 };
 
@@ -183,33 +267,36 @@ __host__ __device__ inline uint32_t first_row(uint32_t block, uint32_t blocks, u
     return (uint32_t)((uint64_t)block * rows / blocks);
 }
 
-// Each block walks adjacent rows, V accesses of N elements per thread, the next
-// row's loads in flight while it sums over this one.  The parameters' columns
-// stay in registers (a gate's until it changes): reading them again for every
-// row, 24 KB beside a row's 16 of 2048 bf16, took 70 us where this takes NNN
-// (16384 x 2048 bf16 with everything, float32 parameters).
-template <typename T, int N, int V, int THREADS, bool BLOCK>
+// Rows copied ahead by each call.
+constexpr int kNormDepth = 4, kGradDepth = 4;
+constexpr size_t kNormSmem = 128 * 1024;  // the most that a block's rows take: 512 threads, 4 matrices
+
+// 1 / sqrt(mean + eps); the hardware's root is off by two ulps at most.
+__device__ __forceinline__ float inverse_root(float sum, float per_width, float eps) { return rsqrtf(fmaf(sum, per_width, eps)); }
+
+// Each block walks adjacent rows.  The parameters' columns stay in registers (a
+// gate's until it changes): reading them again for every row is 24 KB beside a
+// row's 16 (2048 bf16, float32 parameters).
+template <typename T, int N, int V, int THREADS, bool BLOCK, int DEPTH>
 __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(NormArgs<T> p)
 {
     __shared__ __align__(16) float mem[2 * 3 * 32];
+    extern __shared__ __align__(16) unsigned char ring[];
     clear_sums(mem);
     const uint32_t first = first_row(blockIdx.x, gridDim.x, p.rows), last = first_row(blockIdx.x + 1, gridDim.x, p.rows);
     const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
     uint32_t turn = 0, gate = first / per_gate, gate_end = (gate + 1) * per_gate;
     float w[V][N], gw[BLOCK ? V : 1][N];
-    NormRow<T, N, V> next_x, next_b;
-    auto fetch = [&](uint32_t r) {
-        next_x.load(p.x + r * p.x_i, p.width);
-        if constexpr (BLOCK) next_b.load(p.block + r * p.block_i, p.width);
-    };
-    fetch(first);
+    Feed<T, N, V, BLOCK ? 2 : 1, DEPTH> feed;
+    auto source = [&](int k, uint32_t r) -> const T* { return k == 0 ? p.x + r * p.x_i : p.block + r * p.block_i; };
+    feed.clear(ring);
+    feed.start(source, first, last, p.width);
     load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
     if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
     for (uint32_t r = first; r < last; ++r) {
-        NormRow<T, N, V> x = next_x, b;
-        if constexpr (BLOCK) b = next_b;
-        if (r + 1 < last) fetch(r + 1);
+        feed.turn_to(source, r, first, last, p.width);
         float s[1] = {};
+        Vec<T, N> y[V];  // as it is held
         if constexpr (BLOCK) {
             if (r == gate_end) {
                 ++gate;
@@ -221,42 +308,44 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
-                    widen<T, N>(f, b.v[i]);
+                    feed.get(f, 1, i);
 #pragma unroll
                     for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
                 }
                 block_sums(s, mem, turn);
-                rb = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
+                rb = inverse_root(s[0], p.per_width, p.eps);
             }
             s[0] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                 float f[N], u[N];
-                widen<T, N>(f, x.v[i]);
-                widen<T, N>(u, b.v[i]);
+                feed.get(f, 0, i);
+                feed.get(u, 1, i);
 #pragma unroll
                 for (int c = 0; c < N; ++c) u[c] = fmaf(p.scale, f[c], u[c] * rb * gw[i][c]);
-                x.v[i] = narrow<T, N>(u);  // y as it is held
-                if (c0 < p.width) store_vec<T, N>(p.y + r * p.y_i + c0, x.v[i]);
+                y[i] = narrow<T, N>(u);
+                if (c0 < p.width) store_vec<T, N>(p.y + r * p.y_i + c0, y[i]);
             }
             if (!p.weight) continue;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N];
-            widen<T, N>(f, x.v[i]);
+            if constexpr (BLOCK) widen<T, N>(f, y[i]);
+            else feed.get(f, 0, i);
 #pragma unroll
             for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
         }
         block_sums(s, mem, turn);
-        const float rx = 1.0f / sqrtf(fmaf(s[0], p.per_width, p.eps));
+        const float rx = inverse_root(s[0], p.per_width, p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
             if (c0 >= p.width) continue;
             float f[N];
-            widen<T, N>(f, x.v[i]);
+            if constexpr (BLOCK) widen<T, N>(f, y[i]);
+            else feed.get(f, 0, i);
 #pragma unroll
             for (int c = 0; c < N; ++c) f[c] *= rx * w[i][c];
             store_vec<T, N>(p.h + r * p.h_i + c0, narrow<T, N>(f));
@@ -268,29 +357,30 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
 // summed gradients in registers.  Within one gate row, with n = block r,
 //     dgate = block_weight S,  dblock_weight += gate S,  S = the sum of d n,
 // so one sum serves both until the gate changes.
-template <typename T, int N, int V, int THREADS, bool BLOCK>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(NormArgs<T> p)
+template <typename T, int N, int V, int THREADS, bool BLOCK, int DEPTH>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(NormArgs<T> p)
 {
     __shared__ __align__(16) float mem[2 * 3 * 32];
+    extern __shared__ __align__(16) unsigned char ring[];
     start_next_grid();
     clear_sums(mem);
     const uint32_t first = first_row(blockIdx.x, gridDim.x, p.rows), last = first_row(blockIdx.x + 1, gridDim.x, p.rows);
     const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
     uint32_t turn = 0, gate = first / per_gate, gate_end = (gate + 1) * per_gate;
     constexpr int VB = BLOCK ? V : 1;
+    enum { kY, kDh, kDy, kB };
     float w[V][N], gw[VB][N], dw[V][N] = {}, db[VB][N] = {}, sum[VB][N] = {};
-    NormRow<T, N, V> next_y, next_dh, next_dy, next_b;
-    auto fetch = [&](uint32_t r) {
-        if (p.dh) {
-            next_y.load(p.x + r * p.x_i, p.width);
-            next_dh.load(p.dh + r * p.dh_i, p.width);
+    Feed<T, N, V, BLOCK ? 4 : 3, DEPTH> feed;
+    auto source = [&](int k, uint32_t r) -> const T* {
+        switch (k) {
+        case kY: return p.dh ? p.x + r * p.x_i : nullptr;
+        case kDh: return p.dh ? p.dh + r * p.dh_i : nullptr;
+        case kDy: return p.dy ? p.dy + r * p.dy_i : nullptr;
+        default: return p.block + r * p.block_i;
         }
-        if (p.dy) next_dy.load(p.dy + r * p.dy_i, p.width);
-        if constexpr (BLOCK) next_b.load(p.block + r * p.block_i, p.width);
     };
-#pragma unroll
-    for (int i = 0; i < V; ++i) next_y.v[i] = next_dh.v[i] = next_dy.v[i] = Vec<T, N>{};
-    fetch(first);
+    feed.clear(ring);
+    feed.start(source, first, last, p.width);
     load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
     if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
     auto store_part = [&](int kind, int i, const float (&f)[N]) {
@@ -305,40 +395,37 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(N
         }
     };
     for (uint32_t r = first; r < last; ++r) {
-        const NormRow<T, N, V> y = next_y, dh = next_dh, dy = next_dy;
-        NormRow<T, N, V> b;
-        if constexpr (BLOCK) b = next_b;
-        if (r + 1 < last) fetch(r + 1);
+        feed.turn_to(source, r, first, last, p.width);
         float sums[3] = {};  // y^2, <g, y>, block^2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N], g[N];
-            widen<T, N>(f, y.v[i]);
-            widen<T, N>(g, dh.v[i]);
+            feed.get(f, kY, i);
+            feed.get(g, kDh, i);
 #pragma unroll
             for (int c = 0; c < N; ++c) {
                 sums[0] = fmaf(f[c], f[c], sums[0]);
                 sums[1] = fmaf(g[c] * w[i][c], f[c], sums[1]);
             }
             if constexpr (BLOCK) {
-                widen<T, N>(f, b.v[i]);
+                feed.get(f, kB, i);
 #pragma unroll
                 for (int c = 0; c < N; ++c) sums[2] = fmaf(f[c], f[c], sums[2]);
             }
         }
         block_sums(sums, mem, turn);
-        const float rx = p.dh ? 1.0f / sqrtf(fmaf(sums[0], p.per_width, p.eps)) : 0.0f;
+        const float rx = p.dh ? inverse_root(sums[0], p.per_width, p.eps) : 0.0f;
         const float kx = rx * rx * rx * p.per_width * sums[1];
-        const float rb = BLOCK && p.block_weight ? 1.0f / sqrtf(fmaf(sums[2], p.per_width, p.eps)) : 1.0f;
+        const float rb = BLOCK && p.block_weight ? inverse_root(sums[2], p.per_width, p.eps) : 1.0f;
         float dot[1] = {};  // <du, block>
         float du[VB][N];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
             float f[N], g[N], d[N];
-            widen<T, N>(f, y.v[i]);
-            widen<T, N>(g, dh.v[i]);
-            widen<T, N>(d, dy.v[i]);
+            feed.get(f, kY, i);
+            feed.get(g, kDh, i);
+            feed.get(d, kDy, i);
 #pragma unroll
             for (int c = 0; c < N; ++c) {
                 d[c] = fmaf(rx * w[i][c], g[c], fmaf(-kx, f[c], d[c]));
@@ -347,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(N
             }
             if (p.dx && c0 < p.width) store_vec<T, N>(p.dx + r * p.dx_i + c0, narrow<T, N>(g));
             if constexpr (BLOCK) {
-                widen<T, N>(f, b.v[i]);
+                feed.get(f, kB, i);
 #pragma unroll
                 for (int c = 0; c < N; ++c) {
                     sum[i][c] = fmaf(d[c], f[c] * rb, sum[i][c]);
@@ -367,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(N
                 for (int i = 0; i < V; ++i) {
                     const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                     float f[N];
-                    widen<T, N>(f, b.v[i]);
+                    feed.get(f, kB, i);
 #pragma unroll
                     for (int c = 0; c < N; ++c) f[c] = fmaf(rb, du[i][c], -kb * f[c]);
                     if (c0 < p.width) store_vec<T, N>(p.dblock + r * p.dblock_i + c0, narrow<T, N>(f));
@@ -420,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) k_norm_grad(N
 // The summed gradients from the blocks' parts, in the blocks' order: job 0
 // dweight, 1 dblock_weight, 2 + g gate row g (or, with fewer blocks than gate
 // rows, the one that block g shares with the next).
-constexpr int kFinishCols = 32, kFinishRows = 16;
+constexpr int kFinishCols = 32, kFinishRows = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(kFinishCols* kFinishRows) k_norm_finish(NormArgs<T> p, uint32_t blocks, bool by_gate)
@@ -478,19 +565,15 @@ rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s);
 template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s);
 
-// Blocks of `threads` per SM, of as many threads in all; at least one.
-inline size_t norm_blocks_per_sm(size_t threads, size_t of)
-{
-    return threads > of ? 1 : of / threads < 16 ? of / threads : 16;
-}
-
 // Blocks of a gradient: the sizes alone decide, as the order of its sums goes by
-// them.  As many as an SM holds at once, with 128 registers per thread (96
-// without a block).
-inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem, bool block)
+// them.  As many as an SM holds at once, of one thread per 16 bytes of a row (512
+// at most): by their registers 768 threads' worth where rows have up to 256
+// vectors or are no whole number of vectors, else one block.
+inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem)
 {
     const size_t threads = align_up(ceil_div(width * elem, 16), 32);
-    const size_t blocks = 152 * norm_blocks_per_sm(threads, block ? 512 : 640);
+    const bool many = threads <= 256 || (width * elem % 16 && width <= 2048);
+    const size_t per = many && threads <= 384 ? 768 / threads : 1, blocks = 152 * (per < 8 ? per : 8);
     return (uint32_t)(rows < blocks ? rows : blocks);
 }
 

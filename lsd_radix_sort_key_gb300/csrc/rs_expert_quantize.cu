@@ -18,10 +18,10 @@ constexpr int kUnits = kThreads / kLanes;  // blocks of rows that a thread block
 // 16 adjacent elements of a row, as loaded: 2 or 4 vectors.
 template <typename T, bool SHIFT>
 struct Sixteen {
-    static constexpr int N = kVec<T>, C = 16 / N;
+    static constexpr int N = kVec<T>, C = 16 / N, W = 16 * (int)sizeof(T) / 4;
     Vec<T, N> v[C];
     // Rows whose vectors are whole and aligned.
-    __device__ __forceinline__ void load(const T* row, uint32_t at, uint32_t width)
+    __device__ __forceinline__ void load(const T* row, uint32_t at, uint32_t width, const T*, const T*)
     {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -29,14 +29,12 @@ struct Sixteen {
             if (at + i * N < width) v[i] = load_vec<T, N>(row + at + i * N);
         }
     }
-    __device__ __forceinline__ void get(float (&f)[16], const T*, uint32_t, uint32_t) const
+    __device__ __forceinline__ void get(uint32_t (&w)[W], const T*, uint32_t, uint32_t) const
     {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            float part[N];
-            to_floats<T>(part, v[i]);
-#pragma unroll
-            for (int j = 0; j < N; ++j) f[i * N + j] = part[j];
+            const uint4 u = *reinterpret_cast<const uint4*>(&v[i]);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
         }
     }
 };
@@ -44,27 +42,32 @@ struct Sixteen {
 // Rows that are only element-aligned: from the aligned vectors around them.
 template <typename T>
 struct Sixteen<T, true> {
-    static constexpr int N = kVec<T>, C = 16 / N;
+    static constexpr int N = kVec<T>, C = 16 / N, W = 16 * (int)sizeof(T) / 4;
     Shifted<T> v[C];
     __device__ __forceinline__ void load(const T* row, uint32_t at, uint32_t, const T* begin, const T* end)
     {
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i].load(row + at + i * N, begin, end);
     }
-    __device__ __forceinline__ void get(float (&f)[16], const T* row, uint32_t at, uint32_t width) const
+    __device__ __forceinline__ void get(uint32_t (&w)[W], const T* row, uint32_t at, uint32_t width) const
     {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            float part[N];
-            to_floats<T>(part, v[i].get(row, (int)(at + i * N), (int)width));
-            clear_outside<T>(part, (int)(at + i * N), (int)width);
+            const Vec<T, N> r = v[i].get(row, (int)(at + i * N), (int)width);
+            const uint4 u = *reinterpret_cast<const uint4*>(&r);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+        if (at + 16 <= width) return;
 #pragma unroll
-            for (int j = 0; j < N; ++j) f[i * N + j] = part[j];
+        for (int i = 0; i < W; ++i) {  // zeros past the row's end
+            constexpr uint32_t per = 4 / sizeof(T);
+            if (at + i * per >= width) w[i] = 0;
+            else if (per == 2 && at + i * per + 1 >= width) w[i] &= 0xFFFFu;
         }
     }
 };
 
-// The largest magnitude (float bits) over a block's lanes.
+// The largest magnitude over a block's lanes.
 __device__ __forceinline__ uint32_t max_of_lanes(uint32_t m)
 {
 #pragma unroll
@@ -73,29 +76,30 @@ __device__ __forceinline__ uint32_t max_of_lanes(uint32_t m)
 }
 
 // A block's 16 elements of this lane, rounded; *byte receives the scale.
-__device__ __forceinline__ uint4 quantize16(float (&f)[16], uint32_t* byte)
+template <typename T>
+__device__ __forceinline__ uint4 quantize16(uint32_t (&w)[16 * sizeof(T) / 4], uint32_t* byte)
 {
+    constexpr int W = 16 * sizeof(T) / 4;
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) most = max(most, magnitude(f[i]));
-    most = max_of_lanes(most);
-    // (blocks of a warp agree on whether to go on, as the lanes' maximum does)
+    for (int i = 0; i < W; ++i) most = larger<T>(most, w[i]);
+    most = max_of_lanes(largest_bits<T>(most));
+    // (the warp's other blocks come along)
     if (__any_sync(0xFFFFFFFFu, most >= kNotFinite)) {
         most = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            most = max(most, magnitude(f[i]) < kNotFinite ? magnitude(f[i]) : 0u);
-            f[i] = finite_or_nan(f[i]);
+        for (int i = 0; i < W; ++i) {
+            most = larger_finite<T>(most, w[i]);
+            w[i] = without_infinities<T>(w[i]);
         }
-        most = max_of_lanes(most);
+        most = max_of_lanes(largest_bits<T>(most));
     }
     *byte = scale_byte(most);
     const float inverse = scale_inverse(*byte);
-    uint32_t w[4];
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = to_e4m3x4(f[4 * i] * inverse, f[4 * i + 1] * inverse, f[4 * i + 2] * inverse, f[4 * i + 3] * inverse);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) q[i] = quantize4<T>(w + i * (W / 4), inverse);
+    return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 template <typename T>
@@ -137,8 +141,7 @@ __global__ void __launch_bounds__(kThreads) k_quantize_rows(RowArgs<T> p)
         row[v] = u / p.blocks;
         at[v] = (u - row[v] * p.blocks) * RS_QUANT_BLOCK + lane * 16;
         const T* from = p.x + row[v] * p.x_stride;
-        if constexpr (SHIFT) raw[v].load(from, at[v], p.width, p.x, p.x_end);
-        else raw[v].load(from, at[v], p.width);
+        raw[v].load(from, at[v], p.width, p.x, p.x_end);
         if constexpr (DISPATCH) {
             place[v] = 0xFFFFFFFFu;
             if (lane < p.slots) place[v] = (uint32_t)__ldg(p.position + (size_t)row[v] * p.slots + lane);
@@ -146,10 +149,9 @@ __global__ void __launch_bounds__(kThreads) k_quantize_rows(RowArgs<T> p)
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float f[16];
-        raw[v].get(f, p.x + row[v] * p.x_stride, at[v], p.width);
-        uint32_t byte;
-        const uint4 q = quantize16(f, &byte);
+        uint32_t w[16 * sizeof(T) / 4], byte;
+        raw[v].get(w, p.x + row[v] * p.x_stride, at[v], p.width);
+        const uint4 q = quantize16<T>(w, &byte);
         const bool live = first + v * kUnits < p.units;
         auto write = [&](uint32_t r, const uint4& values, uint32_t scale) {
             if (at[v] < p.width) *reinterpret_cast<uint4*>(p.q + r * p.q_stride + at[v]) = values;
@@ -202,101 +204,99 @@ struct WeightArgs {
     uint8_t* scales;
 };
 
-// One block of 128 x 128 weights per thread block.  A thread holds 8 x 8 of
-// them.  K adjacent in memory: 8 rows, 16 apart, of 8 adjacent elements, which
-// go out as they came in.  N adjacent (BY_N): 8 adjacent rows of n in 8 adjacent
-// k, so that what it holds along k for one n is 8 bytes of an output row; these
-// pass through shared memory, whose 8-byte slots are permuted by n so that
-// neither side has bank conflicts.  VEC: 16-byte loads, else single elements.
-// Values stay as they were loaded until they are rounded: widened at once they
-// took 155 registers, one block per SM and 114 us for 16 x 4096 x 2048 bf16.
+constexpr int kWeightThreads = 512;
+
+// One block of 128 x 128 weights per thread block.  A thread holds 4 x 8 of
+// them, as they were loaded until they are rounded.  K adjacent in memory: 4 rows,
+// 32 apart, of 8 adjacent elements, which go out as they came in.  N adjacent
+// (BY_N): 8 adjacent rows of n in 4 adjacent k, so that what it holds along k for
+// one n is 4 bytes of an output row; these pass through shared memory, whose
+// words are permuted by n so that neither side has bank conflicts.  VEC: 16-byte
+// loads, else single elements.
 template <typename T, bool BY_N, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) k_quantize_weights(WeightArgs<T> p)
+__global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 4 ? 2 : 3) k_quantize_weights(WeightArgs<T> p)
 {
-    constexpr int N = kVec<T>;
-    __shared__ uint32_t largest[kThreads / 32];
+    constexpr int N = kVec<T>, WARPS = kWeightThreads / 32;
+    __shared__ uint32_t largest[WARPS];
     __shared__ uint64_t turned[BY_N ? 128 * 16 : 1];
     const uint32_t per = p.down * p.across, e = blockIdx.x / per, b = blockIdx.x - e * per;
     const uint32_t n0 = b / p.across * 128, k0 = (b - b / p.across * p.across) * 128;
     const uint32_t hi = threadIdx.x / 16, lo = threadIdx.x % 16;
     const T* w = p.w + e * p.w_e;
-    // the 8 elements of step i: (n, k) of the first, and along which side
-    auto n_of = [&](int i) { return n0 + (BY_N ? lo * 8 : hi + 16 * i); };
-    auto k_of = [&](int i) { return k0 + (BY_N ? hi * 8 + i : lo * 8); };
-    Vec<T, N> raw[8][8 / N];
+    // the 8 elements of step i: (n, k) of the first
+    auto n_of = [&](int i) { return n0 + (BY_N ? lo * 8 : hi + 32 * i); };
+    auto k_of = [&](int i) { return k0 + (BY_N ? hi * 4 + i : lo * 8); };
+    constexpr int W = 8 * sizeof(T) / 4;  // words of 8 elements
+    uint32_t raw[4][W];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < 8 / N; ++c) {
-            raw[i][c] = Vec<T, N>{};
+            Vec<T, N> v{};
             const uint32_t n = n_of(i) + (BY_N ? c * N : 0), k = k_of(i) + (BY_N ? 0 : c * N);
             if constexpr (VEC) {
-                if (n < p.outer && k < p.inner) raw[i][c] = load_vec<T, N>(w + n * p.w_n + k * p.w_k);
+                if (n < p.outer && k < p.inner) v = load_vec<T, N>(w + n * p.w_n + k * p.w_k);
             } else {
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     const uint32_t nn = n + (BY_N ? j : 0), kk = k + (BY_N ? 0 : j);
-                    if (nn < p.outer && kk < p.inner) raw[i][c].v[j] = w[nn * p.w_n + kk * p.w_k];
+                    if (nn < p.outer && kk < p.inner) v.v[j] = w[nn * p.w_n + kk * p.w_k];
                 }
             }
+            const uint4 u = *reinterpret_cast<const uint4*>(&v);
+            raw[i][4 * c] = u.x, raw[i][4 * c + 1] = u.y, raw[i][4 * c + 2] = u.z, raw[i][4 * c + 3] = u.w;
         }
-    float s = 0.0f;  // 1 / scale, once that is known
-    bool all_finite = true;
-    auto value = [&](int i, int j) {  // the one to be rounded
-        float part[N];
-        to_floats<T>(part, raw[i][j / N]);
-        return (all_finite ? part[j % N] : finite_or_nan(part[j % N])) * s;
-    };
-    auto block_max = [&](uint32_t m) {
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
+    auto of_block = [&](uint32_t most) {
+        most = __reduce_max_sync(0xFFFFFFFFu, largest_bits<T>(most));
         __syncthreads();  // (the values of a round before have been read)
-        if (threadIdx.x % 32 == 0) largest[threadIdx.x / 32] = m;
+        if (threadIdx.x % 32 == 0) largest[threadIdx.x / 32] = most;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) m = max(m, largest[i]);
-        return m;
+        return __reduce_max_sync(0xFFFFFFFFu, largest[threadIdx.x % WARPS]);
     };
-    auto largest_of = [&](bool finite_only) {
-        uint32_t most = 0;
+    uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4 * W; ++i) most = larger<T>(most, raw[i / W][i % W]);
+    most = of_block(most);
+    if (most >= kNotFinite) {
+        most = 0;
 #pragma unroll
-            for (int c = 0; c < 8 / N; ++c) {
-                float part[N];
-                to_floats<T>(part, raw[i][c]);
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    most = max(most, finite_only && magnitude(part[j]) >= kNotFinite ? 0u : magnitude(part[j]));
-            }
-        return block_max(most);
-    };
-    uint32_t most = largest_of(false);
-    all_finite = most < kNotFinite;
-    if (!all_finite) most = largest_of(true);
+        for (int i = 0; i < 4 * W; ++i) {
+            most = larger_finite<T>(most, raw[i / W][i % W]);
+            raw[i / W][i % W] = without_infinities<T>(raw[i / W][i % W]);
+        }
+        most = of_block(most);
+    }
     const uint32_t byte = scale_byte(most);
     if (threadIdx.x == 0) p.scales[blockIdx.x] = (uint8_t)byte;
-    s = scale_inverse(byte);
+    const float s = scale_inverse(byte);
     const uint32_t k_end = (p.inner + 15) / 16 * 16;  // rows are written up to a multiple of 16
     uint8_t* q = p.q + (size_t)e * p.outer * p.q_stride;
     if constexpr (BY_N) {
+        uint32_t* words = reinterpret_cast<uint32_t*>(turned);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t a = to_e4m3x4(value(0, j), value(1, j), value(2, j), value(3, j));
-            const uint32_t c = to_e4m3x4(value(4, j), value(5, j), value(6, j), value(7, j));
-            turned[(lo * 8 + j) * 16 + (hi ^ lo)] = (uint64_t)c << 32 | a;
+            // the four k of this n
+            uint32_t v[sizeof(T)];
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = raw[i][j];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) v[i] = __byte_perm(raw[2 * i][j / 2], raw[2 * i + 1][j / 2], j % 2 ? 0x7632 : 0x5410);
+            }
+            words[(lo * 8 + j) * 32 + (hi ^ 2 * lo)] = quantize4<T>(v, s);
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t n = hi + 16 * i, k = k0 + lo * 8;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = hi + 32 * i, k = k0 + lo * 8;
             if (n0 + n < p.outer && k < k_end)
                 *reinterpret_cast<uint64_t*>(q + (n0 + n) * p.q_stride + k) = turned[n * 16 + (lo ^ (n / 8))];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = to_e4m3x4(value(i, 0), value(i, 1), value(i, 2), value(i, 3));
-            const uint32_t c = to_e4m3x4(value(i, 4), value(i, 5), value(i, 6), value(i, 7));
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = quantize4<T>(raw[i], s), c = quantize4<T>(raw[i] + W / 2, s);
             const uint32_t n = n_of(i), k = k_of(i);
             if (n < p.outer && k < k_end)
                 *reinterpret_cast<uint64_t*>(q + n * p.q_stride + k) = (uint64_t)c << 32 | a;
@@ -439,10 +439,10 @@ rs_status rs_expert_quantize_weights(rs_float_type type, const void* w, size_t w
                         (uint32_t)across, static_cast<uint8_t*>(q), q_stride, static_cast<uint8_t*>(scales)};
         const unsigned grid = (unsigned)(down * across * experts);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        if (by_n && vec) k_quantize_weights<T, true, true><<<grid, kThreads, 0, s>>>(p);
-        else if (by_n) k_quantize_weights<T, true, false><<<grid, kThreads, 0, s>>>(p);
-        else if (vec) k_quantize_weights<T, false, true><<<grid, kThreads, 0, s>>>(p);
-        else k_quantize_weights<T, false, false><<<grid, kThreads, 0, s>>>(p);
+        if (by_n && vec) k_quantize_weights<T, true, true><<<grid, kWeightThreads, 0, s>>>(p);
+        else if (by_n) k_quantize_weights<T, true, false><<<grid, kWeightThreads, 0, s>>>(p);
+        else if (vec) k_quantize_weights<T, false, true><<<grid, kWeightThreads, 0, s>>>(p);
+        else k_quantize_weights<T, false, false><<<grid, kWeightThreads, 0, s>>>(p);
         return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
     });
 }
