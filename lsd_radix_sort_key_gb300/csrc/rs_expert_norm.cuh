@@ -102,6 +102,83 @@ __device__ __forceinline__ void store_params(void* p, size_t i, const float (&f)
     }
 }
 
+// Arithmetic on a thread's N adjacent elements, two to an instruction: the kernels
+// below issue too many to leave all else to memory (a gradient's row of 8 elements per
+// thread about 500, 70% of the issue slots).
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b)
+{
+    a = __uint_as_float((uint32_t)v);
+    b = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// d = a b
+template <int N>
+__device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], const float (&b)[N])
+{
+    if constexpr (N == 1) d[0] = a[0] * b[0];
+    else
+#pragma unroll
+        for (int c = 0; c < N; c += 2) unpair(mul2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1])), d[c], d[c + 1]);
+}
+template <int N>
+__device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], float b)
+{
+    if constexpr (N == 1) d[0] = a[0] * b;
+    else
+#pragma unroll
+        for (int c = 0; c < N; c += 2) unpair(mul2(pair_of(a[c], a[c + 1]), pair_of(b, b)), d[c], d[c + 1]);
+}
+
+// d = a b + e
+template <int N>
+__device__ __forceinline__ void times_plus(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&e)[N])
+{
+    if constexpr (N == 1) d[0] = fmaf(a[0], b[0], e[0]);
+    else
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+            unpair(fma2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1]), pair_of(e[c], e[c + 1])), d[c], d[c + 1]);
+}
+template <int N>
+__device__ __forceinline__ void times_plus(float (&d)[N], const float (&a)[N], float b, const float (&e)[N])
+{
+    if constexpr (N == 1) d[0] = fmaf(a[0], b, e[0]);
+    else
+#pragma unroll
+        for (int c = 0; c < N; c += 2)
+            unpair(fma2(pair_of(a[c], a[c + 1]), pair_of(b, b), pair_of(e[c], e[c + 1])), d[c], d[c + 1]);
+}
+
+// s + <a, b>, by even and odd elements
+struct Sum2 {
+    uint64_t v = 0;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&a)[N], const float (&b)[N])
+    {
+        if constexpr (N == 1) v = __float_as_uint(fmaf(a[0], b[0], __uint_as_float((uint32_t)v)));
+        else
+#pragma unroll
+            for (int c = 0; c < N; c += 2) v = fma2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1]), v);
+    }
+    __device__ __forceinline__ float get() const { return __uint_as_float((uint32_t)v) + __uint_as_float((uint32_t)(v >> 32)); }
+};
+
 // Sums over a block's threads.  mem: two halves of [K][32] floats, used in turn
 // (`turn` counts the calls), so that one barrier per call is enough: a half is
 // written again only after the barrier of the call between.
@@ -154,18 +231,20 @@ __device__ __forceinline__ void wait_groups() { asm volatile("cp.async.wait_grou
 template <typename T, int N, int V, int STREAMS, int DEPTH>
 struct Feed {
     Vec<T, N> now[DEPTH ? 1 : STREAMS][V], next[DEPTH ? 1 : STREAMS][V];
-    unsigned char* ring;  // [DEPTH][STREAMS][V][threads] of 16 bytes
-    uint32_t slot;
+    unsigned char* ring;  // [DEPTH][STREAMS][V][threads] of 16 bytes, this thread's
+    unsigned char* here;  // the slot of the row at hand
+    uint32_t slot, pitch;  // pitch: 16 bytes of every thread
 
     static constexpr size_t smem(size_t threads) { return (size_t)DEPTH * STREAMS * V * threads * 16; }
 
     __device__ __forceinline__ void* at(uint32_t s, int stream, int i) const
     {
-        return ring + ((((s * STREAMS + stream) * V + i) * blockDim.x) + threadIdx.x) * 16;
+        return ring + ((s * STREAMS + stream) * V + i) * pitch;
     }
     __device__ __forceinline__ void clear(unsigned char* mem)
     {
-        ring = mem;
+        pitch = blockDim.x * 16;
+        ring = here = mem + threadIdx.x * 16;
         slot = 0;
         if constexpr (DEPTH > 0) {
             for (uint32_t s = 0; s < DEPTH; ++s)
@@ -218,6 +297,7 @@ struct Feed {
             slot = r == first ? 0 : slot + 1 == DEPTH ? 0 : slot + 1;
             if (r + DEPTH - 1 < last) fetch(source, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, width);
             end_group();
+            here = static_cast<unsigned char*>(at(slot, 0, 0));
             wait_groups<DEPTH - 1>();
         } else {
 #pragma unroll
@@ -229,7 +309,7 @@ struct Feed {
     }
     __device__ __forceinline__ void get(float (&f)[N], int stream, int i) const
     {
-        if constexpr (DEPTH > 0) widen<T, N>(f, *static_cast<const Vec<T, N>*>(at(slot, stream, i)));
+        if constexpr (DEPTH > 0) widen<T, N>(f, *reinterpret_cast<const Vec<T, N>*>(here + (stream * V + i) * pitch));
         else widen<T, N>(f, now[stream][i]);
     }
 };
@@ -295,7 +375,6 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
     if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
     for (uint32_t r = first; r < last; ++r) {
         feed.turn_to(source, r, first, last, p.width);
-        float s[1] = {};
         Vec<T, N> y[V];  // as it is held
         if constexpr (BLOCK) {
             if (r == gate_end) {
@@ -305,38 +384,43 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
             }
             float rb = 1.0f;
             if (p.block_weight) {
+                Sum2 sum;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
                     feed.get(f, 1, i);
-#pragma unroll
-                    for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
+                    sum.add(f, f);
                 }
+                float s[1] = {sum.get()};
                 block_sums(s, mem, turn);
                 rb = inverse_root(s[0], p.per_width, p.eps);
             }
-            s[0] = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                 float f[N], u[N];
-                feed.get(f, 0, i);
                 feed.get(u, 1, i);
-#pragma unroll
-                for (int c = 0; c < N; ++c) u[c] = fmaf(p.scale, f[c], u[c] * rb * gw[i][c]);
+                times(u, u, rb);
+                times(u, u, gw[i]);
+                feed.get(f, 0, i);
+                times_plus(u, f, p.scale, u);
                 y[i] = narrow<T, N>(u);
                 if (c0 < p.width) store_vec<T, N>(p.y + r * p.y_i + c0, y[i]);
             }
             if (!p.weight) continue;
         }
+        auto held = [&](float (&f)[N], int i) {
+            if constexpr (BLOCK) widen<T, N>(f, y[i]);
+            else feed.get(f, 0, i);
+        };
+        Sum2 sum;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N];
-            if constexpr (BLOCK) widen<T, N>(f, y[i]);
-            else feed.get(f, 0, i);
-#pragma unroll
-            for (int c = 0; c < N; ++c) s[0] = fmaf(f[c], f[c], s[0]);
+            held(f, i);
+            sum.add(f, f);
         }
+        float s[1] = {sum.get()};
         block_sums(s, mem, turn);
         const float rx = inverse_root(s[0], p.per_width, p.eps);
 #pragma unroll
@@ -344,10 +428,9 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
             const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
             if (c0 >= p.width) continue;
             float f[N];
-            if constexpr (BLOCK) widen<T, N>(f, y[i]);
-            else feed.get(f, 0, i);
-#pragma unroll
-            for (int c = 0; c < N; ++c) f[c] *= rx * w[i][c];
+            held(f, i);
+            times(f, f, rx);
+            times(f, f, w[i]);
             store_vec<T, N>(p.h + r * p.h_i + c0, narrow<T, N>(f));
         }
     }
@@ -396,28 +479,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
     };
     for (uint32_t r = first; r < last; ++r) {
         feed.turn_to(source, r, first, last, p.width);
-        float sums[3] = {};  // y^2, <g, y>, block^2
+        Sum2 y_y, g_y, b_b;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N], g[N];
             feed.get(f, kY, i);
             feed.get(g, kDh, i);
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                sums[0] = fmaf(f[c], f[c], sums[0]);
-                sums[1] = fmaf(g[c] * w[i][c], f[c], sums[1]);
-            }
+            times(g, g, w[i]);
+            y_y.add(f, f);
+            g_y.add(g, f);
             if constexpr (BLOCK) {
                 feed.get(f, kB, i);
-#pragma unroll
-                for (int c = 0; c < N; ++c) sums[2] = fmaf(f[c], f[c], sums[2]);
+                b_b.add(f, f);
             }
         }
+        float sums[3] = {y_y.get(), g_y.get(), b_b.get()};
         block_sums(sums, mem, turn);
         const float rx = p.dh ? inverse_root(sums[0], p.per_width, p.eps) : 0.0f;
         const float kx = rx * rx * rx * p.per_width * sums[1];
         const float rb = BLOCK && p.block_weight ? inverse_root(sums[2], p.per_width, p.eps) : 1.0f;
-        float dot[1] = {};  // <du, block>
+        Sum2 du_b;
         float du[VB][N];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -426,27 +507,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
             feed.get(f, kY, i);
             feed.get(g, kDh, i);
             feed.get(d, kDy, i);
-#pragma unroll
-            for (int c = 0; c < N; ++c) {
-                d[c] = fmaf(rx * w[i][c], g[c], fmaf(-kx, f[c], d[c]));
-                dw[i][c] = fmaf(g[c], f[c] * rx, dw[i][c]);
-                g[c] = p.scale * d[c];
-            }
+            times_plus(d, f, -kx, d);
+            times(f, f, rx);
+            times_plus(dw[i], g, f, dw[i]);
+            times(g, g, w[i]);
+            times_plus(d, g, rx, d);
+            times(g, d, p.scale);
             if (p.dx && c0 < p.width) store_vec<T, N>(p.dx + r * p.dx_i + c0, narrow<T, N>(g));
             if constexpr (BLOCK) {
                 feed.get(f, kB, i);
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    sum[i][c] = fmaf(d[c], f[c] * rb, sum[i][c]);
-                    du[i][c] = d[c] * gw[i][c];
-                    dot[0] = fmaf(du[i][c], f[c], dot[0]);
-                }
+                times(g, f, rb);
+                times_plus(sum[i], d, g, sum[i]);
+                times(du[i], d, gw[i]);
+                du_b.add(du[i], f);
             }
         }
         if constexpr (BLOCK) {
             if (p.dblock) {
                 float kb = 0.0f;
                 if (p.block_weight) {
+                    float dot[1] = {du_b.get()};
                     block_sums(dot, mem, turn);
                     kb = rb * rb * rb * p.per_width * dot[0];
                 }
@@ -455,8 +535,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
                     const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                     float f[N];
                     feed.get(f, kB, i);
-#pragma unroll
-                    for (int c = 0; c < N; ++c) f[c] = fmaf(rb, du[i][c], -kb * f[c]);
+                    times(f, f, -kb);
+                    times_plus(f, du[i], rb, f);
                     if (c0 < p.width) store_vec<T, N>(p.dblock + r * p.dblock_i + c0, narrow<T, N>(f));
                 }
             }
@@ -507,25 +587,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
 // The summed gradients from the blocks' parts, in the blocks' order: job 0
 // dweight, 1 dblock_weight, 2 + g gate row g (or, with fewer blocks than gate
 // rows, the one that block g shares with the next).
-constexpr int kFinishCols = 32, kFinishRows = 32;
+constexpr int kFinishThreads = 32, kFinishRows = 32;
 
-template <typename T>
-__global__ void __launch_bounds__(kFinishCols* kFinishRows) k_norm_finish(NormArgs<T> p, uint32_t blocks, bool by_gate)
+// C columns to a thread, 4 where rows of parts begin on 16 bytes.
+template <typename T, int C>
+__global__ void __launch_bounds__(kFinishThreads* kFinishRows) k_norm_finish(NormArgs<T> p, uint32_t blocks, bool by_gate)
 {
-    __shared__ float mem[kFinishRows][kFinishCols];
+    __shared__ float mem[kFinishRows][kFinishThreads * C];
     wait_prior_grid();
-    const uint32_t job = blockIdx.y, col = blockIdx.x * kFinishCols + threadIdx.x;
+    const uint32_t job = blockIdx.y, col = (blockIdx.x * kFinishThreads + threadIdx.x) * C;
     void* to = job == 0 ? p.dweight : job == 1 ? p.dblock_weight : p.dgate;
     if (!to) return;
     uint32_t b0 = 0, b_end = blocks, gate = 0;
-    auto block_of = [&](uint32_t row) {  // the block whose rows it is among
-        uint32_t b = (uint32_t)(((uint64_t)row * blocks + blocks - 1) / p.rows);
-        while (b > 0 && first_row(b, blocks, p.rows) > row) --b;
-        while (b + 1 < blocks && first_row(b + 1, blocks, p.rows) <= row) ++b;
-        return b;
-    };
-    const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
     if (job >= 2) {
+        auto block_of = [&](uint32_t row) {  // the block whose rows it is among
+            uint32_t b = (uint32_t)(((uint64_t)row * blocks + blocks - 1) / p.rows);
+            while (b > 0 && first_row(b, blocks, p.rows) > row) --b;
+            while (b + 1 < blocks && first_row(b + 1, blocks, p.rows) <= row) ++b;
+            return b;
+        };
+        const uint32_t per_gate = p.rows / p.gate_rows;
         if (by_gate) {
             gate = job - 2;
         } else {
@@ -540,21 +621,31 @@ __global__ void __launch_bounds__(kFinishCols* kFinishRows) k_norm_finish(NormAr
     }
     // (of the blocks that share a gate row only the first may have begun with another)
     const uint32_t kind = job < 2 ? job : kPartGateFirst;
-    const bool later = job >= 2 && first_row(b0, blocks, p.rows) < gate * per_gate;
-    float s = 0.0f;
+    const bool later = job >= 2 && first_row(b0, blocks, p.rows) < gate * (p.rows / p.gate_rows);
+    float s[C] = {};
     if (col < p.width) {
         const float* from = p.part + (size_t)kind * blocks * p.width + col;
 #pragma unroll 8
-        for (uint32_t b = b0 + threadIdx.y; b < b_end; b += kFinishRows)
-            s += from[((size_t)b + (later && b == b0 ? blocks : 0)) * p.width];
+        for (uint32_t b = b0 + threadIdx.y; b < b_end; b += kFinishRows) {
+            const float* at = from + ((size_t)b + (later && b == b0 ? blocks : 0)) * p.width;
+            if constexpr (C == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(at);
+                s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+            } else {
+                s[0] += at[0];
+            }
+        }
     }
-    mem[threadIdx.y][threadIdx.x] = s;
+#pragma unroll
+    for (int c = 0; c < C; ++c) mem[threadIdx.y][c * kFinishThreads + threadIdx.x] = s[c];
     __syncthreads();
-    if (threadIdx.y == 0 && col < p.width) {
+    if (threadIdx.y < C) {  // row y: column y of each thread
+        const uint32_t at = (blockIdx.x * kFinishThreads + threadIdx.x) * C + threadIdx.y;
+        if (at >= p.width) return;
         float sum[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < kFinishRows; ++i) sum[0] += mem[i][threadIdx.x];
-        store_params<T, 1>(to, (size_t)gate * p.width + col, sum, p.wide_params);
+        for (int i = 0; i < kFinishRows; ++i) sum[0] += mem[i][threadIdx.y * kFinishThreads + threadIdx.x];
+        store_params<T, 1>(to, (size_t)gate * p.width + at, sum, p.wide_params);
     }
 }
 

@@ -71,8 +71,12 @@ rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cud
     if (st != RS_OK || (!p.dweight && !p.dblock_weight && !p.dgate)) return st;
     const bool by_gate = p.gate_rows < blocks;
     const unsigned jobs = 2 + (p.dgate ? by_gate ? p.gate_rows : blocks - 1 : 0);
-    return launch_kernel(k_norm_finish<T>, dim3((unsigned)ceil_div(p.width, kFinishCols), jobs), dim3(kFinishCols, kFinishRows),
-                         0, s, 1, true, p, blocks, by_gate);
+    const dim3 threads(kFinishThreads, kFinishRows);
+    auto finish = [&](auto kernel, int cols) {
+        return launch_kernel(kernel, dim3((unsigned)ceil_div(p.width, (size_t)kFinishThreads * cols), jobs), threads, 0, s, 1, true, p,
+                             blocks, by_gate);
+    };
+    return p.width % 4 == 0 ? finish(k_norm_finish<T, 4>, 4) : finish(k_norm_finish<T, 1>, 1);
 }
 
 }  // namespace rsx
