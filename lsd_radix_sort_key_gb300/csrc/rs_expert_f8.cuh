@@ -53,12 +53,15 @@ struct F8Args {
 
 // 16 epilogue warps of 64 columns each: with 8 the epilogue was what lasted
 // (32768 x 2048 x 4096 with gelu 250 us, 200 without an activation).
-template <bool PAIR>
+template <bool PAIR, bool QUANT>
 struct F8Shape {
     static constexpr int kWarps = 16, kThreads = 32 * (kTcFirstEpilogueWarp + kWarps);
-    static constexpr uint32_t kWarpCols = 64;  // of an epilogue warp
-    // a block's warps that read an accumulator: all, or those whose turn it is
-    static constexpr uint32_t kReaders = PAIR ? 2 * kWarps : kWarps / 2;
+    // Columns of an epilogue warp, and whether half of the warps take every other
+    // tile.  A single block's 128 columns go to all warps, 32 each, as few rows make
+    // few tiles; half a scale block, 64, to each where the result is quantised.
+    static constexpr uint32_t kWarpCols = PAIR || QUANT ? 64 : 32;
+    static constexpr bool kTurns = !PAIR && QUANT;
+    static constexpr uint32_t kReaders = PAIR ? 2 * kWarps : kTurns ? kWarps / 2 : kWarps;  // of an accumulator
     static constexpr uint32_t kCols = PAIR ? 256 : 128, kRows = PAIR ? 2 * kTcRows : kTcRows;  // of a tile
     static constexpr uint32_t kA = kTcRows * kF8Depth, kB = 128 * kF8Depth, kStage = kA + kB;   // of a block
     static constexpr int kStages = 6;
@@ -158,11 +161,11 @@ __device__ __forceinline__ uint4 quantized16(const uint32_t (&z)[16], float inve
 // A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
 // have the reduction index adjacent.  QUANT: D leaves in 8 bits.
 template <typename T, bool PAIR, bool QUANT>
-__global__ void __launch_bounds__(F8Shape<PAIR>::kThreads, 1)
+__global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
     k_product_f8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, F8Args<T> p)
 {
     using namespace rstc;
-    using S = F8Shape<PAIR>;
+    using S = F8Shape<PAIR, QUANT>;
     constexpr uint32_t BN = S::kCols;
     extern __shared__ unsigned char raw[];
     unsigned char* ring = raw + (1024 - smem_addr(raw) % 1024) % 1024;  // stages are 1024-byte aligned
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(F8Shape<PAIR>::kThreads, 1)
             n += some;
             const uint32_t turn = some ? h : seen & 1;
             constexpr uint32_t W = S::kWarpCols, kOfTile = BN / W;  // groups that a tile takes
-            if (!PAIR && turn != group / kOfTile) continue;
+            if (S::kTurns && turn != group / kOfTile) continue;
             const uint32_t i0 = t.i0 + rank * kTcRows + quarter * 32, i = i0 + lane, c_first = group % kOfTile * W;
             const uint32_t j_first = t.j0 + c_first;
             const uint32_t acc = tmem + h * S::kAccStep + c_first + (quarter << 21);

@@ -10,7 +10,7 @@ namespace rsx {
 template <typename T, bool PAIR, bool QUANT>
 rs_status f8_launch(const F8Operands& o, const F8Args<T>& args, int sms, cudaStream_t s)
 {
-    using S = F8Shape<PAIR>;
+    using S = F8Shape<PAIR, QUANT>;
     const auto kernel = k_product_f8<T, PAIR, QUANT>;
     constexpr size_t most = S::smem(RS_EXPERTS_MAX);
     static_assert(most <= kBlockSmem);

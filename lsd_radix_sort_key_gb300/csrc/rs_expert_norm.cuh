@@ -52,57 +52,109 @@ struct NormArgs {
 // is at most one later one that it shares).
 enum { kPartWeight, kPartBlockWeight, kPartGateFirst, kPartGateLater, kParts };
 
-// N adjacent elements as floats and back.
+// How a row is cut: THREADS threads at most, V accesses each of N elements.
+// Adjacent elements are one 16-byte vector; STRIDED ones, for rows that are only
+// element-aligned, lie as many elements apart as the block has threads, so that
+// neighbouring threads have neighbouring elements.  MODE: where rows wait (Feed).
+enum { kRegisters, kOwn, kShared };
+template <int N_, int V_, int THREADS_, int MODE_, bool STRIDED_>
+struct NormShape {
+    static constexpr int N = N_, V = V_, THREADS = THREADS_, MODE = MODE_;
+    static constexpr bool STRIDED = STRIDED_;
+    // The column of element c of access i.
+    __device__ __forceinline__ static uint32_t col(int i, int c)
+    {
+        return STRIDED ? (i * N + c) * blockDim.x + threadIdx.x : (i * blockDim.x + threadIdx.x) * N + c;
+    }
+    // Whether it exists (a vector's elements all do, or none).
+    __device__ __forceinline__ static bool has(int i, int c, uint32_t width) { return col(i, STRIDED ? c : 0) < width; }
+};
+
+// N elements as floats and back.
 template <typename T, int N>
 __device__ __forceinline__ void widen(float (&f)[N], const Vec<T, N>& v)
 {
-    if constexpr (N == 1) f[0] = to_float(v.v[0]);
-    else to_floats<T>(f, v);
+    if constexpr (N == kVec<T>) {
+        to_floats<T>(f, v);
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; ++c) f[c] = to_float(v.v[c]);
+    }
 }
 
 template <typename T, int N>
 __device__ __forceinline__ Vec<T, N> narrow(const float (&f)[N])
 {
-    if constexpr (N == 1) {
-        Vec<T, 1> v;
-        v.v[0] = from_float<T>(f[0]);
-        return v;
-    } else {
+    if constexpr (N == kVec<T>) {
         return from_floats<T>(f);
+    } else {
+        Vec<T, N> v;
+#pragma unroll
+        for (int c = 0; c < N; ++c) v.v[c] = from_float<T>(f[c]);
+        return v;
     }
 }
 
-// N adjacent parameters, float32 or T.
-template <typename T, int N>
-__device__ __forceinline__ void load_params(float (&f)[N], const void* p, size_t i, bool wide)
+// A thread's elements of access i of a row, zero where there are none.
+template <typename S, typename T>
+__device__ __forceinline__ Vec<T, S::N> load_elements(const T* row, int i, uint32_t width)
+{
+    Vec<T, S::N> v{};
+    if constexpr (S::STRIDED) {
+#pragma unroll
+        for (int c = 0; c < S::N; ++c)
+            if (S::has(i, c, width)) v.v[c] = row[S::col(i, c)];
+    } else {
+        if (S::has(i, 0, width)) v = load_vec<T, S::N>(row + S::col(i, 0));
+    }
+    return v;
+}
+
+template <typename S, typename T>
+__device__ __forceinline__ void store_elements(T* row, int i, uint32_t width, const Vec<T, S::N>& v)
+{
+    if constexpr (S::STRIDED) {
+#pragma unroll
+        for (int c = 0; c < S::N; ++c)
+            if (S::has(i, c, width)) row[S::col(i, c)] = v.v[c];
+    } else {
+        if (S::has(i, 0, width)) store_vec<T, S::N>(row + S::col(i, 0), v);
+    }
+}
+
+// A thread's elements of access i of a row of parameters, float32 or T.
+template <typename S, typename T>
+__device__ __forceinline__ void load_params(float (&f)[S::N], const void* p, size_t row, int i, uint32_t width, bool wide)
 {
     if (sizeof(T) == 4 || wide) {
-        const float* from = static_cast<const float*>(p) + i;
-        if constexpr (N == 1) {
-            f[0] = __ldg(from);
-        } else {
+        const float* from = static_cast<const float*>(p) + row;
+        if constexpr (S::STRIDED) {
 #pragma unroll
-            for (int c = 0; c < N; c += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(from + c));
+            for (int c = 0; c < S::N; ++c) f[c] = S::has(i, c, width) ? __ldg(from + S::col(i, c)) : 0.0f;
+        } else if (S::has(i, 0, width)) {
+#pragma unroll
+            for (int c = 0; c < S::N; c += 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(from + S::col(i, c)));
                 f[c] = v.x, f[c + 1] = v.y, f[c + 2] = v.z, f[c + 3] = v.w;
             }
         }
     } else {
-        widen<T, N>(f, load_vec<T, N>(static_cast<const T*>(p) + i));
+        widen<T, S::N>(f, load_elements<S, T>(static_cast<const T*>(p) + row, i, width));
     }
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void store_params(void* p, size_t i, const float (&f)[N], bool wide)
+template <typename S, typename T>
+__device__ __forceinline__ void store_params(void* p, size_t row, int i, uint32_t width, const float (&f)[S::N], bool wide)
 {
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-        if (sizeof(T) == 4 || wide) static_cast<float*>(p)[i + c] = f[c];
-        else static_cast<T*>(p)[i + c] = from_float<T>(f[c]);
+    for (int c = 0; c < S::N; ++c) {
+        if (!S::has(i, c, width)) continue;
+        if (sizeof(T) == 4 || wide) static_cast<float*>(p)[row + S::col(i, c)] = f[c];
+        else static_cast<T*>(p)[row + S::col(i, c)] = from_float<T>(f[c]);
     }
 }
 
-// Arithmetic on a thread's N adjacent elements, two to an instruction: the kernels
+// Arithmetic on a thread's N elements, two to an instruction: the kernels
 // below issue too many to leave all else to memory (a gradient's row of 8 elements per
 // thread about 500, 70% of the issue slots).
 __device__ __forceinline__ uint64_t pair_of(float a, float b)
@@ -131,16 +183,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 template <int N>
 __device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], const float (&b)[N])
 {
-    if constexpr (N == 1) d[0] = a[0] * b[0];
-    else
 #pragma unroll
         for (int c = 0; c < N; c += 2) unpair(mul2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1])), d[c], d[c + 1]);
 }
 template <int N>
 __device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], float b)
 {
-    if constexpr (N == 1) d[0] = a[0] * b;
-    else
 #pragma unroll
         for (int c = 0; c < N; c += 2) unpair(mul2(pair_of(a[c], a[c + 1]), pair_of(b, b)), d[c], d[c + 1]);
 }
@@ -149,8 +197,6 @@ __device__ __forceinline__ void times(float (&d)[N], const float (&a)[N], float 
 template <int N>
 __device__ __forceinline__ void times_plus(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&e)[N])
 {
-    if constexpr (N == 1) d[0] = fmaf(a[0], b[0], e[0]);
-    else
 #pragma unroll
         for (int c = 0; c < N; c += 2)
             unpair(fma2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1]), pair_of(e[c], e[c + 1])), d[c], d[c + 1]);
@@ -158,8 +204,6 @@ __device__ __forceinline__ void times_plus(float (&d)[N], const float (&a)[N], c
 template <int N>
 __device__ __forceinline__ void times_plus(float (&d)[N], const float (&a)[N], float b, const float (&e)[N])
 {
-    if constexpr (N == 1) d[0] = fmaf(a[0], b, e[0]);
-    else
 #pragma unroll
         for (int c = 0; c < N; c += 2)
             unpair(fma2(pair_of(a[c], a[c + 1]), pair_of(b, b), pair_of(e[c], e[c + 1])), d[c], d[c + 1]);
@@ -171,8 +215,6 @@ struct Sum2 {
     template <int N>
     __device__ __forceinline__ void add(const float (&a)[N], const float (&b)[N])
     {
-        if constexpr (N == 1) v = __float_as_uint(fmaf(a[0], b[0], __uint_as_float((uint32_t)v)));
-        else
 #pragma unroll
             for (int c = 0; c < N; c += 2) v = fma2(pair_of(a[c], a[c + 1]), pair_of(b[c], b[c + 1]), v);
     }
@@ -222,123 +264,156 @@ __device__ __forceinline__ void end_group() { asm volatile("cp.async.commit_grou
 template <int LATER>  // all but the last LATER groups have arrived
 __device__ __forceinline__ void wait_groups() { asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory"); }
 
-// This thread's columns of the rows that a block walks: STREAMS matrices, V accesses
-// of N elements each.  DEPTH > 0: rows are copied to shared memory DEPTH - 1 rows
-// ahead, each thread's part by itself and for itself, so no barrier is needed.
-// DEPTH 0 (single elements, or rows too wide): one row ahead, in registers.
-// With one row ahead the SMs had too few bytes in flight (16384 x 2048 bf16: forward
-// 63 us, gradient 182).
-template <typename T, int N, int V, int STREAMS, int DEPTH>
+// A matrix whose rows a block walks.
+template <typename T>
+struct Walked {
+    const T* p;  // nullptr: none, its rows read as zero
+    size_t stride;
+};
+
+// The rows of STREAMS matrices, one after the other, as this thread has them.
+//   kOwn        vectors: each thread copies its own 16 bytes to shared memory, for
+//               itself, three rows ahead, so no barrier is needed
+//   kShared     strided elements: the block copies the 16-byte pieces of memory
+//               that a row lies in, two rows ahead, and meets once per row; pieces that
+//               reach past the matrix's ends are copied element by element
+//   kRegisters  rows too wide for that: one row ahead
+// With one row ahead in registers the SMs had too few bytes in flight (16384 x
+// 2048 bf16: forward 63 us, gradient 182).
+template <typename T, typename S, int STREAMS>
 struct Feed {
-    Vec<T, N> now[DEPTH ? 1 : STREAMS][V], next[DEPTH ? 1 : STREAMS][V];
-    unsigned char* ring;  // [DEPTH][STREAMS][V][threads] of 16 bytes, this thread's
-    unsigned char* here;  // the slot of the row at hand
-    uint32_t slot, pitch;  // pitch: 16 bytes of every thread
+    static constexpr int N = S::N, V = S::V, MODE = S::MODE;
+    static constexpr uint32_t DEPTH = MODE == kOwn ? 4 : MODE == kShared ? 3 : 1;
+    static constexpr int HELD = MODE == kRegisters ? STREAMS : 1;
+    Vec<T, N> now[HELD][V], next[HELD][V];
+    unsigned char* ring;   // [DEPTH][STREAMS][pitch]; kOwn: from this thread's part on
+    unsigned char* here;   // the slot of the row at hand
+    uint32_t slot, pitch;  // pitch: of a row
+    uint32_t shift[MODE == kShared ? STREAMS : 1];  // bytes before the row at hand
 
-    static constexpr size_t smem(size_t threads) { return (size_t)DEPTH * STREAMS * V * threads * 16; }
-
-    __device__ __forceinline__ void* at(uint32_t s, int stream, int i) const
+    static size_t row_bytes(size_t width, size_t threads)
     {
-        return ring + ((s * STREAMS + stream) * V + i) * pitch;
+        return MODE == kOwn ? V * threads * 16 : MODE == kShared ? align_up(width * sizeof(T), 16) + 16 : 0;
     }
-    __device__ __forceinline__ void clear(unsigned char* mem)
+    static size_t smem(size_t width, size_t threads)
     {
-        pitch = blockDim.x * 16;
-        ring = here = mem + threadIdx.x * 16;
+        return MODE == kRegisters ? 0 : DEPTH * STREAMS * row_bytes(width, threads);
+    }
+
+    __device__ __forceinline__ void start(const Walked<T> (&m)[STREAMS], unsigned char* mem, uint32_t first, uint32_t last,
+                                          uint32_t rows, uint32_t width)
+    {
+        pitch = MODE == kOwn ? V * blockDim.x * 16 : (width * (uint32_t)sizeof(T) + 15) / 16 * 16 + 16;
+        ring = here = mem + (MODE == kOwn ? threadIdx.x * 16 : 0);
         slot = 0;
-        if constexpr (DEPTH > 0) {
-            for (uint32_t s = 0; s < DEPTH; ++s)
-#pragma unroll
-                for (int k = 0; k < STREAMS; ++k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) *static_cast<uint4*>(at(s, k, i)) = make_uint4(0, 0, 0, 0);
-        } else {
+        if constexpr (MODE == kRegisters) {
 #pragma unroll
             for (int k = 0; k < STREAMS; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) next[k][i] = Vec<T, N>{};
+            fetch(m, first, 0, rows, width);
+        } else {
+            if constexpr (MODE == kOwn) {  // what is not copied reads as zero
+                for (uint32_t k = 0; k < DEPTH * STREAMS; ++k)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        *reinterpret_cast<uint4*>(ring + k * pitch + i * blockDim.x * 16) = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (uint32_t d = 0; d + 1 < DEPTH; ++d) {
+                if (first + d < last) fetch(m, first + d, d, rows, width);
+                end_group();
+            }
         }
     }
-    // source(k, r): row r of matrix k, or nullptr if there is none (it reads as zero).
-    template <typename F>
-    __device__ __forceinline__ void fetch(F source, uint32_t r, uint32_t to, uint32_t width)
+    __device__ __forceinline__ void fetch(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t to, uint32_t rows, uint32_t width)
     {
 #pragma unroll
         for (int k = 0; k < STREAMS; ++k) {
-            const T* row = source(k, r);
-            if (!row) continue;
+            if (!m[k].p) continue;
+            const T* row = m[k].p + r * m[k].stride;
+            unsigned char* at = ring + (to * STREAMS + k) * pitch;
+            if constexpr (MODE == kRegisters) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const uint32_t c = (i * blockDim.x + threadIdx.x) * N;
-                if (c >= width) continue;
-                if constexpr (DEPTH > 0) copy16(at(to, k, i), row + c);
-                else next[k][i] = load_vec<T, N>(row + c);
-            }
-        }
-    }
-    template <typename F>
-    __device__ __forceinline__ void start(F source, uint32_t first, uint32_t last, uint32_t width)
-    {
-        if constexpr (DEPTH > 0) {
+                for (int i = 0; i < V; ++i) next[k][i] = load_elements<S, T>(row, i, width);
+            } else if constexpr (MODE == kOwn) {
 #pragma unroll
-            for (uint32_t d = 0; d + 1 < DEPTH; ++d) {
-                if (first + d < last) fetch(source, first + d, d, width);
-                end_group();
+                for (int i = 0; i < V; ++i)
+                    if (S::has(i, 0, width)) copy16(at + i * blockDim.x * 16, row + S::col(i, 0));
+            } else {
+                const uintptr_t begin = (uintptr_t)m[k].p, end = (uintptr_t)(m[k].p + (rows - 1) * m[k].stride + width);
+                const uintptr_t from = (uintptr_t)row & ~(uintptr_t)15, row_end = (uintptr_t)(row + width);
+                for (uintptr_t a = from + threadIdx.x * 16; a < row_end; a += blockDim.x * 16) {
+                    if (a >= begin && a + 16 <= end) {
+                        copy16(at + (a - from), reinterpret_cast<const void*>(a));
+                    } else {
+                        for (uintptr_t e = a < (uintptr_t)row ? (uintptr_t)row : a; e < a + 16 && e < row_end; e += sizeof(T))
+                            *reinterpret_cast<T*>(at + (e - from)) = *reinterpret_cast<const T*>(e);
+                    }
+                }
             }
-        } else {
-            fetch(source, first, 0, width);
         }
     }
     // Row r is there afterwards.
-    template <typename F>
-    __device__ __forceinline__ void turn_to(F source, uint32_t r, uint32_t first, uint32_t last, uint32_t width)
+    __device__ __forceinline__ void turn_to(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t first, uint32_t last, uint32_t rows,
+                                            uint32_t width)
     {
-        if constexpr (DEPTH > 0) {
-            slot = r == first ? 0 : slot + 1 == DEPTH ? 0 : slot + 1;
-            if (r + DEPTH - 1 < last) fetch(source, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, width);
-            end_group();
-            here = static_cast<unsigned char*>(at(slot, 0, 0));
-            wait_groups<DEPTH - 1>();
-        } else {
+        if constexpr (MODE == kRegisters) {
 #pragma unroll
             for (int k = 0; k < STREAMS; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) now[k][i] = next[k][i];
-            if (r + 1 < last) fetch(source, r + 1, 0, width);
+            if (r + 1 < last) fetch(m, r + 1, 0, rows, width);
+            return;
         }
+        if (r != first && ++slot == DEPTH) slot = 0;
+        if constexpr (MODE == kShared) {
+            wait_groups<(int)DEPTH - 2>();
+            __syncthreads();  // everybody's pieces are there, and the slot before is free
+#pragma unroll
+            for (int k = 0; k < STREAMS; ++k) shift[k] = (uint32_t)(uintptr_t)(m[k].p + r * m[k].stride) & 15;
+        }
+        if (r + DEPTH - 1 < last) fetch(m, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, rows, width);
+        end_group();
+        if constexpr (MODE == kOwn) wait_groups<(int)DEPTH - 1>();
+        here = ring + slot * STREAMS * pitch;
     }
-    __device__ __forceinline__ void get(float (&f)[N], int stream, int i) const
+    __device__ __forceinline__ void get(const Walked<T> (&m)[STREAMS], float (&f)[N], int stream, int i, uint32_t width) const
     {
-        if constexpr (DEPTH > 0) widen<T, N>(f, *reinterpret_cast<const Vec<T, N>*>(here + (stream * V + i) * pitch));
-        else widen<T, N>(f, now[stream][i]);
+        if constexpr (MODE == kRegisters) {
+            widen<T, N>(f, now[stream][i]);
+        } else if constexpr (MODE == kOwn) {
+            widen<T, N>(f, *reinterpret_cast<const Vec<T, N>*>(here + stream * pitch + i * blockDim.x * 16));
+        } else {
+            const T* row = reinterpret_cast<const T*>(here + stream * pitch + shift[stream]);
+#pragma unroll
+            for (int c = 0; c < N; ++c) f[c] = m[stream].p && S::has(i, c, width) ? to_float(row[S::col(i, c)]) : 0.0f;
+        }
     }
 };
 
 // This thread's columns of a row of parameters; `none` where there is none.
-template <typename T, int N, int V>
-__device__ __forceinline__ void load_columns(float (&f)[V][N], const void* p, size_t at, bool wide, float none, uint32_t width)
+template <typename S, typename T>
+__device__ __forceinline__ void load_columns(float (&f)[S::V][S::N], const void* p, size_t row, bool wide, float none, uint32_t width)
 {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
+    for (int i = 0; i < S::V; ++i) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) f[i][c] = none;
-        if (p && c0 < width) load_params<T, N>(f[i], p, at + c0, wide);
+        for (int c = 0; c < S::N; ++c) f[i][c] = none;
+        if (p) load_params<S, T>(f[i], p, row, i, width, wide);
     }
 }
 
 // The gate times the block's weight, this thread's columns.
-template <typename T, int N, int V>
-__device__ __forceinline__ void load_gate(float (&f)[V][N], const NormArgs<T>& p, uint32_t gate)
+template <typename S, typename T>
+__device__ __forceinline__ void load_gate(float (&f)[S::V][S::N], const NormArgs<T>& p, uint32_t gate)
 {
-    load_columns<T, N, V>(f, p.gate_rows ? p.gate : nullptr, (size_t)gate * p.width, p.wide_params, 1.0f, p.width);
+    load_columns<S, T>(f, p.gate_rows ? p.gate : nullptr, (size_t)gate * p.width, p.wide_params, 1.0f, p.width);
     if (!p.block_weight) return;
-    float w[V][N];
-    load_columns<T, N, V>(w, p.block_weight, 0, p.wide_params, 1.0f, p.width);
+    float w[S::V][S::N];
+    load_columns<S, T>(w, p.block_weight, 0, p.wide_params, 1.0f, p.width);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int c = 0; c < N; ++c) f[i][c] *= w[i][c];
+    for (int i = 0; i < S::V; ++i) times(f[i], f[i], w[i]);
 }
 
 // A block's rows: [first(b), first(b + 1)).
@@ -347,8 +422,6 @@ __host__ __device__ inline uint32_t first_row(uint32_t block, uint32_t blocks, u
     return (uint32_t)((uint64_t)block * rows / blocks);
 }
 
-// Rows copied ahead by each call.
-constexpr int kNormDepth = 4, kGradDepth = 4;
 constexpr size_t kNormSmem = 128 * 1024;  // the most that a block's rows take: 512 threads, 4 matrices
 
 // 1 / sqrt(mean + eps); the hardware's root is off by two ulps at most.
@@ -357,9 +430,10 @@ __device__ __forceinline__ float inverse_root(float sum, float per_width, float 
 // Each block walks adjacent rows.  The parameters' columns stay in registers (a
 // gate's until it changes): reading them again for every row is 24 KB beside a
 // row's 16 (2048 bf16, float32 parameters).
-template <typename T, int N, int V, int THREADS, bool BLOCK, int DEPTH>
-__global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(NormArgs<T> p)
+template <typename T, typename S, bool BLOCK>
+__global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1) k_norm(NormArgs<T> p)
 {
+    constexpr int N = S::N, V = S::V;
     __shared__ __align__(16) float mem[2 * 3 * 32];
     extern __shared__ __align__(16) unsigned char ring[];
     clear_sums(mem);
@@ -367,20 +441,22 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
     const uint32_t per_gate = p.gate_rows ? p.rows / p.gate_rows : p.rows;
     uint32_t turn = 0, gate = first / per_gate, gate_end = (gate + 1) * per_gate;
     float w[V][N], gw[BLOCK ? V : 1][N];
-    Feed<T, N, V, BLOCK ? 2 : 1, DEPTH> feed;
-    auto source = [&](int k, uint32_t r) -> const T* { return k == 0 ? p.x + r * p.x_i : p.block + r * p.block_i; };
-    feed.clear(ring);
-    feed.start(source, first, last, p.width);
-    load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
-    if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
+    constexpr int kStreams = BLOCK ? 2 : 1;
+    Walked<T> m[kStreams];
+    m[0] = {p.x, p.x_i};
+    if constexpr (BLOCK) m[1] = {p.block, p.block_i};
+    Feed<T, S, kStreams> feed;
+    feed.start(m, ring, first, last, p.rows, p.width);
+    load_columns<S, T>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
+    if constexpr (BLOCK) load_gate<S, T>(gw, p, gate);
     for (uint32_t r = first; r < last; ++r) {
-        feed.turn_to(source, r, first, last, p.width);
+        feed.turn_to(m, r, first, last, p.rows, p.width);
         Vec<T, N> y[V];  // as it is held
         if constexpr (BLOCK) {
             if (r == gate_end) {
                 ++gate;
                 gate_end += per_gate;
-                load_gate<T, N, V>(gw, p, gate);
+                load_gate<S, T>(gw, p, gate);
             }
             float rb = 1.0f;
             if (p.block_weight) {
@@ -388,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
-                    feed.get(f, 1, i);
+                    feed.get(m, f, 1, i, p.width);
                     sum.add(f, f);
                 }
                 float s[1] = {sum.get()};
@@ -397,21 +473,20 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                 float f[N], u[N];
-                feed.get(u, 1, i);
+                feed.get(m, u, 1, i, p.width);
                 times(u, u, rb);
                 times(u, u, gw[i]);
-                feed.get(f, 0, i);
+                feed.get(m, f, 0, i, p.width);
                 times_plus(u, f, p.scale, u);
                 y[i] = narrow<T, N>(u);
-                if (c0 < p.width) store_vec<T, N>(p.y + r * p.y_i + c0, y[i]);
+                store_elements<S, T>(p.y + r * p.y_i, i, p.width, y[i]);
             }
             if (!p.weight) continue;
         }
         auto held = [&](float (&f)[N], int i) {
             if constexpr (BLOCK) widen<T, N>(f, y[i]);
-            else feed.get(f, 0, i);
+            else feed.get(m, f, 0, i, p.width);
         };
         Sum2 sum;
 #pragma unroll
@@ -425,13 +500,11 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
         const float rx = inverse_root(s[0], p.per_width, p.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-            if (c0 >= p.width) continue;
             float f[N];
             held(f, i);
             times(f, f, rx);
             times(f, f, w[i]);
-            store_vec<T, N>(p.h + r * p.h_i + c0, narrow<T, N>(f));
+            store_elements<S, T>(p.h + r * p.h_i, i, p.width, narrow<T, N>(f));
         }
     }
 }
@@ -440,9 +513,10 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 1024 / THREADS : 1) k_norm(N
 // summed gradients in registers.  Within one gate row, with n = block r,
 //     dgate = block_weight S,  dblock_weight += gate S,  S = the sum of d n,
 // so one sum serves both until the gate changes.
-template <typename T, int N, int V, int THREADS, bool BLOCK, int DEPTH>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(NormArgs<T> p)
+template <typename T, typename S, bool BLOCK>
+__global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 2 : 3) : 1) k_norm_grad(NormArgs<T> p)
 {
+    constexpr int N = S::N, V = S::V;
     __shared__ __align__(16) float mem[2 * 3 * 32];
     extern __shared__ __align__(16) unsigned char ring[];
     start_next_grid();
@@ -453,43 +527,41 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
     constexpr int VB = BLOCK ? V : 1;
     enum { kY, kDh, kDy, kB };
     float w[V][N], gw[VB][N], dw[V][N] = {}, db[VB][N] = {}, sum[VB][N] = {};
-    Feed<T, N, V, BLOCK ? 4 : 3, DEPTH> feed;
-    auto source = [&](int k, uint32_t r) -> const T* {
-        switch (k) {
-        case kY: return p.dh ? p.x + r * p.x_i : nullptr;
-        case kDh: return p.dh ? p.dh + r * p.dh_i : nullptr;
-        case kDy: return p.dy ? p.dy + r * p.dy_i : nullptr;
-        default: return p.block + r * p.block_i;
-        }
-    };
-    feed.clear(ring);
-    feed.start(source, first, last, p.width);
-    load_columns<T, N, V>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
-    if constexpr (BLOCK) load_gate<T, N, V>(gw, p, gate);
+    constexpr int kStreams = BLOCK ? 4 : 3;
+    Walked<T> m[kStreams];
+    m[kY] = {p.dh ? p.x : nullptr, p.x_i};
+    m[kDh] = {p.dh, p.dh_i};
+    m[kDy] = {p.dy, p.dy_i};
+    if constexpr (BLOCK) m[kB] = {p.block, p.block_i};
+    Feed<T, S, kStreams> feed;
+    feed.start(m, ring, first, last, p.rows, p.width);
+    load_columns<S, T>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
+    if constexpr (BLOCK) load_gate<S, T>(gw, p, gate);
     auto store_part = [&](int kind, int i, const float (&f)[N]) {
-        const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-        if (c0 >= p.width) return;
-        float* to = p.part + ((size_t)kind * gridDim.x + blockIdx.x) * p.width + c0;
-        if constexpr (N == 1) {
-            *to = f[0];
-        } else {
+        float* to = p.part + ((size_t)kind * gridDim.x + blockIdx.x) * p.width;
+        if constexpr (S::STRIDED) {
 #pragma unroll
-            for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+            for (int c = 0; c < N; ++c)
+                if (S::has(i, c, p.width)) to[S::col(i, c)] = f[c];
+        } else if (S::has(i, 0, p.width)) {
+#pragma unroll
+            for (int c = 0; c < N; c += 4)
+                *reinterpret_cast<float4*>(to + S::col(i, c)) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
         }
     };
     for (uint32_t r = first; r < last; ++r) {
-        feed.turn_to(source, r, first, last, p.width);
+        feed.turn_to(m, r, first, last, p.rows, p.width);
         Sum2 y_y, g_y, b_b;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N], g[N];
-            feed.get(f, kY, i);
-            feed.get(g, kDh, i);
+            feed.get(m, f, kY, i, p.width);
+            feed.get(m, g, kDh, i, p.width);
             times(g, g, w[i]);
             y_y.add(f, f);
             g_y.add(g, f);
             if constexpr (BLOCK) {
-                feed.get(f, kB, i);
+                feed.get(m, f, kB, i, p.width);
                 b_b.add(f, f);
             }
         }
@@ -502,20 +574,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
         float du[VB][N];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
             float f[N], g[N], d[N];
-            feed.get(f, kY, i);
-            feed.get(g, kDh, i);
-            feed.get(d, kDy, i);
+            feed.get(m, f, kY, i, p.width);
+            feed.get(m, g, kDh, i, p.width);
+            feed.get(m, d, kDy, i, p.width);
             times_plus(d, f, -kx, d);
             times(f, f, rx);
             times_plus(dw[i], g, f, dw[i]);
             times(g, g, w[i]);
             times_plus(d, g, rx, d);
             times(g, d, p.scale);
-            if (p.dx && c0 < p.width) store_vec<T, N>(p.dx + r * p.dx_i + c0, narrow<T, N>(g));
+            if (p.dx) store_elements<S, T>(p.dx + r * p.dx_i, i, p.width, narrow<T, N>(g));
             if constexpr (BLOCK) {
-                feed.get(f, kB, i);
+                feed.get(m, f, kB, i, p.width);
                 times(g, f, rb);
                 times_plus(sum[i], d, g, sum[i]);
                 times(du[i], d, gw[i]);
@@ -532,12 +603,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
                     float f[N];
-                    feed.get(f, kB, i);
+                    feed.get(m, f, kB, i, p.width);
                     times(f, f, -kb);
                     times_plus(f, du[i], rb, f);
-                    if (c0 < p.width) store_vec<T, N>(p.dblock + r * p.dblock_i + c0, narrow<T, N>(f));
+                    store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(f));
                 }
             }
             if (r + 1 == last || r + 1 == gate_end) {
@@ -546,23 +616,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
                 const bool whole = begin >= first && gate_end <= last;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const uint32_t c0 = (i * blockDim.x + threadIdx.x) * N;
-                    if (c0 >= p.width) continue;
                     float f[N];
                     if (p.dblock_weight) {
 #pragma unroll
                         for (int c = 0; c < N; ++c) f[c] = 1.0f;
-                        if (p.gate_rows) load_params<T, N>(f, p.gate, (size_t)gate * p.width + c0, p.wide_params);
-#pragma unroll
-                        for (int c = 0; c < N; ++c) db[i][c] = fmaf(f[c], sum[i][c], db[i][c]);
+                        if (p.gate_rows) load_params<S, T>(f, p.gate, (size_t)gate * p.width, i, p.width, p.wide_params);
+                        times_plus(db[i], f, sum[i], db[i]);
                     }
                     if (p.dgate) {
 #pragma unroll
                         for (int c = 0; c < N; ++c) f[c] = 1.0f;
-                        if (p.block_weight) load_params<T, N>(f, p.block_weight, c0, p.wide_params);
-#pragma unroll
-                        for (int c = 0; c < N; ++c) f[c] *= sum[i][c];
-                        if (whole) store_params<T, N>(p.dgate, (size_t)gate * p.width + c0, f, p.wide_params);
+                        if (p.block_weight) load_params<S, T>(f, p.block_weight, 0, i, p.width, p.wide_params);
+                        times(f, f, sum[i]);
+                        if (whole) store_params<S, T>(p.dgate, (size_t)gate * p.width, i, p.width, f, p.wide_params);
                         else store_part(begin <= first ? kPartGateFirst : kPartGateLater, i, f);
                     }
 #pragma unroll
@@ -571,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) k_norm_grad(N
                 if (r + 1 < last) {
                     ++gate;
                     gate_end += per_gate;
-                    load_gate<T, N, V>(gw, p, gate);
+                    load_gate<S, T>(gw, p, gate);
                 }
             }
         }
@@ -642,10 +708,12 @@ __global__ void __launch_bounds__(kFinishThreads* kFinishRows) k_norm_finish(Nor
     if (threadIdx.y < C) {  // row y: column y of each thread
         const uint32_t at = (blockIdx.x * kFinishThreads + threadIdx.x) * C + threadIdx.y;
         if (at >= p.width) return;
-        float sum[1] = {0.0f};
+        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kFinishRows; ++i) sum[0] += mem[i][threadIdx.y * kFinishThreads + threadIdx.x];
-        store_params<T, 1>(to, (size_t)gate * p.width + at, sum, p.wide_params);
+        for (int i = 0; i < kFinishRows; ++i) sum += mem[i][threadIdx.y * kFinishThreads + threadIdx.x];
+        const size_t i = (size_t)gate * p.width + at;
+        if (sizeof(T) == 4 || p.wide_params) static_cast<float*>(to)[i] = sum;
+        else static_cast<T*>(to)[i] = from_float<T>(sum);
     }
 }
 
@@ -657,14 +725,14 @@ template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s);
 
 // Blocks of a gradient: the sizes alone decide, as the order of its sums goes by
-// them.  As many as an SM holds at once, of one thread per 16 bytes of a row (512
-// at most): by their registers 768 threads' worth where rows have up to 256
-// vectors or are no whole number of vectors, else one block.
+// them.  As many as an SM holds at once by their registers: 768 threads' worth
+// where a row takes up to 256 (one per 16 bytes), 512 threads' where its elements
+// are strided (one per eight), else one.
 inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem)
 {
-    const size_t threads = align_up(ceil_div(width * elem, 16), 32);
-    const bool many = threads <= 256 || (width * elem % 16 && width <= 2048);
-    const size_t per = many && threads <= 384 ? 768 / threads : 1, blocks = 152 * (per < 8 ? per : 8);
+    const bool strided = width * elem % 16 && width <= 2048;
+    const size_t threads = align_up(strided ? ceil_div(width, 8) : ceil_div(width * elem, 16), 32);
+    const size_t per = threads > 256 ? 1 : (strided ? 512 : 768) / threads, blocks = 152 * (per < 8 ? per : 8);
     return (uint32_t)(rows < blocks ? rows : blocks);
 }
 

@@ -6,32 +6,32 @@
 
 namespace rsx {
 
-// Accesses per thread, the most threads that a kernel is compiled for and whether
-// rows go through shared memory: one access each up to 512 threads, then two;
-// rows past 16 KB two (or four) in up to 1024 threads, through registers; single
-// elements (rows that are only element-aligned) four, then sixteen.
+// The shape for a width: one vector per thread up to 512 threads, rows through
+// shared memory; past 512 vectors two (or four) of them in up to 1024 threads,
+// through registers; strided elements, eight per thread through shared memory up
+// to 2048, else 16 through registers.
 template <typename T, typename F>
 rs_status norm_shape(uint32_t width, bool vectors, F run)
 {
     constexpr int N = kVec<T>;
-    auto with = [&](auto n, auto v, auto most, auto ring) {
-        const uint32_t accesses = width / decltype(n)::value;
-        return run(n, v, most, ring, (unsigned)align_up(ceil_div(accesses, decltype(v)::value), 32));
+    auto with = [&](auto shape) {
+        using S = decltype(shape);
+        return run(shape, (unsigned)align_up(ceil_div(width, (size_t)S::N * S::V), 32));
     };
     if (!vectors) {
-        if (width <= 2048) return with(Int<1>{}, Int<4>{}, Int<512>{}, Int<0>{});
-        if (width <= 8192) return with(Int<1>{}, Int<16>{}, Int<512>{}, Int<0>{});
-        return with(Int<1>{}, Int<16>{}, Int<1024>{}, Int<0>{});
+        if (width <= 2048) return with(NormShape<8, 1, 256, kShared, true>{});
+        if (width <= 8192) return with(NormShape<4, 4, 512, kRegisters, true>{});
+        return with(NormShape<4, 4, 1024, kRegisters, true>{});
     }
-    if (width <= 256 * N) return with(Int<N>{}, Int<1>{}, Int<256>{}, Int<1>{});
-    if (width <= 512 * N) return with(Int<N>{}, Int<1>{}, Int<512>{}, Int<1>{});
+    if (width <= 256 * N) return with(NormShape<N, 1, 256, kOwn, false>{});
+    if (width <= 512 * N) return with(NormShape<N, 1, 512, kOwn, false>{});
     if constexpr (sizeof(T) == 4) {
-        if (width <= 1024 * N) return with(Int<N>{}, Int<2>{}, Int<512>{}, Int<0>{});
-        if (width <= 2048 * N) return with(Int<N>{}, Int<4>{}, Int<512>{}, Int<0>{});
-        return with(Int<N>{}, Int<4>{}, Int<1024>{}, Int<0>{});
+        if (width <= 1024 * N) return with(NormShape<N, 2, 512, kRegisters, false>{});
+        if (width <= 2048 * N) return with(NormShape<N, 4, 512, kRegisters, false>{});
+        return with(NormShape<N, 4, 1024, kRegisters, false>{});
     } else {
-        if (width <= 1024 * N) return with(Int<N>{}, Int<2>{}, Int<512>{}, Int<0>{});
-        return with(Int<N>{}, Int<2>{}, Int<1024>{}, Int<0>{});
+        if (width <= 1024 * N) return with(NormShape<N, 2, 512, kRegisters, false>{});
+        return with(NormShape<N, 2, 1024, kRegisters, false>{});
     }
 }
 
@@ -46,27 +46,25 @@ rs_status norm_launch(K kernel, size_t blocks, unsigned threads, size_t smem, co
 template <typename T>
 rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s)
 {
-    return norm_shape<T>(p.width, vectors, [&](auto n, auto v, auto most, auto ring, unsigned threads) {
-        constexpr int N = decltype(n)::value, V = decltype(v)::value, M = decltype(most)::value;
-        constexpr int D = decltype(ring)::value ? kNormDepth : 0;
+    return norm_shape<T>(p.width, vectors, [&](auto shape, unsigned threads) {
+        using S = decltype(shape);
         // as many blocks as an SM holds at once
-        const size_t of = V == 1 ? 1024 : N == 1 && V == 4 ? 768 : 512;
-        const size_t per = threads > of ? 1 : of / threads < 16 ? of / threads : 16, blocks = p.rows < 152 * per ? p.rows : 152 * per;
+        const size_t of = S::V == 1 ? 1024 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
+        const size_t blocks = p.rows < 152 * per ? p.rows : 152 * per;
         if (p.block)
-            return norm_launch(k_norm<T, N, V, M, true, D>, blocks, threads, Feed<T, N, V, 2, D>::smem(threads), p, s);
-        return norm_launch(k_norm<T, N, V, M, false, D>, blocks, threads, Feed<T, N, V, 1, D>::smem(threads), p, s);
+            return norm_launch(k_norm<T, S, true>, blocks, threads, Feed<T, S, 2>::smem(p.width, threads), p, s);
+        return norm_launch(k_norm<T, S, false>, blocks, threads, Feed<T, S, 1>::smem(p.width, threads), p, s);
     });
 }
 
 template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s)
 {
-    const rs_status st = norm_shape<T>(p.width, vectors, [&](auto n, auto v, auto most, auto ring, unsigned threads) {
-        constexpr int N = decltype(n)::value, V = decltype(v)::value, M = decltype(most)::value;
-        constexpr int D = decltype(ring)::value ? kGradDepth : 0;
+    const rs_status st = norm_shape<T>(p.width, vectors, [&](auto shape, unsigned threads) {
+        using S = decltype(shape);
         if (p.block)
-            return norm_launch(k_norm_grad<T, N, V, M, true, D>, blocks, threads, Feed<T, N, V, 4, D>::smem(threads), p, s);
-        return norm_launch(k_norm_grad<T, N, V, M, false, D>, blocks, threads, Feed<T, N, V, 3, D>::smem(threads), p, s);
+            return norm_launch(k_norm_grad<T, S, true>, blocks, threads, Feed<T, S, 4>::smem(p.width, threads), p, s);
+        return norm_launch(k_norm_grad<T, S, false>, blocks, threads, Feed<T, S, 3>::smem(p.width, threads), p, s);
     });
     if (st != RS_OK || (!p.dweight && !p.dblock_weight && !p.dgate)) return st;
     const bool by_gate = p.gate_rows < blocks;
