@@ -120,6 +120,36 @@ __device__ __forceinline__ Vec<T, kVec<T>> from_floats(const float (&f)[kVec<T>]
     return *reinterpret_cast<const Vec<T, kVec<T>>*>(&u);
 }
 
+// Two floats in one 64-bit register, and the instructions on them.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b)
+{
+    a = __uint_as_float((uint32_t)v);
+    b = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Rows that are only element-aligned (an odd width, say) still move 16 bytes
 // at a time: the vectors of a written row are cut where its addresses are
 // multiples of 16, so element 0 of vector v of a row is v * kVec - lead(row),

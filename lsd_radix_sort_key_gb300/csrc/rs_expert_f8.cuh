@@ -117,6 +117,67 @@ struct Scales8 {
     }
 };
 
+// The epilogue's arithmetic on 16 values, two to an instruction (the same formulas
+// as in rs_expert_groups.cuh): with gelu the issue slots are what lasts.
+template <typename T>
+__device__ __forceinline__ void add_pairs(uint32_t (&z)[16], const uint32_t (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = unpack2<T>(v[i]);
+        const uint64_t sum = add2((uint64_t)z[2 * i + 1] << 32 | z[2 * i], pair_of(f.x, f.y));
+        z[2 * i] = (uint32_t)sum;
+        z[2 * i + 1] = (uint32_t)(sum >> 32);
+    }
+}
+
+__device__ __forceinline__ uint64_t both(float (*f)(float), uint64_t v)
+{
+    return pair_of(f(__uint_as_float((uint32_t)v)), f(__uint_as_float((uint32_t)(v >> 32))));
+}
+
+template <int ACT>
+__device__ __forceinline__ uint64_t activate_pair(uint64_t z)
+{
+    constexpr auto two = [](float c) { return pair_of(c, c); };
+    if constexpr (ACT == RS_ACT_RELU) {
+        return both(activate<RS_ACT_RELU, true>, z);
+    } else if constexpr (ACT == RS_ACT_SILU) {
+        const uint64_t e = both(fast_exp2, mul2(z, two(-kLog2e)));
+        return mul2(z, both(fast_reciprocal, add2(e, two(1.0f))));
+    } else {
+        const uint64_t magnitudes = z & 0x7FFFFFFF7FFFFFFFull;
+        const uint64_t t = both(fast_reciprocal, fma2(two(0.3275911f * 0.70710678118654752f), magnitudes, two(1.0f)));
+        const uint64_t e = both(fast_exp2, mul2(mul2(z, z), two(-0.5f * kLog2e)));
+        uint64_t poly = fma2(t, two(0.5f * 1.061405429f), two(0.5f * -1.453152027f));
+        poly = fma2(t, poly, two(0.5f * 1.421413741f));
+        poly = fma2(t, poly, two(0.5f * -0.284496736f));
+        poly = fma2(t, poly, two(0.5f * 0.254829592f));
+        const uint64_t low = mul2(mul2(t, poly), e), high = fma2(low, two(-1.0f), two(1.0f));
+        const uint32_t a = (int32_t)z < 0 ? (uint32_t)low : (uint32_t)high;
+        const uint32_t b = (int64_t)z < 0 ? (uint32_t)(low >> 32) : (uint32_t)(high >> 32);
+        return mul2(z, (uint64_t)b << 32 | a);
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate_pairs(uint32_t (&z)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const uint64_t v = activate_pair<ACT>((uint64_t)z[i + 1] << 32 | z[i]);
+        z[i] = (uint32_t)v;
+        z[i + 1] = (uint32_t)(v >> 32);
+    }
+}
+
+__device__ __forceinline__ void activate_pairs(uint32_t (&z)[16], int act)
+{
+    if (act == RS_ACT_RELU) activate_pairs<RS_ACT_RELU>(z);
+    else if (act == RS_ACT_GELU) activate_pairs<RS_ACT_GELU>(z);
+    else if (act == RS_ACT_SILU) activate_pairs<RS_ACT_SILU>(z);
+}
+
 // The larger of this lane's value and that of the same lane in the warp that has the
 // other half of its columns.  mine, other: shared memory of the two warps, 32
 // words each; both come here together (barrier `id`).
@@ -440,16 +501,18 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                         if (col(c) >= cols) return;
                     }
                     const uint32_t j = j_first + col(c), left = cols - col(c);
-                    if (p.bias && some) add_bias<T>(v, p.bias + t.e * p.bias_e + j, left, vec_bias);
+                    if (p.bias && some) {
+                        uint32_t bias[8];
+                        load_bias<T>(bias, p.bias + t.e * p.bias_e + j, left, vec_bias);
+                        add_pairs<T>(v, bias);
+                    }
                     if (p.pre) {
                         uint32_t out[8];
                         round_all<T>(out, v);
                         store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                     }
                     // (an activation of zero is zero)
-                    if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(v);
-                    else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(v);
-                    else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(v);
+                    activate_pairs(v, p.act);
                     if (left < 16)
 #pragma unroll
                         for (uint32_t k = 0; k < 16; ++k)
@@ -547,7 +610,7 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                         uint32_t(&zz)[16] = z[o];
                         tmem_load_wait(zz);
                         if (c == W / 16 - 1) release(acc_empty);
-                        if (p.bias && col(c) < cols) add_all<T>(zz, bias);
+                        if (p.bias && col(c) < cols) add_pairs<T>(zz, bias);
                         fetch_bias(c + 1);
                         fetch_residual(c + 1, add[o ^ 1]);
                         uint32_t out[8];
@@ -555,12 +618,10 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                             round_all<T>(out, zz);
                             store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                         }
-                        if (p.act == RS_ACT_RELU) activate_all<RS_ACT_RELU>(zz);
-                        else if (p.act == RS_ACT_GELU) activate_all<RS_ACT_GELU>(zz);
-                        else if (p.act == RS_ACT_SILU) activate_all<RS_ACT_SILU>(zz);
+                        activate_pairs(zz, p.act);
                         if (p.residual && col(c) < cols) {
                             spread_piece<T>(stage, add[o], residual, j, p.cols);
-                            add_all<T>(zz, add[o]);
+                            add_pairs<T>(zz, add[o]);
                         }
                         round_all<T>(out, zz);
                         fetch_acc(c + 2, zz);

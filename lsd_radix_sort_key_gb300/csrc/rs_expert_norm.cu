@@ -94,7 +94,7 @@ private:
 
 size_t grad_temp(const rs_expert_norm_desc* d)
 {
-    const size_t blocks = norm_grad_blocks(d->rows, d->width, type_bytes(d->type));
+    const size_t blocks = norm_grad_blocks(d->rows, d->width, type_bytes(d->type), d->block != nullptr);
     return align_up(kParts * blocks * d->width * 4, 256);
 }
 
@@ -199,7 +199,7 @@ rs_status rs_expert_norm_grad(const rs_expert_norm_desc* d)
         p.dblock_weight = d->dblock_weight;
         p.dgate = d->dgate;
         p.part = static_cast<float*>(d->temp);
-        return norm_gradient<T>(p, vectors, norm_grad_blocks(n, w, eb), s);
+        return norm_gradient<T>(p, vectors, norm_grad_blocks(n, w, eb, d->block != nullptr), s);
     });
 }
 

@@ -56,7 +56,7 @@ enum { kPartWeight, kPartBlockWeight, kPartGateFirst, kPartGateLater, kParts };
 // Adjacent elements are one 16-byte vector; STRIDED ones, for rows that are only
 // element-aligned, lie as many elements apart as the block has threads, so that
 // neighbouring threads have neighbouring elements.  MODE: where rows wait (Feed).
-enum { kRegisters, kOwn, kShared };
+enum { kRegisters, kOwn };
 template <int N_, int V_, int THREADS_, int MODE_, bool STRIDED_>
 struct NormShape {
     static constexpr int N = N_, V = V_, THREADS = THREADS_, MODE = MODE_;
@@ -154,30 +154,9 @@ __device__ __forceinline__ void store_params(void* p, size_t row, int i, uint32_
     }
 }
 
-// Arithmetic on a thread's N elements, two to an instruction: the kernels
-// below issue too many to leave all else to memory (a gradient's row of 8 elements per
-// thread about 500, 70% of the issue slots).
-__device__ __forceinline__ uint64_t pair_of(float a, float b)
-{
-    return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b)
-{
-    a = __uint_as_float((uint32_t)v);
-    b = __uint_as_float((uint32_t)(v >> 32));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
+// Arithmetic on a thread's N elements, two to an instruction: the kernels below issue
+// too many to leave all else to memory (a gradient's row of 8 elements per thread
+// about 500, 70% of the issue slots).
 
 // d = a b
 template <int N>
@@ -274,121 +253,81 @@ struct Walked {
 // The rows of STREAMS matrices, one after the other, as this thread has them.
 //   kOwn        vectors: each thread copies its own 16 bytes to shared memory, for
 //               itself, three rows ahead, so no barrier is needed
-//   kShared     strided elements: the block copies the 16-byte pieces of memory
-//               that a row lies in, two rows ahead, and meets once per row; pieces that
-//               reach past the matrix's ends are copied element by element
-//   kRegisters  rows too wide for that: one row ahead
-// With one row ahead in registers the SMs had too few bytes in flight (16384 x
-// 2048 bf16: forward 63 us, gradient 182).
+//   kRegisters  rows too wide for that, and strided elements: one row ahead
+// With one row ahead in registers the SMs had too few bytes in flight for vectors
+// (16384 x 2048 bf16: forward 63 us, gradient 182).  Strided elements are bound by
+// their instructions instead: copied to shared memory by the block they took
+// longer (8000 x 2047 bf16, gradient without a block 63 us, 48 through registers).
 template <typename T, typename S, int STREAMS>
 struct Feed {
     static constexpr int N = S::N, V = S::V, MODE = S::MODE;
-    static constexpr uint32_t DEPTH = MODE == kOwn ? 4 : MODE == kShared ? 3 : 1;
+    static constexpr uint32_t DEPTH = MODE == kOwn ? 4 : 1;
     static constexpr int HELD = MODE == kRegisters ? STREAMS : 1;
     Vec<T, N> now[HELD][V], next[HELD][V];
-    unsigned char* ring;   // [DEPTH][STREAMS][pitch]; kOwn: from this thread's part on
+    unsigned char* ring;   // [DEPTH][STREAMS][pitch], from this thread's part on
     unsigned char* here;   // the slot of the row at hand
     uint32_t slot, pitch;  // pitch: of a row
-    uint32_t shift[MODE == kShared ? STREAMS : 1];  // bytes before the row at hand
 
-    static size_t row_bytes(size_t width, size_t threads)
-    {
-        return MODE == kOwn ? V * threads * 16 : MODE == kShared ? align_up(width * sizeof(T), 16) + 16 : 0;
-    }
-    static size_t smem(size_t width, size_t threads)
-    {
-        return MODE == kRegisters ? 0 : DEPTH * STREAMS * row_bytes(width, threads);
-    }
+    static size_t smem(size_t threads) { return MODE == kOwn ? DEPTH * STREAMS * V * threads * 16 : 0; }
 
     __device__ __forceinline__ void start(const Walked<T> (&m)[STREAMS], unsigned char* mem, uint32_t first, uint32_t last,
-                                          uint32_t rows, uint32_t width)
+                                          uint32_t width)
     {
-        pitch = MODE == kOwn ? V * blockDim.x * 16 : (width * (uint32_t)sizeof(T) + 15) / 16 * 16 + 16;
-        ring = here = mem + (MODE == kOwn ? threadIdx.x * 16 : 0);
+        pitch = V * blockDim.x * 16;
+        ring = here = mem + threadIdx.x * 16;
         slot = 0;
-        if constexpr (MODE == kRegisters) {
+        if constexpr (MODE == kOwn) {
+            for (uint32_t k = 0; k < DEPTH * STREAMS; ++k)  // what is not copied reads as zero
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    *reinterpret_cast<uint4*>(ring + k * pitch + i * blockDim.x * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (uint32_t d = 0; d + 1 < DEPTH; ++d) {
+                if (first + d < last) fetch(m, first + d, d, width);
+                end_group();
+            }
+        } else {
 #pragma unroll
             for (int k = 0; k < STREAMS; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) next[k][i] = Vec<T, N>{};
-            fetch(m, first, 0, rows, width);
-        } else {
-            if constexpr (MODE == kOwn) {  // what is not copied reads as zero
-                for (uint32_t k = 0; k < DEPTH * STREAMS; ++k)
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        *reinterpret_cast<uint4*>(ring + k * pitch + i * blockDim.x * 16) = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (uint32_t d = 0; d + 1 < DEPTH; ++d) {
-                if (first + d < last) fetch(m, first + d, d, rows, width);
-                end_group();
-            }
+            fetch(m, first, 0, width);
         }
     }
-    __device__ __forceinline__ void fetch(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t to, uint32_t rows, uint32_t width)
+    __device__ __forceinline__ void fetch(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t to, uint32_t width)
     {
 #pragma unroll
         for (int k = 0; k < STREAMS; ++k) {
             if (!m[k].p) continue;
             const T* row = m[k].p + r * m[k].stride;
-            unsigned char* at = ring + (to * STREAMS + k) * pitch;
-            if constexpr (MODE == kRegisters) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) next[k][i] = load_elements<S, T>(row, i, width);
-            } else if constexpr (MODE == kOwn) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (S::has(i, 0, width)) copy16(at + i * blockDim.x * 16, row + S::col(i, 0));
-            } else {
-                const uintptr_t begin = (uintptr_t)m[k].p, end = (uintptr_t)(m[k].p + (rows - 1) * m[k].stride + width);
-                const uintptr_t from = (uintptr_t)row & ~(uintptr_t)15, row_end = (uintptr_t)(row + width);
-                for (uintptr_t a = from + threadIdx.x * 16; a < row_end; a += blockDim.x * 16) {
-                    if (a >= begin && a + 16 <= end) {
-                        copy16(at + (a - from), reinterpret_cast<const void*>(a));
-                    } else {
-                        for (uintptr_t e = a < (uintptr_t)row ? (uintptr_t)row : a; e < a + 16 && e < row_end; e += sizeof(T))
-                            *reinterpret_cast<T*>(at + (e - from)) = *reinterpret_cast<const T*>(e);
-                    }
-                }
+            for (int i = 0; i < V; ++i) {
+                if constexpr (MODE == kRegisters) next[k][i] = load_elements<S, T>(row, i, width);
+                else if (S::has(i, 0, width)) copy16(ring + (to * STREAMS + k) * pitch + i * blockDim.x * 16, row + S::col(i, 0));
             }
         }
     }
     // Row r is there afterwards.
-    __device__ __forceinline__ void turn_to(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t first, uint32_t last, uint32_t rows,
-                                            uint32_t width)
+    __device__ __forceinline__ void turn_to(const Walked<T> (&m)[STREAMS], uint32_t r, uint32_t first, uint32_t last, uint32_t width)
     {
         if constexpr (MODE == kRegisters) {
 #pragma unroll
             for (int k = 0; k < STREAMS; ++k)
 #pragma unroll
                 for (int i = 0; i < V; ++i) now[k][i] = next[k][i];
-            if (r + 1 < last) fetch(m, r + 1, 0, rows, width);
-            return;
-        }
-        if (r != first && ++slot == DEPTH) slot = 0;
-        if constexpr (MODE == kShared) {
-            wait_groups<(int)DEPTH - 2>();
-            __syncthreads();  // everybody's pieces are there, and the slot before is free
-#pragma unroll
-            for (int k = 0; k < STREAMS; ++k) shift[k] = (uint32_t)(uintptr_t)(m[k].p + r * m[k].stride) & 15;
-        }
-        if (r + DEPTH - 1 < last) fetch(m, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, rows, width);
-        end_group();
-        if constexpr (MODE == kOwn) wait_groups<(int)DEPTH - 1>();
-        here = ring + slot * STREAMS * pitch;
-    }
-    __device__ __forceinline__ void get(const Walked<T> (&m)[STREAMS], float (&f)[N], int stream, int i, uint32_t width) const
-    {
-        if constexpr (MODE == kRegisters) {
-            widen<T, N>(f, now[stream][i]);
-        } else if constexpr (MODE == kOwn) {
-            widen<T, N>(f, *reinterpret_cast<const Vec<T, N>*>(here + stream * pitch + i * blockDim.x * 16));
+            if (r + 1 < last) fetch(m, r + 1, 0, width);
         } else {
-            const T* row = reinterpret_cast<const T*>(here + stream * pitch + shift[stream]);
-#pragma unroll
-            for (int c = 0; c < N; ++c) f[c] = m[stream].p && S::has(i, c, width) ? to_float(row[S::col(i, c)]) : 0.0f;
+            if (r != first && ++slot == DEPTH) slot = 0;
+            if (r + DEPTH - 1 < last) fetch(m, r + DEPTH - 1, slot == 0 ? DEPTH - 1 : slot - 1, width);
+            end_group();
+            wait_groups<(int)DEPTH - 1>();
+            here = ring + slot * STREAMS * pitch;
         }
+    }
+    __device__ __forceinline__ void get(float (&f)[N], int stream, int i) const
+    {
+        if constexpr (MODE == kRegisters) widen<T, N>(f, now[stream][i]);
+        else widen<T, N>(f, *reinterpret_cast<const Vec<T, N>*>(here + stream * pitch + i * blockDim.x * 16));
     }
 };
 
@@ -446,11 +385,11 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1)
     m[0] = {p.x, p.x_i};
     if constexpr (BLOCK) m[1] = {p.block, p.block_i};
     Feed<T, S, kStreams> feed;
-    feed.start(m, ring, first, last, p.rows, p.width);
+    feed.start(m, ring, first, last, p.width);
     load_columns<S, T>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
     if constexpr (BLOCK) load_gate<S, T>(gw, p, gate);
     for (uint32_t r = first; r < last; ++r) {
-        feed.turn_to(m, r, first, last, p.rows, p.width);
+        feed.turn_to(m, r, first, last, p.width);
         Vec<T, N> y[V];  // as it is held
         if constexpr (BLOCK) {
             if (r == gate_end) {
@@ -464,7 +403,7 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
-                    feed.get(m, f, 1, i, p.width);
+                    feed.get(f, 1, i);
                     sum.add(f, f);
                 }
                 float s[1] = {sum.get()};
@@ -474,10 +413,10 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float f[N], u[N];
-                feed.get(m, u, 1, i, p.width);
+                feed.get(u, 1, i);
                 times(u, u, rb);
                 times(u, u, gw[i]);
-                feed.get(m, f, 0, i, p.width);
+                feed.get(f, 0, i);
                 times_plus(u, f, p.scale, u);
                 y[i] = narrow<T, N>(u);
                 store_elements<S, T>(p.y + r * p.y_i, i, p.width, y[i]);
@@ -486,7 +425,7 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1)
         }
         auto held = [&](float (&f)[N], int i) {
             if constexpr (BLOCK) widen<T, N>(f, y[i]);
-            else feed.get(m, f, 0, i, p.width);
+            else feed.get(f, 0, i);
         };
         Sum2 sum;
 #pragma unroll
@@ -534,7 +473,7 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 
     m[kDy] = {p.dy, p.dy_i};
     if constexpr (BLOCK) m[kB] = {p.block, p.block_i};
     Feed<T, S, kStreams> feed;
-    feed.start(m, ring, first, last, p.rows, p.width);
+    feed.start(m, ring, first, last, p.width);
     load_columns<S, T>(w, p.weight, 0, p.wide_params, 0.0f, p.width);
     if constexpr (BLOCK) load_gate<S, T>(gw, p, gate);
     auto store_part = [&](int kind, int i, const float (&f)[N]) {
@@ -550,18 +489,18 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 
         }
     };
     for (uint32_t r = first; r < last; ++r) {
-        feed.turn_to(m, r, first, last, p.rows, p.width);
+        feed.turn_to(m, r, first, last, p.width);
         Sum2 y_y, g_y, b_b;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N], g[N];
-            feed.get(m, f, kY, i, p.width);
-            feed.get(m, g, kDh, i, p.width);
+            feed.get(f, kY, i);
+            feed.get(g, kDh, i);
             times(g, g, w[i]);
             y_y.add(f, f);
             g_y.add(g, f);
             if constexpr (BLOCK) {
-                feed.get(m, f, kB, i, p.width);
+                feed.get(f, kB, i);
                 b_b.add(f, f);
             }
         }
@@ -575,9 +514,9 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float f[N], g[N], d[N];
-            feed.get(m, f, kY, i, p.width);
-            feed.get(m, g, kDh, i, p.width);
-            feed.get(m, d, kDy, i, p.width);
+            feed.get(f, kY, i);
+            feed.get(g, kDh, i);
+            feed.get(d, kDy, i);
             times_plus(d, f, -kx, d);
             times(f, f, rx);
             times_plus(dw[i], g, f, dw[i]);
@@ -586,7 +525,7 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 
             times(g, d, p.scale);
             if (p.dx) store_elements<S, T>(p.dx + r * p.dx_i, i, p.width, narrow<T, N>(g));
             if constexpr (BLOCK) {
-                feed.get(m, f, kB, i, p.width);
+                feed.get(f, kB, i);
                 times(g, f, rb);
                 times_plus(sum[i], d, g, sum[i]);
                 times(du[i], d, gw[i]);
@@ -604,7 +543,7 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
-                    feed.get(m, f, kB, i, p.width);
+                    feed.get(f, kB, i);
                     times(f, f, -kb);
                     times_plus(f, du[i], rb, f);
                     store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(f));
@@ -724,15 +663,15 @@ rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s);
 template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s);
 
-// Blocks of a gradient: the sizes alone decide, as the order of its sums goes by
-// them.  As many as an SM holds at once by their registers: 768 threads' worth
-// where a row takes up to 256 (one per 16 bytes), 512 threads' where its elements
-// are strided (one per eight), else one.
-inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem)
+// Blocks of a gradient: the sizes and whether there is a block decide, as the
+// order of its sums goes by them.  As many as an SM holds at once by their
+// registers: 768 threads' worth where a row takes up to 256 (one per 16 bytes),
+// about 576 where its elements are strided (four or eight to a thread), else one.
+inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem, bool block)
 {
     const bool strided = width * elem % 16 && width <= 2048;
-    const size_t threads = align_up(strided ? ceil_div(width, 8) : ceil_div(width * elem, 16), 32);
-    const size_t per = threads > 256 ? 1 : (strided ? 512 : 768) / threads, blocks = 152 * (per < 8 ? per : 8);
+    const size_t threads = align_up(strided ? ceil_div(width, block ? 4 : 8) : ceil_div(width * elem, 16), 32);
+    const size_t per = threads > (strided ? 288 : 256) ? 1 : (strided ? 576 : 768) / threads, blocks = 152 * (per < 8 ? per : 8);
     return (uint32_t)(rows < blocks ? rows : blocks);
 }
 

@@ -2,15 +2,18 @@
 // kernel takes which width.  Included by one translation unit per type.
 #pragma once
 
+#include <type_traits>
+
 #include "rs_expert_norm.cuh"
 
 namespace rsx {
 
 // The shape for a width: one vector per thread up to 512 threads, rows through
 // shared memory; past 512 vectors two (or four) of them in up to 1024 threads,
-// through registers; strided elements, eight per thread through shared memory up
-// to 2048, else 16 through registers.
-template <typename T, typename F>
+// through registers; strided elements up to 2048 four per thread with a block and
+// eight without (a gradient of 4099 x 1037 float32 without a block 29 us with four
+// and 20 with eight; with one, 16 bits, 51 and 79), else 16.
+template <typename T, bool BLOCK, typename F>
 rs_status norm_shape(uint32_t width, bool vectors, F run)
 {
     constexpr int N = kVec<T>;
@@ -19,7 +22,8 @@ rs_status norm_shape(uint32_t width, bool vectors, F run)
         return run(shape, (unsigned)align_up(ceil_div(width, (size_t)S::N * S::V), 32));
     };
     if (!vectors) {
-        if (width <= 2048) return with(NormShape<8, 1, 256, kShared, true>{});
+        using Short = std::conditional_t<BLOCK, NormShape<4, 1, 512, kRegisters, true>, NormShape<8, 1, 256, kRegisters, true>>;
+        if (width <= 2048) return with(Short{});
         if (width <= 8192) return with(NormShape<4, 4, 512, kRegisters, true>{});
         return with(NormShape<4, 4, 1024, kRegisters, true>{});
     }
@@ -46,26 +50,30 @@ rs_status norm_launch(K kernel, size_t blocks, unsigned threads, size_t smem, co
 template <typename T>
 rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s)
 {
-    return norm_shape<T>(p.width, vectors, [&](auto shape, unsigned threads) {
-        using S = decltype(shape);
-        // as many blocks as an SM holds at once
-        const size_t of = S::V == 1 ? 1024 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
-        const size_t blocks = p.rows < 152 * per ? p.rows : 152 * per;
-        if (p.block)
-            return norm_launch(k_norm<T, S, true>, blocks, threads, Feed<T, S, 2>::smem(p.width, threads), p, s);
-        return norm_launch(k_norm<T, S, false>, blocks, threads, Feed<T, S, 1>::smem(p.width, threads), p, s);
-    });
+    auto launch = [&](auto block) {
+        constexpr bool BLOCK = decltype(block)::value != 0;
+        return norm_shape<T, BLOCK>(p.width, vectors, [&](auto shape, unsigned threads) {
+            using S = decltype(shape);
+            // as many blocks as an SM holds at once
+            const size_t of = S::V == 1 ? 1024 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
+            return norm_launch(k_norm<T, S, BLOCK>, p.rows < 152 * per ? p.rows : 152 * per, threads,
+                               Feed<T, S, BLOCK ? 2 : 1>::smem(threads), p, s);
+        });
+    };
+    return p.block ? launch(Int<1>{}) : launch(Int<0>{});
 }
 
 template <typename T>
 rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cudaStream_t s)
 {
-    const rs_status st = norm_shape<T>(p.width, vectors, [&](auto shape, unsigned threads) {
-        using S = decltype(shape);
-        if (p.block)
-            return norm_launch(k_norm_grad<T, S, true>, blocks, threads, Feed<T, S, 4>::smem(p.width, threads), p, s);
-        return norm_launch(k_norm_grad<T, S, false>, blocks, threads, Feed<T, S, 3>::smem(p.width, threads), p, s);
-    });
+    auto launch = [&](auto block) {
+        constexpr bool BLOCK = decltype(block)::value != 0;
+        return norm_shape<T, BLOCK>(p.width, vectors, [&](auto shape, unsigned threads) {
+            using S = decltype(shape);
+            return norm_launch(k_norm_grad<T, S, BLOCK>, blocks, threads, Feed<T, S, BLOCK ? 4 : 3>::smem(threads), p, s);
+        });
+    };
+    const rs_status st = p.block ? launch(Int<1>{}) : launch(Int<0>{});
     if (st != RS_OK || (!p.dweight && !p.dblock_weight && !p.dgate)) return st;
     const bool by_gate = p.gate_rows < blocks;
     const unsigned jobs = 2 + (p.dgate ? by_gate ? p.gate_rows : blocks - 1 : 0);
