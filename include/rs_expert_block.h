@@ -57,7 +57,8 @@ extern "C" {
  *
  * Nothing to write (rows, tokens, width, outer or inner 0): RS_OK.  Sizes:
  * rows <= RS_EXPERT_SLOTS_MAX, width, outer, inner <= RS_EXPERT_WIDTH_MAX,
- * num_experts <= RS_EXPERTS_MAX.
+ * num_experts <= RS_EXPERTS_MAX, fewer than 2^32 blocks of rows (tokens, for
+ * a dispatch) and 2^31 of weights.
  */
 rs_status rs_expert_quantize(rs_float_type type, const void* x, size_t x_stride, size_t rows, size_t width, void* q,
                              size_t q_stride, void* scales, size_t scales_stride, void* stream);
@@ -148,7 +149,8 @@ rs_status rs_expert_matmul_quantized(const rs_expert_matmul_quantized_desc* desc
  * input is missing is refused.
  *
  * Errors: RS_ERR_INVALID_ARG (also width > RS_EXPERT_NORM_WIDTH_MAX, an eps
- * that is negative or not finite, rows not a multiple of gate_rows),
+ * that is negative, an eps or residual_scale that is not finite, rows not a
+ * multiple of gate_rows),
  * RS_ERR_TEMP_TOO_SMALL, RS_ERR_ALIAS, RS_ERR_CUDA.  rows == 0 writes zeros to
  * the summed gradients; width == 0 does nothing.  Row strides may be 0 for
  * inputs (one row for all).

@@ -30,7 +30,9 @@ rs_status check_sizes(const rs_expert_norm_desc* d)
 {
     if (!d || !valid_type(d->type) || (d->param_type != d->type && d->param_type != RS_FLOAT32)) return RS_ERR_INVALID_ARG;
     if (d->rows > RS_EXPERT_SLOTS_MAX || d->width > RS_EXPERT_NORM_WIDTH_MAX) return RS_ERR_INVALID_ARG;
-    if (!(d->eps >= 0.0f && d->eps <= 3.4e38f)) return RS_ERR_INVALID_ARG;
+    constexpr float most = 3.402823466e38f;
+    if (!(d->eps >= 0.0f && d->eps <= most) || !(d->residual_scale >= -most && d->residual_scale <= most))
+        return RS_ERR_INVALID_ARG;
     if (d->gate_rows > d->rows && d->rows) return RS_ERR_INVALID_ARG;
     if (d->gate_rows && d->rows % d->gate_rows) return RS_ERR_INVALID_ARG;
     return RS_OK;

@@ -461,8 +461,9 @@ PyObject* matmul_quantized(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t rows = x->size(0), inner = x->size(1), experts = w->size(0), outer = w->size(1);
     for (const at::Tensor* t : {xs, w, ws, offsets})
         if (t->device() != x->device()) return none();
-    // (rows, experts and columns enough that every stride says something)
-    if (rows < 2 || experts < 1 || experts > RS_EXPERTS_MAX || outer < 2 || inner < 2 || w->size(2) != inner ||
+    if (rows == 1) d.x_stride = (size_t)up(inner, 16);  // a single row's stride is not used
+    // (experts and columns enough that every other stride says something)
+    if (rows < 1 || experts < 1 || experts > RS_EXPERTS_MAX || outer < 2 || inner < 2 || w->size(2) != inner ||
         w->stride(2) != 1 || (experts > 1 && w->stride(0) != outer * w->stride(1)) || xs->size(0) != rows ||
         xs->size(1) != blocks_of(inner) || ws->size(0) != experts || ws->size(1) != blocks_of(outer) ||
         ws->size(2) != blocks_of(inner) || !ws->is_contiguous() || offsets->size(0) != experts + 1 ||

@@ -347,8 +347,11 @@ def _params(what, t, x, width, rows=None):
 
 
 def _norm_inputs(x, weight, block, block_weight, gate, residual_scale, eps):
-    """The checks that a norm and its gradient share: (head of the descriptor up
-    to the parameters, the parameters' one type, contiguous parameters)."""
+    """The checks that a norm and its gradient share: (the head of the descriptor
+    up to the parameters, these)."""
+    for what, v in (("residual_scale", residual_scale), ("eps", eps)):
+        if isinstance(v, _x.torch.Tensor):  # its value would have to be waited for
+            raise TypeError(f"{what}: a number is wanted, got a tensor")
     ft = _ftype(x, "x")
     if block is None and weight is None:
         raise TypeError("weight: a tensor is wanted (or a block)")
@@ -373,10 +376,16 @@ def _norm_inputs(x, weight, block, block_weight, gate, residual_scale, eps):
         kind = t.dtype
     if gate is not None and (gate_rows < 1 or rows % gate_rows):
         raise ValueError(f"gate: a number of rows that divides {rows} is wanted, got {gate_rows}")
-    flat = [None if t is None else t.contiguous() for _, t, _ in params]
     head = (ft, ft if kind is None else FTYPES[kind], rows, width, eps, residual_scale, gate_rows, x.data_ptr(), xs,
-            0 if block is None else block.data_ptr(), bs, *(0 if t is None else t.data_ptr() for t in flat))
-    return head, flat
+            0 if block is None else block.data_ptr(), bs)
+    return head, (weight, block_weight, gate)
+
+
+def _contiguous(params):
+    """The parameters, copied where they are not contiguous (on the stream that
+    reads them), and their addresses."""
+    flat = [None if t is None else t.contiguous() for t in params]
+    return flat, [0 if t is None else t.data_ptr() for t in flat]
 
 
 def expert_norm(x, weight, *, block=None, block_weight=None, gate=None, residual_scale=1.0, eps=1e-6, stream=None):
@@ -400,19 +409,20 @@ def expert_norm(x, weight, *, block=None, block_weight=None, gate=None, residual
         out = _x._fast.norm(x, weight, block, block_weight, gate, residual_scale, eps)
         if out is not None:
             return out
-    head, flat = _norm_inputs(x, weight, block, block_weight, gate, residual_scale, eps)
+    head, params = _norm_inputs(x, weight, block, block_weight, gate, residual_scale, eps)
     s = _current(x.device, stream)
     if s is None:
-        with _other(x.device, stream, (x, block, *flat)) as s:
-            return _norm(head, x, weight, block, s)
-    return _norm(head, x, weight, block, s)
+        with _other(x.device, stream, (x, block, *params)) as s:
+            return _norm(head, x, block, params, s)
+    return _norm(head, x, block, params, s)
 
 
-def _norm(head, x, weight, block, s):
+def _norm(head, x, block, params, s):
     torch, width = _x.torch, x.shape[1]
+    flat, at = _contiguous(params)
     y = None if block is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    h = None if weight is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(_rs().rs_expert_norm(_NORM.pack(*head, 0 if y is None else y.data_ptr(), width or 1,
+    h = None if flat[0] is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(_rs().rs_expert_norm(_NORM.pack(*head, *at, 0 if y is None else y.data_ptr(), width or 1,
                                            0 if h is None else h.data_ptr(), width or 1, *([0] * 13), s)), "rs_expert_norm")
     return h if block is None else (y, h)
 
@@ -438,7 +448,7 @@ def expert_norm_grad(dh, y, weight, *, dy=None, block=None, block_weight=None, g
         raise TypeError("dh and weight go together")
     if dh is None and dy is None:
         raise TypeError("dh or dy: a tensor is wanted")
-    head, flat = _norm_inputs(y, weight, block, block_weight, gate, residual_scale, eps)
+    head, params = _norm_inputs(y, weight, block, block_weight, gate, residual_scale, eps)
     grads = []
     for what, t in (("dh", dh), ("dy", dy)):
         if t is not None:
@@ -446,17 +456,18 @@ def expert_norm_grad(dh, y, weight, *, dy=None, block=None, block_weight=None, g
         grads += (0, 0) if t is None else (t.data_ptr(), _rows(what, t)[2])
     s = _current(y.device, stream)
     if s is None:
-        with _other(y.device, stream, (dh, y, dy, block, *flat)) as s:
-            return _norm_grad(head, grads, y, block, (weight, block_weight, gate), s)
-    return _norm_grad(head, grads, y, block, (weight, block_weight, gate), s)
+        with _other(y.device, stream, (dh, y, dy, block, *params)) as s:
+            return _norm_grad(head, grads, y, block, params, s)
+    return _norm_grad(head, grads, y, block, params, s)
 
 
 def _norm_grad(head, grads, y, block, params, s):
     torch, h, width = _x.torch, _rs(), y.shape[1]
+    flat, at = _contiguous(params)
     dx = torch.empty(y.shape, dtype=y.dtype, device=y.device)
     dblock = None if block is None else torch.empty(y.shape, dtype=y.dtype, device=y.device)
-    sums = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=y.device) for t in params]
-    body = (*head, 0, 0, 0, 0, *grads, dx.data_ptr(), width or 1, 0 if dblock is None else dblock.data_ptr(), width or 1,
+    sums = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=y.device) for t in flat]
+    body = (*head, *at, 0, 0, 0, 0, *grads, dx.data_ptr(), width or 1, 0 if dblock is None else dblock.data_ptr(), width or 1,
             *(0 if t is None else t.data_ptr() for t in sums))
     tb = h.rs_expert_norm_grad_temp_bytes(_NORM.pack(*body, 0, 0, 0))
     if tb == _SIZE_ERROR:

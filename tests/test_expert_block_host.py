@@ -124,7 +124,8 @@ def norm(grad=False, **kw):
 
 
 NORM = [(dict(type=3), 1), (dict(param_type=1), 1), (dict(width=16385), 1), (dict(rows=(1 << 30) + 4), 1), (dict(eps=-1.0), 1),
-        (dict(eps=float("inf")), 1), (dict(eps=float("nan")), 1), (dict(gate_rows=5), 1), (dict(gate_rows=24), 1), (dict(gate=None), 1),
+        (dict(eps=float("inf")), 1), (dict(eps=float("nan")), 1), (dict(residual_scale=float("inf")), 1),
+        (dict(residual_scale=float("nan")), 1), (dict(gate_rows=5), 1), (dict(gate_rows=24), 1), (dict(gate=None), 1),
         (dict(x=None), 1), (dict(x=F + 1), 1), (dict(x_stride=263), 1), (dict(block=2 * F + 1), 1), (dict(block_stride=10), 1),
         (dict(weight=3 * F + 2), 1), (dict(block_weight=4 * F + 2), 1), (dict(gate=5 * F + 2), 1), (dict(block=None), 1),
         (dict(width=0), 0)]

@@ -189,6 +189,48 @@ def test_many_rows_and_tiles():
         check_quantized(got[0], got[1], y, mag, inner)
 
 
+@pytest.mark.parametrize("counts,inner,outer", [([0, 1, 3, 0] * 256, 128, 264), ([5], 65552, 40), ([3, 4], 64, 70000),
+                                                ([900] * 3, 16400, 272)])
+def test_many_experts_long_sums_and_wide_outputs(counts, inner, outer):
+    x, xs, w, ws, off = operands(counts, inner, outer, unused=3)
+    y, z, mag = plain(x, xs, w, ws, off)
+    check(y, z, rs.expert_matmul_quantized(x, xs, w, ws, off, dtype=torch.float16), None, mag, inner, torch.float16)
+    q, scales = rs.expert_matmul_quantized(x, xs, w, ws, off, quantize=True)
+    check_quantized(q, scales, y, mag, inner)
+
+
+def test_refusals(way):
+    x, xs, w, ws, off = operands([33, 70], 272, 200)
+    bias = torch.zeros(2, 200, dtype=torch.bfloat16, device=DEV)
+    res = torch.zeros(103, 200, dtype=torch.bfloat16, device=DEV)
+    tight = x.view(torch.uint8)[:, :271].contiguous().view(torch.float8_e4m3fn)  # rows of 271 bytes
+    for error, call in [
+            (TypeError, lambda: rs.expert_matmul_quantized(x.float(), xs, w, ws, off)),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs.float(), w, ws, off)),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs, w, ws.float(), off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs[:, :2], w, ws, off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws[:1], off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x[:, :256], xs[:, :2], w, ws, off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(tight, xs, w[:, :, :271], ws, off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x[:, 1:257], xs[:, :2], w[:, :, :256], ws[:, :, :2].contiguous(), off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w.transpose(1, 2), ws, off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w[:, :100], ws[:, :1].contiguous(), off)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off[:2])),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off.long())),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, bias=bias.half())),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, bias=bias[:1])),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, residual=res[:5])),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, residual=res, quantize=True)),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, dtype=torch.float32)),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, activation="tanh")),
+            (ValueError, lambda: rs.expert_matmul_quantized(x, xs, w, ws.cpu(), off)),
+            (TypeError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off, temp=torch.empty(100, device=DEV))),
+            (rs.RadixSortError, lambda: rs.expert_matmul_quantized(x, xs, w, ws, off,
+                                                                   temp=torch.empty(100, dtype=torch.uint8, device=DEV)))]:
+        with pytest.raises(error):
+            call()
+
+
 def test_offsets_that_are_no_plan():
     # clamped to ascending values in [0, rows]: wrong rows, no access outside
     x, xs, w, ws, _ = operands([40, 60, 30], 256, 256)

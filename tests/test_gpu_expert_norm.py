@@ -223,6 +223,60 @@ def test_sums_do_not_depend_on_timing_and_calls_can_be_captured():
     assert all(torch.equal(p, q) for p, q in zip(got, first[2:]))
 
 
+def test_parameters_are_copied_on_the_stream_that_reads_them():
+    # strided parameters on another stream, which is busy when the call is made
+    g = gen(4)
+    x, b = (torch.randn(200, 264, device=DEV, generator=g).bfloat16() for _ in range(2))
+    wide = torch.randn(3, 528, device=DEV, generator=g)
+    w, a, gate = (wide[i, ::2] for i in range(3))
+    want = rs.expert_norm(x, w, block=b, block_weight=a, gate=gate)
+    grad = rs.expert_norm_grad(x, want[0], w, dy=b, block=b, block_weight=a, gate=gate)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kept = wide.clone()
+    with torch.cuda.stream(side):
+        wide.zero_()
+        torch.cuda._sleep(100_000_000)
+        wide.copy_(kept)
+    got = rs.expert_norm(x, w, block=b, block_weight=a, gate=gate, stream=side)
+    got_grad = rs.expert_norm_grad(x, want[0], w, dy=b, block=b, block_weight=a, gate=gate, stream=side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip((*got, *got_grad), (*want, *grad)))
+
+
+def test_numbers(way):
+    x, w, b, a, g = inputs(6, 264, "f32")
+    check(x, w, b, a, g, scale=2)
+    check(x, w, b, a, g, scale=0.0)
+    with pytest.raises(TypeError):
+        rs.expert_norm(x, w, block=b, residual_scale=torch.ones((), device=DEV))
+    with pytest.raises(TypeError):
+        rs.expert_norm(x, w, eps=torch.ones((), device=DEV))
+    for number in (1e300, float("inf"), float("nan")):
+        with pytest.raises(rs.RadixSortError):
+            rs.expert_norm(x, w, block=b, residual_scale=number)
+    for eps in (-1.0, float("inf"), float("nan")):
+        with pytest.raises(rs.RadixSortError):
+            rs.expert_norm(x, w, eps=eps)
+
+
+def test_refusals(way):
+    x, w, b, a, g = inputs(12, 264, "bf16", gate=4)
+    for error, call in [
+            (ValueError, lambda: rs.expert_norm(x, w[:200])), (TypeError, lambda: rs.expert_norm(x, w.half())),
+            (ValueError, lambda: rs.expert_norm(x, w.cpu())), (ValueError, lambda: rs.expert_norm(x.T, w)),
+            (ValueError, lambda: rs.expert_norm(x, w, gate=g)), (ValueError, lambda: rs.expert_norm(x, w, block_weight=a)),
+            (ValueError, lambda: rs.expert_norm(x, w, block=b[:6])), (TypeError, lambda: rs.expert_norm(x, w, block=b.float())),
+            (TypeError, lambda: rs.expert_norm(x, w, block=b, block_weight=a.bfloat16())),
+            (ValueError, lambda: rs.expert_norm(x, w, block=b, gate=g.repeat(2, 1)[:5])),
+            (ValueError, lambda: rs.expert_norm(x, w, block=b, gate=g[:0])),
+            (ValueError, lambda: rs.expert_norm_grad(x[:6], x, w)), (TypeError, lambda: rs.expert_norm_grad(x, x, None, dy=x, block=b)),
+            (TypeError, lambda: rs.expert_norm_grad(None, x, None, block=b)),
+            (rs.RadixSortError, lambda: rs.expert_norm(x.new_zeros(2, 16392), w.new_zeros(16392)))]:
+        with pytest.raises(error):
+            call()
+
+
 def test_long_matrices():
     # past 2^31 elements: the last rows are theirs
     rows, width = (1 << 19) + 3, 4104
