@@ -29,26 +29,33 @@ rs_status f8_launch(const F8Operands& o, const F8Args<T>& args, int sms, cudaStr
                          mb, args);
 }
 
-// Pairs or single blocks, by a model of the time (us) as for the 16-bit products:
-// a block's slices times the waves of tiles over the SMs, 0.33 per slice of a
-// narrow tile, 0.34 of a pair's and 2 to start, and 0.38 where every block reads
-// weights that nobody has read yet.
+// Pairs or single blocks, by a model of the time (us): the waves of tiles over the
+// SMs, each of
+//   narrow  0.31 per slice of 128, and 0.8
+//   pair    0.27 per slice, and 2.6 (its epilogue is four times the work of a narrow
+//           tile's); 2.5 once, to start and to end
+// but 0.38 per slice where every block reads weights that nobody has read yet, as
+// long as device memory needs when all SMs ask at once.  A fit to timings on GB300 of
+// 1 to 16 experts with 8 to 2048 rows each, narrow / pair, us:
+//   1 expert,    512 rows, 4096 x 4096   20.5   22.5
+//   1 expert,   2048 rows, 4096 x 4096   51.2   34.8
+//   8 experts, 3001 rows in all, 1000 x 1160   14.5   16.4
+//   8 experts,  1000 rows, 1024 x 1024   22.5   20.5
+//   16 experts, 2048 rows, 512 x 1024    38.9   34.8
+//   16 experts, 2048 rows, 4096 x 4096    567    311
 inline bool f8_pairs(size_t rows, size_t experts, size_t cols, size_t slices, int sms)
 {
     if (cols <= 128) return false;
     // The offsets are on the device: with `owners` experts that can have rows,
     // half of them are taken to end in a partly filled tile.
     const size_t owners = rows < experts ? rows : experts;
-    auto down = [&](size_t tile_rows) {
-        const size_t t = rows / tile_rows + owners / 2;
-        return t > owners ? t : owners;
+    auto time = [&](double slice, double wave, size_t tile_rows, size_t tile_cols, int at_once) {
+        const size_t t = rows / tile_rows + owners / 2, down = t > owners ? t : owners;
+        const double first = 0.38 * (double)owners / (double)down;
+        return ((slice > first ? slice : first) * (double)slices + wave) *
+               (double)ceil_div(down * ceil_div(cols, tile_cols), at_once);
     };
-    auto time = [&](double slice, size_t tile_rows, size_t tile_cols, int at_once) {
-        const size_t d = down(tile_rows);
-        const double first = 0.38 * (double)owners / (double)d;
-        return (slice > first ? slice : first) * (double)slices * (double)ceil_div(d * ceil_div(cols, tile_cols), at_once);
-    };
-    return time(0.34, 2 * kTcRows, 256, sms / 2) + 2.0 < time(0.33, kTcRows, 128, sms);
+    return time(0.27, 2.6, 2 * kTcRows, 256, sms / 2) + 2.5 < time(0.31, 0.8, kTcRows, 128, sms);
 }
 
 template <typename T, bool QUANT>
