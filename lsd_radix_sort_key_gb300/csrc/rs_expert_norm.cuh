@@ -370,7 +370,7 @@ __device__ __forceinline__ float inverse_root(float sum, float per_width, float 
 // gate's until it changes): reading them again for every row is 24 KB beside a
 // row's 16 (2048 bf16, float32 parameters).
 template <typename T, typename S, bool BLOCK>
-__global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1) k_norm(NormArgs<T> p)
+__global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : S::THREADS == 128 ? 6 : 1) k_norm(NormArgs<T> p)
 {
     constexpr int N = S::N, V = S::V;
     __shared__ __align__(16) float mem[2 * 3 * 32];
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : 1)
 //     dgate = block_weight S,  dblock_weight += gate S,  S = the sum of d n,
 // so one sum serves both until the gate changes.
 template <typename T, typename S, bool BLOCK>
-__global__ void __launch_bounds__(S::THREADS, S::THREADS == 256 ? (S::STRIDED ? 2 : 3) : 1) k_norm_grad(NormArgs<T> p)
+__global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED ? 2 : 3) k_norm_grad(NormArgs<T> p)
 {
     constexpr int N = S::N, V = S::V;
     __shared__ __align__(16) float mem[2 * 3 * 32];

@@ -9,11 +9,14 @@
 namespace rsx {
 
 // The shape for a width: one vector per thread up to 512 threads, rows through
-// shared memory; past 512 vectors two (or four) of them in up to 1024 threads,
-// through registers; strided elements up to 2048 four per thread with a block and
-// eight without (a gradient of 4099 x 1037 float32 without a block 29 us with four
+// shared memory, but two where a row has 65 to 256 of them (unless it is the
+// forward call with a block): what a thread does once per row then counts for more
+// elements (16384 x 2048 bf16: gradient 86 -> 73 us, norm alone 22.8 -> 20.7, but with a
+// block 48 -> 50; rows of 256 33 -> 43 and more).  Past 512 vectors two (or four) of
+// them in up to 1024 threads, through registers; strided elements up to 2048 four
+// per thread with a block and eight without (a gradient of 4099 x 1037 float32 without a block 29 us with four
 // and 20 with eight; with one, 16 bits, 51 and 79), else 16.
-template <typename T, bool BLOCK, typename F>
+template <typename T, bool BLOCK, bool TWO, typename F>
 rs_status norm_shape(uint32_t width, bool vectors, F run)
 {
     constexpr int N = kVec<T>;
@@ -27,7 +30,9 @@ rs_status norm_shape(uint32_t width, bool vectors, F run)
         if (width <= 8192) return with(NormShape<4, 4, 512, kRegisters, true>{});
         return with(NormShape<4, 4, 1024, kRegisters, true>{});
     }
-    if (width <= 256 * N) return with(NormShape<N, 1, 256, kOwn, false>{});
+    if constexpr (TWO)
+        if (width > 64 * N && width <= 256 * N) return with(NormShape<N, 2, 128, kOwn, false>{});
+    if (width <= (TWO ? 64 : 256) * N) return with(NormShape<N, 1, 256, kOwn, false>{});
     if (width <= 512 * N) return with(NormShape<N, 1, 512, kOwn, false>{});
     if constexpr (sizeof(T) == 4) {
         if (width <= 1024 * N) return with(NormShape<N, 2, 512, kRegisters, false>{});
@@ -52,10 +57,10 @@ rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s)
 {
     auto launch = [&](auto block) {
         constexpr bool BLOCK = decltype(block)::value != 0;
-        return norm_shape<T, BLOCK>(p.width, vectors, [&](auto shape, unsigned threads) {
+        return norm_shape<T, BLOCK, !BLOCK>(p.width, vectors, [&](auto shape, unsigned threads) {
             using S = decltype(shape);
             // as many blocks as an SM holds at once
-            const size_t of = S::V == 1 ? 1024 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
+            const size_t of = S::V == 1 ? 1024 : S::THREADS == 128 ? 768 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
             return norm_launch(k_norm<T, S, BLOCK>, p.rows < 152 * per ? p.rows : 152 * per, threads,
                                Feed<T, S, BLOCK ? 2 : 1>::smem(threads), p, s);
         });
@@ -68,7 +73,7 @@ rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cud
 {
     auto launch = [&](auto block) {
         constexpr bool BLOCK = decltype(block)::value != 0;
-        return norm_shape<T, BLOCK>(p.width, vectors, [&](auto shape, unsigned threads) {
+        return norm_shape<T, BLOCK, true>(p.width, vectors, [&](auto shape, unsigned threads) {
             using S = decltype(shape);
             return norm_launch(k_norm_grad<T, S, BLOCK>, blocks, threads, Feed<T, S, BLOCK ? 4 : 3>::smem(threads), p, s);
         });
