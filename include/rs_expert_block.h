@@ -137,7 +137,8 @@ rs_status rs_expert_matmul_quantized(const rs_expert_matmul_quantized_desc* desc
  * Forward.  block == NULL: h = rms(x) weight (y, block_weight, gate unused).
  * Else y = residual_scale x + gate u, u = block_weight ? rms(block)
  * block_weight : block, and, if weight is not NULL, h = rms(y) weight, where y
- * is taken as it is held, after its rounding.  Sums are float32.
+ * is taken as it is held, after its rounding.  Sums are float32, so the squares
+ * of a row have to add up inside its range (magnitudes of about 1e-18 to 1e17).
  *
  * Gradient.  Reads y (block == NULL: x itself, in `x`; else the forward's y,
  * in `x`), dh (NULL only if weight is) and dy, the gradient that reaches y by

@@ -453,7 +453,9 @@ __global__ void __launch_bounds__(S::THREADS, S::V == 1 ? 1024 / S::THREADS : S:
 // Each block walks adjacent rows as above and keeps its threads' columns of the
 // summed gradients in registers.  Within one gate row, with n = block r,
 //     dgate = block_weight S,  dblock_weight += gate S,  S = the sum of d n,
-// so one sum serves both until the gate changes.
+// so one sum serves both until the gate changes.  The gradients of a row are
+// multiplied out as r (g - (r <g, v> / W) v r): r^3 alone leaves float32's range for
+// rows of magnitude 10^13 or 10^-13.
 template <typename T, typename S, bool BLOCK>
 __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED ? 2 : 3) k_norm_grad(NormArgs<T> p)
 {
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED 
         float sums[3] = {y_y.get(), g_y.get(), b_b.get()};
         block_sums(sums, mem, turn);
         const float rx = p.dh ? inverse_root(sums[0], p.per_width, p.eps) : 0.0f;
-        const float kx = rx * rx * rx * p.per_width * sums[1];
+        const float cx = rx * sums[1] * p.per_width;
         const float rb = BLOCK && p.block_weight ? inverse_root(sums[2], p.per_width, p.eps) : 1.0f;
         Sum2 du_b;
         float du[VB][N];
@@ -519,10 +521,10 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED 
             feed.get(f, kY, i);
             feed.get(g, kDh, i);
             feed.get(d, kDy, i);
-            times_plus(d, f, -kx, d);
             times(f, f, rx);
             times_plus(dw[i], g, f, dw[i]);
             times(g, g, w[i]);
+            times_plus(g, f, -cx, g);
             times_plus(d, g, rx, d);
             times(g, d, p.scale);
             if (p.dx) store_elements<S, T>(p.dx + r * p.dx_i, i, p.width, narrow<T, N>(g));
@@ -536,18 +538,18 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED 
         }
         if constexpr (BLOCK) {
             if (p.dblock) {
-                float kb = 0.0f;
+                float cb = 0.0f;
                 if (p.block_weight) {
                     float dot[1] = {du_b.get()};
                     block_sums(dot, mem, turn);
-                    kb = rb * rb * rb * p.per_width * dot[0];
+                    cb = rb * dot[0] * p.per_width * rb;
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float f[N];
                     feed.get(f, kB, i);
-                    times(f, f, -kb);
-                    times_plus(f, du[i], rb, f);
+                    times_plus(f, f, -cb, du[i]);
+                    times(f, f, rb);
                     store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(f));
                 }
             }

@@ -175,6 +175,20 @@ def test_a_zero_row_and_eps():
     assert bool(torch.isnan(h[2]).all()) and not bool(torch.isnan(h[3]).any())  # 0 / 0, as the formula says
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-46, 46])
+@pytest.mark.parametrize("width", [264, 1037])
+def test_rows_of_extreme_magnitude(dt, power, width):
+    # r^3 is 2^138 or 2^-138, outside float32's range; the squares and every result are inside
+    x, w, b, a, g = inputs(24, width, dt)
+    x, b = x * 2.0**power, b * 2.0**power
+    check(x, w, b, a, g, scale=2.0**-power, eps=0.0)
+    check(x, w, None, None, None, eps=0.0)
+    dh, dy = (torch.randn(24, width, device=DEV, generator=gen(s)).to(x.dtype) for s in (5, 6))
+    check_grad(x, w, b, a, g, dh, dy * 2.0**-power, eps=0.0)
+    check_grad(x, w, None, None, None, dh, None, eps=0.0)
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     x, w, b, a, g = inputs(40, 1037, "f32")
     x[3, 5], b[7, 900], x[9, 0] = float("nan"), float("inf"), float("inf")
