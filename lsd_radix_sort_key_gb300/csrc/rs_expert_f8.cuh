@@ -450,6 +450,7 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
         const Rows<T> pre(p.pre, p.pre_i, 0);
         const Rows<const T> residual(p.residual, p.residual_i, 0);
         const bool vec_bias = ((uintptr_t)p.bias | p.bias_e * sizeof(T)) % 16 == 0;
+        const bool q_sectors = ((uintptr_t)p.q | p.q_i) % 32 == 0;
         uint32_t n = 0, seen = 0;
         for (uint32_t tile = first_tile; tile < tiles; tile += tile_step, ++seen) {
             const TcTile t = tile_at(tile);
@@ -565,18 +566,31 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                 const uint32_t byte = scale_byte(most);
                 const float inverse = scale_inverse(byte);
                 const bool live = i < t.i_end;
-                auto put = [&](uint32_t c, const uint32_t (&v)[16]) {
+                // Two pieces are 32 adjacent bytes: one store where those are aligned.
+                auto put = [&](const uint32_t (&v)[16], const uint4& before, uint32_t c) {
                     const uint4 q = quantized16(v, inverse, all_finite);
-                    if (live && col(c) < cols) *reinterpret_cast<uint4*>(p.q + i * p.q_i + j_first + col(c)) = q;
+                    if (c % 2 == 0) return q;
+                    uint8_t* to = p.q + i * p.q_i + j_first;
+                    const uint4 lo = down ? q : before, hi = down ? before : q;
+                    const uint32_t at = min(col(c), col(c - 1));
+                    if (live && q_sectors && at + 16 < cols) {
+                        const uint32_t both[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        store_sector(to + at, both);
+                    } else if (live) {
+                        if (at < cols) *reinterpret_cast<uint4*>(to + at) = lo;
+                        if (at + 16 < cols) *reinterpret_cast<uint4*>(to + at + 16) = hi;
+                    }
+                    return q;
                 };
+                uint4 q{};
 #pragma unroll 1
                 for (uint32_t c = 2; c < 4; ++c) {
                     again(c);
                     if (c == 3 && some) release(acc_empty);
-                    put(c, z);
+                    q = put(z, q, c);
                 }
-                put(0, kept[0]);
-                put(1, kept[1]);
+                q = put(kept[0], q, 0);
+                put(kept[1], q, 1);
                 if (live && j_first % RS_QUANT_BLOCK == 0) p.q_scales[i * p.q_scales_i + j_first / RS_QUANT_BLOCK] = (uint8_t)byte;
             } else if (some) {
                 // Two pieces of 16 columns at a time: one is on its way while the other is
