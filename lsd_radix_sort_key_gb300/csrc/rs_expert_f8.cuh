@@ -18,8 +18,8 @@
 // overlap by 32 columns, which the epilogue reads first (`early`).
 //
 // What bounds it: the tensor pipe and, over a second, power.  8192^3 takes 297 us
-// (3.7 PFLOP/s; 4.1 with neither copies nor scales), 32768 x 2048 x 4096 172 us
-// without an epilogue and 215 with gelu and the values before it kept.  A tile of
+// (3.7 PFLOP/s; 4.1 with neither copies nor scales), 32768 x 2048 x 4096 168 us
+// without an activation, 174 with gelu and 203 with the values before it kept.  A tile of
 // 16 slices is 8200 cycles of the pipe and about 1300 until the next one's first
 // instruction.  Copying A once for two pairs (multicast in clusters of four) changed
 // nothing and left 8 SMs idle (36 such clusters fit).  Few rows are bound by the
@@ -141,7 +141,8 @@ __device__ __forceinline__ void add_pairs(uint32_t (&z)[16], const uint32_t (&v)
     }
 }
 
-__device__ __forceinline__ uint64_t both(float (*f)(float), uint64_t v)
+template <typename F>
+__device__ __forceinline__ uint64_t both(F f, uint64_t v)
 {
     return pair_of(f(__uint_as_float((uint32_t)v)), f(__uint_as_float((uint32_t)(v >> 32))));
 }
@@ -156,17 +157,17 @@ __device__ __forceinline__ uint64_t activate_pair(uint64_t z)
         const uint64_t e = both(fast_exp2, mul2(z, two(-kLog2e)));
         return mul2(z, both(fast_reciprocal, add2(e, two(1.0f))));
     } else {
-        const uint64_t magnitudes = z & 0x7FFFFFFF7FFFFFFFull;
-        const uint64_t t = both(fast_reciprocal, fma2(two(0.3275911f * 0.70710678118654752f), magnitudes, two(1.0f)));
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|), so that no sign decides; `minus` is -|z|,
+        // finite, as infinity times the zero of Phi would be NaN.
+        const uint64_t minus = both([](float v) { return fmaxf(-fabsf(v), -3.402823466e38f); }, z);
+        const uint64_t above = both([](float v) { return fmaxf(v, 0.0f); }, z);
+        const uint64_t t = both(fast_reciprocal, fma2(two(-0.3275911f * 0.70710678118654752f), minus, two(1.0f)));
         const uint64_t e = both(fast_exp2, mul2(mul2(z, z), two(-0.5f * kLog2e)));
         uint64_t poly = fma2(t, two(0.5f * 1.061405429f), two(0.5f * -1.453152027f));
         poly = fma2(t, poly, two(0.5f * 1.421413741f));
         poly = fma2(t, poly, two(0.5f * -0.284496736f));
         poly = fma2(t, poly, two(0.5f * 0.254829592f));
-        const uint64_t low = mul2(mul2(t, poly), e), high = fma2(low, two(-1.0f), two(1.0f));
-        const uint32_t a = (int32_t)z < 0 ? (uint32_t)low : (uint32_t)high;
-        const uint32_t b = (int64_t)z < 0 ? (uint32_t)(low >> 32) : (uint32_t)(high >> 32);
-        return mul2(z, (uint64_t)b << 32 | a);
+        return fma2(minus, mul2(mul2(t, poly), e), above);
     }
 }
 
@@ -230,8 +231,11 @@ __device__ __forceinline__ uint4 quantized16(const uint32_t (&z)[16], float inve
 }
 
 // A is rows of map_a, B is rows of map_b, expert e's from row e * cols; both
-// have the reduction index adjacent.  QUANT: D leaves in 8 bits.
-template <typename T, bool PAIR, bool QUANT>
+// have the reduction index adjacent.  QUANT: D leaves in 8 bits.  RESIDUAL: p.residual
+// is added; a form of its own, as the registers that fetch it ahead keep the
+// activations of one piece from overlapping (32768 x 512 x 4096 with gelu 152 us with
+// them and 133 without).
+template <typename T, bool PAIR, bool QUANT, bool RESIDUAL>
 __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
     k_product_f8(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, F8Args<T> p)
 {
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                 uint32_t z[2][16], add[2][8], bias[8];
                 auto col = [&](uint32_t c) { return (down ? W / 16 - 1 - c : c) * 16; };
                 auto fetch_residual = [&](uint32_t c, uint32_t (&r)[8]) {
-                    if (p.residual && c < W / 16 && col(c) < cols)
+                    if (RESIDUAL && c < W / 16 && col(c) < cols)
                         fetch_piece<T>(r, residual, i0, t.i_end, j_first + col(c), p.cols);
                 };
                 auto fetch_bias = [&](uint32_t c) {
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                             store_piece<T>(stage, out, pre, i0, t.i_end, j, p.cols);
                         }
                         activate_pairs(zz, p.act);
-                        if (p.residual && col(c) < cols) {
+                        if (RESIDUAL && col(c) < cols) {
                             spread_piece<T>(stage, add[o], residual, j, p.cols);
                             add_pairs<T>(zz, add[o]);
                         }

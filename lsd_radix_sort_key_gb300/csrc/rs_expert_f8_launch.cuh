@@ -7,11 +7,11 @@
 
 namespace rsx {
 
-template <typename T, bool PAIR, bool QUANT>
+template <typename T, bool PAIR, bool QUANT, bool RESIDUAL>
 rs_status f8_launch(const F8Operands& o, const F8Args<T>& args, int sms, cudaStream_t s)
 {
     using S = F8Shape<PAIR, QUANT>;
-    const auto kernel = k_product_f8<T, PAIR, QUANT>;
+    const auto kernel = k_product_f8<T, PAIR, QUANT, RESIDUAL>;
     constexpr size_t most = S::smem(RS_EXPERTS_MAX);
     static_assert(most <= kBlockSmem);
     if (!allow_smem(kernel, most)) return RS_ERR_CUDA;
@@ -58,19 +58,19 @@ inline bool f8_pairs(size_t rows, size_t experts, size_t cols, size_t slices, in
     return time(0.27, 2.6, 2 * kTcRows, 256, sms / 2) + 2.5 < time(0.31, 0.8, kTcRows, 128, sms);
 }
 
-template <typename T, bool QUANT>
+template <typename T, bool QUANT, bool RESIDUAL>
 rs_status f8_run(const F8Operands& o, const F8Args<T>& args, cudaStream_t s)
 {
     const int sms = sm_count();
     if (sms < 2) return RS_ERR_CUDA;
     const bool pair = f8_pairs(args.rows, args.experts, args.cols, ceil_div(args.reduce, kF8Depth), sms);
-    return pair ? f8_launch<T, true, QUANT>(o, args, sms, s) : f8_launch<T, false, QUANT>(o, args, sms, s);
+    return pair ? f8_launch<T, true, QUANT, RESIDUAL>(o, args, sms, s) : f8_launch<T, false, QUANT, RESIDUAL>(o, args, sms, s);
 }
 
 template <typename T>
 rs_status f8_product(const F8Operands& o, const F8Args<T>& args, cudaStream_t s)
 {
-    return args.q ? f8_run<T, true>(o, args, s) : f8_run<T, false>(o, args, s);
+    return args.q ? f8_run<T, true, false>(o, args, s) : args.residual ? f8_run<T, false, true>(o, args, s) : f8_run<T, false, false>(o, args, s);
 }
 
 }  // namespace rsx

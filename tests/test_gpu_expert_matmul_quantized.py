@@ -264,6 +264,20 @@ def test_nan_and_infinity_stay_in_their_rows():
     assert bool(torch.isnan(q[20].double()[inf]).all()) and bool((scales[20].double() <= 2.0**120).all())
 
 
+@pytest.mark.parametrize("rows", [40, 4096])
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+def test_activations_of_infinity(rows, act):
+    # sums of zero, so that the values before the activation are the biases
+    x, xs, w, ws, off = operands([rows], 256, 512)
+    x = torch.zeros_like(x.view(torch.uint8)).view(torch.float8_e4m3fn)
+    bias = torch.randn(1, 512, device=DEV, generator=gen(3)).bfloat16()
+    bias[0, :6] = torch.tensor([float("inf"), float("nan"), 3e38, -3e38, 1e20, -1e20])
+    y = rs.expert_matmul_quantized(x, xs, w, ws, off, bias=bias, activation=act)
+    assert bool(torch.isposinf(y[:, 0]).all()) and bool(torch.isnan(y[:, 1]).all())
+    assert torch.equal(y[:, 2:6], torch.tensor([3e38, 0, 1e20, 0], device=DEV).bfloat16().expand(rows, 4))
+    assert bool(torch.isfinite(y[:, 6:]).all())
+
+
 def test_views_and_strides(way):
     g = gen(5)
     x, xs, w, ws, off = operands([33, 70], 272, 200)
