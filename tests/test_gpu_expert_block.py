@@ -182,6 +182,95 @@ def test_a_training_step_captured_beside_an_eager_one():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("before", ["nothing", "copy", "fill", "kernel", "join", "kernel and join", "join and kernel"])
+def test_what_a_call_reads_is_there(captured, before):
+    # The work before a call has ended when the call reads, whatever it is and
+    # whichever stream it was on.
+    rows, width = 4096, 512
+    fresh = torch.randn(rows, width, device="cuda", generator=gen(4)).bfloat16()
+    big, late = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.empty_like(fresh)
+    weight = torch.ones(width, device="cuda")
+    w = torch.randn(1, 512, width, device="cuda", generator=gen(5)).bfloat16()
+    offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    position = torch.arange(rows, dtype=torch.int32, device="cuda")[:, None]
+    wq, ws = rs.expert_quantize_weights(w)
+    q0, s0 = rs.expert_quantize(fresh)
+    side = torch.cuda.Stream()
+
+    def produce(into, source):
+        if "join" in before:
+            ready = torch.cuda.current_stream()
+            side.wait_stream(ready)
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(100000)
+                into.copy_(source)
+            if before.startswith("kernel"):
+                big[:4096].add_(1)
+            ready.wait_stream(side)
+            if before.endswith("kernel"):
+                big[:4096].add_(1)
+        elif before != "nothing":
+            torch.cuda._sleep(100000)
+            if before == "copy":
+                big[:1 << 27].copy_(big[1 << 27:])
+                into.copy_(source)
+            elif before == "fill":
+                into.copy_(source)
+                big.zero_()
+            else:
+                torch.mul(source.view(torch.uint8), 1, out=into.view(torch.uint8))
+        else:
+            into.copy_(source)
+
+    def call():
+        out = []
+        q, s = torch.zeros_like(q0.view(torch.uint8)), torch.zeros_like(s0.view(torch.uint8))
+        produce(late, fresh)
+        out += [rs.expert_norm(late, weight)]
+        late.zero_()
+        produce(late, fresh)
+        out += rs.expert_quantize(late)
+        late.zero_()
+        produce(late, fresh)
+        out += rs.expert_dispatch_quantized(late, position, offsets)
+        late.zero_()
+        produce(late, fresh)
+        out += rs.expert_norm_grad(late, late, weight)[:2]
+        produce(q, q0.view(torch.uint8))
+        produce(s, s0.view(torch.uint8))
+        out += [rs.expert_matmul_quantized(q.view(q0.dtype), s.view(s0.dtype), wq, ws, offsets)]
+        q.zero_()
+        s.zero_()
+        return [t.view(torch.uint8) if t.dtype.itemsize == 1 else t for t in out]
+
+    def plain_calls():
+        out = [rs.expert_norm(fresh, weight), *rs.expert_quantize(fresh),
+               *rs.expert_dispatch_quantized(fresh, position, offsets), *rs.expert_norm_grad(fresh, fresh, weight)[:2],
+               rs.expert_matmul_quantized(q0, s0, wq, ws, offsets)]
+        torch.cuda.synchronize()
+        return [t.view(torch.uint8) if t.dtype.itemsize == 1 else t for t in out]
+
+    want = plain_calls()
+    torch.cuda.synchronize()
+    if captured:
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    else:
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
 def test_the_example_runs():
     argv = sys.argv
     sys.argv = ["expert_layer.py", "--tokens", "256", "--width", "128", "--steps", "2"]
