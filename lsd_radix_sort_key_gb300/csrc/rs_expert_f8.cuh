@@ -201,14 +201,24 @@ __device__ __forceinline__ uint32_t max_of_both(uint32_t v, uint32_t* mine, cons
     return v;
 }
 
-// The largest magnitude of 16 values, or of the finite ones among them.
-__device__ __forceinline__ uint32_t largest16(const uint32_t (&z)[16], bool finite_only)
+// The largest magnitude of 16 values (NaN, as bits above all others, if one is NaN).
+__device__ __forceinline__ uint32_t largest16(const uint32_t (&z)[16])
+{
+    float most = 0.0f;
+#pragma unroll
+    for (uint32_t c = 0; c < 16; ++c)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(__uint_as_float(z[c]))));
+    return __float_as_uint(most);
+}
+
+// The largest magnitude of the finite ones among 16 values.
+__device__ __forceinline__ uint32_t largest_finite16(const uint32_t (&z)[16])
 {
     uint32_t most = 0;
 #pragma unroll
     for (uint32_t c = 0; c < 16; ++c) {
         const uint32_t m = z[c] & 0x7FFFFFFFu;
-        most = max(most, finite_only && m >= kNotFinite ? 0u : m);
+        most = max(most, m >= kNotFinite ? 0u : m);
     }
     return most;
 }
@@ -216,6 +226,7 @@ __device__ __forceinline__ uint32_t largest16(const uint32_t (&z)[16], bool fini
 // 16 values rounded to 8 bits.
 __device__ __forceinline__ uint4 quantized16(const uint32_t (&z)[16], float inverse, bool all_finite)
 {
+    const uint64_t by = pair_of(inverse, inverse);
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -223,8 +234,10 @@ __device__ __forceinline__ uint4 quantized16(const uint32_t (&z)[16], float inve
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             f[c] = __uint_as_float(z[4 * k + c]);
-            f[c] = (all_finite ? f[c] : finite_or_nan(f[c])) * inverse;
+            if (!all_finite) f[c] = finite_or_nan(f[c]);
         }
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) unpair(mul2(pair_of(f[c], f[c + 1]), by), f[c], f[c + 1]);
         w[k] = to_e4m3x4(f[0], f[1], f[2], f[3]);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -541,13 +554,13 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                         tmem_load_wait(z);
                     }
                     finish(c, z);
-                    most = max(most, largest16(z, false));
+                    most = max(most, largest16(z));
                     if (some && cols) tmem_store16(acc + col(c), z);
                 }
 #pragma unroll
                 for (uint32_t c = 0; c < 2; ++c) {
                     finish(c, kept[c]);
-                    most = max(most, largest16(kept[c], false));
+                    most = max(most, largest16(kept[c]));
                 }
                 tmem_store_wait();
                 most = max_of_both(most, mine, other, id);
@@ -559,11 +572,11 @@ __global__ void __launch_bounds__((F8Shape<PAIR, QUANT>::kThreads), 1)
                     }
                 };
                 if (!all_finite) {
-                    most = max(largest16(kept[0], true), largest16(kept[1], true));
+                    most = max(largest_finite16(kept[0]), largest_finite16(kept[1]));
 #pragma unroll 1
                     for (uint32_t c = 2; c < 4; ++c) {
                         again(c);
-                        most = max(most, largest16(z, true));
+                        most = max(most, largest_finite16(z));
                     }
                     most = max_of_both(most, mine, other, id);
                 }
