@@ -673,6 +673,7 @@ rs_status norm_gradient(const NormArgs<T>& p, bool vectors, uint32_t blocks, cud
 // about 576 where its elements are strided (four or eight to a thread), else one.
 inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem, bool block)
 {
+    if (width == 0) return 0;
     const bool strided = width * elem % 16 && width <= 2048;
     const size_t threads = align_up(strided ? ceil_div(width, block ? 4 : 8) : ceil_div(width * elem, 16), 32);
     const size_t per = threads > (strided ? 288 : 256) ? 1 : (strided ? 576 : 768) / threads, blocks = 152 * (per < 8 ? per : 8);
