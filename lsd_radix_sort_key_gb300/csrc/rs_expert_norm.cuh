@@ -546,11 +546,13 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED 
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float f[N];
-                    feed.get(f, kB, i);
-                    times_plus(f, f, -cb, du[i]);
-                    times(f, f, rb);
-                    store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(f));
+                    if (p.block_weight) {  // (else the block itself has no part in it, whatever it holds)
+                        float f[N];
+                        feed.get(f, kB, i);
+                        times_plus(f, f, -cb, du[i]);
+                        times(du[i], f, rb);
+                    }
+                    store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(du[i]));
                 }
             }
             if (r + 1 == last || r + 1 == gate_end) {
