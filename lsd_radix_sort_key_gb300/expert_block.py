@@ -374,7 +374,7 @@ def _norm_inputs(x, weight, block, block_weight, gate, residual_scale, eps):
         if kind is not None and t.dtype != kind:
             raise TypeError(f"{what}: {kind} wanted, as the other parameters are, got {t.dtype}")
         kind = t.dtype
-    if gate is not None and (gate_rows < 1 or rows % gate_rows):
+    if gate is not None and rows and (gate_rows < 1 or rows % gate_rows):
         raise ValueError(f"gate: a number of rows that divides {rows} is wanted, got {gate_rows}")
     head = (ft, ft if kind is None else FTYPES[kind], rows, width, eps, residual_scale, gate_rows, x.data_ptr(), xs,
             0 if block is None else block.data_ptr(), bs)

@@ -1,5 +1,5 @@
-"""Norms and their gradients at the edges: rows without columns, infinities
-and NaN."""
+"""Norms and their gradients at the edges: rows without columns, no
+sequences, infinities and NaN."""
 import pytest
 
 import lsd_radix_sort_key_gb300 as rs
@@ -42,6 +42,19 @@ def test_no_columns(way, dt, rows):
     got = rs.expert_norm_grad(x, x, w, dy=x, block=x, block_weight=w, gate=w)
     assert [tuple(t.shape) for t in got] == [(rows, 0), (0,), (rows, 0), (0,), (0,)]
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("sequences", [0, 5])
+def test_no_rows_with_a_gate_for_each_sequence(way, dt, sequences):
+    # an empty batch, of no sequences or of empty ones
+    x, w = torch.empty(0, 264, dtype=TYPES[dt], device=DEV), torch.ones(264, device=DEV)
+    gate = torch.ones(sequences, 264, device=DEV)
+    y, h = rs.expert_norm(x, w, block=x, block_weight=w, gate=gate)
+    assert y.shape == h.shape == (0, 264)
+    got = rs.expert_norm_grad(x, y, w, dy=x, block=x, block_weight=w, gate=gate)
+    assert [tuple(t.shape) for t in got] == [(0, 264), (264,), (0, 264), (264,), (sequences, 264)]
+    assert all(bool((got[i] == 0).all()) for i in (1, 3, 4))
 
 
 @pytest.mark.parametrize("dt", TYPES)
