@@ -537,22 +537,21 @@ __global__ void __launch_bounds__(S::THREADS, S::THREADS > 256 ? 1 : S::STRIDED 
             }
         }
         if constexpr (BLOCK) {
-            if (p.dblock) {
-                float cb = 0.0f;
-                if (p.block_weight) {
-                    float dot[1] = {du_b.get()};
-                    block_sums(dot, mem, turn);
-                    cb = rb * dot[0] * p.per_width * rb;
-                }
+            // (a block without a weight has no part in its gradient, whatever it holds)
+            if (p.dblock && !p.block_weight) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(du[i]));
+            } else if (p.dblock) {
+                float dot[1] = {du_b.get()};
+                block_sums(dot, mem, turn);
+                const float cb = rb * dot[0] * p.per_width * rb;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    if (p.block_weight) {  // (else the block itself has no part in it, whatever it holds)
-                        float f[N];
-                        feed.get(f, kB, i);
-                        times_plus(f, f, -cb, du[i]);
-                        times(du[i], f, rb);
-                    }
-                    store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(du[i]));
+                    float f[N];
+                    feed.get(f, kB, i);
+                    times_plus(f, f, -cb, du[i]);
+                    times(f, f, rb);
+                    store_elements<S, T>(p.dblock + r * p.dblock_i, i, p.width, narrow<T, N>(f));
                 }
             }
             if (r + 1 == last || r + 1 == gate_end) {
