@@ -111,3 +111,28 @@ def test_infinities_and_nan_before_the_rounding(act):
     want = act64(torch.tensor([3.0], dtype=torch.float64, device=DEV), act)
     assert bool((scales[:, 0].double() == scale_of(want)).all()) and bool((scales[:, 1].double() == 1).all())
     assert bool((q[:, 4] == round_e4m3(want / scale_of(want))).all())
+
+
+@pytest.mark.parametrize("rows", [40, 4096])
+@pytest.mark.parametrize("outer", [520, 1000, 72])
+def test_blocks_of_zeros_have_a_scale_of_one(rows, outer):
+    # rows of an expert, not unused ones: zero sums, and sums that relu makes zero
+    x, xs, w, ws = zeros(rows, 256, 2, outer)
+    offsets = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device=DEV)
+    for act in ("none", "relu", "gelu", "silu"):
+        q, scales = rs.expert_matmul_quantized(x, xs, w, ws, offsets, activation=act, quantize=True)
+        assert bool((q.double() == 0).all()) and bool((scales.view(torch.uint8) == 127).all())
+    g = gen(outer)
+    x = (torch.randn(rows, 256, device=DEV, generator=g) * 60).to(E4M3)
+    w = (torch.randn(2, outer, 256, device=DEV, generator=g) * 60).to(E4M3)
+    # sums of at most 256 * 448 * 448 < 2^26 with a bias far below them in every other block
+    blocks = torch.arange(outer, device=DEV) // 128
+    for gone in (0, 1):
+        bias = torch.where(blocks % 2 == gone, -2.0**30, 0.0).expand(2, outer).bfloat16()
+        q, scales = rs.expert_matmul_quantized(x, xs, w, ws, offsets, bias=bias, activation="relu", quantize=True)
+        live = torch.arange(scales.shape[1], device=DEV) % 2 != gone
+        assert bool((scales.view(torch.uint8)[:, ~live] == 127).all()) and bool((q.double()[:, blocks % 2 == gone] == 0).all())
+        # the other blocks hold something, but where every sum of a few columns is negative
+        held = torch.nn.functional.pad(q.double(), (0, -outer % 128)).view(rows, -1, 128).amax(2) > 0
+        assert bool((scales.view(torch.uint8)[~held] == 127).all())
+        assert int(held[:, live].sum()) >= 0.9 * held[:, live].numel()
