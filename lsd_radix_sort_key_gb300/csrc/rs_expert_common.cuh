@@ -248,6 +248,10 @@ __device__ __forceinline__ void store_partial(T* row, int i, int width, const Ve
 
 constexpr size_t kBlockSmem = 227 * 1024;  // that a block can have
 
+// SMs, for choices of tiles and blocks.  Not asked of the device: temp's size and the
+// order of summed gradients go by them, and those are the descriptor's alone.
+constexpr size_t kSms = 152;
+
 // Lets a kernel be launched with up to `most` bytes of dynamic shared memory.
 // The limit belongs to the kernel on the device, not to the calling thread, so
 // `most` is what the kernel may ever need and no call lowers it under another
@@ -296,6 +300,17 @@ template <int N>
 struct Int {
     static constexpr int value = N;
 };
+
+// f of a value of an element type.
+template <typename F>
+rs_status by_type(int type, F f)
+{
+    switch (type) {
+    case RS_FLOAT32: return f(float{});
+    case RS_FLOAT16: return f(__half{});
+    default:         return f(__nv_bfloat16{});
+    }
+}
 
 inline bool valid_type(int t) { return t == RS_FLOAT32 || t == RS_FLOAT16 || t == RS_BFLOAT16; }
 inline size_t type_bytes(int t) { return t == RS_FLOAT32 ? 4 : 2; }

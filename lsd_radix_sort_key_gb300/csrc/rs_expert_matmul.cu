@@ -30,10 +30,6 @@ namespace {
 
 using namespace rsx;
 
-// SMs, for the sizes of tiles below.  Not asked of the device: temp's size and the
-// order of dbias's additions go by them, and those are the descriptor's alone.
-constexpr size_t kSms = 152;
-
 // -------------------------------------------- products by multiply-adds
 
 // Element (i, k) of A is a[i*a_i + k*a_k]; element (j, k) of B in range e is
@@ -703,16 +699,6 @@ rs_status gradient(const rs_expert_matmul_desc* d)
         }
     }
     return RS_OK;
-}
-
-template <typename F>
-rs_status by_type(int type, F f)
-{
-    switch (type) {
-    case RS_FLOAT32: return f(float{});
-    case RS_FLOAT16: return f(__half{});
-    default:         return f(__nv_bfloat16{});
-    }
 }
 
 }  // namespace

@@ -16,16 +16,6 @@ namespace {
 
 using namespace rsx;
 
-template <typename F>
-rs_status by_type(int type, F f)
-{
-    switch (type) {
-    case RS_FLOAT32: return f(float{});
-    case RS_FLOAT16: return f(__half{});
-    default:         return f(__nv_bfloat16{});
-    }
-}
-
 rs_status check_sizes(const rs_expert_norm_desc* d)
 {
     if (!d || !valid_type(d->type) || (d->param_type != d->type && d->param_type != RS_FLOAT32)) return RS_ERR_INVALID_ARG;

@@ -677,7 +677,7 @@ inline uint32_t norm_grad_blocks(size_t rows, size_t width, size_t elem, bool bl
     if (width == 0) return 0;
     const bool strided = width * elem % 16 && width <= 2048;
     const size_t threads = align_up(strided ? ceil_div(width, block ? 4 : 8) : ceil_div(width * elem, 16), 32);
-    const size_t per = threads > (strided ? 288 : 256) ? 1 : (strided ? 576 : 768) / threads, blocks = 152 * (per < 8 ? per : 8);
+    const size_t per = threads > (strided ? 288 : 256) ? 1 : (strided ? 576 : 768) / threads, blocks = kSms * (per < 8 ? per : 8);
     return (uint32_t)(rows < blocks ? rows : blocks);
 }
 

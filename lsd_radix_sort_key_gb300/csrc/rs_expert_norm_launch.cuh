@@ -61,7 +61,7 @@ rs_status norm_forward(const NormArgs<T>& p, bool vectors, cudaStream_t s)
             using S = decltype(shape);
             // as many blocks as an SM holds at once
             const size_t of = S::V == 1 ? 1024 : S::THREADS == 128 ? 768 : 512, per = threads > of ? 1 : of / threads < 16 ? of / threads : 16;
-            return norm_launch(k_norm<T, S, BLOCK>, p.rows < 152 * per ? p.rows : 152 * per, threads,
+            return norm_launch(k_norm<T, S, BLOCK>, p.rows < kSms * per ? p.rows : kSms * per, threads,
                                Feed<T, S, BLOCK ? 2 : 1>::smem(threads), p, s);
         });
     };

@@ -186,7 +186,7 @@ rs_status launch_rows(const RowArgs<T>& p, bool vectors, cudaStream_t s)
         return cudaGetLastError() == cudaSuccess ? RS_OK : RS_ERR_CUDA;
     };
     constexpr int V = sizeof(T) == 4 ? 2 : 4;
-    const bool few = p.units < (size_t)kUnits * V * 4 * 152;  // would leave SMs without work
+    const bool few = p.units < (size_t)kUnits * V * 4 * kSms;  // would leave SMs without work
     if (vectors)
         return few ? run(k_quantize_rows<T, false, DISPATCH, 1>, 1) : run(k_quantize_rows<T, false, DISPATCH, V>, V);
     return few ? run(k_quantize_rows<T, true, DISPATCH, 1>, 1) : run(k_quantize_rows<T, true, DISPATCH, 2>, 2);
@@ -307,16 +307,6 @@ __global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 4 ? 2 : 3) k_quan
 }
 
 // ------------------------------------------------------------- host side
-
-template <typename F>
-rs_status by_type(int type, F f)
-{
-    switch (type) {
-    case RS_FLOAT32: return f(float{});
-    case RS_FLOAT16: return f(__half{});
-    default:         return f(__nv_bfloat16{});
-    }
-}
 
 // Quantised rows and their scales, which `rows` rows of `width` values need.
 struct Quantized {
