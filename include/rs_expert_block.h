@@ -71,7 +71,8 @@ rs_status rs_expert_quantize_weights(rs_float_type type, const void* w, size_t w
 
 /*
  * The experts' products of quantised rows and weights, on the tensor cores
- * with float32 sums.  x: rows x inner, 16-byte aligned rows (base and
+ * with float32 sums (which cut off below the last bit once for every 32
+ * products).  x: rows x inner, 16-byte aligned rows (base and
  * x_stride); w: row (e, n) at w + (e*outer + n)*w_stride, 16-byte aligned;
  * scales as the quantisers write them, x's with a row stride.  bias,
  * residual, y and pre are of `type`, binary16 or bfloat16, with any stride >=
@@ -80,6 +81,9 @@ rs_status rs_expert_quantize_weights(rs_float_type type, const void* w, size_t w
  * Either y (outer values per row), or q and q_scales (y quantised, from its
  * float32 values; rows as rs_expert_quantize writes them; no residual) is
  * given, and pre if the values before the activation are wanted.  inner >= 1.
+ * Activations of results in 16 bits are as in rs_expert_matmul; of quantised
+ * ones they are off by a few units of float32's last place (silu 8 + 1.25 |z|,
+ * gelu 16 + 1.25 z^2 times 2^-24 of the value, z being the sum plus bias).
  * The exponents of two blocks that meet in a product may add up to anything a
  * float32 holds; a scale byte of 255 is NaN.
  *

@@ -5,7 +5,9 @@
 // 256 x 256, a cluster of two on neighbouring SMs).  Scales are powers of two,
 // which tcgen05.mma.kind::mxf8f6f4 applies itself to every 32 products that it
 // adds, exactly, so the sums stay in one float32 accumulator in tensor memory
-// and nothing is added up outside the tensor pipe.  Warp 0 copies 128-deep
+// and nothing is added up outside the tensor pipe.  Each instruction's addition to it
+// (32 products) cuts off below float32's last bit, where an adder in registers would
+// round.  Warp 0 copies 128-deep
 // slices of A and B, one scale block each, into a ring of shared-memory stages
 // (TMA, 128-byte swizzle); warp 3 gathers the scales of eight slices at a time, a
 // 32-bit word for each four of a row, into a ring of its own; one thread of warp 1
@@ -18,9 +20,11 @@
 // overlap by 32 columns, which the epilogue reads first (`early`).
 //
 // What bounds it: the tensor pipe and, over a second, power.  8192^3 takes 297 us
-// (3.7 PFLOP/s; 4.1 with neither copies nor scales), 32768 x 2048 x 4096 168 us
-// without an activation, 174 with gelu and 203 with the values before it kept.  A tile of
-// 16 slices is 8200 cycles of the pipe and about 1300 until the next one's first
+// (3.7 PFLOP/s; 4.1 with neither copies nor scales), 32768 x 2048 x 4096 of 16 even
+// groups in a short burst 168 us without an activation, 174 with gelu and 203 with the
+// values before it kept; in longer runs, where power counts, 182, 188 and 217, and
+// 226 with uneven groups.  Quantised results are bound by their epilogue: 16384 x
+// 2048 x 2048 with silu 63 us.  A tile of 16 slices is 8200 cycles of the pipe and about 1300 until the next one's first
 // instruction.  Copying A once for two pairs (multicast in clusters of four) changed
 // nothing and left 8 SMs idle (36 such clusters fit).  Few rows are bound by the
 // weights' way from device memory (128 rows, 64 experts of 2048 x 2048: 48 us,

@@ -365,7 +365,8 @@ __host__ __device__ inline uint32_t first_row(uint32_t block, uint32_t blocks, u
 
 constexpr size_t kNormSmem = 128 * 1024;  // the most that a block's rows take: 512 threads, 4 matrices
 
-// 1 / sqrt(mean + eps); the hardware's root is off by two ulps at most.
+// 1 / sqrt(mean + eps); the hardware's root is off by two ulps at most.  (Rounded
+// correctly it costs the gradient of 16384 x 2048 5 us of 73, for errors 4 to 8% smaller.)
 __device__ __forceinline__ float inverse_root(float sum, float per_width, float eps) { return rsqrtf(fmaf(sum, per_width, eps)); }
 
 // Each block walks adjacent rows.  The parameters' columns stay in registers (a
