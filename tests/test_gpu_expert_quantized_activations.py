@@ -136,3 +136,19 @@ def test_blocks_of_zeros_have_a_scale_of_one(rows, outer):
         held = torch.nn.functional.pad(q.double(), (0, -outer % 128)).view(rows, -1, 128).amax(2) > 0
         assert bool((scales.view(torch.uint8)[~held] == 127).all())
         assert int(held[:, live].sum()) >= 0.9 * held[:, live].numel()
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_values_do_not_depend_on_their_neighbours(act):
+    # values far below zero take a longer way, and leave those beside them as they are
+    g = gen(8)
+    z = torch.randn(1, 512, device=DEV, generator=g).bfloat16()
+    x, xs, w, ws = zeros(300, 128, 1, 512)
+    offsets = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    want = rs.expert_matmul_quantized(x, xs, w, ws, offsets, bias=z, activation=act, quantize=True)[0]
+    deep = z.clone()
+    deep[0, 5::16] = -95.0 if act == "silu" else -13.5
+    got = rs.expert_matmul_quantized(x, xs, w, ws, offsets, bias=deep, activation=act, quantize=True)[0]
+    same = torch.ones(512, dtype=torch.bool, device=DEV)
+    same[5::16] = False
+    assert torch.equal(got.view(torch.uint8)[:, same], want.view(torch.uint8)[:, same])
