@@ -5,15 +5,14 @@
 // 256 x 256, a cluster of two on neighbouring SMs).  Scales are powers of two,
 // which tcgen05.mma.kind::mxf8f6f4 applies itself to every 32 products that it
 // adds, exactly, so the sums stay in one float32 accumulator in tensor memory
-// and nothing is added up outside the tensor pipe.  Each instruction's addition to it
-// (32 products) cuts off below float32's last bit, where an adder in registers would
-// round.  Warp 0 copies 128-deep
-// slices of A and B, one scale block each, into a ring of shared-memory stages
-// (TMA, 128-byte swizzle); warp 3 gathers the scales of eight slices at a time, a
-// 32-bit word for each four of a row, into a ring of its own; one thread of warp 1
-// has those of four slices at a time copied to tensor memory and issues the
-// products; 16 epilogue warps read finished accumulators, apply the epilogue and
-// store.
+// and nothing is added up outside the tensor pipe.  (Each instruction's addition to
+// it, of 32 products, cuts off below float32's last bit, where an adder in registers
+// would round.)  Warp 0 copies 128-deep slices of A and B, one scale block each, into
+// a ring of shared-memory stages (TMA, 128-byte swizzle); warp 3 gathers the scales of
+// eight slices at a time, a 32-bit word for each four of a row, into a ring of its
+// own; one thread of warp 1 has those of four slices at a time copied to tensor memory
+// and issues the products; 16 epilogue warps read finished accumulators, apply the
+// epilogue and store.
 //
 // Tensor memory (512 columns): two accumulators and two sets of scales.  A
 // pair's accumulators are 256 columns each and there is room for 480: they
@@ -24,11 +23,11 @@
 // groups in a short burst 168 us without an activation, 174 with gelu and 203 with the
 // values before it kept; in longer runs, where power counts, 182, 188 and 217, and
 // 226 with uneven groups.  Quantised results are bound by their epilogue: 16384 x
-// 2048 x 2048 with silu 63 us.  A tile of 16 slices is 8200 cycles of the pipe and about 1300 until the next one's first
-// instruction.  Copying A once for two pairs (multicast in clusters of four) changed
-// nothing and left 8 SMs idle (36 such clusters fit).  Few rows are bound by the
-// weights' way from device memory (128 rows, 64 experts of 2048 x 2048: 48 us,
-// 5.6 TB/s).
+// 2048 x 2048 with silu 63 us.  A tile of 16 slices is 8200 cycles of the pipe and
+// about 1300 until the next one's first instruction.  Copying A once for two pairs
+// (multicast in clusters of four) changed nothing and left 8 SMs idle (36 such
+// clusters fit).  Few rows are bound by the weights' way from device memory (128 rows,
+// 64 experts of 2048 x 2048: 48 us, 5.6 TB/s).
 #pragma once
 
 #include "rs_expert_e4m3.cuh"
